@@ -9,6 +9,9 @@ ones numpy arrays; calls run on torch's current stream unless given one.
     seq = model.new_sequence(max_ctx_rows)
     model.ctx_append(seq, pos, taps)      # taps [n][n_taps*hidden] float32
     logits, tokens = model.block([seq], [anchor_tok], [anchor_pos], block_len)
+
+The target's own pass over a drafted block (target.py): paged_append,
+paged_attention and verify_drafts.
 """
 from __future__ import annotations
 
@@ -18,6 +21,8 @@ import numpy as np
 
 from . import _abi
 from ._abi import QUANT_F32, QUANT_Q4G32, MAT_FC, MAT_HEAD, mat_layer  # noqa: F401
+from .target import (paged_append, paged_attention, paged_attention_workspace, rope_inv_freq,  # noqa: F401
+                     verify_drafts, verify_workspace)
 
 _lib = None
 

@@ -51,7 +51,33 @@ class Weights(C.Structure):
                 ("successor_codebook", C.c_void_p)]
 
 
+# element types of the target's verification pass
+F32, BF16, F16, E4M3 = 0, 1, 2, 3
+
 _VP = C.c_void_p
+
+
+class PagedCache(C.Structure):
+    _fields_ = [("k", _VP), ("v", _VP), ("dtype", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("page_size", C.c_int32), ("n_pages", C.c_int64), ("k_strides", C.c_int64 * 3),
+                ("v_strides", C.c_int64 * 3), ("k_scale", _VP), ("v_scale", _VP)]
+
+
+class PagedRows(C.Structure):
+    _fields_ = [("n_seqs", C.c_int32), ("max_pages", C.c_int32), ("n_rows", C.c_int64), ("row_start", _VP),
+                ("kv_len", _VP), ("table", _VP), ("table_stride", C.c_int64)]
+
+
+class HeadRows(C.Structure):
+    _fields_ = [("data", _VP), ("dtype", C.c_int32), ("heads", C.c_int32), ("row_stride", C.c_int64),
+                ("head_stride", C.c_int64)]
+
+
+class Rotation(C.Structure):
+    _fields_ = [("inv_freq", _VP), ("rotary", C.c_int32), ("interleaved", C.c_int32), ("scale", C.c_float)]
+
+
+_PC, _PR, _PH = C.POINTER(PagedCache), C.POINTER(PagedRows), C.POINTER(HeadRows)
 _SIGS = {
     "dflash_init": (C.c_int, [C.POINTER(Geometry), C.POINTER(Weights), C.c_int, _VP, C.POINTER(_VP)]),
     "dflash_free": (None, [_VP]),
@@ -86,6 +112,12 @@ _SIGS = {
                                          _VP, _VP, _VP]),
     "dflash_attention_noalloc": (C.c_int, [_VP, C.POINTER(_VP), C.c_int32, C.c_int32, C.POINTER(C.c_int64),
                                            C.c_int32, _VP, _VP, _VP]),
+    "dflash_paged_append": (C.c_int, [_PC, _PR, _PH, _PH, _PH, _PH, _VP, _VP, C.c_float, C.POINTER(Rotation), _VP]),
+    "dflash_paged_attention": (C.c_int, [_PC, _PR, _PH, _PH, _VP, C.c_float, C.c_int32, _VP, C.c_int64, _VP]),
+    "dflash_paged_attention_workspace": (C.c_int64, [_PC, C.c_int32, C.c_int64, C.c_int32]),
+    "dflash_verify": (C.c_int, [_VP, C.c_int32, C.c_int64, _VP, C.c_int64, _VP, _VP, _VP, _VP, _VP, C.c_int32,
+                                C.c_int64, C.c_int64, _VP, _VP, _VP, _VP, C.c_int64, _VP]),
+    "dflash_verify_workspace": (C.c_int64, [C.c_int32, C.c_int64, C.c_int64]),
 }
 
 

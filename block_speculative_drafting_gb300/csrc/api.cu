@@ -210,6 +210,20 @@ int cuda_fail(dflash_model* m, int e, const char* what) {
     return set_err(m, (e == cudaErrorMemoryAllocation) ? DFLASH_ENOMEM : DFLASH_ECUDA, msg);
 }
 
+}  // namespace
+
+// The reason of a failed call that has no model (dflash_last_error(NULL)).
+int dflash::set_thread_error(int code, const char* msg) {
+    try {
+        g_init_error = msg;
+    } catch (...) {
+        g_init_error.clear();  // no memory for the text: the code alone
+    }
+    return code;
+}
+
+namespace {
+
 #define CK(m, expr)                                                      \
     do {                                                                 \
         int e__ = (int)(expr);                                           \

@@ -1,0 +1,810 @@
+// Attention of a pass's new rows (one token a sequence, or a drafted block)
+// over a paged key/value cache.
+//
+// The query heads that share a key/value head share its reads: the unit of
+// work is a (sequence, key/value head, tile of MT rows of the sequence's rows x
+// group heads), its keys go by in tiles of 128, and softmax runs online in one
+// pass (a running reference m and sum l a row, the output rescaled when m
+// moves).  The memory it cannot do without is each key and value once.
+//
+// Work split.  All tiles of all units, in order, are one line that the CTAs
+// (one an SM) cut into equal parts: a CTA takes whole units, and the head and
+// tail of units that its neighbours share.  The line's length comes from
+// kv_len on the device, so sequences of any mix of lengths are balanced and a
+// captured call follows the lengths of its replay.  A unit that one CTA holds
+// whole is written out at once; a shared one leaves (m, l, O) per part in the
+// workspace, and a second small kernel joins the parts.
+//
+// In a CTA, 8 warps form KG key groups of RW row warps.  A warp holds 16 rows
+// (m16n8k16 MMAs: scores from K by ldmatrix, P from the scores' registers,
+// values by transposed ldmatrix).  A group's RW warps share its stages (16 RW
+// keys and values, each warp copies 16 of both with 16-byte asynchronous
+// copies) and meet once a stage; groups run on their own and meet once a unit.
+// A warp finds the pages of its next stage's keys while it copies this one's.
+//
+// Masking.  Keys that no row may see (past the end, pages not held) are not
+// read: their slots are zero-filled and a bit mask sends their scores to -inf.
+// A key that some rows see and others do not (the new rows among themselves, a
+// window's edge) is masked per row; P is then 0 there, and 0 times an infinite
+// or NaN value would not be, so such stages look for non-finite values and,
+// where there are any, add P V row by row with the hidden keys left out.
+#include "kernels.cuh"
+#include "paged.cuh"
+
+namespace dflash {
+
+constexpr int kPaThreads = 256, kPaWarps = 8;
+constexpr int kPaTile = 128;     // keys a CTA takes at once: 16 a warp
+constexpr float kPaLazy = 8.f;   // log2 units a score may pass the reference before a rescale
+
+struct PaArgs {
+    PagedCache C;
+    PagedRows R;
+    HeadRows q, out;
+    float* lse;
+    float* ws_o;     // [2 CTAs][MT][HD]
+    float2* ws_ml;   // [2 CTAs][MT]
+    float scale_log2;
+    int window, group;
+};
+
+// What the walk needs of one sequence.
+struct PaSeq {
+    int row0, rows, p0;  // its rows of the call; the position of the first
+    int lo, hi;          // keys that any of its rows may see
+    int ntiles, nunits;
+};
+
+DF_DEV PaSeq pa_seq(const PaArgs& A, int s, int mt) {
+    PaSeq q;
+    int b;
+    rows_of(A.R, s, q.row0, b);
+    q.rows = b - q.row0;
+    const int len = A.R.kv_len[s];
+    q.p0 = max(len, -1) - q.rows;  // a length below 0 reads as -1: no position of any row is held
+    q.hi = min(max(len, 0), A.R.cap);
+    q.lo = A.window > 0 ? max(0, q.p0 - A.window + 1) : 0;
+    q.ntiles = max(1, (q.hi - q.lo + kPaTile - 1) / kPaTile);  // a sequence with rows but no keys: one tile of nothing
+    q.nunits = (int)(((int64_t)q.rows * A.group + mt - 1) / mt) * A.C.kv_heads;
+    return q;
+}
+
+// Warp-wide: the line's length, and the share of a CTA.
+DF_DEV int64_t pa_total(const PaArgs& A, int mt, int lane) {
+    int64_t t = 0;
+    for (int s = lane; s < A.R.n_seqs; s += 32) {
+        const PaSeq q = pa_seq(A, s, mt);
+        t += (int64_t)q.ntiles * q.nunits;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    return t;
+}
+// Tiles before sequence `upto` (warp-wide).
+DF_DEV int64_t pa_before(const PaArgs& A, int mt, int lane, int upto) {
+    int64_t t = 0;
+    for (int s = lane; s < upto; s += 32) {
+        const PaSeq q = pa_seq(A, s, mt);
+        t += (int64_t)q.ntiles * q.nunits;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    return t;
+}
+// The sequence that holds tile t of the line, and the tiles before it.
+DF_DEV int pa_find(const PaArgs& A, int mt, int lane, int64_t t, int64_t& before) {
+    int64_t run = 0;
+    for (int s0 = 0; s0 < A.R.n_seqs; s0 += 32) {
+        int64_t w = 0;
+        if (s0 + lane < A.R.n_seqs) {
+            const PaSeq q = pa_seq(A, s0 + lane, mt);
+            w = (int64_t)q.ntiles * q.nunits;
+        }
+        int64_t in = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, in, o);
+            if (lane >= o) in += y;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, run + in > t);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            before = run + __shfl_sync(0xffffffffu, in - w, l);
+            return s0 + l;
+        }
+        run += __shfl_sync(0xffffffffu, in, 31);
+    }
+    before = run;
+    return A.R.n_seqs;
+}
+
+// A place on the line: tile `tile` of unit `u` of sequence `s`.
+struct PaCur {
+    PaSeq q;
+    int s, u, tile;
+    int64_t left;  // tiles of the CTA's share from here on
+};
+DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c) {
+    --c.left;
+    if (++c.tile < c.q.ntiles) return;
+    c.tile = 0;
+    if (++c.u < c.q.nunits || c.left <= 0) return;
+    c.u = 0;
+    do {
+        if (++c.s >= A.R.n_seqs) {  // (never, while the lengths stay as they were counted)
+            c.left = 0;
+            return;
+        }
+        c.q = pa_seq(A, c.s, mt);
+    } while (c.q.nunits == 0);
+}
+
+DF_DEV void cp16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+DF_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+DF_DEV void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+DF_DEV void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+DF_DEV void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+template <bool BF>
+DF_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 2^x by the special-function unit (relative error about 2^-22: the level of f32 rounding)
+DF_DEV float pa_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// two e4m3 codes -> two f16 (exact)
+DF_DEV uint32_t e4m3x2_f16x2(uint32_t codes) {
+    uint32_t y;
+    asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(y) : "r"(codes));
+    return y;
+}
+// (a, b) -> a pair of 16-bit floats, and what the rounding left
+template <bool BF>
+DF_DEV uint32_t pack2(float a, float b) {
+    if constexpr (BF) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+template <bool BF>
+DF_DEV float2 unpack2(uint32_t u) {
+    if constexpr (BF)
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
+    else
+        return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+
+// BF: MMAs and cache in bf16 (else f16).  E8: an e4m3 cache; its codes become
+// f16 exactly, and a query row is brought into f16 by a power of two.
+template <bool BF, bool E8, int HD, int RW>
+struct PaShape {
+    static constexpr int KG = kPaWarps / RW, SK = 16 * RW, MT = 16 * RW;
+    static constexpr int RB = HD * (E8 ? 1 : 2);  // bytes of a key row
+    static constexpr int CH = RB / 16;            // its 16-byte chunks
+    static constexpr int kStage = 2 * SK * RB;    // a group's stage: keys, then values
+    static constexpr int kRound = KG * kStage;
+    static constexpr int NST = 196608 / kRound < 6 ? 196608 / kRound : 6;
+    static constexpr int NF = HD / 8;             // output fragments of a warp
+    static constexpr int kMerge = KG > 1 ? KG / 2 * MT * HD * 4 : 0;
+    static constexpr size_t kSmem = (size_t)NST * kRound + kMerge;
+    // P as hi + lo pairs: the MMAs then add no rounding of their own to the
+    // output's.  Two more MMAs a value fragment: free while copies are awaited
+    // (one row warp a key), not with many row warps on the same keys.
+    static constexpr bool kSplitP = RW <= 2;
+};
+
+// byte offset of chunk c of key row r, so that eight rows' chunks of one column sit in different banks
+template <int CH>
+DF_DEV uint32_t pa_off(int r, int c) {
+    return (uint32_t)(r * CH * 16 + ((CH >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
+}
+
+template <bool BF, bool E8, int HD, int RW>
+__global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_constant__ PaArgs A) {
+    using S = PaShape<BF, E8, HD, RW>;
+    constexpr int NST = S::NST, CH = S::CH, MT = S::MT, NF = S::NF, KG = S::KG;
+    extern __shared__ __align__(128) unsigned char sm[];
+    __shared__ uint32_t vbits[kPaWarps][NST];  // a stage's valid keys, by copying warp
+    __shared__ float2 ml[KG][MT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+    const int kg = warp / RW, wr = warp % RW;
+    const uint32_t base = smem_addr(sm) + kg * NST * S::kStage;
+    pdl_wait();
+    pdl_trigger();
+
+    const int64_t total = pa_total(A, MT, lane);
+    const int64_t chunk = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t t0 = (int64_t)blockIdx.x * chunk;
+    if (t0 >= total) return;
+    PaCur cur;
+    {
+        int64_t before;
+        cur.s = pa_find(A, MT, lane, t0, before);
+        cur.q = pa_seq(A, cur.s, MT);
+        cur.u = (int)((t0 - before) / cur.q.ntiles);
+        cur.tile = (int)((t0 - before) % cur.q.ntiles);
+        cur.left = min(chunk, total - t0);
+    }
+
+    // ---------------------------------------------------------------- copies
+    // Lanes 0-15 hold the places of a stage's 16 key rows of this warp, lanes
+    // 16-31 those of its value rows; `ahead` belongs to the stage to copy next.
+    PaCur put = cur;
+    const unsigned char* ahead = nullptr;
+    auto place = [&](const PaCur& c) -> const unsigned char* {
+        const int key = c.q.lo + c.tile * kPaTile + kg * S::SK + wr * 16 + (lane & 15);
+        int slot = 0;
+        if (key >= c.q.hi) return nullptr;
+        const int64_t page = page_of(A.R, A.C.n_pages, c.s, key, slot);
+        if (page < 0) return nullptr;
+        const int h = c.u % A.C.kv_heads;
+        return lane < 16 ? A.C.k + page * A.C.ks[0] + slot * A.C.ks[1] + h * A.C.ks[2]
+                         : A.C.v + page * A.C.vs[0] + slot * A.C.vs[1] + h * A.C.vs[2];
+    };
+    if (put.left > 0) ahead = place(put);
+    int stage_put = 0;
+    auto copy = [&]() {
+        if (put.left > 0) {
+            const uint32_t st = base + stage_put * S::kStage;
+            const unsigned char* now = ahead;
+            const uint32_t bits = __ballot_sync(0xffffffffu, now != nullptr) & 0xffffu;
+            if (lane == 0) vbits[warp][stage_put] = bits;
+            pa_next(A, MT, put);
+            if (put.left > 0) ahead = place(put);
+            constexpr int RPI = 32 / CH;  // rows a copy instruction covers
+#pragma unroll
+            for (int i = 0; i < 32 / RPI; ++i) {
+                const int r = i * RPI + lane / CH, c = lane % CH;
+                const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(now), r);
+                const uint32_t dst = st + (r >> 4) * (S::SK * S::RB) + pa_off<CH>(wr * 16 + (r & 15), c);
+                const void* src = p ? reinterpret_cast<const unsigned char*>(p) + 16 * c : A.C.k;
+                cp16(dst, src, p ? 16 : 0);
+            }
+            stage_put = stage_put + 1 == NST ? 0 : stage_put + 1;
+        }
+        cp_commit();
+    };
+    auto group_sync = [&]() {
+        if constexpr (RW == 1)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * RW) : "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i) copy();
+
+    int stage = 0;
+    while (cur.left > 0) {
+        // ------------------------------------------------------------ a unit
+        const PaSeq sq = cur.q;
+        const int u = cur.u, tile0 = cur.tile;
+        const int h = u % A.C.kv_heads, rt = u / A.C.kv_heads;
+        const int mvalid = min(MT, sq.rows * A.group - rt * MT);
+        // this thread's rows gq and gq + 8: positions (-1: no row)
+        int pos[2], wlo[2];
+        uint32_t qf[HD / 16][4];
+        float rf[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int m = wr * 16 + gq + 8 * e;
+            const bool in = m < mvalid;
+            const int mm = rt * MT + m, r = mm / A.group, hq = h * A.group + mm % A.group;
+            pos[e] = in ? sq.p0 + r : -1;
+            wlo[e] = A.window > 0 ? pos[e] - A.window + 1 : 0;
+            const unsigned char* p = A.q.p + (int64_t)(sq.row0 + r) * A.q.rs + (int64_t)hq * A.q.hs;
+            rf[e] = 1.f;
+            if constexpr (!E8) {
+#pragma unroll
+                for (int j = 0; j < HD / 16; ++j) {
+                    qf[j][e] = in ? *reinterpret_cast<const uint32_t*>(p + (16 * j + 2 * tq) * 2) : 0u;
+                    qf[j][2 + e] = in ? *reinterpret_cast<const uint32_t*>(p + (16 * j + 8 + 2 * tq) * 2) : 0u;
+                }
+            } else {
+                // columns 16 j + 4 tq + {0, 1, 2, 3}: the order in which the codes come (below)
+                uint2 w[HD / 16];
+                float mx = 0.f;
+                const bool qb = A.q.dtype == kBF16;
+#pragma unroll
+                for (int j = 0; j < HD / 16; ++j) {
+                    w[j] = in ? *reinterpret_cast<const uint2*>(p + (16 * j + 4 * tq) * 2) : make_uint2(0u, 0u);
+                    if (qb) {
+                        const float2 a = unpack2<true>(w[j].x), b = unpack2<true>(w[j].y);
+                        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))));
+                    }
+                }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                // a bf16 row times 2^-x, its largest element in [1, 2): what f16 cannot hold of it then
+                // is under 2^-25 of that element
+                float down = 1.f;
+                if (qb && mx > 0.f && mx < INFINITY) {
+                    const int x = min(max(ilogbf(mx), -120), 120);
+                    down = ldexpf(1.f, -x);
+                    rf[e] = ldexpf(1.f, x);
+                }
+#pragma unroll
+                for (int j = 0; j < HD / 16; ++j) {
+                    if (qb) {
+                        const float2 a = unpack2<true>(w[j].x), b = unpack2<true>(w[j].y);
+                        qf[j][e] = pack2<false>(a.x * down, a.y * down);
+                        qf[j][2 + e] = pack2<false>(b.x * down, b.y * down);
+                    } else {
+                        qf[j][e] = w[j].x;
+                        qf[j][2 + e] = w[j].y;
+                    }
+                }
+            }
+        }
+        // scores in log2 units: (S rf) * c; never 0, so that -inf stays -inf
+        float c[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float ks = E8 && A.C.k_scale != nullptr ? A.C.k_scale[h] : 1.f;
+            c[e] = fminf(fmaxf(A.scale_log2 * ks * rf[e], 1e-37f), 3e38f);
+        }
+        // positions between which every row of the unit's tile sees every key
+        const int pmin = sq.p0 + (rt * MT) / A.group;
+        const int pmax = sq.p0 + (rt * MT + mvalid - 1) / A.group;
+        const int wtop = A.window > 0 ? pmax - A.window + 1 : 0;
+
+        float o[NF][4];
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[f][e] = 0.f;
+
+        bool last_tile;
+        do {
+            cp_wait<NST - 2>();
+            group_sync();
+            copy();
+            const uint32_t st = base + stage * S::kStage;
+            const uint32_t sv = st + S::SK * S::RB;
+            const int key0 = sq.lo + cur.tile * kPaTile + kg * S::SK;
+            constexpr int KB = S::SK < 32 ? S::SK : 32;  // keys of one softmax step
+#pragma unroll 1
+            for (int kb = 0; kb < S::SK; kb += KB) {
+                constexpr int NT = KB / 8;
+                uint32_t bits = vbits[kg * RW + kb / 16][stage];
+                if constexpr (KB == 32) bits |= vbits[kg * RW + kb / 16 + 1][stage] << 16;
+                if (bits == 0) continue;
+                const int kfirst = key0 + kb, klast = kfirst + KB - 1;
+                float sc[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
+                if constexpr (!E8) {
+#pragma unroll
+                    for (int j = 0; j < HD / 32; ++j)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            uint32_t b[4];
+                            ldsm4(b, st + pa_off<CH>(kb + n * 8 + (lane & 7), 4 * j + (lane >> 3)));
+                            mma16816<BF>(sc[n], qf[2 * j], b[0], b[1]);
+                            mma16816<BF>(sc[n], qf[2 * j + 1], b[2], b[3]);
+                        }
+                } else {
+                    // a chunk is 16 codes; lane 4 gq + tq receives codes 4 tq .. 4 tq + 3 of key gq
+#pragma unroll
+                    for (int j = 0; j < HD / 64; ++j)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            uint32_t b[4];
+                            ldsm4(b, st + pa_off<CH>(kb + n * 8 + (lane & 7), 4 * j + (lane >> 3)));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mma16816<false>(sc[n], qf[4 * j + i], e4m3x2_f16x2(b[i]), e4m3x2_f16x2(b[i] >> 16));
+                        }
+                }
+                const bool full = bits == (KB == 32 ? 0xffffffffu : 0xffffu) && klast <= pmin && kfirst >= wtop;
+                // bit 4 n + e of `hid`: this thread's score sc[n][e] is not in its row's view
+                uint32_t hid = 0;
+                if (!full) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int kk = n * 8 + 2 * tq + (e & 1), key = kfirst + kk;
+                            const bool see = ((bits >> kk) & 1u) && key <= pos[e >> 1] && key >= wlo[e >> 1];
+                            if (!see) {
+                                sc[n][e] = -INFINITY;
+                                hid |= 1u << (4 * n + e);
+                            }
+                        }
+                }
+                float mx[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[e] = fmaxf(sc[0][2 * e], sc[0][2 * e + 1]);
+#pragma unroll
+                    for (int n = 1; n < NT; ++n) mx[e] = fmaxf(mx[e], fmaxf(sc[n][2 * e], sc[n][2 * e + 1]));
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+                    mx[e] *= c[e];
+                }
+                const bool move = mx[0] > m[0] + kPaLazy || mx[1] > m[1] + kPaLazy;
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float to = mx[e] > m[e] + kPaLazy ? mx[e] : m[e];
+                        const float f = to == m[e] ? 1.f : pa_exp2(m[e] - to);
+                        m[e] = to;
+                        l[e] *= f;
+#pragma unroll
+                        for (int i = 0; i < NF; ++i) {
+                            o[i][2 * e] *= f;
+                            o[i][2 * e + 1] *= f;
+                        }
+                    }
+                }
+                const float mr[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sc[n][e] = pa_exp2(fmaf(sc[n][e], c[e >> 1], -mr[e >> 1]));
+                        l[e >> 1] += sc[n][e];
+                    }
+                // keys that some row of the tile sees and another does not: are their values finite?
+                bool plain = true;
+                if (!full && (klast > pmin || kfirst < wtop)) {
+                    uint32_t bad = 0;
+                    for (int i = lane; i < KB * CH; i += 32) {
+                        uint32_t w[4];
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                     : "r"(sv + pa_off<CH>(kb + i / CH, i % CH)));
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            if constexpr (E8) {
+                                // only S.1111.111 is not finite
+                                const uint32_t y = (w[x] & 0x7f7f7f7fu) + 0x01010101u;
+                                bad |= y & 0x80808080u;
+                            } else {
+                                constexpr uint32_t ex = BF ? 0x7f80u : 0x7c00u;
+                                bad |= (w[x] & ex) == ex;
+                                bad |= ((w[x] >> 16) & ex) == ex;
+                            }
+                        }
+                    }
+                    plain = !__any_sync(0xffffffffu, bad != 0);
+                }
+                if (plain) {
+#pragma unroll
+                    for (int k = 0; k < KB / 16; ++k) {
+                        uint32_t ph[4], pl[4];
+                        constexpr bool PB = BF && !E8;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float x = sc[2 * k + (i >> 1)][2 * (i & 1)], y = sc[2 * k + (i >> 1)][2 * (i & 1) + 1];
+                            ph[i] = pack2<PB>(x, y);
+                            if constexpr (S::kSplitP) {
+                                const float2 r = unpack2<PB>(ph[i]);
+                                pl[i] = pack2<PB>(x - r.x, y - r.y);
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < CH / 2; ++j) {
+                            uint32_t b[4];
+                            ldsm4t(b, sv + pa_off<CH>(kb + 16 * k + (lane & 15), 2 * j + (lane >> 4)));
+                            if constexpr (!E8) {
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    mma16816<BF>(o[2 * j + i], ph, b[2 * i], b[2 * i + 1]);
+                                    if constexpr (S::kSplitP) mma16816<BF>(o[2 * j + i], pl, b[2 * i], b[2 * i + 1]);
+                                }
+                            } else {
+                                // a register: two neighbouring columns of keys 2 tq, 2 tq + 1 -> even
+                                // columns to fragment 2 ch, odd ones to 2 ch + 1 (chunk ch)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const uint32_t x0 = __byte_perm(b[2 * i], 0, 0x3120),
+                                                   x1 = __byte_perm(b[2 * i + 1], 0, 0x3120);
+                                    const uint32_t e0 = e4m3x2_f16x2(x0), e1 = e4m3x2_f16x2(x1),
+                                                   d0 = e4m3x2_f16x2(x0 >> 16), d1 = e4m3x2_f16x2(x1 >> 16);
+                                    const int f = 2 * (2 * j + i);
+                                    mma16816<false>(o[f], ph, e0, e1);
+                                    mma16816<false>(o[f + 1], ph, d0, d1);
+                                    if constexpr (S::kSplitP) {
+                                        mma16816<false>(o[f], pl, e0, e1);
+                                        mma16816<false>(o[f + 1], pl, d0, d1);
+                                    }
+                                }
+                            }
+                        }
+                    }
+                } else {
+                    // key by key, the hidden ones left out
+#pragma unroll 1
+                    for (int kk = 0; kk < KB; ++kk) {
+                        const int n = kk >> 3, src = (lane & ~3) | ((kk & 7) >> 1);
+                        float p[2];
+                        bool out[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float x = 0.f;
+#pragma unroll
+                            for (int i = 0; i < NT; ++i)
+                                if (i == n) x = (kk & 1) ? sc[i][2 * e + 1] : sc[i][2 * e];
+                            p[e] = __shfl_sync(0xffffffffu, x, src);
+                            const uint32_t hb = __shfl_sync(0xffffffffu, hid, src);
+                            out[e] = (hb >> (4 * n + 2 * e + (kk & 1))) & 1u;
+                        }
+#pragma unroll
+                        for (int f = 0; f < NF; ++f)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                // the column of this thread's o[f][y] and o[f][2 + y]
+                                const int col = E8 ? 16 * (f >> 1) + 4 * tq + 2 * y + (f & 1) : 8 * f + 2 * tq + y;
+                                float val;
+                                const uint32_t at = sv + pa_off<CH>(kb + kk, col * (E8 ? 1 : 2) / 16) +
+                                                    (col * (E8 ? 1 : 2)) % 16;
+                                if constexpr (E8) {
+                                    uint32_t w;
+                                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(w) : "r"(at));
+                                    val = unpack2<false>(e4m3x2_f16x2(w)).x;
+                                } else {
+                                    uint16_t w;
+                                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(at));
+                                    val = unpack2<BF>(w).x;
+                                }
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (!out[e]) o[f][2 * e + y] = fmaf(p[e], val, o[f][2 * e + y]);
+                            }
+                    }
+                }
+            }
+            stage = stage + 1 == NST ? 0 : stage + 1;
+            last_tile = cur.tile + 1 == sq.ntiles;
+            pa_next(A, MT, cur);
+        } while (!last_tile && cur.left > 0);
+
+        // ------------------------------------------------------------ the unit's end
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        }
+        const bool whole = tile0 == 0 && last_tile;
+        // a part of a shared unit: its start goes to the CTA's second slot, any other part to the first
+        const int part = blockIdx.x * 2 + (tile0 == 0 ? 1 : 0);
+        float big[2];
+        if constexpr (KG > 1) {
+            if (tq == 0) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) ml[kg][wr * 16 + gq + 8 * e] = make_float2(m[e], l[e]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = wr * 16 + gq + 8 * e;
+                big[e] = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < KG; ++g) big[e] = fmaxf(big[e], ml[g][r].x);
+                float sum = 0.f;
+#pragma unroll
+                for (int g = 0; g < KG; ++g) {
+                    const float2 x = ml[g][r];
+                    sum += x.x == -INFINITY ? x.y : x.y * pa_exp2(x.x - big[e]);  // (a NaN sum without a maximum stays)
+                }
+                const float f = m[e] == -INFINITY ? 1.f : pa_exp2(m[e] - big[e]);
+                l[e] = sum;
+                m[e] = big[e];
+#pragma unroll
+                for (int i = 0; i < NF; ++i) {
+                    o[i][2 * e] *= f;
+                    o[i][2 * e + 1] *= f;
+                }
+            }
+            // the upper half of the groups hand their sums to the lower half
+            float* mg = reinterpret_cast<float*>(sm + (size_t)NST * S::kRound);
+            constexpr int H = KG / 2;
+            auto at = [&](int g, int i) { return mg + ((size_t)(g * RW + wr) * (NF * 4) + i) * 32 + lane; };
+            if (kg >= H) {
+#pragma unroll
+                for (int i = 0; i < NF * 4; ++i) *at(kg - H, i) = o[i / 4][i % 4];
+            }
+            __syncthreads();
+            if (kg < H) {
+#pragma unroll
+                for (int i = 0; i < NF * 4; ++i) o[i / 4][i % 4] += *at(kg, i);
+            }
+            if constexpr (H > 1) {
+                if (kg > 0 && kg < H) {
+#pragma unroll
+                    for (int i = 0; i < NF * 4; ++i) *at(kg, i) = o[i / 4][i % 4];
+                }
+                __syncthreads();
+                if (kg == 0) {
+#pragma unroll
+                    for (int g = 1; g < H; ++g)
+#pragma unroll
+                        for (int i = 0; i < NF * 4; ++i) o[i / 4][i % 4] += *at(g, i);
+                }
+            }
+        }
+        if (kg == 0) {
+            const float vs = E8 && A.C.v_scale != nullptr ? A.C.v_scale[h] : 1.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int mrow = wr * 16 + gq + 8 * e;
+                if (mrow >= mvalid) continue;
+                if (whole) {
+                    const int mm = rt * MT + mrow, r = sq.row0 + mm / A.group, hq = h * A.group + mm % A.group;
+                    const float inv = l[e] == 0.f ? 0.f : vs / l[e];
+                    unsigned char* p = A.out.p + (int64_t)r * A.out.rs + (int64_t)hq * A.out.hs;
+                    const bool ob = A.out.dtype == kBF16;
+#pragma unroll
+                    for (int f = 0; f < NF; f += E8 ? 2 : 1) {
+                        auto w2 = [&](int col, float x, float y) {
+                            *reinterpret_cast<uint32_t*>(p + col * 2) =
+                                ob ? pack2<true>(x * inv, y * inv) : pack2<false>(x * inv, y * inv);
+                        };
+                        if constexpr (E8) {
+                            w2(8 * f + 4 * tq, o[f][2 * e], o[f + 1][2 * e]);
+                            w2(8 * f + 4 * tq + 2, o[f][2 * e + 1], o[f + 1][2 * e + 1]);
+                        } else {
+                            w2(8 * f + 2 * tq, o[f][2 * e], o[f][2 * e + 1]);
+                        }
+                    }
+                    if (A.lse != nullptr && tq == 0)
+                        A.lse[(int64_t)r * A.q.heads + hq] =
+                            l[e] == 0.f ? -INFINITY : (m[e] == -INFINITY ? l[e] : (m[e] + log2f(l[e])) * 0.69314718056f);
+                } else {
+                    float* p = A.ws_o + ((int64_t)part * MT + mrow) * HD;
+#pragma unroll
+                    for (int f = 0; f < NF; f += E8 ? 2 : 1) {
+                        if constexpr (E8)
+                            *reinterpret_cast<float4*>(p + 8 * f + 4 * tq) =
+                                make_float4(o[f][2 * e], o[f + 1][2 * e], o[f][2 * e + 1], o[f + 1][2 * e + 1]);
+                        else
+                            *reinterpret_cast<float2*>(p + 8 * f + 2 * tq) = make_float2(o[f][2 * e], o[f][2 * e + 1]);
+                    }
+                    if (tq == 0) A.ws_ml[(int64_t)part * MT + mrow] = make_float2(m[e], l[e]);
+                }
+            }
+        }
+    }
+}
+
+// The shared units' parts joined: a warp per (row, query head).
+template <int HD>
+__global__ void __launch_bounds__(kPaThreads)
+    paged_join_kernel(const __grid_constant__ PaArgs A, int mt, int ctas, int e8) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t id = (int64_t)blockIdx.x * kPaWarps + warp;
+    const int row = (int)(id / A.q.heads), hq = (int)(id % A.q.heads);
+    // lengths and row starts are final: the attention kernel lets this one start only after its own wait
+    const int s = row < A.R.n_rows ? seq_of(A.R, row) : -1;
+    int64_t c0 = 0, c1 = 0;
+    int mrow = 0, h = 0;
+    if (s >= 0) {
+        const PaSeq q = pa_seq(A, s, mt);
+        const int64_t total = pa_total(A, mt, lane), chunk = (total + ctas - 1) / ctas;
+        h = hq / A.group;
+        const int mm = (row - q.row0) * A.group + hq % A.group;
+        mrow = mm % mt;
+        const int64_t u = (int64_t)(mm / mt) * A.C.kv_heads + h;
+        const int64_t a = pa_before(A, mt, lane, s) + u * q.ntiles;
+        c0 = a / chunk;
+        c1 = (a + q.ntiles - 1) / chunk;
+    }
+    pdl_wait();
+    if (c0 == c1) return;
+    constexpr int V = HD / 32;  // columns a lane
+    float m = -INFINITY, l = 0.f, o[V] = {};
+    // parts in order, 32 references and sums at a time
+    for (int64_t b = c0; b <= c1; b += 32) {
+        const int64_t n = min((int64_t)32, c1 - b + 1);
+        float2 x = make_float2(-INFINITY, 0.f);
+        auto slot = [&](int64_t c) { return (c * 2 + (c == c0 ? 1 : 0)) * mt + mrow; };
+        if (lane < n) x = A.ws_ml[slot(b + lane)];
+        const float to = fmaxf(m, warp_max(x.x));
+        const float fm = m == to ? 1.f : pa_exp2(m - to);
+        const float f = x.x == -INFINITY ? 1.f : pa_exp2(x.x - to);  // (without a maximum the sums are 0 or NaN)
+        m = to;
+        l = l * fm + warp_sum(x.y * f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] *= fm;
+#pragma unroll 4
+        for (int k = 0; k < (int)n; ++k) {
+            const float w = __shfl_sync(0xffffffffu, f, k);
+            const float* p = A.ws_o + slot(b + k) * HD + V * lane;
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = fmaf(w, p[i], o[i]);
+        }
+    }
+    const float inv = l == 0.f ? 0.f : (e8 && A.C.v_scale != nullptr ? A.C.v_scale[h] : 1.f) / l;
+    unsigned char* p = A.out.p + (int64_t)row * A.out.rs + (int64_t)hq * A.out.hs + V * lane * 2;
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+        *reinterpret_cast<uint32_t*>(p + 2 * i) = A.out.dtype == kBF16 ? pack2<true>(o[i] * inv, o[i + 1] * inv)
+                                                                       : pack2<false>(o[i] * inv, o[i + 1] * inv);
+    if (A.lse != nullptr && lane == 0)
+        A.lse[(int64_t)row * A.q.heads + hq] =
+            l == 0.f ? -INFINITY : (m == -INFINITY ? l : (m + log2f(l)) * 0.69314718056f);
+}
+
+// Rows a unit's tile holds: by what a sequence of average length brings.
+static int pa_row_warps(int n_seqs, int64_t n_rows, int group) {
+    const int64_t per = n_seqs > 0 ? (n_rows + n_seqs - 1) / n_seqs : 0;
+    const int64_t m = per * group;
+    return m <= 16 ? 1 : m <= 32 ? 2 : m <= 64 ? 4 : 8;
+}
+
+int64_t paged_attention_workspace(int hd, int n_seqs, int64_t n_rows, int heads, int kv_heads, int num_sms) {
+    const int64_t mt = 16 * pa_row_warps(n_seqs, n_rows, heads / kv_heads);
+    return 2 * (int64_t)num_sms * mt * (hd * 4 + 8);
+}
+
+template <bool BF, bool E8, int HD, int RW>
+static int pa_launch(const PaArgs& A, int num_sms, cudaStream_t st) {
+    using S = PaShape<BF, E8, HD, RW>;
+    // the limit is a device's own: one record each
+    static size_t limit[kMaxDevices] = {};
+    auto kern = paged_attn_kernel<BF, E8, HD, RW>;
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return (int)e;
+    if (cudaError_t e = raise_smem_limit(kern, S::kSmem, &limit[dev])) return (int)e;
+    if (cudaError_t e = launch(kern, dim3(num_sms), dim3(kPaThreads), S::kSmem, st, A)) return (int)e;
+    const int64_t jobs = (int64_t)A.R.n_rows * A.q.heads;
+    return (int)launch(paged_join_kernel<HD>, dim3((unsigned)((jobs + kPaWarps - 1) / kPaWarps)), dim3(kPaThreads), 0,
+                       st, A, S::MT, num_sms, (int)E8);
+}
+template <bool BF, bool E8, int HD>
+static int pa_rw(const PaArgs& A, int rw, int num_sms, cudaStream_t st) {
+    return rw == 1   ? pa_launch<BF, E8, HD, 1>(A, num_sms, st)
+           : rw == 2 ? pa_launch<BF, E8, HD, 2>(A, num_sms, st)
+           : rw == 4 ? pa_launch<BF, E8, HD, 4>(A, num_sms, st)
+                     : pa_launch<BF, E8, HD, 8>(A, num_sms, st);
+}
+
+int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& q,
+                    const HeadRows& out, float* lse, float scale, int window, void* ws, int num_sms, cudaStream_t st) {
+    PaArgs A{};
+    A.C = C, A.R = R, A.q = q, A.out = out, A.lse = lse, A.window = window;
+    A.scale_log2 = scale * 1.4426950408889634f;
+    A.group = q.heads / C.kv_heads;
+    const int rw = pa_row_warps(R.n_seqs, R.n_rows, A.group);
+    A.ws_o = static_cast<float*>(ws);
+    A.ws_ml = reinterpret_cast<float2*>(A.ws_o + 2 * (int64_t)num_sms * 16 * rw * hd);
+    if (hd == 64)
+        return cache_dtype == kBF16  ? pa_rw<true, false, 64>(A, rw, num_sms, st)
+               : cache_dtype == kF16 ? pa_rw<false, false, 64>(A, rw, num_sms, st)
+                                     : pa_rw<false, true, 64>(A, rw, num_sms, st);
+    return cache_dtype == kBF16  ? pa_rw<true, false, 128>(A, rw, num_sms, st)
+           : cache_dtype == kF16 ? pa_rw<false, false, 128>(A, rw, num_sms, st)
+                                 : pa_rw<false, true, 128>(A, rw, num_sms, st);
+}
+
+}  // namespace dflash

@@ -43,6 +43,9 @@ cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// The reason that dflash_last_error(NULL) gives on this thread; returns `code` (api.cu).
+int set_thread_error(int code, const char* msg);
+
 // Raises a kernel's dynamic shared-memory limit to `bytes` where `*limit` (the
 // call site's record of what it set) is below it.  One lock guards every such
 // record and call, so host threads may run the library's entry points at once.

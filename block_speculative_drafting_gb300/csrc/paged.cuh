@@ -1,0 +1,115 @@
+// What the kernels of the target's verification pass share: the paged cache
+// and the call's rows as kernel parameters, the walk from a row to its
+// sequence and position, element conversions, and the launchers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace dflash {
+
+// element types: the values of DFLASH_F32 .. DFLASH_E4M3
+constexpr int kF32 = 0, kBF16 = 1, kF16 = 2, kE4M3 = 3;
+
+constexpr int kMaxDevices = 64;
+
+// Division of 0 <= n < 2^31 by a fixed d: one high product, one addition and
+// a shift (a page size is any number, and every key row divides by it).
+struct FastDiv {
+    uint32_t mul, shift;
+    int d;
+};
+inline FastDiv fast_div(int d) {
+    uint32_t s = 0;
+    while ((1ull << s) < (uint64_t)d) ++s;
+    return {(uint32_t)((((1ull << s) - (uint64_t)d) << 32) / (uint64_t)d + 1), s, d};
+}
+DF_DEV int div_by(const FastDiv& f, int n) { return (int)((__umulhi((uint32_t)n, f.mul) + (uint32_t)n) >> f.shift); }
+
+struct PagedCache {
+    unsigned char *k, *v;
+    int64_t ks[3], vs[3];  // page, slot, head strides in bytes
+    const float *k_scale, *v_scale;
+    int64_t n_pages;
+    int kv_heads;
+};
+struct PagedRows {
+    int n_seqs, max_pages, per;  // per: rows of every sequence where row_start is null
+    int n_rows, cap;             // cap: max_pages * page size
+    const int32_t *row_start, *kv_len, *table;
+    int64_t table_stride;
+    FastDiv page;
+};
+struct HeadRows {
+    unsigned char* p;
+    int64_t rs, hs;  // row, head strides in bytes
+    int dtype, heads;
+};
+
+// Rows [a, b) of sequence s, inside [0, n_rows] whatever the array holds.
+DF_DEV void rows_of(const PagedRows& R, int s, int& a, int& b) {
+    if (R.row_start == nullptr) {
+        a = s * R.per;
+        b = a + R.per;
+    } else {
+        a = min(max(R.row_start[s], 0), R.n_rows);
+        b = min(max(R.row_start[s + 1], a), R.n_rows);
+    }
+}
+// The sequence that holds row r, or -1: the last whose start is at most r.
+DF_DEV int seq_of(const PagedRows& R, int r) {
+    if (R.row_start == nullptr) return R.per > 0 ? r / R.per : -1;
+    int lo = 0, hi = R.n_seqs;  // row_start[lo] <= r is not known for lo = 0
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (R.row_start[mid] <= r)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    int a, b;
+    rows_of(R, lo, a, b);
+    return r >= a && r < b ? lo : -1;
+}
+// The page of position p of sequence s, or -1 where it is not held.
+DF_DEV int64_t page_of(const PagedRows& R, int64_t n_pages, int s, int p, int& slot) {
+    if (p < 0 || p >= R.cap) return -1;
+    const int idx = div_by(R.page, p);
+    slot = p - idx * R.page.d;
+    const int64_t id = R.table[(int64_t)s * R.table_stride + idx];
+    return id >= 0 && id < n_pages ? id : -1;
+}
+
+// ---- launchers (0 = queued fine, else a cudaError_t)
+struct Rotation {
+    const double* inv_freq;
+    int rotary, interleaved;
+    float scale;
+};
+int paged_append(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& k, const HeadRows& v,
+                 const HeadRows& q, const HeadRows& qo, const float* q_norm, const float* k_norm, float eps,
+                 const Rotation& rot, cudaStream_t st);
+
+int64_t paged_attention_workspace(int hd, int n_seqs, int64_t n_rows, int heads, int kv_heads, int num_sms);
+int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& q,
+                    const HeadRows& out, float* lse, float scale, int window, void* ws, int num_sms, cudaStream_t st);
+
+struct VerifyArgs {
+    const void* target;
+    int target_dtype;
+    int64_t target_stride, draft_stride;  // elements
+    const float* draft;                   // nullptr: all of q at the draft
+    const uint32_t* draft_tok;
+    const int32_t* draft_start;
+    const float *temperature, *accept_u, *sample_u;
+    int n_seqs, n_drafts, per, vocab;
+    int32_t *accepted, *next_tok;
+    float* prob;
+};
+int64_t verify_workspace(int n_seqs, int64_t n_drafts, int64_t vocab, int num_sms);
+int verify(const VerifyArgs& A, void* ws, int num_sms, cudaStream_t st);
+
+}  // namespace dflash

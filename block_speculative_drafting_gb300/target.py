@@ -1,0 +1,332 @@
+"""The target's verification pass: operators for a caller that runs the target model beside the drafter
+(include/dflash.h, "The target's verification pass").
+
+    logits, draft_tok = model.block(seqs, anchors, ...)            # the drafter's block
+    for every target layer:
+        q = paged_append(k_cache, v_cache, k, v, table, kv_len, q=q, inv_freq=f)
+        y = paged_attention(q, k_cache, v_cache, table, kv_len)
+    accepted, token, prob = verify_drafts(target_logits, draft_tok, u, v, draft_logits=logits)
+
+Argument marshalling only: every step runs in the library's kernels.  Arguments are torch CUDA tensors of one device
+(any, current or not); calls run on that device's current stream, or on the stream whose handle is given.  A call may
+be captured into a CUDA graph; outputs and workspaces that it allocates then belong to the graph's memory.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes as C
+import math
+
+import numpy as np
+
+from . import _abi
+
+
+def _lib():
+    from . import lib
+    return lib()
+
+
+def _check(rc: int) -> int:
+    if rc < 0:
+        from . import DFlashError
+        raise DFlashError(rc, _lib().dflash_last_error(None).decode())
+    return rc
+
+
+def _refuse(msg: str):
+    from . import DFlashError
+    raise DFlashError(_abi.DFLASH_EINVAL, msg)
+
+
+_DTYPES: dict = {}
+
+
+def _dtype(t, name: str) -> int:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: _abi.F32, torch.bfloat16: _abi.BF16, torch.float16: _abi.F16,
+                        torch.float8_e4m3fn: _abi.E4M3})
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        _refuse(f"{name} has dtype {t.dtype}")
+    return d
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            _refuse(f"{name} is on {t.device}, not on {dev}")
+
+
+def _vector(t, name: str, n: int, dtype):
+    """Pointer of a contiguous vector of n elements of one of the given dtypes (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype not in dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        _refuse(f"{name} has to be a contiguous vector of {n} elements of {dtype[0]}, "
+                f"got {tuple(t.shape)} of {t.dtype}")
+    return t.data_ptr() or None
+
+
+@contextlib.contextmanager
+def _on(dev, stream):
+    """The device and the stream of a call, current while it allocates and launches; yields the stream's handle.
+    (An allocation belongs to the stream that is current, so that its memory is not dealt out again before that
+    stream is done with it.)"""
+    import torch
+    if dev.type != "cuda":
+        _refuse(f"tensors have to be on a CUDA device, got {dev}")
+    with contextlib.ExitStack() as st:
+        if dev.index != torch.cuda.current_device():
+            st.enter_context(torch.cuda.device(dev))
+        cur = torch.cuda.current_stream(dev).cuda_stream
+        if stream is not None and int(stream) != cur:
+            cur = int(stream)
+            st.enter_context(torch.cuda.stream(torch.cuda.ExternalStream(cur, device=dev)))
+        yield C.c_void_p(cur)
+
+
+def _head_rows(t, name: str, written: bool = False) -> _abi.HeadRows:
+    """A [rows][heads][head_dim] tensor."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        _refuse(f"{name} has to be [rows][heads][head_dim] with contiguous columns, got {tuple(t.shape)}")
+    if written and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+        _refuse(f"{name} is written and may not be an expanded tensor")
+    return _abi.HeadRows(t.data_ptr() or None, _dtype(t, name), t.shape[1], t.stride(0) if t.shape[0] > 1 else 0,
+                         t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, written: bool = False) -> _abi.PagedCache:
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        _refuse("k_cache and v_cache have to be [pages][page_size][kv_heads][head_dim] of one shape and type, got "
+                f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+    n, page, heads, hd = k_cache.shape
+    c = _abi.PagedCache(k_cache.data_ptr() or None, v_cache.data_ptr() or None, _dtype(k_cache, "k_cache"), heads, hd,
+                        page, n)
+    for name, t, st in (("k_cache", k_cache, c.k_strides), ("v_cache", v_cache, c.v_strides)):
+        if hd > 1 and t.stride(3) != 1:
+            _refuse(f"{name} needs contiguous columns")
+        if written and any(m > 1 and s == 0 for m, s in zip(t.shape, t.stride())):
+            _refuse(f"{name} is written and may not be an expanded tensor")
+        for i in range(3):
+            st[i] = t.stride(i) if t.shape[i] > 1 else 0
+    if k_scale is not None or v_scale is not None:
+        import torch
+        c.k_scale = _vector(k_scale, "k_scale", heads, (torch.float32,))
+        c.v_scale = _vector(v_scale, "v_scale", heads, (torch.float32,))
+    return c
+
+
+def _rows(table, kv_len, row_start, n_rows: int) -> _abi.PagedRows:
+    import torch
+    i32 = (torch.int32,)
+    if table.dim() != 2 or table.dtype != torch.int32 or (table.shape[1] > 1 and table.stride(1) != 1):
+        _refuse(f"table has to be int32 [sequences][pages] with contiguous rows, got {tuple(table.shape)} of "
+                f"{table.dtype}")
+    n, width = table.shape
+    return _abi.PagedRows(n, width, n_rows, _vector(row_start, "row_start", n + 1, i32),
+                          _vector(kv_len, "kv_len", n, i32), table.data_ptr() or None,
+                          table.stride(0) if n > 1 else width)
+
+
+def rope_inv_freq(rotary: int, theta: float = 1e6, scaling: str | None = None, factor: float = 1.0,
+                  trained: int | None = None, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """Rotation frequencies for `paged_append` and the scale that goes with them: (float64 [rotary/2] tensor, scale).
+
+    theta^(-2i/rotary), and for contexts `factor` times longer than trained
+      "linear"  every frequency / factor
+      "yarn"    frequencies that turn fewer than beta_slow times in `trained` positions / factor, those that turn more
+                than beta_fast times as they are, a linear ramp over the pairs between; scale 0.1 ln(factor) + 1
+    """
+    import torch
+    if rotary < 2 or rotary % 2 or not theta > 0 or not factor > 0:
+        raise ValueError(f"rotary {rotary}, theta {theta}, factor {factor}")
+    f = theta ** (-np.arange(0, rotary, 2, dtype=np.float64) / rotary)
+    scale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if not trained or trained < 1:
+            raise ValueError("yarn needs the trained length")
+
+        def pair(turns):  # the pair that turns so many times in `trained` positions
+            return rotary * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(theta))
+
+        lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), rotary - 1)
+        ramp = np.clip((np.arange(rotary // 2) - lo) / max(hi - lo, 1e-3), 0.0, 1.0)
+        f = f / factor * ramp + f * (1.0 - ramp)
+        scale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    elif scaling is not None:
+        raise ValueError(f"scaling {scaling!r} is not linear or yarn")
+    return torch.from_numpy(f).to(device if device is not None else "cuda"), scale
+
+
+def paged_append(k_cache, v_cache, k, v, table, kv_len, *, row_start=None, q=None, q_out=None, inv_freq=None,
+                 interleaved: bool = False, rope_scale: float = 1.0, q_norm=None, k_norm=None, eps: float = 1e-6,
+                 k_scale=None, v_scale=None, stream=None):
+    """Write a pass's keys and values into a paged cache, normed and rotated on the way, and return its rotated
+    queries (None without q).
+
+    k_cache, v_cache  [pages][page_size][kv_heads][head_dim] bfloat16, float16 or float8_e4m3fn, any strides with
+                      contiguous columns; k_scale, v_scale [kv_heads] float32: an 8-bit element is code * scale
+    k, v, q           [rows][heads][head_dim] float32, bfloat16 or float16 (slices of a fused projection fit)
+    table             int32 [sequences][pages]; a page id outside the cache: not held, not written
+    kv_len            int32 [sequences]: tokens in each sequence's cache with its new rows in; row i of its r rows
+                      stands at position kv_len - r + i
+    row_start         int32 [sequences + 1]: each sequence's rows; None: equally many
+    q_out             where the queries go (default: a new tensor like q; q itself is allowed)
+    inv_freq          float64 [rotary / 2] (`rope_inv_freq`); None: no rotation.  Pairs are columns (i, i + rotary/2),
+                      or (2i, 2i + 1) when interleaved; columns from `rotary` on stay
+    q_norm, k_norm    float32 [head_dim] gains of an RMS norm before the rotation; None: none
+    """
+    import torch
+    dev = k_cache.device
+    _same_device(dev, v_cache=v_cache, k=k, v=v, table=table, kv_len=kv_len, row_start=row_start, q=q, q_out=q_out,
+                 inv_freq=inv_freq, q_norm=q_norm, k_norm=k_norm, k_scale=k_scale, v_scale=v_scale)
+    if k.dim() != 3 or v.shape != k.shape or k.shape[1:] != k_cache.shape[2:]:
+        _refuse(f"k and v have to be [rows][kv_heads][head_dim] of the cache, got {tuple(k.shape)} and "
+                f"{tuple(v.shape)}")
+    n, _, hd = k.shape
+    cache = _cache(k_cache, v_cache, k_scale, v_scale, written=True)
+    rows = _rows(table, kv_len, row_start, n)
+    kr, vr, qr, qo, rot = _head_rows(k, "k"), _head_rows(v, "v"), None, None, None
+    f32 = (torch.float32,)
+    if inv_freq is not None:
+        f = _vector(inv_freq, "inv_freq", inv_freq.numel(), (torch.float64,))
+        rot = C.byref(_abi.Rotation(f, 2 * inv_freq.numel(), int(interleaved), rope_scale))
+    with _on(dev, stream) as st:
+        if q is not None:
+            if q.dim() != 3 or q.shape[0] != n or q.shape[2] != hd:
+                _refuse(f"q has to be [{n}][heads][{hd}], got {tuple(q.shape)}")
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            elif q_out.shape != q.shape:
+                _refuse(f"q_out has to be {tuple(q.shape)}, got {tuple(q_out.shape)}")
+            qr, qo = C.byref(_head_rows(q, "q")), C.byref(_head_rows(q_out, "q_out", written=True))
+        elif q_out is not None:
+            _refuse("q_out without q")
+        _check(_lib().dflash_paged_append(C.byref(cache), C.byref(rows), C.byref(kr), C.byref(vr), qr, qo,
+                                          _vector(q_norm, "q_norm", hd, f32), _vector(k_norm, "k_norm", hd, f32),
+                                          eps, rot, st))
+    return q_out
+
+
+def paged_attention(q, k_cache, v_cache, table, kv_len, *, row_start=None, scale: float | None = None, window: int = 0,
+                    k_scale=None, v_scale=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of a pass's rows over the paged cache, which holds their own keys and values (`paged_append`):
+    returns out [rows][heads][head_dim] in q's type.
+
+    q          [rows][heads][head_dim] of the cache's type (bfloat16 or float16 for an 8-bit cache); query head h
+               reads key/value head h / (heads / kv_heads)
+    scale      of the scores; None: head_dim ** -0.5
+    window     > 0: the row at position p sees the positions p - window + 1 .. p; 0: all up to p
+    lse        float32 [rows][heads] to fill with ln sum exp of the row's scores (-inf: the row sees nothing)
+    workspace  uint8 tensor of `paged_attention_workspace` bytes for callers that may not allocate (calls that may
+               overlap need one each); None: allocated for the call
+    The other arguments are `paged_append`'s.
+    """
+    import torch
+    dev = q.device
+    _same_device(dev, k_cache=k_cache, v_cache=v_cache, table=table, kv_len=kv_len, row_start=row_start,
+                 k_scale=k_scale, v_scale=v_scale, out=out, lse=lse, workspace=workspace)
+    if q.dim() != 3 or k_cache.dim() != 4 or q.shape[2] != k_cache.shape[3]:
+        _refuse(f"q has to be [rows][heads][head_dim] of the cache, got {tuple(q.shape)}")
+    n, heads, hd = q.shape
+    cache = _cache(k_cache, v_cache, k_scale, v_scale)
+    rows = _rows(table, kv_len, row_start, n)
+    qr = _head_rows(q, "q")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous()):
+        _refuse(f"lse has to be contiguous float32 [{n}][{heads}]")
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        elif out.shape != q.shape:
+            _refuse(f"out has to be {tuple(q.shape)}, got {tuple(out.shape)}")
+        orr = _head_rows(out, "out", written=True)
+        if workspace is None:
+            need = _check(_lib().dflash_paged_attention_workspace(C.byref(cache), rows.n_seqs, n, heads))
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif not workspace.is_contiguous():
+            _refuse("workspace has to be contiguous")
+        _check(_lib().dflash_paged_attention(C.byref(cache), C.byref(rows), C.byref(qr), C.byref(orr),
+                                             None if lse is None else lse.data_ptr() or None,
+                                             hd ** -0.5 if scale is None else scale, window,
+                                             workspace.data_ptr() or None, workspace.nbytes, st))
+    return out
+
+
+def paged_attention_workspace(q, k_cache, n_seqs: int) -> int:
+    """Bytes of workspace that `paged_attention` needs for q's rows over n_seqs sequences."""
+    with _on(q.device, None):
+        cache = _cache(k_cache, k_cache, None, None)
+        return _check(_lib().dflash_paged_attention_workspace(C.byref(cache), n_seqs, q.shape[0], q.shape[1]))
+
+
+def verify_drafts(target_logits, draft_tokens, accept_u, sample_u, *, draft_logits=None, draft_start=None,
+                  temperature=None, accepted=None, next_token=None, prob=None, workspace=None, stream=None):
+    """Which drafted tokens the target keeps, and the token after them, from given random numbers: returns
+    (accepted int32 [sequences], next_token int32 [sequences], prob float32 [drafts]).
+
+    target_logits  [drafts + sequences][vocab] float32, bfloat16 or float16: sequence by sequence, a row for each
+                   draft and one for the token after them all
+    draft_tokens   int32 or uint32, `Model.block`'s tokens as they are ([sequences][drafts]) or [drafts]
+    accept_u       float32 [drafts], sample_u float32 [sequences], uniform in [0, 1)
+    draft_logits   float32 [..][vocab], a row a draft, `Model.block`'s logits as they are: drafts drawn from their
+                   softmax; None: drafts that were chosen, not drawn (a draft stays with probability p(draft))
+    draft_start    int32 [sequences + 1]: each sequence's drafts; None: equally many
+    temperature    float32 [sequences], 0: greedy; None: 1 for all
+    A draft stays while accept_u * q(draft) < p(draft); the next token comes from max(p - q, 0) of the first refused
+    draft's row, or from p of the last row, at the running sum that passes sample_u.  prob is min(1, p / q).  A row
+    without any probability yields token -1.  Sequences are refused or served alike: include/dflash.h, dflash_verify.
+    """
+    import torch
+    dev = target_logits.device
+    _same_device(dev, draft_tokens=draft_tokens, accept_u=accept_u, sample_u=sample_u, draft_logits=draft_logits,
+                 draft_start=draft_start, temperature=temperature, accepted=accepted, next_token=next_token, prob=prob,
+                 workspace=workspace)
+    f32, i32 = (torch.float32,), (torch.int32,)
+    if target_logits.dim() != 2 or (target_logits.shape[1] > 1 and target_logits.stride(1) != 1):
+        _refuse(f"target_logits has to be [rows][vocab] with contiguous rows, got {tuple(target_logits.shape)}")
+    n, d, vocab = sample_u.numel(), draft_tokens.numel(), target_logits.shape[1]
+    if target_logits.shape[0] != n + d:
+        _refuse(f"{d} drafts of {n} sequences need {n + d} target rows, got {target_logits.shape[0]}")
+    if not draft_tokens.is_contiguous():
+        _refuse("draft_tokens has to be contiguous")
+    draft_tokens = draft_tokens.view(-1)
+    dl = ds = None
+    if draft_logits is not None:
+        if draft_logits.dtype != torch.float32 or draft_logits.shape[-1] != vocab or draft_logits.numel() != d * vocab:
+            _refuse(f"draft_logits has to be float32 [{d}][{vocab}], got {tuple(draft_logits.shape)}")
+        if draft_logits.dim() != 2:
+            if not draft_logits.is_contiguous():
+                _refuse("draft_logits of more than two dimensions has to be contiguous")
+            draft_logits = draft_logits.view(d, vocab)
+        if vocab > 1 and draft_logits.stride(1) != 1:
+            _refuse("draft_logits needs contiguous rows")
+        dl, ds = draft_logits.data_ptr() or None, draft_logits.stride(0) if d > 1 else vocab
+    with _on(dev, stream) as st:
+        if accepted is None:
+            accepted = torch.empty(n, dtype=torch.int32, device=dev)
+        if next_token is None:
+            next_token = torch.empty(n, dtype=torch.int32, device=dev)
+        if prob is None:
+            prob = torch.empty(d, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(_check(_lib().dflash_verify_workspace(n, d, vocab)), dtype=torch.uint8, device=dev)
+        elif not workspace.is_contiguous():
+            _refuse("workspace has to be contiguous")
+        _check(_lib().dflash_verify(
+            target_logits.data_ptr() or None, _dtype(target_logits, "target_logits"),
+            target_logits.stride(0) if n + d > 1 else vocab, dl, ds or 0,
+            _vector(draft_tokens, "draft_tokens", d, (torch.int32, torch.uint32)),
+            _vector(draft_start, "draft_start", n + 1, i32), _vector(temperature, "temperature", n, f32),
+            _vector(accept_u, "accept_u", d, f32), _vector(sample_u, "sample_u", n, f32), n, d, vocab,
+            _vector(accepted, "accepted", n, i32), _vector(next_token, "next_token", n, i32),
+            _vector(prob, "prob", d, f32), workspace.data_ptr() or None, workspace.nbytes, st))
+    return accepted, next_token, prob
+
+
+def verify_workspace(n_seqs: int, n_drafts: int, vocab: int) -> int:
+    """Bytes of workspace that `verify_drafts` needs on the current device."""
+    return _check(_lib().dflash_verify_workspace(n_seqs, n_drafts, vocab))

@@ -182,8 +182,9 @@ DFLASH_API int dflash_init(const dflash_geometry* geom, const dflash_weights* we
 /* Free a model and its device memory (sequences must be freed first). NULL is a no-op. */
 DFLASH_API void dflash_free(dflash_model* model);
 
-/* The reason of the last failed call on `model` (NULL: the last failed
- * dflash_init of this thread).  Never NULL; "" when nothing failed. */
+/* The reason of the last failed call on `model` (NULL: this thread's last
+ * failed dflash_init or call without a model).  Never NULL; "" when nothing
+ * failed. */
 DFLASH_API const char* dflash_last_error(const dflash_model* model);
 
 /* Copy the geometry a model was built with into *out. */
@@ -470,6 +471,189 @@ DFLASH_API int dflash_debug_attention(dflash_model* model, dflash_seq* const* se
 DFLASH_API int dflash_attention_noalloc(dflash_model* model, dflash_seq* const* seqs, int32_t n_seqs, int32_t layer,
                                         const int64_t* anchor_pos, int32_t block_len, const float* qkv, float* y,
                                         void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The target's verification pass.  The drafter's blocks (dflash_block) are
+ * answered by the target model in one pass over its own cache; these calls
+ * are that pass's operators, for a caller that runs the target itself:
+ *
+ *   dflash_paged_append     rotate the pass's q and k, write k and v into
+ *                           the target's paged cache
+ *   dflash_paged_attention  its rows' attention over that cache
+ *   dflash_verify           which drafts stay, and the token after them
+ *
+ * (The pages leave the target to the engine around the drafter and have no
+ * counterpart.)  They take no model: every buffer is the caller's device
+ * memory, on the current device, and nothing is allocated or kept between
+ * calls; work is queued on `stream`, and a call may be captured into a graph
+ * and replayed with new contents of the same buffers.  Calls that share no
+ * output and no workspace may overlap.  A failed call's reason is
+ * dflash_last_error(NULL) of the calling thread; a refused call (EINVAL,
+ * EGEOM, ECAPACITY) launches nothing.  Counts, lengths and page ids that sit
+ * in device memory cannot be refused by the host: what is done with bad ones
+ * is said at each call, and none of them makes a kernel leave its buffers.
+ * ------------------------------------------------------------------------- */
+
+/* element types of the calls below */
+#define DFLASH_F32 0
+#define DFLASH_BF16 1
+#define DFLASH_F16 2
+#define DFLASH_E4M3 3 /* 8-bit float, 4 exponent bits, largest 448, no infinity */
+
+/*
+ * A paged key/value cache.  Slot t of page p of head h holds head_dim
+ * contiguous elements at k + p * k_strides[0] + t * k_strides[1] + h *
+ * k_strides[2] (elements; v likewise), so that [page][slot][head] and
+ * [page][head][slot] are both served.
+ * Rules (EINVAL / EGEOM): dtype DFLASH_BF16, DFLASH_F16 or DFLASH_E4M3;
+ * head_dim 64 or 128; kv_heads >= 1; page_size 1 .. 65536; n_pages >= 0; bases
+ * and strides multiples of 16 bytes, strides >= 0.
+ * k_scale, v_scale (E4M3 only, both or neither; NULL: 1): one positive f32 a
+ * head on the device; an element is its code times the head's scale.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    int32_t dtype;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int64_t n_pages;
+    int64_t k_strides[3]; /* page, slot, head; in elements */
+    int64_t v_strides[3];
+    const float* k_scale; /* [kv_heads] */
+    const float* v_scale; /* [kv_heads] */
+} dflash_paged_cache;
+
+/*
+ * The new rows of a call: sequence s has rows row_start[s] .. row_start[s+1]
+ * of the call's row tensors (row_start NULL: n_rows / n_seqs rows each, which
+ * has to divide).  kv_len[s] counts the sequence's tokens with its new rows
+ * in: row i of its r rows stands at position kv_len[s] - r + i.  Position p
+ * sits in slot p % page_size of page table[s * table_stride + p / page_size].
+ * All three arrays are int32 on the device.  max_pages * page_size < 2^31;
+ * n_rows < 2^24.
+ * Not held: positions below 0 or from max_pages * page_size on, and positions
+ * whose page id lies outside [0, n_pages).  row_start is read clamped to
+ * [0, n_rows] and to ascending order; rows outside every sequence are left as
+ * they were.
+ */
+typedef struct {
+    int32_t n_seqs;
+    int32_t max_pages; /* columns of the table */
+    int64_t n_rows;
+    const int32_t* row_start; /* [n_seqs + 1] or NULL */
+    const int32_t* kv_len;    /* [n_seqs] */
+    const int32_t* table;
+    int64_t table_stride; /* entries from one sequence's pages to the next's */
+} dflash_paged_rows;
+
+/* Rows of heads in device memory: element d of head h of row r at data + r *
+ * row_stride + h * head_stride + d (elements; base and strides multiples of
+ * 16 bytes, strides >= 0). */
+typedef struct {
+    void* data;
+    int32_t dtype; /* DFLASH_F32, DFLASH_BF16 or DFLASH_F16 */
+    int32_t heads;
+    int64_t row_stride;
+    int64_t head_stride;
+} dflash_head_rows;
+
+/*
+ * The rotation of a head's first `rotary` columns (a multiple of 16, at most
+ * head_dim): with the angle a = p * inv_freq[i] of position p, held in 64
+ * bits, the pair (x, y) of columns (i, i + rotary/2), or (2i, 2i + 1) when
+ * interleaved, becomes scale * (x cos a - y sin a, x sin a + y cos a).
+ * Frequencies slowed for long contexts, with the scale that goes with them,
+ * come in as inv_freq and scale.
+ */
+typedef struct {
+    const double* inv_freq; /* [rotary / 2] on the device */
+    int32_t rotary;
+    int32_t interleaved;
+    float scale;
+} dflash_rotation;
+
+/*
+ * Append the call's rows to the cache, rotated on the way: k' = rot_p(norm(k))
+ * and v go to their slots in the cache's type (rounded to nearest; E4M3:
+ * x / scale, clamped to +-448, NaN kept), q' = rot_p(norm(q)) to q_out.
+ * norm(x) = x / sqrt(mean(x^2) + eps) * gain over a head, with f32 gains
+ * q_norm, k_norm [head_dim] on the device (NULL: no norm).  rotation NULL: no
+ * rotation.  q NULL: keys and values alone.  q_out may be q itself and may be
+ * of another type.  A row whose position is not held is not written to the
+ * cache (its q' is written).  A table that maps two of the call's rows to one
+ * slot leaves either row's elements there.
+ * Errors: EINVAL, EGEOM, ECUDA.
+ */
+DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_rows* rows,
+                                   const dflash_head_rows* k, const dflash_head_rows* v, const dflash_head_rows* q,
+                                   const dflash_head_rows* q_out, const float* q_norm, const float* k_norm, float eps,
+                                   const dflash_rotation* rotation, void* stream);
+
+/*
+ * Attention of the call's rows over the cache (which holds their own keys and
+ * values already): row at position p, query head h, key/value head h /
+ * (heads / kv_heads):
+ *   out = sum_j softmax_j(scale * q . k_j) v_j over the held positions j <= p
+ *         (window w > 0: and j > p - w)
+ *   lse = ln sum_j exp(scale * q . k_j)          f32 [n_rows][heads], or NULL
+ * A row that sees nothing gets out = 0 and lse = -inf.  What positions outside
+ * a row's view hold (infinities, NaN, freed pages) does not reach it.  q and
+ * out have one type: the cache's, or BF16 / F16 for an E4M3 cache.
+ * workspace: at least dflash_paged_attention_workspace bytes of device
+ * memory, 16-byte aligned, needing no initial contents; calls that may
+ * overlap need one each.
+ * Errors: EINVAL, EGEOM, ECAPACITY (workspace too small), ECUDA.
+ */
+DFLASH_API int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_rows* rows,
+                                      const dflash_head_rows* q, const dflash_head_rows* out, float* lse, float scale,
+                                      int32_t window, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace a dflash_paged_attention call of `n_rows` rows in all over
+ * `n_seqs` sequences needs on the current device: >= 0, or an error. */
+DFLASH_API int64_t dflash_paged_attention_workspace(const dflash_paged_cache* cache, int32_t n_seqs, int64_t n_rows,
+                                                    int32_t heads);
+
+/*
+ * Verify drafted tokens.  Sequence s has the drafts draft_start[s] ..
+ * draft_start[s+1] (device int32 [n_seqs + 1]; NULL: n_drafts / n_seqs each,
+ * which has to divide), one target row a draft and one after them: target row
+ * draft_start[s] + s + i holds the logits of the token that draft i proposes.
+ * With p_i = softmax(target row / T), T = temperature[s] (device f32 [n_seqs];
+ * NULL: 1):
+ *   q_i      softmax(draft_logits row i / T) (f32), or, draft_logits NULL, all
+ *            of it at the draft x_i
+ *   kept     while accept_u[i] * q_i(x_i) < p_i(x_i);  a drafts before the first refusal
+ *   token    the first index whose running sum passes sample_u[s] times the
+ *            whole, of max(p_a - q_a, 0) after a refusal (of p_a where that
+ *            is nowhere positive), of p_a when every draft is kept
+ *   prob[i]  min(1, p_i(x_i) / q_i(x_i)) of every draft
+ * T <= 0 (or NaN) is greedy: p_i is all at the target's largest logit (the
+ * lowest index among equals), q_i all at x_i, and the token is that largest
+ * one.  accept_u, sample_u: f32 in [0, 1).  Logits of -inf, and NaN, count as
+ * probability 0; at +inf the row's +inf entries share it all.  A row with no
+ * probability at all refuses its draft and yields token -1.  A draft outside
+ * the vocabulary is refused.
+ * target [n_drafts + n_seqs] rows of f32, BF16 or F16, draft_logits
+ * [n_drafts] rows of f32, target_stride / draft_stride elements apart, vocab
+ * contiguous logits each; draft_tok u32 [n_drafts] (dflash_block's logits and
+ * draft_tok fit as they are).  accepted, next_tok int32 [n_seqs], prob f32
+ * [n_drafts] or NULL.  draft_start is read clamped to [0, n_drafts] and to
+ * ascending order; entries of no sequence are left as they were.  n_drafts +
+ * n_seqs < 2^24, vocab < 2^30.
+ * workspace: at least dflash_verify_workspace bytes, as for the attention.
+ * Errors: EINVAL, ECAPACITY (workspace too small), ECUDA.
+ */
+DFLASH_API int dflash_verify(const void* target, int32_t target_dtype, int64_t target_stride,
+                             const float* draft_logits, int64_t draft_stride, const uint32_t* draft_tok,
+                             const int32_t* draft_start, const float* temperature, const float* accept_u,
+                             const float* sample_u, int32_t n_seqs, int64_t n_drafts, int64_t vocab,
+                             int32_t* accepted, int32_t* next_tok, float* prob, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace a dflash_verify call needs on the current device: >= 0, or an error. */
+DFLASH_API int64_t dflash_verify_workspace(int32_t n_seqs, int64_t n_drafts, int64_t vocab);
 
 #ifdef __cplusplus
 }
