@@ -21,16 +21,27 @@ import numpy as np
 
 from . import _abi
 
+# The calls below run once a layer and step: what they do on the host is kept to a few microseconds (the C descriptors
+# are packed in one go, the library and torch are looked up once).
+torch = None
+_lib = None
+_DTYPES: dict = {}
 
-def _lib():
+
+def _init():
+    global torch, _lib
+    import torch as t
+
     from . import lib
-    return lib()
+    _lib = lib()
+    _DTYPES.update({t.float32: _abi.F32, t.bfloat16: _abi.BF16, t.float16: _abi.F16, t.float8_e4m3fn: _abi.E4M3})
+    torch = t
 
 
 def _check(rc: int) -> int:
     if rc < 0:
         from . import DFlashError
-        raise DFlashError(rc, _lib().dflash_last_error(None).decode())
+        raise DFlashError(rc, _lib.dflash_last_error(None).decode())
     return rc
 
 
@@ -39,95 +50,95 @@ def _refuse(msg: str):
     raise DFlashError(_abi.DFLASH_EINVAL, msg)
 
 
-_DTYPES: dict = {}
+def _direct(dev: int, stream) -> bool:
+    """Whether a call can run where it stands: on the current device, on its current stream."""
+    if dev < 0:
+        _refuse("tensors have to be on a CUDA device")
+    return stream is None and dev == torch.cuda.current_device()
+
+
+def _current_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+@contextlib.contextmanager
+def _moved(dev: int, stream):
+    """The call's device and stream made current.  (What a call allocates belongs to the stream that is current, so
+    that it is not dealt out again before that stream is done with it.)"""
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev)):
+                yield
+
+
+def _same_device(dev: int, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _refuse(f"a tensor of shape {tuple(t.shape)} is on {t.device}, not on cuda:{dev}")
 
 
 def _dtype(t, name: str) -> int:
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float32: _abi.F32, torch.bfloat16: _abi.BF16, torch.float16: _abi.F16,
-                        torch.float8_e4m3fn: _abi.E4M3})
     d = _DTYPES.get(t.dtype)
     if d is None:
         _refuse(f"{name} has dtype {t.dtype}")
     return d
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            _refuse(f"{name} is on {t.device}, not on {dev}")
-
-
 def _vector(t, name: str, n: int, dtype):
-    """Pointer of a contiguous vector of n elements of one of the given dtypes (None: NULL)."""
+    """Pointer of a contiguous vector of n elements (None: 0)."""
     if t is None:
-        return None
-    if t.dtype not in dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        _refuse(f"{name} has to be a contiguous vector of {n} elements of {dtype[0]}, "
-                f"got {tuple(t.shape)} of {t.dtype}")
-    return t.data_ptr() or None
+        return 0
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        _refuse(f"{name} has to be a contiguous vector of {n} elements of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+    return t.data_ptr()
 
 
-@contextlib.contextmanager
-def _on(dev, stream):
-    """The device and the stream of a call, current while it allocates and launches; yields the stream's handle.
-    (An allocation belongs to the stream that is current, so that its memory is not dealt out again before that
-    stream is done with it.)"""
-    import torch
-    if dev.type != "cuda":
-        _refuse(f"tensors have to be on a CUDA device, got {dev}")
-    with contextlib.ExitStack() as st:
-        if dev.index != torch.cuda.current_device():
-            st.enter_context(torch.cuda.device(dev))
-        cur = torch.cuda.current_stream(dev).cuda_stream
-        if stream is not None and int(stream) != cur:
-            cur = int(stream)
-            st.enter_context(torch.cuda.stream(torch.cuda.ExternalStream(cur, device=dev)))
-        yield C.c_void_p(cur)
-
-
-def _head_rows(t, name: str, written: bool = False) -> _abi.HeadRows:
-    """A [rows][heads][head_dim] tensor."""
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-        _refuse(f"{name} has to be [rows][heads][head_dim] with contiguous columns, got {tuple(t.shape)}")
-    if written and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+def _written(t, name: str):
+    if 0 in t.stride() and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
         _refuse(f"{name} is written and may not be an expanded tensor")
-    return _abi.HeadRows(t.data_ptr() or None, _dtype(t, name), t.shape[1], t.stride(0) if t.shape[0] > 1 else 0,
-                         t.stride(1) if t.shape[1] > 1 else 0)
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale, written: bool = False) -> _abi.PagedCache:
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+def _head_rows(t, name: str) -> bytes:
+    """A [rows][heads][head_dim] tensor as a dflash_head_rows."""
+    if t.dim() != 3:
+        _refuse(f"{name} has to be [rows][heads][head_dim], got {tuple(t.shape)}")
+    (n, h, w), (sr, sh, sw) = t.shape, t.stride()
+    if sw != 1 and w > 1:
+        _refuse(f"{name} needs contiguous columns")
+    return _abi.HEAD_ROWS.pack(t.data_ptr(), _dtype(t, name), h, sr if n > 1 else 0, sh if h > 1 else 0)
+
+
+def _cache(k, v, k_scale, v_scale) -> bytes:
+    """The two cache tensors as a dflash_paged_cache."""
+    if k.dim() != 4 or k.shape != v.shape or k.dtype is not v.dtype:
         _refuse("k_cache and v_cache have to be [pages][page_size][kv_heads][head_dim] of one shape and type, got "
-                f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
-    n, page, heads, hd = k_cache.shape
-    c = _abi.PagedCache(k_cache.data_ptr() or None, v_cache.data_ptr() or None, _dtype(k_cache, "k_cache"), heads, hd,
-                        page, n)
-    for name, t, st in (("k_cache", k_cache, c.k_strides), ("v_cache", v_cache, c.v_strides)):
-        if hd > 1 and t.stride(3) != 1:
-            _refuse(f"{name} needs contiguous columns")
-        if written and any(m > 1 and s == 0 for m, s in zip(t.shape, t.stride())):
-            _refuse(f"{name} is written and may not be an expanded tensor")
-        for i in range(3):
-            st[i] = t.stride(i) if t.shape[i] > 1 else 0
+                f"{tuple(k.shape)} and {tuple(v.shape)}")
+    n, page, heads, hd = k.shape
+    k0, k1, k2, k3 = k.stride()
+    v0, v1, v2, v3 = v.stride()
+    if (k3 != 1 or v3 != 1) and hd > 1:
+        _refuse("k_cache and v_cache need contiguous columns")
+    if n == 1 or page == 1 or heads == 1:  # the stride of a dimension of one element is anything
+        k0, v0 = (0, 0) if n == 1 else (k0, v0)
+        k1, v1 = (0, 0) if page == 1 else (k1, v1)
+        k2, v2 = (0, 0) if heads == 1 else (k2, v2)
+    ks = vs = 0
     if k_scale is not None or v_scale is not None:
-        import torch
-        c.k_scale = _vector(k_scale, "k_scale", heads, (torch.float32,))
-        c.v_scale = _vector(v_scale, "v_scale", heads, (torch.float32,))
-    return c
+        ks, vs = (_vector(x, "k_scale and v_scale", heads, torch.float32) for x in (k_scale, v_scale))
+    return _abi.PAGED_CACHE.pack(k.data_ptr(), v.data_ptr(), _dtype(k, "k_cache"), heads, hd, page, n, k0, k1, k2, v0,
+                                 v1, v2, ks, vs)
 
 
-def _rows(table, kv_len, row_start, n_rows: int) -> _abi.PagedRows:
-    import torch
-    i32 = (torch.int32,)
-    if table.dim() != 2 or table.dtype != torch.int32 or (table.shape[1] > 1 and table.stride(1) != 1):
+def _rows(table, kv_len, row_start, n_rows: int) -> bytes:
+    if table.dim() != 2 or table.dtype is not torch.int32 or (table.stride(1) != 1 and table.shape[1] > 1):
         _refuse(f"table has to be int32 [sequences][pages] with contiguous rows, got {tuple(table.shape)} of "
                 f"{table.dtype}")
     n, width = table.shape
-    return _abi.PagedRows(n, width, n_rows, _vector(row_start, "row_start", n + 1, i32),
-                          _vector(kv_len, "kv_len", n, i32), table.data_ptr() or None,
-                          table.stride(0) if n > 1 else width)
+    return _abi.PAGED_ROWS.pack(n, width, n_rows, _vector(row_start, "row_start", n + 1, torch.int32),
+                                _vector(kv_len, "kv_len", n, torch.int32), table.data_ptr(),
+                                table.stride(0) if n > 1 else width)
 
 
 def rope_inv_freq(rotary: int, theta: float = 1e6, scaling: str | None = None, factor: float = 1.0,
@@ -139,7 +150,8 @@ def rope_inv_freq(rotary: int, theta: float = 1e6, scaling: str | None = None, f
       "yarn"    frequencies that turn fewer than beta_slow times in `trained` positions / factor, those that turn more
                 than beta_fast times as they are, a linear ramp over the pairs between; scale 0.1 ln(factor) + 1
     """
-    import torch
+    if torch is None:
+        _init()
     if rotary < 2 or rotary % 2 or not theta > 0 or not factor > 0:
         raise ValueError(f"rotary {rotary}, theta {theta}, factor {factor}")
     f = theta ** (-np.arange(0, rotary, 2, dtype=np.float64) / rotary)
@@ -180,35 +192,42 @@ def paged_append(k_cache, v_cache, k, v, table, kv_len, *, row_start=None, q=Non
                       or (2i, 2i + 1) when interleaved; columns from `rotary` on stay
     q_norm, k_norm    float32 [head_dim] gains of an RMS norm before the rotation; None: none
     """
-    import torch
-    dev = k_cache.device
-    _same_device(dev, v_cache=v_cache, k=k, v=v, table=table, kv_len=kv_len, row_start=row_start, q=q, q_out=q_out,
-                 inv_freq=inv_freq, q_norm=q_norm, k_norm=k_norm, k_scale=k_scale, v_scale=v_scale)
+    if torch is None:
+        _init()
+    dev = k_cache.get_device()
+    if not _direct(dev, stream):
+        with _moved(dev, stream):
+            return paged_append(k_cache, v_cache, k, v, table, kv_len, row_start=row_start, q=q, q_out=q_out,
+                                inv_freq=inv_freq, interleaved=interleaved, rope_scale=rope_scale, q_norm=q_norm,
+                                k_norm=k_norm, eps=eps, k_scale=k_scale, v_scale=v_scale)
+    _same_device(dev, v_cache, k, v, table, kv_len, row_start, q, q_out, inv_freq, q_norm, k_norm, k_scale, v_scale)
     if k.dim() != 3 or v.shape != k.shape or k.shape[1:] != k_cache.shape[2:]:
         _refuse(f"k and v have to be [rows][kv_heads][head_dim] of the cache, got {tuple(k.shape)} and "
                 f"{tuple(v.shape)}")
     n, _, hd = k.shape
-    cache = _cache(k_cache, v_cache, k_scale, v_scale, written=True)
-    rows = _rows(table, kv_len, row_start, n)
-    kr, vr, qr, qo, rot = _head_rows(k, "k"), _head_rows(v, "v"), None, None, None
-    f32 = (torch.float32,)
+    cache = _cache(k_cache, v_cache, k_scale, v_scale)
+    _written(k_cache, "k_cache")
+    _written(v_cache, "v_cache")
+    qr = qo = rot = None
     if inv_freq is not None:
-        f = _vector(inv_freq, "inv_freq", inv_freq.numel(), (torch.float64,))
-        rot = C.byref(_abi.Rotation(f, 2 * inv_freq.numel(), int(interleaved), rope_scale))
-    with _on(dev, stream) as st:
-        if q is not None:
-            if q.dim() != 3 or q.shape[0] != n or q.shape[2] != hd:
-                _refuse(f"q has to be [{n}][heads][{hd}], got {tuple(q.shape)}")
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            elif q_out.shape != q.shape:
-                _refuse(f"q_out has to be {tuple(q.shape)}, got {tuple(q_out.shape)}")
-            qr, qo = C.byref(_head_rows(q, "q")), C.byref(_head_rows(q_out, "q_out", written=True))
-        elif q_out is not None:
-            _refuse("q_out without q")
-        _check(_lib().dflash_paged_append(C.byref(cache), C.byref(rows), C.byref(kr), C.byref(vr), qr, qo,
-                                          _vector(q_norm, "q_norm", hd, f32), _vector(k_norm, "k_norm", hd, f32),
-                                          eps, rot, st))
+        f = inv_freq.numel()
+        rot = _abi.ROTATION.pack(_vector(inv_freq, "inv_freq", f, torch.float64), 2 * f, 1 if interleaved else 0,
+                                 rope_scale)
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != hd:
+            _refuse(f"q has to be [{n}][heads][{hd}], got {tuple(q.shape)}")
+        if q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        elif q_out.shape != q.shape:
+            _refuse(f"q_out has to be {tuple(q.shape)}, got {tuple(q_out.shape)}")
+        _written(q_out, "q_out")
+        qr, qo = _head_rows(q, "q"), _head_rows(q_out, "q_out")
+    elif q_out is not None:
+        _refuse("q_out without q")
+    _check(_lib.dflash_paged_append(cache, _rows(table, kv_len, row_start, n), _head_rows(k, "k"), _head_rows(v, "v"),
+                                    qr, qo, _vector(q_norm, "q_norm", hd, torch.float32),
+                                    _vector(k_norm, "k_norm", hd, torch.float32), eps, rot,
+                                    _current_stream(dev)))
     return q_out
 
 
@@ -226,41 +245,47 @@ def paged_attention(q, k_cache, v_cache, table, kv_len, *, row_start=None, scale
                overlap need one each); None: allocated for the call
     The other arguments are `paged_append`'s.
     """
-    import torch
-    dev = q.device
-    _same_device(dev, k_cache=k_cache, v_cache=v_cache, table=table, kv_len=kv_len, row_start=row_start,
-                 k_scale=k_scale, v_scale=v_scale, out=out, lse=lse, workspace=workspace)
+    if torch is None:
+        _init()
+    dev = q.get_device()
+    if not _direct(dev, stream):
+        with _moved(dev, stream):
+            return paged_attention(q, k_cache, v_cache, table, kv_len, row_start=row_start, scale=scale, window=window,
+                                   k_scale=k_scale, v_scale=v_scale, out=out, lse=lse, workspace=workspace)
+    _same_device(dev, k_cache, v_cache, table, kv_len, row_start, k_scale, v_scale, out, lse, workspace)
     if q.dim() != 3 or k_cache.dim() != 4 or q.shape[2] != k_cache.shape[3]:
         _refuse(f"q has to be [rows][heads][head_dim] of the cache, got {tuple(q.shape)}")
     n, heads, hd = q.shape
-    cache = _cache(k_cache, v_cache, k_scale, v_scale)
-    rows = _rows(table, kv_len, row_start, n)
-    qr = _head_rows(q, "q")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous()):
+    cache, rows = _cache(k_cache, v_cache, k_scale, v_scale), _rows(table, kv_len, row_start, n)
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous()):
         _refuse(f"lse has to be contiguous float32 [{n}][{heads}]")
-    with _on(dev, stream) as st:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        elif out.shape != q.shape:
-            _refuse(f"out has to be {tuple(q.shape)}, got {tuple(out.shape)}")
-        orr = _head_rows(out, "out", written=True)
-        if workspace is None:
-            need = _check(_lib().dflash_paged_attention_workspace(C.byref(cache), rows.n_seqs, n, heads))
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        elif not workspace.is_contiguous():
-            _refuse("workspace has to be contiguous")
-        _check(_lib().dflash_paged_attention(C.byref(cache), C.byref(rows), C.byref(qr), C.byref(orr),
-                                             None if lse is None else lse.data_ptr() or None,
-                                             hd ** -0.5 if scale is None else scale, window,
-                                             workspace.data_ptr() or None, workspace.nbytes, st))
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif out.shape != q.shape:
+        _refuse(f"out has to be {tuple(q.shape)}, got {tuple(out.shape)}")
+    else:
+        _written(out, "out")
+    if workspace is None:
+        need = _check(_lib.dflash_paged_attention_workspace(cache, table.shape[0], n, heads))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        _refuse("workspace has to be contiguous")
+    _check(_lib.dflash_paged_attention(cache, rows, _head_rows(q, "q"), _head_rows(out, "out"),
+                                       None if lse is None else lse.data_ptr(), hd ** -0.5 if scale is None else scale,
+                                       window, workspace.data_ptr(), workspace.nbytes, _current_stream(dev)))
     return out
 
 
 def paged_attention_workspace(q, k_cache, n_seqs: int) -> int:
     """Bytes of workspace that `paged_attention` needs for q's rows over n_seqs sequences."""
-    with _on(q.device, None):
-        cache = _cache(k_cache, k_cache, None, None)
-        return _check(_lib().dflash_paged_attention_workspace(C.byref(cache), n_seqs, q.shape[0], q.shape[1]))
+    if torch is None:
+        _init()
+    dev = q.get_device()
+    if not _direct(dev, None):
+        with _moved(dev, None):
+            return paged_attention_workspace(q, k_cache, n_seqs)
+    return _check(_lib.dflash_paged_attention_workspace(_cache(k_cache, k_cache, None, None), n_seqs, q.shape[0],
+                                                        q.shape[1]))
 
 
 def verify_drafts(target_logits, draft_tokens, accept_u, sample_u, *, draft_logits=None, draft_start=None,
@@ -280,53 +305,60 @@ def verify_drafts(target_logits, draft_tokens, accept_u, sample_u, *, draft_logi
     draft's row, or from p of the last row, at the running sum that passes sample_u.  prob is min(1, p / q).  A row
     without any probability yields token -1.  Sequences are refused or served alike: include/dflash.h, dflash_verify.
     """
-    import torch
-    dev = target_logits.device
-    _same_device(dev, draft_tokens=draft_tokens, accept_u=accept_u, sample_u=sample_u, draft_logits=draft_logits,
-                 draft_start=draft_start, temperature=temperature, accepted=accepted, next_token=next_token, prob=prob,
-                 workspace=workspace)
-    f32, i32 = (torch.float32,), (torch.int32,)
-    if target_logits.dim() != 2 or (target_logits.shape[1] > 1 and target_logits.stride(1) != 1):
-        _refuse(f"target_logits has to be [rows][vocab] with contiguous rows, got {tuple(target_logits.shape)}")
-    n, d, vocab = sample_u.numel(), draft_tokens.numel(), target_logits.shape[1]
-    if target_logits.shape[0] != n + d:
-        _refuse(f"{d} drafts of {n} sequences need {n + d} target rows, got {target_logits.shape[0]}")
-    if not draft_tokens.is_contiguous():
-        _refuse("draft_tokens has to be contiguous")
-    draft_tokens = draft_tokens.view(-1)
-    dl = ds = None
+    if torch is None:
+        _init()
+    dev = target_logits.get_device()
+    if not _direct(dev, stream):
+        with _moved(dev, stream):
+            return verify_drafts(target_logits, draft_tokens, accept_u, sample_u, draft_logits=draft_logits,
+                                 draft_start=draft_start, temperature=temperature, accepted=accepted,
+                                 next_token=next_token, prob=prob, workspace=workspace)
+    _same_device(dev, draft_tokens, accept_u, sample_u, draft_logits, draft_start, temperature, accepted, next_token,
+                 prob, workspace)
+    f32, i32 = torch.float32, torch.int32
+    if target_logits.dim() != 2:
+        _refuse(f"target_logits has to be [rows][vocab], got {tuple(target_logits.shape)}")
+    n, d, (rows, vocab), (stride, one) = sample_u.numel(), draft_tokens.numel(), target_logits.shape, target_logits.stride()
+    if one != 1 and vocab > 1:
+        _refuse("target_logits needs contiguous rows")
+    if rows != n + d:
+        _refuse(f"{d} drafts of {n} sequences need {n + d} target rows, got {rows}")
+    if draft_tokens.dtype is not i32 and draft_tokens.dtype is not torch.uint32 or not draft_tokens.is_contiguous():
+        _refuse(f"draft_tokens has to be contiguous int32 or uint32, got {draft_tokens.dtype}")
+    dl, ds = None, 0
     if draft_logits is not None:
-        if draft_logits.dtype != torch.float32 or draft_logits.shape[-1] != vocab or draft_logits.numel() != d * vocab:
+        if draft_logits.dtype is not f32 or draft_logits.shape[-1] != vocab or draft_logits.numel() != d * vocab:
             _refuse(f"draft_logits has to be float32 [{d}][{vocab}], got {tuple(draft_logits.shape)}")
-        if draft_logits.dim() != 2:
-            if not draft_logits.is_contiguous():
-                _refuse("draft_logits of more than two dimensions has to be contiguous")
-            draft_logits = draft_logits.view(d, vocab)
-        if vocab > 1 and draft_logits.stride(1) != 1:
-            _refuse("draft_logits needs contiguous rows")
-        dl, ds = draft_logits.data_ptr() or None, draft_logits.stride(0) if d > 1 else vocab
-    with _on(dev, stream) as st:
-        if accepted is None:
-            accepted = torch.empty(n, dtype=torch.int32, device=dev)
-        if next_token is None:
-            next_token = torch.empty(n, dtype=torch.int32, device=dev)
-        if prob is None:
-            prob = torch.empty(d, dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(_check(_lib().dflash_verify_workspace(n, d, vocab)), dtype=torch.uint8, device=dev)
-        elif not workspace.is_contiguous():
-            _refuse("workspace has to be contiguous")
-        _check(_lib().dflash_verify(
-            target_logits.data_ptr() or None, _dtype(target_logits, "target_logits"),
-            target_logits.stride(0) if n + d > 1 else vocab, dl, ds or 0,
-            _vector(draft_tokens, "draft_tokens", d, (torch.int32, torch.uint32)),
-            _vector(draft_start, "draft_start", n + 1, i32), _vector(temperature, "temperature", n, f32),
-            _vector(accept_u, "accept_u", d, f32), _vector(sample_u, "sample_u", n, f32), n, d, vocab,
-            _vector(accepted, "accepted", n, i32), _vector(next_token, "next_token", n, i32),
-            _vector(prob, "prob", d, f32), workspace.data_ptr() or None, workspace.nbytes, st))
+        if draft_logits.dim() == 2 and (vocab == 1 or draft_logits.stride(1) == 1):
+            ds = draft_logits.stride(0) if d > 1 else vocab
+        elif draft_logits.is_contiguous():
+            ds = vocab
+        else:
+            _refuse("draft_logits needs contiguous rows (more than two dimensions: contiguous as a whole)")
+        dl = draft_logits.data_ptr()
+    if accepted is None:
+        accepted = torch.empty(n, dtype=i32, device=target_logits.device)
+    if next_token is None:
+        next_token = torch.empty_like(accepted)
+    if prob is None:
+        prob = torch.empty_like(accept_u, memory_format=torch.contiguous_format)
+    if workspace is None:
+        need = _check(_lib.dflash_verify_workspace(n, d, vocab))
+        workspace = torch.empty(need, dtype=torch.uint8, device=target_logits.device)
+    elif not workspace.is_contiguous():
+        _refuse("workspace has to be contiguous")
+    _check(_lib.dflash_verify(
+        target_logits.data_ptr(), _dtype(target_logits, "target_logits"), stride if rows > 1 else vocab, dl, ds,
+        draft_tokens.data_ptr(), _vector(draft_start, "draft_start", n + 1, i32),
+        _vector(temperature, "temperature", n, f32), _vector(accept_u, "accept_u", d, f32),
+        _vector(sample_u, "sample_u", n, f32), n, d, vocab, _vector(accepted, "accepted", n, i32),
+        _vector(next_token, "next_token", n, i32), _vector(prob, "prob", d, f32), workspace.data_ptr(),
+        workspace.nbytes, _current_stream(dev)))
     return accepted, next_token, prob
 
 
 def verify_workspace(n_seqs: int, n_drafts: int, vocab: int) -> int:
     """Bytes of workspace that `verify_drafts` needs on the current device."""
-    return _check(_lib().dflash_verify_workspace(n_seqs, n_drafts, vocab))
+    if torch is None:
+        _init()
+    return _check(_lib.dflash_verify_workspace(n_seqs, n_drafts, vocab))
