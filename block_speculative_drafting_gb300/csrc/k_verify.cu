@@ -8,16 +8,18 @@
 // are joined, each draft's p and q formed in 64 bits and compared with the
 // given number, and one row -- the first refused, or the last -- is read again
 // to sample the next token: the cluster's warps sum what is left of equal
-// parts of the vocabulary, every CTA finds the part in which the running sum
-// passes the given number's share of the whole, and the warp that owns it
-// finds the chunk and the entry.
+// parts of the vocabulary, and the CTA in which the running sum passes the
+// given number's share of the whole finds the part and, by 32nds, the entry.  That kernel runs once through its code, so its
+// code is kept small (rolled loops): what it waits for most is instructions.
 //
-// Arithmetic.  The sums decide whole numbers, so they carry about 48 bits: f32
-// batches of 16 or 32 exponentials (each within 2^-22) are added to a pair
-// (hi, lo) by error-free additions -- the 64-bit units of this part are too
-// few for that (two lanes a clock and SM).  c is a pair too, so that its
-// rounding does not tilt the distribution, and R is an integer, so that moving
-// a sum to another reference is exact and x c - R is rounded once.
+// Arithmetic.  A softmax sum is a tree of f32 additions of exponentials within
+// 2^-22 each; c is a pair (hi, lo), so that its rounding does not tilt the
+// distribution, and R is an integer, so that moving a sum to another reference
+// is exact and x c - R is rounded once.  The running sum over a vocabulary
+// decides which of 10^5 entries is drawn: it is carried in pairs of f32 by
+// error-free additions, about 48 bits, since the 64-bit units of this part are
+// few (two lanes a clock and SM: 64-bit sums in every warp took 30 us of a
+// 40 us call).  The drafts' p and q are formed in 64 bits, a lane a draft.
 //
 // Memory bound: the logits, once (the re-read row comes out of L2).
 #include <cooperative_groups.h>
@@ -30,10 +32,8 @@ namespace dflash {
 namespace cg = cooperative_groups;
 
 constexpr int kVsThreads = 256;
-constexpr int kVpThreads = 512, kVpWarps = kVpThreads / 32;
 constexpr int kVpCluster = 8;
-constexpr int kVpParts = kVpCluster * kVpWarps;  // vocabulary parts of the sampled row
-constexpr int kVpChunks = 64;                    // chunks of a part, at most
+constexpr int kVpKept = 24576;  // entries of a CTA's parts whose weights are kept in shared memory
 constexpr float kRefNone = -3e38f;               // the reference of a sum of nothing
 
 // A sum as an unevaluated pair, about 48 bits.
@@ -46,13 +46,23 @@ DF_DEV Pair operator+(Pair a, Pair b) {
     const float h = s + e;
     return {h, e - (h - s)};
 }
-DF_DEV Pair scaled(Pair a, float f) { return {a.hi * f, a.lo * f}; }  // (f a power of two: exact)
-DF_DEV double wide(Pair a) { return (double)a.hi + (double)a.lo; }
+DF_DEV Pair operator-(Pair a, Pair b) { return a + Pair{-b.hi, -b.lo}; }
+DF_DEV bool positive(Pair a) { return a.hi > 0.f; }  // (normalised: lo cannot turn the sign)
 DF_DEV Pair shfl_xor(Pair a, int o) {
     return {__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)};
 }
+DF_DEV Pair shfl(Pair a, int l) { return {__shfl_sync(0xffffffffu, a.hi, l), __shfl_sync(0xffffffffu, a.lo, l)}; }
+// sums of the lanes up to and with this one
+DF_DEV Pair warp_running(Pair a, int lane) {
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const Pair b{__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
+        if (lane >= o) a = a + b;
+    }
+    return a;
+}
 DF_DEV Pair warp_sum(Pair a) {
-#pragma unroll
+#pragma unroll 1
     for (int o = 16; o > 0; o >>= 1) a = a + shfl_xor(a, o);
     return a;
 }
@@ -68,11 +78,9 @@ DF_DEV float ex2(float z) {
 // Careful, where that form does not hold (a NaN, an infinite logit, entries so
 // far apart that x c overflows or every weight underflows): the sum of
 // 2^((x - max) c), 1 at the largest, 0 at NaN.
-struct VerifyStat {
-    Pair sum;
-    float ref, max;
-    int32_t arg;  // (greedy) the lowest index of the largest logit
-    int32_t careful;
+struct __align__(16) VerifyStat {
+    float sum, ref, max;
+    int32_t tag;  // a greedy sequence's: the lowest index of the largest logit; else 1: careful
 };
 
 struct VerifyParams {
@@ -91,20 +99,18 @@ DF_DEV void draft_range(const VerifyArgs& A, int s, int& a, int& b) {
     }
 }
 // The last sequence whose drafts (shift 0) or target rows (shift 1) start at
-// or before entry i; -1 where no sequence holds it.
-DF_DEV int verify_seq(const VerifyArgs& A, int i, int shift) {
+// or before entry i; -1 where no sequence holds it.  By a warp, 32 starts at once.
+DF_DEV int verify_seq(const VerifyArgs& A, int i, int shift, int lane) {
     if (A.draft_start == nullptr) return i / (A.per + shift);
-    int lo = 0, hi = A.n_seqs;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (A.draft_start[mid] + shift * mid <= i)
-            lo = mid;
-        else
-            hi = mid;
+    int s = -1;
+    for (int b = 0; b < A.n_seqs; b += 32) {
+        const int j = b + lane;
+        s += __popc(__ballot_sync(0xffffffffu, j < A.n_seqs && A.draft_start[j] + shift * j <= i));
     }
-    int a, b;
-    draft_range(A, lo, a, b);
-    return i >= a + shift * lo && i < b + shift * (lo + 1) ? lo : -1;
+    if (s < 0) return -1;
+    int a, e;
+    draft_range(A, s, a, e);
+    return i >= a + shift * s && i < e + shift * (s + 1) ? s : -1;
 }
 
 // c = log2(e) / T as hi + lo, lo > 0 (so that -inf * lo is -inf); hi = 0
@@ -145,9 +151,9 @@ template <>
 struct Vec<kF32> {
     static constexpr int N = 4;
     using T = float;
-    DF_DEV static void get(const float* p, float* x) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    DF_DEV static void split(uint4 v, float* x) {
+        x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
+        x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
     }
     DF_DEV static float one(const float* p) { return __ldg(p); }
 };
@@ -159,8 +165,7 @@ struct Vec16 {
         if constexpr (BF) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
         return __half22float2(*reinterpret_cast<const __half2*>(&u));
     }
-    DF_DEV static void get(const uint16_t* p, float* x) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    DF_DEV static void split(uint4 v, float* x) {
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -176,40 +181,66 @@ template <>
 struct Vec<kF16> : Vec16<false> {};
 
 // The batches of a thread: f(x[4 N], first indices) over [v0, v1) of a row, absent entries -inf.  The entries
-// up to the first 16-byte boundary and the last few come as a batch of their own.
-template <int DT, class F>
-DF_DEV void each_batch(const typename Vec<DT>::T* row, int v0, int v1, F f) {
+// up to the first 16-byte boundary and the last few come as a batch of their own.  A batch's four 16-byte
+// loads are in flight while the one before it is worked on.
+template <int DT>
+struct Batches {
     using V = Vec<DT>;
-    constexpr int N = V::N, U = 4;
-    const int mis = (int)((reinterpret_cast<uintptr_t>(row + v0) & 15) / sizeof(typename V::T));
-    const int a = min(v1, v0 + (mis ? N - mis : 0)), nv = (v1 - a) / N, b = a + nv * N;
-    float x[U * N];
-    int at[U];
-    if (a > v0 || v1 > b) {
-#pragma unroll
-        for (int i = 0; i < U * N; ++i) x[i] = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < U; ++k) at[k] = v0;
-        const int h = v0 + threadIdx.x, t = b + threadIdx.x;
-        if (h < a) x[0] = V::one(row + h), at[0] = h;
-        if (t < v1) x[N] = V::one(row + t), at[1] = t;
-        if (h < a || t < v1) f(x, at);
+    using T = typename V::T;
+    static constexpr int N = V::N, U = 4, M = U * N;
+    const T* row;
+    const uint4* vec;
+    int v0, v1, a, b, nv, i;
+    uint4 next[U];
+    DF_DEV Batches(const T* r, int from, int to) : row(r), v0(from), v1(to) {
+        const int mis = (int)((reinterpret_cast<uintptr_t>(row + v0) & 15) / sizeof(T));
+        a = min(v1, v0 + (mis ? N - mis : 0));
+        nv = (v1 - a) / N;
+        b = a + nv * N;
+        vec = reinterpret_cast<const uint4*>(row + a);
+        start();
     }
-    for (int i = threadIdx.x; i < nv; i += U * kVsThreads) {
+    DF_DEV void start() {
+        i = threadIdx.x;
+        load();
+    }
+    DF_DEV void load() {
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int j = i + k * kVsThreads;
-            at[k] = a + j * N;
-            if (j < nv) {
-                V::get(row + at[k], x + k * N);
-            } else {
+        for (int k = 0; k < U; ++k)
+            if (i + k * kVsThreads < nv) next[k] = __ldg(vec + i + k * kVsThreads);
+    }
+    template <class F>
+    DF_DEV void each(F f) {
+        float x[M];
+        int at[U];
+        if (a > v0 || v1 > b) {
 #pragma unroll
-                for (int n = 0; n < N; ++n) x[k * N + n] = -INFINITY;
-            }
+            for (int j = 0; j < M; ++j) x[j] = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < U; ++k) at[k] = v0;
+            const int h = v0 + threadIdx.x, t = b + threadIdx.x;
+            if (h < a) x[0] = V::one(row + h), at[0] = h;
+            if (t < v1) x[N] = V::one(row + t), at[1] = t;
+            if (h < a || t < v1) f(x, at);
         }
-        f(x, at);
+        while (i < nv) {
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int j = i + k * kVsThreads;
+                at[k] = a + j * N;
+                if (j < nv) {
+                    V::split(next[k], x + k * N);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < N; ++n) x[k * N + n] = -INFINITY;
+                }
+            }
+            i += U * kVsThreads;
+            load();
+            f(x, at);
+        }
     }
-}
+};
 template <int M>
 DF_DEV float max_of(const float* x) {
     float m = fmaxf(x[0], x[1]);
@@ -218,17 +249,24 @@ DF_DEV float max_of(const float* x) {
     return m;
 }
 
-// One part of one row, by the whole CTA; thread 0 has the answer.
+// One part of one row, by the whole CTA: target row or (drafter) draft row `entry`.
 template <int DT>
-DF_DEV VerifyStat row_part(const typename Vec<DT>::T* row, int v0, int v1, Scale c, VerifyStat* warps) {
-    constexpr int N = Vec<DT>::N, M = 4 * N;
+DF_DEV void row_part(const typename Vec<DT>::T* row, int v0, int v1, const VerifyArgs& A, int entry, int drafter,
+                     VerifyStat* warps, VerifyStat* out) {
+    constexpr int M = Batches<DT>::M, N = Vec<DT>::N, W = kVsThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    VerifyStat r{{0.f, 0.f}, kRefNone, -INFINITY, 0x7fffffff, 0};
+    // the first loads go out before the sequence and its temperature are looked up
+    Batches<DT> batches(row, v0, v1);
+    const int s = verify_seq(A, entry, 1 - drafter, lane);
+    if (s < 0) return;
+    const Scale c = scale_of(A, s);
+    if (drafter && c.greedy()) return;  // a greedy sequence's drafter is not asked
+    VerifyStat r{0.f, kRefNone, -INFINITY, 0x7fffffff};
     if (c.greedy()) {
         auto join = [&](float m, int arg) {
-            if (m > r.max || (m == r.max && arg < r.arg)) r.max = m, r.arg = arg;
+            if (m > r.max || (m == r.max && arg < r.tag)) r.max = m, r.tag = arg;
         };
-        each_batch<DT>(row, v0, v1, [&](const float* x, const int* at) {
+        batches.each([&](const float* x, const int* at) {
             const float m = max_of<M>(x);
             if (m >= r.max && m > -INFINITY) {
                 int arg = 0x7fffffff;
@@ -238,131 +276,137 @@ DF_DEV VerifyStat row_part(const typename Vec<DT>::T* row, int v0, int v1, Scale
                 join(m, arg);
             }
         });
+        auto fold = [&](int from) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            join(__shfl_xor_sync(0xffffffffu, r.max, o), __shfl_xor_sync(0xffffffffu, r.arg, o));
+            for (int o = from; o > 0; o >>= 1)
+                join(__shfl_xor_sync(0xffffffffu, r.max, o), __shfl_xor_sync(0xffffffffu, r.tag, o));
+        };
+        fold(16);
         if (lane == 0) warps[warp] = r;
         __syncthreads();
-        if (threadIdx.x == 0)
-            for (int w = 1; w < kVsThreads / 32; ++w) join(warps[w].max, warps[w].arg);
-        return r;
+        r = warps[lane % W];
+        fold(W / 2);
+        if (threadIdx.x == 0) *out = r;
+        return;
     }
-    each_batch<DT>(row, v0, v1, [&](const float* x, const int*) {
+    batches.each([&](const float* x, const int*) {
         const float m = max_of<M>(x);
         r.max = fmaxf(r.max, m);
         const float ref = fmaxf(r.ref, ceilf(m * c.hi));
-        r.sum = scaled(r.sum, pow2(r.ref - ref));
+        float s[4] = {r.sum * pow2(r.ref - ref), 0.f, 0.f, 0.f};
         r.ref = ref;
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < M; ++i) s[i & 3] += weight(x[i], c, ref);
-        r.sum = r.sum + Pair{(s[0] + s[1]) + (s[2] + s[3]), 0.f};
+        for (int i = 0; i < M; ++i) s[(i + 1) & 3] += weight(x[i], c, ref);
+        r.sum = (s[0] + s[1]) + (s[2] + s[3]);
     });
-    bool plain = !__syncthreads_or(!(r.sum.hi < INFINITY));
-    if (plain) {
-        auto join = [&](Pair s, float ref, float m) {
-            const float to = fmaxf(r.ref, ref);
-            r.sum = scaled(r.sum, pow2(r.ref - to)) + scaled(s, pow2(ref - to));
-            r.ref = to;
-            r.max = fmaxf(r.max, m);
-        };
+    auto fold = [&](int from) {
+        float to = r.ref;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            join(shfl_xor(r.sum, o), __shfl_xor_sync(0xffffffffu, r.ref, o), __shfl_xor_sync(0xffffffffu, r.max, o));
-        if (lane == 0) warps[warp] = r;
-        __syncthreads();
-        if (threadIdx.x == 0)
-            for (int w = 1; w < kVsThreads / 32; ++w) join(warps[w].sum, warps[w].ref, warps[w].max);
-        plain = !__syncthreads_or(threadIdx.x == 0 && r.sum.hi == 0.f && r.max > -INFINITY);
-        if (plain) return r;
+        for (int o = from; o > 0; o >>= 1) {
+            to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+            r.max = fmaxf(r.max, __shfl_xor_sync(0xffffffffu, r.max, o));
+        }
+        r.sum *= pow2(r.ref - to);
+        r.ref = to;
+#pragma unroll
+        for (int o = from; o > 0; o >>= 1) r.sum += __shfl_xor_sync(0xffffffffu, r.sum, o);
+    };
+    fold(16);
+    r.tag = 0;
+    if (lane == 0) warps[warp] = r;
+    __syncthreads();
+    r = warps[lane % W];
+    fold(W / 2);
+    // (a NaN or an infinite entry makes the sum NaN; no weight at all although there are entries: too far apart)
+    if (r.sum < INFINITY && (r.sum > 0.f || r.max == -INFINITY)) {
+        if (threadIdx.x == 0) *out = r;
+        return;
     }
     // again, with the part's largest logit taken off first
-    float m = warp_max(fmaxf(r.max, -INFINITY));
-    if (lane == 0) warps[warp].max = m;
-    __syncthreads();
-    for (int w = 0; w < kVsThreads / 32; ++w) m = fmaxf(m, warps[w].max);
-    __syncthreads();
-    r = VerifyStat{{0.f, 0.f}, kRefNone, m, 0x7fffffff, 1};
+    const float m = fmaxf(r.max, -INFINITY);
+    r = VerifyStat{0.f, kRefNone, m, 1};
+    batches.start();
     if (m > -INFINITY)
-        each_batch<DT>(row, v0, v1, [&](const float* x, const int*) {
+        batches.each([&](const float* x, const int*) {
             float s = 0.f;
 #pragma unroll
             for (int i = 0; i < M; ++i) s += weight_careful(x[i], c, m);
-            r.sum = r.sum + Pair{s, 0.f};
+            r.sum += s;
         });
     r.sum = warp_sum(r.sum);
-    if (lane == 0) warps[warp] = r;
     __syncthreads();
-    if (threadIdx.x == 0)
-        for (int w = 1; w < kVsThreads / 32; ++w) r.sum = r.sum + warps[w].sum;
-    return r;
+    if (lane == 0) warps[warp].sum = r.sum;
+    __syncthreads();
+    r.sum = 0.f;
+    for (int w = 0; w < W; ++w) r.sum += warps[w].sum;
+    if (threadIdx.x == 0) *out = r;
 }
 
-__global__ void __launch_bounds__(kVsThreads) verify_stats_kernel(const __grid_constant__ VerifyParams P) {
+__global__ void __launch_bounds__(kVsThreads, 4) verify_stats_kernel(const __grid_constant__ VerifyParams P) {
     const VerifyArgs& A = P.A;
     __shared__ VerifyStat warps[kVsThreads / 32];
     const int part = blockIdx.x % P.parts, row = blockIdx.x / P.parts;
     const int nt = A.n_drafts + A.n_seqs;
     pdl_wait();
     pdl_trigger();
-    const int s = row < nt ? verify_seq(A, row, 1) : verify_seq(A, row - nt, 0);
-    if (s < 0) return;
-    const Scale c = scale_of(A, s);
-    if (row >= nt && c.greedy()) return;  // a greedy sequence's drafter is not asked
     const int v0 = (int)((int64_t)A.vocab * part / P.parts), v1 = (int)((int64_t)A.vocab * (part + 1) / P.parts);
-    VerifyStat r;
+    VerifyStat* out = P.stats + (int64_t)row * P.parts + part;
     if (row >= nt)
-        r = row_part<kF32>(A.draft + (int64_t)(row - nt) * A.draft_stride, v0, v1, c, warps);
+        row_part<kF32>(A.draft + (int64_t)(row - nt) * A.draft_stride, v0, v1, A, row - nt, 1, warps, out);
     else if (A.target_dtype == kF32)
-        r = row_part<kF32>(static_cast<const float*>(A.target) + (int64_t)row * A.target_stride, v0, v1, c, warps);
+        row_part<kF32>(static_cast<const float*>(A.target) + (int64_t)row * A.target_stride, v0, v1, A, row, 0, warps, out);
     else if (A.target_dtype == kBF16)
-        r = row_part<kBF16>(static_cast<const uint16_t*>(A.target) + (int64_t)row * A.target_stride, v0, v1, c, warps);
+        row_part<kBF16>(static_cast<const uint16_t*>(A.target) + (int64_t)row * A.target_stride, v0, v1, A, row, 0, warps,
+                        out);
     else
-        r = row_part<kF16>(static_cast<const uint16_t*>(A.target) + (int64_t)row * A.target_stride, v0, v1, c, warps);
-    if (threadIdx.x == 0) P.stats[(int64_t)row * P.parts + part] = r;
+        row_part<kF16>(static_cast<const uint16_t*>(A.target) + (int64_t)row * A.target_stride, v0, v1, A, row, 0, warps,
+                       out);
 }
 
 // A row's parts joined (warp-wide, every lane gets the answer).  A row with a
 // careful part is careful as a whole.
 DF_DEV VerifyStat row_stat(const VerifyParams& P, int64_t row, Scale c, int lane) {
     const VerifyStat* st = P.stats + row * P.parts;
-    VerifyStat r{{0.f, 0.f}, kRefNone, -INFINITY, 0x7fffffff, 0};
+    VerifyStat r{0.f, kRefNone, -INFINITY, 0};
     if (c.greedy()) {
-        for (int i = lane; i < P.parts; i += 32)
-            if (st[i].max > r.max || (st[i].max == r.max && st[i].arg < r.arg)) r.max = st[i].max, r.arg = st[i].arg;
+        r.tag = 0x7fffffff;
+        auto join = [&](float m, int arg) {
+            if (m > r.max || (m == r.max && arg < r.tag)) r.max = m, r.tag = arg;
+        };
+        for (int i = lane; i < P.parts; i += 32) join(st[i].max, st[i].tag);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float m = __shfl_xor_sync(0xffffffffu, r.max, o);
-            const int arg = __shfl_xor_sync(0xffffffffu, r.arg, o);
-            if (m > r.max || (m == r.max && arg < r.arg)) r.max = m, r.arg = arg;
-        }
+        for (int o = 16; o > 0; o >>= 1)
+            join(__shfl_xor_sync(0xffffffffu, r.max, o), __shfl_xor_sync(0xffffffffu, r.tag, o));
         return r;
     }
     for (int i = lane; i < P.parts; i += 32) {
-        r.ref = fmaxf(r.ref, st[i].ref);
-        r.max = fmaxf(r.max, st[i].max);
-        r.careful |= st[i].careful;
+        const VerifyStat x = st[i];
+        const float to = fmaxf(r.ref, x.ref);
+        r.sum = r.sum * pow2(r.ref - to) + x.sum * pow2(x.ref - to);
+        r.ref = to;
+        r.max = fmaxf(r.max, x.max);
+        r.tag |= x.tag;
     }
-    r.ref = warp_max(r.ref);
+    r.tag = __any_sync(0xffffffffu, r.tag);
     r.max = warp_max(r.max);
-    r.careful = __any_sync(0xffffffffu, r.careful);
-    if (!r.careful) {
-        for (int i = lane; i < P.parts; i += 32) r.sum = r.sum + scaled(st[i].sum, pow2(st[i].ref - r.ref));
+    if (!r.tag) {
+        const float to = warp_max(r.ref);
+        r.sum *= pow2(r.ref - to);
+        r.ref = to;
     } else {
         // in 64 bits: every part's sum to the row's largest logit
+        double sum = 0.0;
         for (int i = lane; i < P.parts; i += 32) {
             const VerifyStat x = st[i];
-            if (x.sum.hi == 0.f) continue;
+            if (x.sum == 0.f) continue;
             double f = 1.0;
-            if (x.careful) {
-                if (x.max != r.max) f = exp2(((double)x.max - (double)r.max) * c.wide());
-            } else {
+            if (!x.tag)
                 f = exp2((double)x.ref - (double)r.max * c.wide());
-            }
-            const double y = wide(x.sum) * f;
-            const float hi = (float)y;
-            r.sum = r.sum + Pair{hi, (float)(y - (double)hi)};
+            else if (x.max != r.max)
+                f = exp2(((double)x.max - (double)r.max) * c.wide());
+            sum += (double)x.sum * f;
         }
+        r.sum = (float)sum;
     }
     r.sum = warp_sum(r.sum);
     return r;
@@ -372,13 +416,28 @@ DF_DEV float logit_at(const void* base, int dtype, int64_t i) {
            : dtype == kBF16 ? Vec<kBF16>::one(static_cast<const uint16_t*>(base) + i)
                             : Vec<kF16>::one(static_cast<const uint16_t*>(base) + i);
 }
-// p(x) of one entry, in 64 bits.
-DF_DEV double prob_at(float x, const VerifyStat& r, Scale c) {
-    if (r.max == -INFINITY || !(x > -INFINITY)) return 0.0;
-    const double w = !r.careful     ? exp2((double)x * c.wide() - (double)r.ref)
-                     : x == r.max ? 1.0
-                                  : exp2(((double)x - (double)r.max) * c.wide());
-    return w / wide(r.sum);
+// The weight of one entry of a row (its probability times the row's sum) to about 2^-22 however small it is,
+// for the numbers that accept a draft: the exponent as a pair, its whole part apart.
+DF_DEV float weight_exact(float x, const VerifyStat& r, Scale c) {
+    if (r.max == -INFINITY || !(x > -INFINITY)) return 0.f;
+    if (x == r.max && r.tag) return 1.f;
+    float y = x, yl = 0.f, ref = r.ref;
+    if (r.tag) {
+        y = x - r.max;
+        if (!(y > -INFINITY)) return 0.f;
+        const float t = y - x;
+        yl = (x - (y - t)) + (-r.max - t);
+        ref = 0.f;
+    }
+    const float p = y * c.hi, s = p - ref, t = s - p;
+    if (!(s > -1e9f)) return 0.f;
+    const float n = rintf(s), f = (s - n) + (fmaf(y, c.hi, -p) + ((p - (s - t)) + (-ref - t)) + fmaf(y, c.lo, yl * c.hi));
+    return ldexpf(exp2f(f), (int)n);
+}
+
+// The weight of an entry of a row.  A row without any probability has an infinite reference.
+DF_DEV float weight_any(float x, const VerifyStat& r, Scale c) {
+    return r.tag ? weight_careful(x, c, r.max) : weight(x, c, r.ref);
 }
 
 // What is left at the entries of the sampled row: mode 0 the target's
@@ -387,103 +446,132 @@ struct Left {
     const unsigned char* target;
     const float* draft;
     int dtype, mode, x;
-    bool aligned;  // both rows start at 16-byte boundaries
     VerifyStat t, q;
     float tz, qz;  // 1 / the rows' sums
     Scale c;
-    // the eight entries from i on (i a multiple of 8), 0 from `end` on
-    DF_DEV void eight(int i, int end, float (&w)[8]) const {
-        float a[8], b[8];
-        const bool vec = aligned && i + 8 <= end;
-        if (vec) {
-            if (dtype == kF32) {
-                Vec<kF32>::get(reinterpret_cast<const float*>(target) + i, a);
-                Vec<kF32>::get(reinterpret_cast<const float*>(target) + i + 4, a + 4);
-            } else if (dtype == kBF16) {
-                Vec<kBF16>::get(reinterpret_cast<const uint16_t*>(target) + i, a);
-            } else {
-                Vec<kF16>::get(reinterpret_cast<const uint16_t*>(target) + i, a);
-            }
-            if (mode == 2) {
-                Vec<kF32>::get(draft + i, b);
-                Vec<kF32>::get(draft + i + 4, b + 4);
+    // entries i, i + 32, .. (N of them, 0 from `end` on): all loads first
+    template <int N>
+    DF_DEV void get(int i, int end, float (&w)[N]) const {
+        float y[N];
+        if (dtype == kF32) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                w[k] = i + 32 * k < end ? __ldg(reinterpret_cast<const float*>(target) + i + 32 * k) : -INFINITY;
+        } else {
+            uint32_t u[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                u[k] = i + 32 * k < end ? __ldg(reinterpret_cast<const uint16_t*>(target) + i + 32 * k)
+                       : dtype == kBF16 ? 0xff80u
+                                        : 0xfc00u;
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                w[k] = dtype == kBF16 ? __uint_as_float(u[k] << 16) : __half2float(__ushort_as_half((uint16_t)u[k]));
+        }
+        if (mode == 2) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) y[k] = i + 32 * k < end ? __ldg(draft + i + 32 * k) : -INFINITY;
+        }
+        // (plain rows, nearly all there are, first: a weight is three instructions)
+        if (!t.tag && !q.tag) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                w[k] = weight(w[k], c, t.ref);
+                if (mode == 2) w[k] = fmaxf(fmaf(w[k], tz, -weight(y[k], c, q.ref) * qz), 0.f);
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                a[k] = i + k < end ? logit_at(target, dtype, i + k) : -INFINITY;
-                if (mode == 2) b[k] = i + k < end ? __ldg(draft + i + k) : -INFINITY;
+            for (int k = 0; k < N; ++k) {
+                w[k] = weight_any(w[k], t, c);
+                if (mode == 2) w[k] = fmaxf(fmaf(w[k], tz, -weight_any(y[k], q, c) * qz), 0.f);
             }
         }
+        // (absent entries are logits of -inf: no weight)
+        if (mode == 1) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            w[k] = t.careful ? weight_careful(a[k], c, t.max) : weight(a[k], c, t.ref);
-            if (mode == 1 && i + k == x) w[k] = 0.f;
-            if (mode == 2) {
-                float y = 0.f;
-                if (q.max > -INFINITY) y = (q.careful ? weight_careful(b[k], c, q.max) : weight(b[k], c, q.ref)) * qz;
-                w[k] = fmaxf(fmaf(w[k], tz, -y), 0.f);
-            }
-            if (i + k >= end) w[k] = 0.f;
+            for (int k = 0; k < N; ++k)
+                if (i + 32 * k == x) w[k] = 0.f;
         }
-    }
-    // their sums over [p0, p1), warp-wide: lane l holds the entries p0 + 8 l .. of every 256
-    DF_DEV float lane_sum(int i, int end, float (&w)[8]) const {
-        eight(i, end, w);
-        return ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
     }
 };
 
-__global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(kVpThreads)
+template <int WARPS>
+__global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
     verify_pick_kernel(const __grid_constant__ VerifyParams P) {
+    constexpr int kParts = kVpCluster * WARPS;  // vocabulary parts of the sampled row
+    constexpr int kKept = kVpKept / WARPS;      // entries of a warp's part that are kept
     const VerifyArgs& A = P.A;
+    // a round of 32 rows of the sequence: the target's statistics and the drafter's, the draft's logits
+    __shared__ VerifyStat stat[2][32];
+    __shared__ float logit[2][32];
     __shared__ int refused;
-    __shared__ double part_sum[2][kVpWarps];  // (two passes at most: each has its own)
-    __shared__ double chunk_sum[kVpWarps][kVpChunks];
+    __shared__ float2 part_sum[WARPS];           // the warps' sums
+    __shared__ float2 cta_sum[2][kVpCluster];    // the CTAs' (two passes at most: each has its own)
+    extern __shared__ float kept[];         // [WARPS][kKept]
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), s = blockIdx.x / kVpCluster;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) refused = 0x7fffffff;
-    __syncthreads();
     // the inputs are final before the statistics kernel lets this one start
     int a, b;
     draft_range(A, s, a, b);
     const int d = b - a;
     const Scale c = scale_of(A, s);
     const bool drawn = A.draft != nullptr && !c.greedy();  // q is the drafter's distribution, not one token
-    const int64_t nt = (int64_t)A.n_drafts + A.n_seqs;
+    const int64_t nt = (int64_t)A.n_drafts + A.n_seqs, row0 = (int64_t)a + s;
+    const float u_token = A.sample_u[s];
 
     // every CTA of the cluster decides alike; the first one writes
-    for (int i = warp; i < d; i += kVpWarps) {
-        const int64_t row = (int64_t)a + s + i;
-        const uint32_t x = A.draft_tok[a + i];
-        const bool known = x < (uint32_t)A.vocab;
-        const float u = A.accept_u[a + i];
-        const float lt = known ? logit_at(A.target, A.target_dtype, row * A.target_stride + x) : -INFINITY;
-        const float ld = known && drawn ? __ldg(A.draft + (int64_t)(a + i) * A.draft_stride + x) : -INFINITY;
-        pdl_wait();
-        const VerifyStat t = row_stat(P, row, c, lane);
-        double p, q = 1.0;
-        if (c.greedy())
-            p = known && t.max > -INFINITY && t.arg == (int)x ? 1.0 : 0.0;
-        else
-            p = known ? prob_at(lt, t, c) : 0.0;
-        if (drawn) {
-            const VerifyStat g = row_stat(P, nt + a + i, c, lane);
-            q = known ? prob_at(ld, g, c) : 0.0;
+    if (threadIdx.x == 0) refused = 0x7fffffff;
+    int i0 = 0;
+    for (;; i0 += 32) {
+        const int n = min(32, d + 1 - i0);  // rows of the round, the one after the last draft among them
+        for (int j = warp; j < (drawn ? 2 : 1) * n; j += WARPS) {
+            const int i = i0 + j % n, side = j / n;
+            float l = -INFINITY;
+            if (i < d) {
+                const uint32_t x = A.draft_tok[a + i];
+                if (x < (uint32_t)A.vocab)
+                    l = side ? __ldg(A.draft + (int64_t)(a + i) * A.draft_stride + x)
+                             : logit_at(A.target, A.target_dtype, (row0 + i) * A.target_stride + x);
+            }
+            pdl_wait();
+            if (side && i == d) continue;
+            const VerifyStat t = row_stat(P, side ? nt + a + i : row0 + i, c, lane);
+            if (lane == 0) {
+                stat[side][i - i0] = t;
+                logit[side][i - i0] = l;
+            }
         }
-        if (lane == 0) {
-            if (!((double)u * q < p)) atomicMin(&refused, i);
+        __syncthreads();
+        if (warp == 0 && i0 + lane < d) {
+            const int i = i0 + lane;
+            // p = wp / sp and q = wq / sq: compared as u wq sp < wp sq
+            const VerifyStat t = stat[0][lane];
+            float wp, sp = 1.f, wq = 1.f, sq = 1.f;
+            if (c.greedy()) {
+                wp = t.max > -INFINITY && t.tag == (int)A.draft_tok[a + i] ? 1.f : 0.f;
+            } else {
+                wp = weight_exact(logit[0][lane], t, c);
+                if (t.max > -INFINITY) sp = t.sum;
+            }
+            if (drawn) {
+                const VerifyStat g = stat[1][lane];
+                wq = weight_exact(logit[1][lane], g, c);
+                if (g.max > -INFINITY) sq = g.sum;
+            }
+            const double p = (double)wp * (double)sq, q = (double)wq * (double)sp;
+            if (!((double)A.accept_u[a + i] * q < p)) atomicMin(&refused, i);
             // (q = 0: a draft the drafter could not make; kept when p is not 0)
-            if (rank == 0 && A.prob != nullptr) A.prob[a + i] = (float)(p < q ? p / q : p > 0.0 ? 1.0 : 0.0);
+            if (rank == 0 && A.prob != nullptr) A.prob[a + i] = p < q ? (wp / sp) / (wq / sq) : wp > 0.f ? 1.f : 0.f;
         }
+        __syncthreads();
+        if (i0 + 32 > d) break;
     }
     pdl_wait();
-    __syncthreads();
     const int acc = min(refused, d);
-    const int64_t row = (int64_t)a + s + acc;
-    const VerifyStat t = row_stat(P, row, c, lane);
-    int token = t.max == -INFINITY ? -1 : t.arg;
+    const int64_t row = row0 + acc;
+    const VerifyStat t = acc >= i0 ? stat[0][acc - i0] : row_stat(P, row, c, lane);
+    int token = t.max == -INFINITY ? -1 : t.tag;
     bool writes = rank == 0 && threadIdx.x == 0;
     const bool sampled = !c.greedy() && t.max > -INFINITY;
     if (sampled) {
@@ -493,8 +581,9 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(kVpThreads)
         L.draft = nullptr;
         L.dtype = A.target_dtype;
         L.c = c;
-        L.t = L.q = t;
-        L.tz = (float)(1.0 / wide(t.sum));
+        L.t = t;
+        L.q = t;
+        L.tz = 1.f / t.sum;
         L.qz = 0.f;
         L.x = -1;
         L.mode = 0;
@@ -502,117 +591,88 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(kVpThreads)
             L.x = (int)min(A.draft_tok[a + acc], 0x7fffffffu);
             L.mode = 1;
             if (drawn) {
-                L.q = row_stat(P, nt + a + acc, c, lane);
+                const VerifyStat g = acc >= i0 ? stat[1][acc - i0] : row_stat(P, nt + a + acc, c, lane);
+                L.q = g;
+                if (g.max == -INFINITY) L.q.ref = INFINITY;
                 L.draft = A.draft + (int64_t)(a + acc) * A.draft_stride;
                 L.mode = 2;
-                L.qz = L.q.max == -INFINITY ? 0.f : (float)(1.0 / wide(L.q.sum));
+                L.qz = g.max == -INFINITY ? 0.f : 1.f / g.sum;
             }
         }
-        L.aligned = ((reinterpret_cast<uintptr_t>(L.target) | reinterpret_cast<uintptr_t>(L.draft)) & 15) == 0;
-        // this warp's part of the vocabulary, in chunks of a multiple of 256 entries
-        const int w = rank * kVpWarps + warp;
-        const int64_t v8 = ((int64_t)A.vocab + 7) / 8;
-        const int v0 = (int)(v8 * w / kVpParts) * 8, v1 = min((int)(v8 * (w + 1) / kVpParts) * 8, A.vocab);
-        const int chunk = 256 * max(1, (v1 - v0 + 256 * kVpChunks - 1) / (256 * kVpChunks));
-        const int nchunks = (max(v1 - v0, 0) + chunk - 1) / chunk;
-        const float u = A.sample_u[s];
+        // this warp's part of the vocabulary
+        const int w = rank * WARPS + warp;
+        const int v0 = (int)((int64_t)A.vocab * w / kParts), v1 = (int)((int64_t)A.vocab * (w + 1) / kParts);
+        float* mine_kept = kept + warp * kKept;
         for (int pass = 0; pass < 2; ++pass) {
-            double mine = 0.0;
-            for (int k = 0; k < nchunks; ++k) {
-                const int e = min(v0 + (k + 1) * chunk, v1);
-                Pair sum;
-#pragma unroll 2
-                for (int i = v0 + k * chunk + 8 * lane; i < e; i += 256) {
-                    float x[8];
-                    sum = sum + Pair{L.lane_sum(i, e, x), 0.f};
-                }
-                const double y = wide(warp_sum(sum));
-                if (lane == 0) chunk_sum[warp][k] = y;
-                mine += y;
+            Pair mine;
+            constexpr int N = 8;
+#pragma unroll 1
+            for (int i = v0 + lane; i < v1; i += 32 * N) {
+                float x[N];
+                L.get<N>(i, v1, x);
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    if (i - v0 + 32 * k < kKept) mine_kept[i - v0 + 32 * k] = x[k];
+                mine = mine + Pair{((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])), 0.f};
             }
-            if (lane == 0) part_sum[pass][warp] = mine;
+            mine = warp_sum(mine);
+            if (lane == 0) part_sum[warp] = make_float2(mine.hi, mine.lo);
+            __syncthreads();
+            // the running sums of the CTA's parts (warp 0; the others keep pace), its whole sum to every CTA
+            Pair own, up;
+            if (warp == 0) {
+                if (lane < WARPS) own = Pair{part_sum[lane].x, part_sum[lane].y};
+                up = warp_running(own, lane);
+                const Pair sum = shfl(up, 31);
+                if (lane < kVpCluster) *cl.map_shared_rank(&cta_sum[pass][rank], lane) = make_float2(sum.hi, sum.lo);
+            }
             cl.sync();
-            // the cluster's sums, kVpParts / 32 a lane in order, and their running sums
-            constexpr int PL = kVpParts / 32;
-            double sum[PL], run = 0.0;
-#pragma unroll
-            for (int k = 0; k < PL; ++k) {
-                const int j = lane * PL + k;
-                sum[k] = *cl.map_shared_rank(&part_sum[pass][j % kVpWarps], j / kVpWarps);
-                run += sum[k];
-            }
-            double in = run;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, in, o);
-                if (lane >= o) in += y;
-            }
-            const double whole = __shfl_sync(0xffffffffu, in, 31);
-            if (whole == 0.0 && L.mode != 0) {
+            Pair cta;
+            if (lane < kVpCluster) cta = Pair{cta_sum[pass][lane].x, cta_sum[pass][lane].y};
+            const Pair to = warp_running(cta, lane), whole = shfl(to, 31);
+            if (!positive(whole) && L.mode != 0) {
                 L.mode = 0;  // the draft had all of it: the target's own distribution
                 continue;
             }
-            double rest = (double)u * whole;
-            // the first part whose running sum passes the number's share (the last with any of it, should
-            // rounding or a number of 1 leave none)
-            int hit = 0x7fffffff, some = -1;
-            double before = in - run, hit_before = 0.0;
-#pragma unroll
-            for (int k = 0; k < PL; ++k) {
-                if (sum[k] > 0.0) {
-                    some = lane * PL + k;
-                    if (hit == 0x7fffffff && before + sum[k] > rest) hit = lane * PL + k, hit_before = before;
+            if (warp != 0) break;
+            Pair rest;  // u * whole
+            rest.hi = u_token * whole.hi;
+            rest.lo = fmaf(u_token, whole.hi, -rest.hi) + u_token * whole.lo;
+            // the first CTA whose running sum passes `rest`, then its first warp, a 32nd of that warp's part and
+            // so on to the entry; where none passes (rounding, or a number of 1), the last that has any weight
+            bool inside = true;
+            auto narrow = [&](Pair piece, Pair upto) -> int {
+                const uint32_t any = __ballot_sync(0xffffffffu, positive(piece));
+                const uint32_t over = __ballot_sync(0xffffffffu, inside && positive(piece) && positive(upto - rest));
+                const int l = over ? __ffs(over) - 1 : 31 - __clz(any);
+                inside = over != 0;
+                if (inside) rest = rest - shfl(upto - piece, l);
+                return l;
+            };
+            if (narrow(cta, to) != rank) break;
+            const int part = rank * WARPS + narrow(own, up);
+            const float* its_kept = kept + (part % WARPS) * kKept;
+            const int f0 = (int)((int64_t)A.vocab * part / kParts);
+            int p0 = f0, p1 = (int)((int64_t)A.vocab * (part + 1) / kParts);
+#pragma unroll 1
+            while (p1 - p0 > 1) {
+                const int per = (p1 - p0 + 31) / 32, q0 = min(p0 + lane * per, p1), q1 = min(q0 + per, p1);
+                float sum = 0.f;
+#pragma unroll 2
+                for (int i = q0; i < q1; ++i) {
+                    float x[1];
+                    if (i - f0 < kKept)
+                        x[0] = its_kept[i - f0];
+                    else
+                        L.get<1>(i, q1, x);
+                    sum += x[0];
                 }
-                before += sum[k];
+                const Pair piece{sum, 0.f};
+                const int l = narrow(piece, warp_running(piece, lane));
+                p0 = __shfl_sync(0xffffffffu, q0, l);
+                p1 = __shfl_sync(0xffffffffu, q1, l);
             }
-            const int first = (int)__reduce_min_sync(0xffffffffu, (unsigned)hit);
-            const int last = __reduce_max_sync(0xffffffffu, some);
-            if ((first != 0x7fffffff ? first : last) != w) break;
-            rest = first != 0x7fffffff ? rest - __shfl_sync(0xffffffffu, hit_before, first / PL) : INFINITY;
-            // the chunk, in order, the same way
-            int at = 0, k = 0;
-            for (; k < nchunks; ++k) {
-                const double y = chunk_sum[warp][k];
-                if (y <= 0.0) continue;
-                at = k;
-                if (y > rest) break;
-                rest -= y;
-            }
-            if (k == nchunks) rest = INFINITY;
-            // and the entry: 256 at a time, eight neighbours a lane
-            const int e = min(v0 + (at + 1) * chunk, v1);
-            int found = -1;
-            for (int i0 = v0 + at * chunk; i0 < e; i0 += 256) {
-                float x[8];
-                const double y = (double)L.lane_sum(i0 + 8 * lane, e, x);
-                double up = y;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double z = __shfl_up_sync(0xffffffffu, up, o);
-                    if (lane >= o) up += z;
-                }
-                const uint32_t any = __ballot_sync(0xffffffffu, y > 0.0);
-                const uint32_t over = __ballot_sync(0xffffffffu, y > 0.0 && up > rest);
-                if (any) {
-                    const int l = over ? __ffs(over) - 1 : 31 - __clz(any);
-                    // the lane's own entries: the first over what remains, else its last with any of it
-                    double r = over ? rest - (up - y) : INFINITY;
-                    int mine_at = -1;
-                    bool done = false;
-#pragma unroll
-                    for (int n = 0; n < 8; ++n) {
-                        if (!done && x[n] > 0.f) {
-                            mine_at = i0 + 8 * lane + n;
-                            if ((double)x[n] > r) done = true;
-                            r -= (double)x[n];
-                        }
-                    }
-                    found = __shfl_sync(0xffffffffu, mine_at, l);
-                }
-                if (over) break;
-                rest -= __shfl_sync(0xffffffffu, up, 31);
-            }
-            token = found;
+            token = p0;
             writes = lane == 0;
             break;
         }
@@ -624,11 +684,11 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(kVpThreads)
     if (sampled) cl.sync();  // no CTA leaves while its sums may be read
 }
 
-// Parts of a row: of at least 16 KB each, and where there are few rows enough
-// of them for a few CTAs an SM.
+// Parts of a row: of up to 32K entries, and where there are few rows as many
+// as give a few CTAs an SM, of 4K entries at least.
 static int verify_parts(int64_t rows, int64_t vocab, int num_sms) {
     const int64_t want = (16 * (int64_t)num_sms + rows - 1) / (rows > 0 ? rows : 1);
-    const int64_t most = (vocab + 4095) / 4096, least = (vocab + 16383) / 16384;
+    const int64_t most = (vocab + 4095) / 4096, least = (vocab + 32767) / 32768;
     const int64_t p = want < least ? least : want;
     return (int)(p > most ? most : p);
 }
@@ -644,6 +704,16 @@ int64_t verify_workspace(int n_seqs, int64_t n_drafts, int64_t vocab, int num_sm
     return most * (int64_t)sizeof(VerifyStat);
 }
 
+template <int WARPS>
+static int launch_pick(const VerifyParams& P, cudaStream_t st) {
+    constexpr size_t smem = kVpKept * sizeof(float);
+    static size_t limit[kMaxDevices] = {};
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return (int)e;
+    if (cudaError_t e = raise_smem_limit(verify_pick_kernel<WARPS>, smem, &limit[dev])) return (int)e;
+    return (int)launch(verify_pick_kernel<WARPS>, dim3((unsigned)P.A.n_seqs * kVpCluster), dim3(WARPS * 32), smem, st, P);
+}
+
 int verify(const VerifyArgs& A, void* ws, int num_sms, cudaStream_t st) {
     VerifyParams P;
     P.A = A;
@@ -652,7 +722,8 @@ int verify(const VerifyArgs& A, void* ws, int num_sms, cudaStream_t st) {
     P.parts = verify_parts(rows, A.vocab, num_sms);
     if (cudaError_t e = launch(verify_stats_kernel, dim3((unsigned)(rows * P.parts)), dim3(kVsThreads), 0, st, P))
         return (int)e;
-    return (int)launch(verify_pick_kernel, dim3((unsigned)A.n_seqs * kVpCluster), dim3(kVpThreads), 0, st, P);
+    // 32 warps a CTA while every CTA has an SM to itself, else 16 (two CTAs an SM)
+    return A.n_seqs * kVpCluster <= num_sms ? launch_pick<32>(P, st) : launch_pick<16>(P, st);
 }
 
 }  // namespace dflash
