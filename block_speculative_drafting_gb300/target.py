@@ -21,20 +21,23 @@ import numpy as np
 
 from . import _abi
 
-# The calls below run once a layer and step: what they do on the host is kept to a few microseconds (the C descriptors
-# are packed in one go, the library and torch are looked up once).
+# The calls below run once a layer and step, so what they do on the host is kept to some ten microseconds: the C
+# descriptors are packed in one go, attributes are asked for once, the library and torch are looked up once.
 torch = None
 _lib = None
 _DTYPES: dict = {}
+_current_device = _raw_stream = None
 
 
 def _init():
-    global torch, _lib
+    global torch, _lib, _current_device, _raw_stream
     import torch as t
 
     from . import lib
     _lib = lib()
     _DTYPES.update({t.float32: _abi.F32, t.bfloat16: _abi.BF16, t.float16: _abi.F16, t.float8_e4m3fn: _abi.E4M3})
+    _current_device = t.cuda.current_device
+    _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda d: t.cuda.current_stream(d).cuda_stream)
     torch = t
 
 
@@ -54,11 +57,7 @@ def _direct(dev: int, stream) -> bool:
     """Whether a call can run where it stands: on the current device, on its current stream."""
     if dev < 0:
         _refuse("tensors have to be on a CUDA device")
-    return stream is None and dev == torch.cuda.current_device()
-
-
-def _current_stream(dev: int) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+    return stream is None and dev == _current_device()
 
 
 @contextlib.contextmanager
@@ -79,66 +78,70 @@ def _same_device(dev: int, *tensors):
             _refuse(f"a tensor of shape {tuple(t.shape)} is on {t.device}, not on cuda:{dev}")
 
 
-def _dtype(t, name: str) -> int:
-    d = _DTYPES.get(t.dtype)
-    if d is None:
-        _refuse(f"{name} has dtype {t.dtype}")
-    return d
-
-
-def _vector(t, name: str, n: int, dtype):
+def _vector(t, name: str, n: int, dtype) -> int:
     """Pointer of a contiguous vector of n elements (None: 0)."""
     if t is None:
         return 0
-    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.dtype is not dtype or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         _refuse(f"{name} has to be a contiguous vector of {n} elements of {dtype}, got {tuple(t.shape)} of {t.dtype}")
     return t.data_ptr()
 
 
-def _written(t, name: str):
-    if 0 in t.stride() and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
-        _refuse(f"{name} is written and may not be an expanded tensor")
-
-
-def _head_rows(t, name: str) -> bytes:
-    """A [rows][heads][head_dim] tensor as a dflash_head_rows."""
-    if t.dim() != 3:
-        _refuse(f"{name} has to be [rows][heads][head_dim], got {tuple(t.shape)}")
-    (n, h, w), (sr, sh, sw) = t.shape, t.stride()
-    if sw != 1 and w > 1:
+def _head_rows(t, name: str, n: int, hd: int, written: bool = False) -> bytes:
+    """A [n][heads][hd] tensor as a dflash_head_rows (a type it has no code for: -1, which the library refuses)."""
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != n or shape[2] != hd:
+        _refuse(f"{name} has to be [{n}][heads][{hd}], got {tuple(shape)}")
+    h = shape[1]
+    sr, sh, sc = t.stride()
+    if sc != 1:
         _refuse(f"{name} needs contiguous columns")
-    return _abi.HEAD_ROWS.pack(t.data_ptr(), _dtype(t, name), h, sr if n > 1 else 0, sh if h > 1 else 0)
+    if n <= 1:  # the stride of a dimension of one element is anything
+        sr = 0
+    elif written and sr == 0:
+        _refuse(f"{name} is written and may not be an expanded tensor")
+    if h <= 1:
+        sh = 0
+    elif written and sh == 0:
+        _refuse(f"{name} is written and may not be an expanded tensor")
+    return _HEAD_ROWS(t.data_ptr(), _DTYPES.get(t.dtype, -1), h, sr, sh)
 
 
-def _cache(k, v, k_scale, v_scale) -> bytes:
-    """The two cache tensors as a dflash_paged_cache."""
-    if k.dim() != 4 or k.shape != v.shape or k.dtype is not v.dtype:
+_HEAD_ROWS, _PAGED_CACHE, _PAGED_ROWS = _abi.HEAD_ROWS.pack, _abi.PAGED_CACHE.pack, _abi.PAGED_ROWS.pack
+
+
+def _cache(k, v, shape, k_scale, v_scale, written: bool = False) -> bytes:
+    """The two cache tensors, k of the given shape, as a dflash_paged_cache."""
+    if len(shape) != 4 or v.shape != shape or v.dtype is not k.dtype:
         _refuse("k_cache and v_cache have to be [pages][page_size][kv_heads][head_dim] of one shape and type, got "
-                f"{tuple(k.shape)} and {tuple(v.shape)}")
-    n, page, heads, hd = k.shape
+                f"{tuple(shape)} of {k.dtype} and {tuple(v.shape)} of {v.dtype}")
+    n, page, heads, hd = shape
     k0, k1, k2, k3 = k.stride()
     v0, v1, v2, v3 = v.stride()
-    if (k3 != 1 or v3 != 1) and hd > 1:
+    if k3 != 1 or v3 != 1:
         _refuse("k_cache and v_cache need contiguous columns")
-    if n == 1 or page == 1 or heads == 1:  # the stride of a dimension of one element is anything
-        k0, v0 = (0, 0) if n == 1 else (k0, v0)
-        k1, v1 = (0, 0) if page == 1 else (k1, v1)
-        k2, v2 = (0, 0) if heads == 1 else (k2, v2)
+    if n <= 1 or page <= 1 or heads <= 1:  # the stride of a dimension of one element is anything
+        k0, v0 = (0, 0) if n <= 1 else (k0, v0)
+        k1, v1 = (0, 0) if page <= 1 else (k1, v1)
+        k2, v2 = (0, 0) if heads <= 1 else (k2, v2)
+    if written and not (k0 and k1 and k2 and v0 and v1 and v2) and (
+            n > 1 and not (k0 and v0) or page > 1 and not (k1 and v1) or heads > 1 and not (k2 and v2)):
+        _refuse("k_cache and v_cache are written and may not be expanded tensors")
     ks = vs = 0
     if k_scale is not None or v_scale is not None:
-        ks, vs = (_vector(x, "k_scale and v_scale", heads, torch.float32) for x in (k_scale, v_scale))
-    return _abi.PAGED_CACHE.pack(k.data_ptr(), v.data_ptr(), _dtype(k, "k_cache"), heads, hd, page, n, k0, k1, k2, v0,
-                                 v1, v2, ks, vs)
+        ks = _vector(k_scale, "k_scale", heads, torch.float32)
+        vs = _vector(v_scale, "v_scale", heads, torch.float32)
+    return _PAGED_CACHE(k.data_ptr(), v.data_ptr(), _DTYPES.get(k.dtype, -1), heads, hd, page, n, k0, k1, k2, v0, v1,
+                        v2, ks, vs)
 
 
 def _rows(table, kv_len, row_start, n_rows: int) -> bytes:
-    if table.dim() != 2 or table.dtype is not torch.int32 or (table.stride(1) != 1 and table.shape[1] > 1):
-        _refuse(f"table has to be int32 [sequences][pages] with contiguous rows, got {tuple(table.shape)} of "
-                f"{table.dtype}")
-    n, width = table.shape
-    return _abi.PAGED_ROWS.pack(n, width, n_rows, _vector(row_start, "row_start", n + 1, torch.int32),
-                                _vector(kv_len, "kv_len", n, torch.int32), table.data_ptr(),
-                                table.stride(0) if n > 1 else width)
+    i32, shape = torch.int32, table.shape
+    if table.dtype is not i32 or len(shape) != 2 or (shape[1] > 1 and table.stride(1) != 1):
+        _refuse(f"table has to be int32 [sequences][pages] with contiguous rows, got {tuple(shape)} of {table.dtype}")
+    n, width = shape
+    return _PAGED_ROWS(n, width, n_rows, 0 if row_start is None else _vector(row_start, "row_start", n + 1, i32),
+                       _vector(kv_len, "kv_len", n, i32), table.data_ptr(), table.stride(0) if n > 1 else width)
 
 
 def rope_inv_freq(rotary: int, theta: float = 1e6, scaling: str | None = None, factor: float = 1.0,
@@ -201,33 +204,33 @@ def paged_append(k_cache, v_cache, k, v, table, kv_len, *, row_start=None, q=Non
                                 inv_freq=inv_freq, interleaved=interleaved, rope_scale=rope_scale, q_norm=q_norm,
                                 k_norm=k_norm, eps=eps, k_scale=k_scale, v_scale=v_scale)
     _same_device(dev, v_cache, k, v, table, kv_len, row_start, q, q_out, inv_freq, q_norm, k_norm, k_scale, v_scale)
-    if k.dim() != 3 or v.shape != k.shape or k.shape[1:] != k_cache.shape[2:]:
-        _refuse(f"k and v have to be [rows][kv_heads][head_dim] of the cache, got {tuple(k.shape)} and "
-                f"{tuple(v.shape)}")
-    n, _, hd = k.shape
-    cache = _cache(k_cache, v_cache, k_scale, v_scale)
-    _written(k_cache, "k_cache")
-    _written(v_cache, "v_cache")
+    shape, n = k_cache.shape, k.shape[0] if k.dim() else 0
+    cache = _cache(k_cache, v_cache, shape, k_scale, v_scale, True)
+    kv_heads, hd = shape[2], shape[3]
+    kr, vr = _head_rows(k, "k", n, hd), _head_rows(v, "v", n, hd)
     qr = qo = rot = None
     if inv_freq is not None:
         f = inv_freq.numel()
         rot = _abi.ROTATION.pack(_vector(inv_freq, "inv_freq", f, torch.float64), 2 * f, 1 if interleaved else 0,
                                  rope_scale)
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != hd:
-            _refuse(f"q has to be [{n}][heads][{hd}], got {tuple(q.shape)}")
+        qr = _head_rows(q, "q", n, hd)
         if q_out is None:
             q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         elif q_out.shape != q.shape:
             _refuse(f"q_out has to be {tuple(q.shape)}, got {tuple(q_out.shape)}")
-        _written(q_out, "q_out")
-        qr, qo = _head_rows(q, "q"), _head_rows(q_out, "q_out")
+        qo = _head_rows(q_out, "q_out", n, hd, True)
     elif q_out is not None:
         _refuse("q_out without q")
-    _check(_lib.dflash_paged_append(cache, _rows(table, kv_len, row_start, n), _head_rows(k, "k"), _head_rows(v, "v"),
-                                    qr, qo, _vector(q_norm, "q_norm", hd, torch.float32),
-                                    _vector(k_norm, "k_norm", hd, torch.float32), eps, rot,
-                                    _current_stream(dev)))
+    qn = kn = 0
+    if q_norm is not None:
+        qn = _vector(q_norm, "q_norm", hd, torch.float32)
+    if k_norm is not None:
+        kn = _vector(k_norm, "k_norm", hd, torch.float32)
+    rc = _lib.dflash_paged_append(cache, _rows(table, kv_len, row_start, n), kr, vr, qr, qo, qn, kn, eps, rot,
+                                  _raw_stream(dev))
+    if rc < 0:
+        _check(rc)
     return q_out
 
 
@@ -253,26 +256,30 @@ def paged_attention(q, k_cache, v_cache, table, kv_len, *, row_start=None, scale
             return paged_attention(q, k_cache, v_cache, table, kv_len, row_start=row_start, scale=scale, window=window,
                                    k_scale=k_scale, v_scale=v_scale, out=out, lse=lse, workspace=workspace)
     _same_device(dev, k_cache, v_cache, table, kv_len, row_start, k_scale, v_scale, out, lse, workspace)
-    if q.dim() != 3 or k_cache.dim() != 4 or q.shape[2] != k_cache.shape[3]:
-        _refuse(f"q has to be [rows][heads][head_dim] of the cache, got {tuple(q.shape)}")
-    n, heads, hd = q.shape
-    cache, rows = _cache(k_cache, v_cache, k_scale, v_scale), _rows(table, kv_len, row_start, n)
+    shape, qshape = k_cache.shape, q.shape
+    cache = _cache(k_cache, v_cache, shape, k_scale, v_scale)
+    if len(qshape) != 3:
+        _refuse(f"q has to be [rows][heads][head_dim], got {tuple(qshape)}")
+    n, heads, hd = qshape[0], qshape[1], shape[3]
+    qr, rows = _head_rows(q, "q", n, hd), _rows(table, kv_len, row_start, n)
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous()):
         _refuse(f"lse has to be contiguous float32 [{n}][{heads}]")
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    elif out.shape != q.shape:
-        _refuse(f"out has to be {tuple(q.shape)}, got {tuple(out.shape)}")
-    else:
-        _written(out, "out")
+    elif out.shape != qshape:
+        _refuse(f"out has to be {tuple(qshape)}, got {tuple(out.shape)}")
     if workspace is None:
         need = _check(_lib.dflash_paged_attention_workspace(cache, table.shape[0], n, heads))
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif not workspace.is_contiguous():
-        _refuse("workspace has to be contiguous")
-    _check(_lib.dflash_paged_attention(cache, rows, _head_rows(q, "q"), _head_rows(out, "out"),
-                                       None if lse is None else lse.data_ptr(), hd ** -0.5 if scale is None else scale,
-                                       window, workspace.data_ptr(), workspace.nbytes, _current_stream(dev)))
+    else:
+        if not workspace.is_contiguous():
+            _refuse("workspace has to be contiguous")
+        need = workspace.nbytes
+    rc = _lib.dflash_paged_attention(cache, rows, qr, _head_rows(out, "out", n, hd, True),
+                                     0 if lse is None else lse.data_ptr(), hd ** -0.5 if scale is None else scale,
+                                     window, workspace.data_ptr(), need, _raw_stream(dev))
+    if rc < 0:
+        _check(rc)
     return out
 
 
@@ -284,8 +291,8 @@ def paged_attention_workspace(q, k_cache, n_seqs: int) -> int:
     if not _direct(dev, None):
         with _moved(dev, None):
             return paged_attention_workspace(q, k_cache, n_seqs)
-    return _check(_lib.dflash_paged_attention_workspace(_cache(k_cache, k_cache, None, None), n_seqs, q.shape[0],
-                                                        q.shape[1]))
+    cache = _cache(k_cache, k_cache, k_cache.shape, None, None)
+    return _check(_lib.dflash_paged_attention_workspace(cache, n_seqs, q.shape[0], q.shape[1]))
 
 
 def verify_drafts(target_logits, draft_tokens, accept_u, sample_u, *, draft_logits=None, draft_start=None,
@@ -345,15 +352,19 @@ def verify_drafts(target_logits, draft_tokens, accept_u, sample_u, *, draft_logi
     if workspace is None:
         need = _check(_lib.dflash_verify_workspace(n, d, vocab))
         workspace = torch.empty(need, dtype=torch.uint8, device=target_logits.device)
-    elif not workspace.is_contiguous():
-        _refuse("workspace has to be contiguous")
-    _check(_lib.dflash_verify(
-        target_logits.data_ptr(), _dtype(target_logits, "target_logits"), stride if rows > 1 else vocab, dl, ds,
+    else:
+        if not workspace.is_contiguous():
+            _refuse("workspace has to be contiguous")
+        need = workspace.nbytes
+    rc = _lib.dflash_verify(
+        target_logits.data_ptr(), _DTYPES.get(target_logits.dtype, -1), stride if rows > 1 else vocab, dl, ds,
         draft_tokens.data_ptr(), _vector(draft_start, "draft_start", n + 1, i32),
         _vector(temperature, "temperature", n, f32), _vector(accept_u, "accept_u", d, f32),
         _vector(sample_u, "sample_u", n, f32), n, d, vocab, _vector(accepted, "accepted", n, i32),
-        _vector(next_token, "next_token", n, i32), _vector(prob, "prob", d, f32), workspace.data_ptr(),
-        workspace.nbytes, _current_stream(dev)))
+        _vector(next_token, "next_token", n, i32), _vector(prob, "prob", d, f32), workspace.data_ptr(), need,
+        _raw_stream(dev))
+    if rc < 0:
+        _check(rc)
     return accepted, next_token, prob
 
 
