@@ -156,6 +156,8 @@ int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_rows
             (q->dtype != q_out->dtype || q->row_stride != q_out->row_stride || q->head_stride != q_out->head_stride))
             return fail(DFLASH_EINVAL, "q_out in q's place needs q's type and strides");
     }
+    if (v->dtype != k->dtype || (q != nullptr && q->dtype != k->dtype))
+        return fail(DFLASH_EINVAL, "q, k and v need one type");
     if (!al16(q_norm) || !al16(k_norm)) return fail(DFLASH_EINVAL, "norm gains need 16-byte alignment");
     if ((q_norm != nullptr || k_norm != nullptr) && !(eps >= 0.f && std::isfinite(eps)))
         return fail(DFLASH_EINVAL, "eps %g", (double)eps);
@@ -169,7 +171,9 @@ int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_rows
         rot = Rotation{rotation->inv_freq, rotation->rotary, rotation->interleaved != 0, rotation->scale};
     }
     if (R.n_rows == 0) return DFLASH_OK;
-    return launched(paged_append(C, cache->dtype, cache->head_dim, R, K, V, Q, QO, q_norm, k_norm, eps, rot,
+    int n = 0;
+    TRY(sms(&n));
+    return launched(paged_append(C, cache->dtype, cache->head_dim, R, K, V, Q, QO, q_norm, k_norm, eps, rot, n,
                                  static_cast<cudaStream_t>(stream)),
                     "dflash_paged_append");
 }

@@ -91,7 +91,7 @@ struct Rotation {
 };
 int paged_append(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& k, const HeadRows& v,
                  const HeadRows& q, const HeadRows& qo, const float* q_norm, const float* k_norm, float eps,
-                 const Rotation& rot, cudaStream_t st);
+                 const Rotation& rot, int num_sms, cudaStream_t st);
 
 int64_t paged_attention_workspace(int hd, int n_seqs, int64_t n_rows, int heads, int kv_heads, int num_sms);
 int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& q,

@@ -185,7 +185,8 @@ def paged_append(k_cache, v_cache, k, v, table, kv_len, *, row_start=None, q=Non
 
     k_cache, v_cache  [pages][page_size][kv_heads][head_dim] bfloat16, float16 or float8_e4m3fn, any strides with
                       contiguous columns; k_scale, v_scale [kv_heads] float32: an 8-bit element is code * scale
-    k, v, q           [rows][heads][head_dim] float32, bfloat16 or float16 (slices of a fused projection fit)
+    k, v, q           [rows][heads][head_dim] of one type: float32, bfloat16 or float16 (slices of a fused projection
+                      fit)
     table             int32 [sequences][pages]; a page id outside the cache: not held, not written
     kv_len            int32 [sequences]: tokens in each sequence's cache with its new rows in; row i of its r rows
                       stands at position kv_len - r + i

@@ -580,8 +580,8 @@ typedef struct {
  * x / scale, clamped to +-448, NaN kept), q' = rot_p(norm(q)) to q_out.
  * norm(x) = x / sqrt(mean(x^2) + eps) * gain over a head, with f32 gains
  * q_norm, k_norm [head_dim] on the device (NULL: no norm).  rotation NULL: no
- * rotation.  q NULL: keys and values alone.  q_out may be q itself and may be
- * of another type.  A row whose position is not held is not written to the
+ * rotation.  q NULL: keys and values alone.  q, k and v have one type; q_out
+ * may be q itself, or of another type.  A row whose position is not held is not written to the
  * cache (its q' is written).  A table that maps two of the call's rows to one
  * slot leaves either row's elements there.
  * Errors: EINVAL, EGEOM, ECUDA.
