@@ -29,124 +29,12 @@
 // or NaN value would not be, so such stages look for non-finite values and,
 // where there are any, add P V row by row with the hidden keys left out.
 #include "kernels.cuh"
-#include "paged.cuh"
+#include "paged_attn.cuh"
 
 namespace dflash {
 
 constexpr int kPaThreads = 256, kPaWarps = 8;
-constexpr int kPaTile = 128;     // keys a CTA takes at once: 16 a warp
-constexpr float kPaLazy = 8.f;   // log2 units a score may pass the reference before a rescale
 
-struct PaArgs {
-    PagedCache C;
-    PagedRows R;
-    HeadRows q, out;
-    float* lse;
-    float* ws_o;     // [2 CTAs][MT][HD]
-    float2* ws_ml;   // [2 CTAs][MT]
-    float scale_log2;
-    int window, group;
-};
-
-// What the walk needs of one sequence.
-struct PaSeq {
-    int row0, rows, p0;  // its rows of the call; the position of the first
-    int lo, hi;          // keys that any of its rows may see
-    int ntiles, nunits;
-};
-
-DF_DEV PaSeq pa_seq(const PaArgs& A, int s, int mt) {
-    PaSeq q;
-    int b;
-    rows_of(A.R, s, q.row0, b);
-    q.rows = b - q.row0;
-    const int len = A.R.kv_len[s];
-    q.p0 = max(len, -1) - q.rows;  // a length below 0 reads as -1: no position of any row is held
-    q.hi = min(max(len, 0), A.R.cap);
-    q.lo = A.window > 0 ? max(0, q.p0 - A.window + 1) : 0;
-    q.ntiles = max(1, (q.hi - q.lo + kPaTile - 1) / kPaTile);  // a sequence with rows but no keys: one tile of nothing
-    q.nunits = (int)(((int64_t)q.rows * A.group + mt - 1) / mt) * A.C.kv_heads;
-    return q;
-}
-
-// Warp-wide: the line's length, and the share of a CTA.
-DF_DEV int64_t pa_total(const PaArgs& A, int mt, int lane) {
-    int64_t t = 0;
-    for (int s = lane; s < A.R.n_seqs; s += 32) {
-        const PaSeq q = pa_seq(A, s, mt);
-        t += (int64_t)q.ntiles * q.nunits;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    return t;
-}
-// Tiles before sequence `upto` (warp-wide).
-DF_DEV int64_t pa_before(const PaArgs& A, int mt, int lane, int upto) {
-    int64_t t = 0;
-    for (int s = lane; s < upto; s += 32) {
-        const PaSeq q = pa_seq(A, s, mt);
-        t += (int64_t)q.ntiles * q.nunits;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    return t;
-}
-// The sequence that holds tile t of the line, and the tiles before it.
-DF_DEV int pa_find(const PaArgs& A, int mt, int lane, int64_t t, int64_t& before) {
-    int64_t run = 0;
-    for (int s0 = 0; s0 < A.R.n_seqs; s0 += 32) {
-        int64_t w = 0;
-        if (s0 + lane < A.R.n_seqs) {
-            const PaSeq q = pa_seq(A, s0 + lane, mt);
-            w = (int64_t)q.ntiles * q.nunits;
-        }
-        int64_t in = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, in, o);
-            if (lane >= o) in += y;
-        }
-        const uint32_t hit = __ballot_sync(0xffffffffu, run + in > t);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            before = run + __shfl_sync(0xffffffffu, in - w, l);
-            return s0 + l;
-        }
-        run += __shfl_sync(0xffffffffu, in, 31);
-    }
-    before = run;
-    return A.R.n_seqs;
-}
-
-// A place on the line: tile `tile` of unit `u` of sequence `s`.
-struct PaCur {
-    PaSeq q;
-    int s, u, tile;
-    int64_t left;  // tiles of the CTA's share from here on
-};
-DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c) {
-    --c.left;
-    if (++c.tile < c.q.ntiles) return;
-    c.tile = 0;
-    if (++c.u < c.q.nunits || c.left <= 0) return;
-    c.u = 0;
-    do {
-        if (++c.s >= A.R.n_seqs) {  // (never, while the lengths stay as they were counted)
-            c.left = 0;
-            return;
-        }
-        c.q = pa_seq(A, c.s, mt);
-    } while (c.q.nunits == 0);
-}
-
-DF_DEV void cp16(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-DF_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-DF_DEV void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 DF_DEV void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -170,37 +58,6 @@ DF_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// 2^x by the special-function unit (relative error about 2^-22: the level of f32 rounding)
-DF_DEV float pa_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// two e4m3 codes -> two f16 (exact)
-DF_DEV uint32_t e4m3x2_f16x2(uint32_t codes) {
-    uint32_t y;
-    asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(y) : "r"(codes));
-    return y;
-}
-// (a, b) -> a pair of 16-bit floats, and what the rounding left
-template <bool BF>
-DF_DEV uint32_t pack2(float a, float b) {
-    if constexpr (BF) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-}
-template <bool BF>
-DF_DEV float2 unpack2(uint32_t u) {
-    if constexpr (BF)
-        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
-    else
-        return __half22float2(*reinterpret_cast<const __half2*>(&u));
-}
-
 // BF: MMAs and cache in bf16 (else f16).  E8: an e4m3 cache; its codes become
 // f16 exactly, and a query row is brought into f16 by a power of two.
 template <bool BF, bool E8, int HD, int RW>
@@ -755,15 +612,16 @@ __global__ void __launch_bounds__(kPaThreads)
             l == 0.f ? -INFINITY : (m == -INFINITY ? l : (m + log2f(l)) * 0.69314718056f);
 }
 
-// Rows a unit's tile holds: by what a sequence of average length brings.
-static int pa_row_warps(int n_seqs, int64_t n_rows, int group) {
+// Rows a unit's tile holds, by what a sequence of average length brings: 16 or
+// 32 on the warp MMAs, beyond that the tcgen05 kernel's 128.
+static int pa_tile_rows(int n_seqs, int64_t n_rows, int group) {
     const int64_t per = n_seqs > 0 ? (n_rows + n_seqs - 1) / n_seqs : 0;
     const int64_t m = per * group;
-    return m <= 16 ? 1 : m <= 32 ? 2 : m <= 64 ? 4 : 8;
+    return m <= 16 ? 16 : m <= 32 ? 32 : 128;
 }
 
 int64_t paged_attention_workspace(int hd, int n_seqs, int64_t n_rows, int heads, int kv_heads, int num_sms) {
-    const int64_t mt = 16 * pa_row_warps(n_seqs, n_rows, heads / kv_heads);
+    const int64_t mt = pa_tile_rows(n_seqs, n_rows, heads / kv_heads);
     return 2 * (int64_t)num_sms * mt * (hd * 4 + 8);
 }
 
@@ -776,17 +634,20 @@ static int pa_launch(const PaArgs& A, int num_sms, cudaStream_t st) {
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return (int)e;
     if (cudaError_t e = raise_smem_limit(kern, S::kSmem, &limit[dev])) return (int)e;
-    if (cudaError_t e = launch(kern, dim3(num_sms), dim3(kPaThreads), S::kSmem, st, A)) return (int)e;
-    const int64_t jobs = (int64_t)A.R.n_rows * A.q.heads;
-    return (int)launch(paged_join_kernel<HD>, dim3((unsigned)((jobs + kPaWarps - 1) / kPaWarps)), dim3(kPaThreads), 0,
-                       st, A, S::MT, num_sms, (int)E8);
+    return (int)launch(kern, dim3(num_sms), dim3(kPaThreads), S::kSmem, st, A);
 }
 template <bool BF, bool E8, int HD>
-static int pa_rw(const PaArgs& A, int rw, int num_sms, cudaStream_t st) {
-    return rw == 1   ? pa_launch<BF, E8, HD, 1>(A, num_sms, st)
-           : rw == 2 ? pa_launch<BF, E8, HD, 2>(A, num_sms, st)
-           : rw == 4 ? pa_launch<BF, E8, HD, 4>(A, num_sms, st)
-                     : pa_launch<BF, E8, HD, 8>(A, num_sms, st);
+static int pa_rw(const PaArgs& A, int mt, int num_sms, cudaStream_t st) {
+    return mt == 16 ? pa_launch<BF, E8, HD, 1>(A, num_sms, st) : pa_launch<BF, E8, HD, 2>(A, num_sms, st);
+}
+static int pa_warp(const PaArgs& A, int cache_dtype, int hd, int mt, int num_sms, cudaStream_t st) {
+    if (hd == 64)
+        return cache_dtype == kBF16  ? pa_rw<true, false, 64>(A, mt, num_sms, st)
+               : cache_dtype == kF16 ? pa_rw<false, false, 64>(A, mt, num_sms, st)
+                                     : pa_rw<false, true, 64>(A, mt, num_sms, st);
+    return cache_dtype == kBF16  ? pa_rw<true, false, 128>(A, mt, num_sms, st)
+           : cache_dtype == kF16 ? pa_rw<false, false, 128>(A, mt, num_sms, st)
+                                 : pa_rw<false, true, 128>(A, mt, num_sms, st);
 }
 
 int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& q,
@@ -795,16 +656,17 @@ int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRow
     A.C = C, A.R = R, A.q = q, A.out = out, A.lse = lse, A.window = window;
     A.scale_log2 = scale * 1.4426950408889634f;
     A.group = q.heads / C.kv_heads;
-    const int rw = pa_row_warps(R.n_seqs, R.n_rows, A.group);
+    const int mt = pa_tile_rows(R.n_seqs, R.n_rows, A.group);
     A.ws_o = static_cast<float*>(ws);
-    A.ws_ml = reinterpret_cast<float2*>(A.ws_o + 2 * (int64_t)num_sms * 16 * rw * hd);
-    if (hd == 64)
-        return cache_dtype == kBF16  ? pa_rw<true, false, 64>(A, rw, num_sms, st)
-               : cache_dtype == kF16 ? pa_rw<false, false, 64>(A, rw, num_sms, st)
-                                     : pa_rw<false, true, 64>(A, rw, num_sms, st);
-    return cache_dtype == kBF16  ? pa_rw<true, false, 128>(A, rw, num_sms, st)
-           : cache_dtype == kF16 ? pa_rw<false, false, 128>(A, rw, num_sms, st)
-                                 : pa_rw<false, true, 128>(A, rw, num_sms, st);
+    A.ws_ml = reinterpret_cast<float2*>(A.ws_o + 2 * (int64_t)num_sms * mt * hd);
+    const int e = mt == 128 ? paged_attention_tc(A, cache_dtype, hd, num_sms, st)
+                            : pa_warp(A, cache_dtype, hd, mt, num_sms, st);
+    if (e != 0) return e;
+    const int64_t jobs = (int64_t)R.n_rows * q.heads;
+    const dim3 grid((unsigned)((jobs + kPaWarps - 1) / kPaWarps));
+    const int e8 = cache_dtype == kE4M3;
+    return hd == 64 ? (int)launch(paged_join_kernel<64>, grid, dim3(kPaThreads), 0, st, A, mt, num_sms, e8)
+                    : (int)launch(paged_join_kernel<128>, grid, dim3(kPaThreads), 0, st, A, mt, num_sms, e8);
 }
 
 }  // namespace dflash

@@ -1,0 +1,157 @@
+// What the two kernels of the attention over a paged cache share: the line of
+// work that the CTAs cut into equal parts and the walk along it, asynchronous
+// copies, and conversions of 16-bit and 8-bit floats.
+#pragma once
+
+#include "paged.cuh"
+
+namespace dflash {
+
+constexpr int kPaTile = 128;     // keys a CTA takes at once: 16 a warp
+constexpr float kPaLazy = 8.f;   // log2 units a score may pass the reference before a rescale
+
+struct PaArgs {
+    PagedCache C;
+    PagedRows R;
+    HeadRows q, out;
+    float* lse;
+    float* ws_o;     // [2 CTAs][MT][HD]
+    float2* ws_ml;   // [2 CTAs][MT]
+    float scale_log2;
+    int window, group;
+};
+
+// What the walk needs of one sequence.
+struct PaSeq {
+    int row0, rows, p0;  // its rows of the call; the position of the first
+    int lo, hi;          // keys that any of its rows may see
+    int ntiles, nunits;
+};
+
+DF_DEV PaSeq pa_seq(const PaArgs& A, int s, int mt) {
+    PaSeq q;
+    int b;
+    rows_of(A.R, s, q.row0, b);
+    q.rows = b - q.row0;
+    const int len = A.R.kv_len[s];
+    q.p0 = max(len, -1) - q.rows;  // a length below 0 reads as -1: no position of any row is held
+    q.hi = min(max(len, 0), A.R.cap);
+    q.lo = A.window > 0 ? max(0, q.p0 - A.window + 1) : 0;
+    q.ntiles = max(1, (q.hi - q.lo + kPaTile - 1) / kPaTile);  // a sequence with rows but no keys: one tile of nothing
+    q.nunits = (int)(((int64_t)q.rows * A.group + mt - 1) / mt) * A.C.kv_heads;
+    return q;
+}
+
+// Warp-wide: the line's length, and the share of a CTA.
+DF_DEV int64_t pa_total(const PaArgs& A, int mt, int lane) {
+    int64_t t = 0;
+    for (int s = lane; s < A.R.n_seqs; s += 32) {
+        const PaSeq q = pa_seq(A, s, mt);
+        t += (int64_t)q.ntiles * q.nunits;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    return t;
+}
+// Tiles before sequence `upto` (warp-wide).
+DF_DEV int64_t pa_before(const PaArgs& A, int mt, int lane, int upto) {
+    int64_t t = 0;
+    for (int s = lane; s < upto; s += 32) {
+        const PaSeq q = pa_seq(A, s, mt);
+        t += (int64_t)q.ntiles * q.nunits;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    return t;
+}
+// The sequence that holds tile t of the line, and the tiles before it.
+DF_DEV int pa_find(const PaArgs& A, int mt, int lane, int64_t t, int64_t& before) {
+    int64_t run = 0;
+    for (int s0 = 0; s0 < A.R.n_seqs; s0 += 32) {
+        int64_t w = 0;
+        if (s0 + lane < A.R.n_seqs) {
+            const PaSeq q = pa_seq(A, s0 + lane, mt);
+            w = (int64_t)q.ntiles * q.nunits;
+        }
+        int64_t in = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, in, o);
+            if (lane >= o) in += y;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, run + in > t);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            before = run + __shfl_sync(0xffffffffu, in - w, l);
+            return s0 + l;
+        }
+        run += __shfl_sync(0xffffffffu, in, 31);
+    }
+    before = run;
+    return A.R.n_seqs;
+}
+
+// A place on the line: tile `tile` of unit `u` of sequence `s`.
+struct PaCur {
+    PaSeq q;
+    int s, u, tile;
+    int64_t left;  // tiles of the CTA's share from here on
+};
+DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c) {
+    --c.left;
+    if (++c.tile < c.q.ntiles) return;
+    c.tile = 0;
+    if (++c.u < c.q.nunits || c.left <= 0) return;
+    c.u = 0;
+    do {
+        if (++c.s >= A.R.n_seqs) {  // (never, while the lengths stay as they were counted)
+            c.left = 0;
+            return;
+        }
+        c.q = pa_seq(A, c.s, mt);
+    } while (c.q.nunits == 0);
+}
+
+DF_DEV void cp16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+DF_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+DF_DEV void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// 2^x by the special-function unit (relative error about 2^-22: the level of f32 rounding)
+DF_DEV float pa_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// two e4m3 codes -> two f16 (exact)
+DF_DEV uint32_t e4m3x2_f16x2(uint32_t codes) {
+    uint32_t y;
+    asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(y) : "r"(codes));
+    return y;
+}
+// (a, b) -> a pair of 16-bit floats, and what the rounding left
+template <bool BF>
+DF_DEV uint32_t pack2(float a, float b) {
+    if constexpr (BF) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+template <bool BF>
+DF_DEV float2 unpack2(uint32_t u) {
+    if constexpr (BF)
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
+    else
+        return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+
+// The tcgen05 kernel (k_paged_attn_tc.cu): units of up to 128 rows.
+int paged_attention_tc(const PaArgs& A, int cache_dtype, int hd, int num_sms, cudaStream_t st);
+
+}  // namespace dflash
