@@ -580,12 +580,29 @@ __global__ void __launch_bounds__(kPaThreads)
     if (c0 == c1) return;
     constexpr int V = HD / 32;  // columns a lane
     float m = -INFINITY, l = 0.f, o[V] = {};
-    // parts in order, 32 references and sums at a time
+    // parts in order, 32 references and sums at a time, 16 outputs in flight
     for (int64_t b = c0; b <= c1; b += 32) {
-        const int64_t n = min((int64_t)32, c1 - b + 1);
+        const int n = (int)min((int64_t)32, c1 - b + 1);
         float2 x = make_float2(-INFINITY, 0.f);
         auto slot = [&](int64_t c) { return (c * 2 + (c == c0 ? 1 : 0)) * mt + mrow; };
         if (lane < n) x = A.ws_ml[slot(b + lane)];
+        constexpr int U = 16;
+        float y[U][V];
+        auto load = [&](int k0) {
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (k0 + k < n) {
+                    const float* p = A.ws_o + slot(b + k0 + k) * HD + V * lane;
+                    if constexpr (V == 4) {
+                        const float4 q = *reinterpret_cast<const float4*>(p);
+                        y[k][0] = q.x, y[k][1] = q.y, y[k][2] = q.z, y[k][3] = q.w;
+                    } else {
+                        const float2 q = *reinterpret_cast<const float2*>(p);
+                        y[k][0] = q.x, y[k][1] = q.y;
+                    }
+                }
+        };
+        load(0);
         const float to = fmaxf(m, warp_max(x.x));
         const float fm = m == to ? 1.f : pa_exp2(m - to);
         const float f = x.x == -INFINITY ? 1.f : pa_exp2(x.x - to);  // (without a maximum the sums are 0 or NaN)
@@ -593,12 +610,16 @@ __global__ void __launch_bounds__(kPaThreads)
         l = l * fm + warp_sum(x.y * f);
 #pragma unroll
         for (int i = 0; i < V; ++i) o[i] *= fm;
-#pragma unroll 4
-        for (int k = 0; k < (int)n; ++k) {
-            const float w = __shfl_sync(0xffffffffu, f, k);
-            const float* p = A.ws_o + slot(b + k) * HD + V * lane;
+        for (int k0 = 0; k0 < n; k0 += U) {
+            if (k0 > 0) load(k0);
 #pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = fmaf(w, p[i], o[i]);
+            for (int k = 0; k < U; ++k) {
+                const float w = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+                if (k0 + k < n) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) o[i] = fmaf(w, y[k][i], o[i]);
+                }
+            }
         }
     }
     const float inv = l == 0.f ? 0.f : (e8 && A.C.v_scale != nullptr ? A.C.v_scale[h] : 1.f) / l;
@@ -613,11 +634,11 @@ __global__ void __launch_bounds__(kPaThreads)
 }
 
 // Rows a unit's tile holds, by what a sequence of average length brings: 16 or
-// 32 on the warp MMAs, beyond that the tcgen05 kernel's 128.
+// 32 on the warp MMAs, beyond that the tcgen05 kernel's 64 or 128.
 static int pa_tile_rows(int n_seqs, int64_t n_rows, int group) {
     const int64_t per = n_seqs > 0 ? (n_rows + n_seqs - 1) / n_seqs : 0;
     const int64_t m = per * group;
-    return m <= 16 ? 16 : m <= 32 ? 32 : 128;
+    return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
 }
 
 int64_t paged_attention_workspace(int hd, int n_seqs, int64_t n_rows, int heads, int kv_heads, int num_sms) {
@@ -659,8 +680,8 @@ int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRow
     const int mt = pa_tile_rows(R.n_seqs, R.n_rows, A.group);
     A.ws_o = static_cast<float*>(ws);
     A.ws_ml = reinterpret_cast<float2*>(A.ws_o + 2 * (int64_t)num_sms * mt * hd);
-    const int e = mt == 128 ? paged_attention_tc(A, cache_dtype, hd, num_sms, st)
-                            : pa_warp(A, cache_dtype, hd, mt, num_sms, st);
+    const int e = mt > 32 ? paged_attention_tc(A, cache_dtype, hd, mt, num_sms, st)
+                          : pa_warp(A, cache_dtype, hd, mt, num_sms, st);
     if (e != 0) return e;
     const int64_t jobs = (int64_t)R.n_rows * q.heads;
     const dim3 grid((unsigned)((jobs + kPaWarps - 1) / kPaWarps));

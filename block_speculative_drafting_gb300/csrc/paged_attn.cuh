@@ -151,7 +151,7 @@ DF_DEV float2 unpack2(uint32_t u) {
         return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
-// The tcgen05 kernel (k_paged_attn_tc.cu): units of up to 128 rows.
-int paged_attention_tc(const PaArgs& A, int cache_dtype, int hd, int num_sms, cudaStream_t st);
+// The tcgen05 kernel (k_paged_attn_tc.cu): units of up to mt = 64 or 128 rows.
+int paged_attention_tc(const PaArgs& A, int cache_dtype, int hd, int mt, int num_sms, cudaStream_t st);
 
 }  // namespace dflash
