@@ -34,6 +34,7 @@
 namespace dflash {
 
 constexpr int kPaThreads = 256, kPaWarps = 8;
+constexpr int kPaOver = 2;  // tiles' time that a unit's end and the next one's beginning take
 
 DF_DEV void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -96,45 +97,44 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
     pdl_wait();
     pdl_trigger();
 
-    const int64_t total = pa_total(A, MT, lane);
-    const int64_t chunk = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t t0 = (int64_t)blockIdx.x * chunk;
-    if (t0 >= total) return;
-    PaCur cur;
-    {
-        int64_t before;
-        cur.s = pa_find(A, MT, lane, t0, before);
-        cur.q = pa_seq(A, cur.s, MT);
-        cur.u = (int)((t0 - before) / cur.q.ntiles);
-        cur.tile = (int)((t0 - before) % cur.q.ntiles);
-        cur.left = min(chunk, total - t0);
-    }
+    int64_t chunk;
+    PaCur cur = pa_share(A, MT, kPaOver, lane, chunk);
+    if (threadIdx.x == 0) A.ws_join[blockIdx.x].last = -1;
+    if (cur.left <= 0) return;
 
     // ---------------------------------------------------------------- copies
     // Lanes 0-15 hold the places of a stage's 16 key rows of this warp, lanes
     // 16-31 those of its value rows; `ahead` belongs to the stage to copy next.
-    PaCur put = cur;
-    const unsigned char* ahead = nullptr;
-    auto place = [&](const PaCur& c) -> const unsigned char* {
-        const int key = c.q.lo + c.tile * kPaTile + kg * S::SK + wr * 16 + (lane & 15);
-        int slot = 0;
-        if (key >= c.q.hi) return nullptr;
-        const int64_t page = page_of(A.R, A.C.n_pages, c.s, key, slot);
-        if (page < 0) return nullptr;
-        const int h = c.u % A.C.kv_heads;
-        return lane < 16 ? A.C.k + page * A.C.ks[0] + slot * A.C.ks[1] + h * A.C.ks[2]
-                         : A.C.v + page * A.C.vs[0] + slot * A.C.vs[1] + h * A.C.vs[2];
+    // (the page's number alone: a pointer made of it here would wait for it)
+    struct Look {
+        int id, slot, h;
     };
-    if (put.left > 0) ahead = place(put);
+    PaCur put = cur;
+    Look ahead{-1, 0, 0};
+    auto look = [&](const PaCur& c) -> Look {
+        Look k{-1, 0, c.u % A.C.kv_heads};
+        const int key = c.q.lo + c.tile * kPaTile + kg * S::SK + wr * 16 + (lane & 15);
+        if (key >= 0 && key < c.q.hi) {
+            const int idx = div_by(A.R.page, key);
+            k.slot = key - idx * A.R.page.d;
+            k.id = A.R.table[(int64_t)c.s * A.R.table_stride + idx];
+        }
+        return k;
+    };
+    const unsigned char* tensor = lane < 16 ? A.C.k : A.C.v;
+    const int64_t sp = lane < 16 ? A.C.ks[0] : A.C.vs[0], ss = lane < 16 ? A.C.ks[1] : A.C.vs[1],
+                  sh = lane < 16 ? A.C.ks[2] : A.C.vs[2];
+    if (put.left > 0) ahead = look(put);
     int stage_put = 0;
     auto copy = [&]() {
         if (put.left > 0) {
             const uint32_t st = base + stage_put * S::kStage;
-            const unsigned char* now = ahead;
+            const unsigned char* now =
+                ahead.id < 0 || ahead.id >= A.C.n_pages ? nullptr : tensor + ahead.id * sp + ahead.slot * ss + ahead.h * sh;
             const uint32_t bits = __ballot_sync(0xffffffffu, now != nullptr) & 0xffffu;
             if (lane == 0) vbits[warp][stage_put] = bits;
             pa_next(A, MT, put);
-            if (put.left > 0) ahead = place(put);
+            if (put.left > 0) ahead = look(put);
             constexpr int RPI = 32 / CH;  // rows a copy instruction covers
 #pragma unroll
             for (int i = 0; i < 32 / RPI; ++i) {
@@ -160,7 +160,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
     int stage = 0;
     while (cur.left > 0) {
         // ------------------------------------------------------------ a unit
-        const PaSeq sq = cur.q;
+        const PaCur unit = cur;
+        const PaSeq& sq = unit.q;
         const int u = cur.u, tile0 = cur.tile;
         const int h = u % A.C.kv_heads, rt = u / A.C.kv_heads;
         const int mvalid = min(MT, sq.rows * A.group - rt * MT);
@@ -239,6 +240,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
             for (int e = 0; e < 4; ++e) o[f][e] = 0.f;
 
         bool last_tile;
+        int done = tile0;  // tiles of the unit behind us
         do {
             cp_wait<NST - 2>();
             group_sync();
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
                 }
             }
             stage = stage + 1 == NST ? 0 : stage + 1;
-            last_tile = cur.tile + 1 == sq.ntiles;
+            last_tile = ++done == sq.ntiles;
             pa_next(A, MT, cur);
         } while (!last_tile && cur.left > 0);
 
@@ -453,6 +455,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
         }
         const bool whole = tile0 == 0 && last_tile;
+        if (!whole && tile0 == 0 && threadIdx.x == 0)
+            A.ws_join[blockIdx.x] = pa_join_entry(unit, rt, MT, mvalid, h, sq.ntiles - done, chunk);
         // a part of a shared unit: its start goes to the CTA's second slot, any other part to the first
         const int part = blockIdx.x * 2 + (tile0 == 0 ? 1 : 0);
         float big[2];
@@ -554,37 +558,25 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
     }
 }
 
-// The shared units' parts joined: a warp per (row, query head).
+// The shared units' parts joined: CTA (c, y) takes rows 16 y .. of the unit that
+// starts in share c and ends in another, a warp a row.
 template <int HD>
-__global__ void __launch_bounds__(kPaThreads)
-    paged_join_kernel(const __grid_constant__ PaArgs A, int mt, int ctas, int e8) {
+__global__ void __launch_bounds__(kPaThreads) paged_join_kernel(const __grid_constant__ PaArgs A, int mt, int e8) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t id = (int64_t)blockIdx.x * kPaWarps + warp;
-    const int row = (int)(id / A.q.heads), hq = (int)(id % A.q.heads);
-    // lengths and row starts are final: the attention kernel lets this one start only after its own wait
-    const int s = row < A.R.n_rows ? seq_of(A.R, row) : -1;
-    int64_t c0 = 0, c1 = 0;
-    int mrow = 0, h = 0;
-    if (s >= 0) {
-        const PaSeq q = pa_seq(A, s, mt);
-        const int64_t total = pa_total(A, mt, lane), chunk = (total + ctas - 1) / ctas;
-        h = hq / A.group;
-        const int mm = (row - q.row0) * A.group + hq % A.group;
-        mrow = mm % mt;
-        const int64_t u = (int64_t)(mm / mt) * A.C.kv_heads + h;
-        const int64_t a = pa_before(A, mt, lane, s) + u * q.ntiles;
-        c0 = a / chunk;
-        c1 = (a + q.ntiles - 1) / chunk;
-    }
     pdl_wait();
-    if (c0 == c1) return;
+    const PaJoin e = A.ws_join[blockIdx.x];
+    const int c0 = blockIdx.x, c1 = e.last, h = e.head;
+    if (c1 <= c0) return;
+#pragma unroll 1
+    for (int mrow = 16 * blockIdx.y + warp; mrow < min(e.rows, 16 * (int)blockIdx.y + 16); mrow += kPaWarps) {
+    const int mm = e.m0 + mrow, row = e.row0 + mm / A.group, hq = h * A.group + mm % A.group;
     constexpr int V = HD / 32;  // columns a lane
     float m = -INFINITY, l = 0.f, o[V] = {};
     // parts in order, 32 references and sums at a time, 16 outputs in flight
-    for (int64_t b = c0; b <= c1; b += 32) {
-        const int n = (int)min((int64_t)32, c1 - b + 1);
+    for (int b = c0; b <= c1; b += 32) {
+        const int n = min(32, c1 - b + 1);
         float2 x = make_float2(-INFINITY, 0.f);
-        auto slot = [&](int64_t c) { return (c * 2 + (c == c0 ? 1 : 0)) * mt + mrow; };
+        auto slot = [&](int c) { return (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * mt + mrow; };
         if (lane < n) x = A.ws_ml[slot(b + lane)];
         constexpr int U = 16;
         float y[U][V];
@@ -631,6 +623,7 @@ __global__ void __launch_bounds__(kPaThreads)
     if (A.lse != nullptr && lane == 0)
         A.lse[(int64_t)row * A.q.heads + hq] =
             l == 0.f ? -INFINITY : (m == -INFINITY ? l : (m + log2f(l)) * 0.69314718056f);
+    }
 }
 
 // Rows a unit's tile holds, by what a sequence of average length brings: 16 or
@@ -643,7 +636,7 @@ static int pa_tile_rows(int n_seqs, int64_t n_rows, int group) {
 
 int64_t paged_attention_workspace(int hd, int n_seqs, int64_t n_rows, int heads, int kv_heads, int num_sms) {
     const int64_t mt = pa_tile_rows(n_seqs, n_rows, heads / kv_heads);
-    return 2 * (int64_t)num_sms * mt * (hd * 4 + 8);
+    return num_sms * (2 * mt * (hd * 4 + 8) + (int64_t)sizeof(PaJoin));
 }
 
 template <bool BF, bool E8, int HD, int RW>
@@ -680,14 +673,14 @@ int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRow
     const int mt = pa_tile_rows(R.n_seqs, R.n_rows, A.group);
     A.ws_o = static_cast<float*>(ws);
     A.ws_ml = reinterpret_cast<float2*>(A.ws_o + 2 * (int64_t)num_sms * mt * hd);
+    A.ws_join = reinterpret_cast<PaJoin*>(A.ws_ml + 2 * (int64_t)num_sms * mt);
     const int e = mt > 32 ? paged_attention_tc(A, cache_dtype, hd, mt, num_sms, st)
                           : pa_warp(A, cache_dtype, hd, mt, num_sms, st);
     if (e != 0) return e;
-    const int64_t jobs = (int64_t)R.n_rows * q.heads;
-    const dim3 grid((unsigned)((jobs + kPaWarps - 1) / kPaWarps));
+    const dim3 grid(num_sms, mt / 16);
     const int e8 = cache_dtype == kE4M3;
-    return hd == 64 ? (int)launch(paged_join_kernel<64>, grid, dim3(kPaThreads), 0, st, A, mt, num_sms, e8)
-                    : (int)launch(paged_join_kernel<128>, grid, dim3(kPaThreads), 0, st, A, mt, num_sms, e8);
+    return hd == 64 ? (int)launch(paged_join_kernel<64>, grid, dim3(kPaThreads), 0, st, A, mt, e8)
+                    : (int)launch(paged_join_kernel<128>, grid, dim3(kPaThreads), 0, st, A, mt, e8);
 }
 
 }  // namespace dflash

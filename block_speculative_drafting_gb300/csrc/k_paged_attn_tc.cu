@@ -51,6 +51,7 @@ constexpr int kPtM = 128;
 constexpr int kPtSoft = 128;  // softmax threads: warps 0-3
 constexpr int kPtQk = kPtSoft / 32, kPtPv = kPtQk + 1, kPtLoad = kPtPv + 1;  // warps
 constexpr uint64_t kPtWait = 1000000000ull;
+constexpr int kPtOver = 4;   // tiles' time that a unit's end and the next one's beginning take
 constexpr int kPtBits = 16;  // tiles whose key masks are kept: more than the loaders can be ahead of the softmax
 
 template <bool BF, bool E8, int HD>
@@ -71,7 +72,7 @@ struct PtShape {
 struct PtCtl {
     // a slot's data written / its MMAs done; a tile's scores in S; its P in
     // place of them (a barrier a buffer: a thread may be a tile ahead of
-    // another); its P V added; a unit's Q in place and O cleared
+    // another); its P V added; a unit's Q in place
     uint64_t full[2][6], empty[2][6], s_full[2], p_full[2], o_done[2], q_full, fin[2];
     uint32_t tmem;
     uint32_t bits[kPtBits][4];  // a tile's valid keys
@@ -181,18 +182,9 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
     pdl_wait();
     pdl_trigger();
     // this CTA's share of the line
-    const int64_t total = pa_total(A, MT, lane);
-    const int64_t chunk = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t t0 = (int64_t)blockIdx.x * chunk;
-    PaCur cur{};
-    if (t0 < total) {
-        int64_t before;
-        cur.s = pa_find(A, MT, lane, t0, before);
-        cur.q = pa_seq(A, cur.s, MT);
-        cur.u = (int)((t0 - before) / cur.q.ntiles);
-        cur.tile = (int)((t0 - before) % cur.q.ntiles);
-        cur.left = min(chunk, total - t0);
-    }
+    int64_t chunk;
+    const PaCur cur = pa_share(A, MT, kPtOver, lane, chunk);
+    if (threadIdx.x == 0) A.ws_join[blockIdx.x].last = -1;
 
     if (warp >= kPtLoad) {
         // ------------------------------------------------------------ loads
@@ -381,9 +373,49 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
         constexpr int NC = 4 / D;         // 32-key chunks of a lane
         const int t = threadIdx.x, r = t % MT, copy = t / MT;  // this lane's row of the unit, and its share of the keys
         const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
+        // A unit's queries to tensor memory; returns what this lane's row was scaled down by.
+        auto queries = [&](const PaCur& c) -> float {
+            const int h = c.u % A.C.kv_heads, mm = (c.u / A.C.kv_heads) * MT + r;
+            const bool in = mm < c.q.rows * A.group;
+            const int row = c.q.row0 + mm / A.group, hq = h * A.group + mm % A.group;
+            float rf = 1.f, down = 1.f;
+            const unsigned char* qp = A.q.p + (int64_t)row * A.q.rs + (int64_t)hq * A.q.hs;
+            uint4 x[HD / 8];
+#pragma unroll
+            for (int j = 0; j < HD / 8; ++j)
+                x[j] = in ? *reinterpret_cast<const uint4*>(qp + 16 * j) : make_uint4(0u, 0u, 0u, 0u);
+            uint32_t (&w)[HD / 2] = *reinterpret_cast<uint32_t(*)[HD / 2]>(x);
+            if (E8 && A.q.dtype == kBF16) {
+                float mx = 0.f;
+#pragma unroll
+                for (int j = 0; j < HD / 2; ++j) {
+                    const float2 f = unpack2<true>(w[j]);
+                    mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+                // times 2^-x, the largest in [1, 2): what f16 cannot hold of the row then is under 2^-25 of that
+                if (mx > 0.f && mx < INFINITY) {
+                    const int e = min(max(ilogbf(mx), -120), 120);
+                    down = ldexpf(1.f, -e);
+                    rf = ldexpf(1.f, e);
+                }
+#pragma unroll
+                for (int j = 0; j < HD / 2; ++j) {
+                    const float2 f = unpack2<true>(w[j]);
+                    w[j] = pack2<false>(f.x * down, f.y * down);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < HD / 32; ++i)
+                pt_st16(lane_addr + S::kColQ + 16 * i, *reinterpret_cast<const uint32_t(*)[16]>(w + 16 * i));
+            at_wait_st();
+            at_fence_before();
+            mbar_arrive(&ctl.q_full);
+            return rf;
+        };
         bool ok = true;
         int tg = 0;
         PaCur c = cur;
+        float rf_next = c.left > 0 ? queries(c) : 1.f;
         while (c.left > 0) {
             const PaSeq sq = c.q;
             const int u = c.u, tile0 = c.tile, tiles = pt_tiles(c);
@@ -395,44 +427,14 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
             const int wlo = A.window > 0 ? pos - A.window + 1 : 0;
             const int pmin = sq.p0 + (rt * MT) / A.group, pmax = sq.p0 + (rt * MT + mvalid - 1) / A.group;
             const int wtop = A.window > 0 ? pmax - A.window + 1 : 0;
-            // the row's query to tensor memory, O cleared (the unit before has read it)
-            float rf = 1.f, down = 1.f;
+            const float rf = rf_next;
             {
-                const unsigned char* qp = A.q.p + (int64_t)row * A.q.rs + (int64_t)hq * A.q.hs;
-                uint4 x[HD / 8];
-#pragma unroll
-                for (int j = 0; j < HD / 8; ++j)
-                    x[j] = in ? *reinterpret_cast<const uint4*>(qp + 16 * j) : make_uint4(0u, 0u, 0u, 0u);
+                // O cleared (the unit before has read it)
                 const uint32_t zero[16] = {};
 #pragma unroll 1
                 for (int i = 0; i < HD / 16; ++i) pt_st16(lane_addr + S::kColO + 16 * i, zero);
-                uint32_t (&w)[HD / 2] = *reinterpret_cast<uint32_t(*)[HD / 2]>(x);
-                if (E8 && A.q.dtype == kBF16) {
-                    float mx = 0.f;
-#pragma unroll
-                    for (int j = 0; j < HD / 2; ++j) {
-                        const float2 f = unpack2<true>(w[j]);
-                        mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    }
-                    // times 2^-x, the largest in [1, 2): what f16 cannot hold of the row then is under 2^-25 of that
-                    if (mx > 0.f && mx < INFINITY) {
-                        const int e = min(max(ilogbf(mx), -120), 120);
-                        down = ldexpf(1.f, -e);
-                        rf = ldexpf(1.f, e);
-                    }
-#pragma unroll
-                    for (int j = 0; j < HD / 2; ++j) {
-                        const float2 f = unpack2<true>(w[j]);
-                        w[j] = pack2<false>(f.x * down, f.y * down);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < HD / 32; ++i)
-                    pt_st16(lane_addr + S::kColQ + 16 * i, *reinterpret_cast<const uint32_t(*)[16]>(w + 16 * i));
+                at_wait_st();
             }
-            at_wait_st();
-            at_fence_before();
-            mbar_arrive(&ctl.q_full);
             const float ks = E8 && A.C.k_scale != nullptr ? A.C.k_scale[h] : 1.f;
             const float cs = fminf(fmaxf(A.scale_log2 * ks * rf, 1e-37f), 3e38f);
 
@@ -629,6 +631,12 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
             // ------------------------------------------------------------ the unit's end
             const bool whole = tile0 == 0 && tile0 + tiles == sq.ntiles;
             const int part = blockIdx.x * 2 + (tile0 == 0 ? 1 : 0);
+            if (!whole && tile0 == 0 && t == 0)
+                A.ws_join[blockIdx.x] = pa_join_entry(c, rt, MT, mvalid, h, sq.ntiles - tiles, chunk);
+            // the next unit's queries, whose scores may then be multiplied while this one's outputs are written
+            // (its last scores have been read: Q is free)
+            pt_skip<MT>(A, c, tiles);
+            if (c.left > 0) rf_next = queries(c);
             ok = __all_sync(0xffffffffu, ok && mbar_wait(&ctl.o_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1, kPtWait));
             at_fence_after();
             if (!ok) l = NAN;
@@ -694,7 +702,6 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                         l == 0.f ? -INFINITY : (m == -INFINITY ? l : (m + log2f(l)) * 0.69314718056f);
             }
             at_fence_before();
-            pt_skip<MT>(A, c, tiles);
         }
     }
     at_fence_before();

@@ -17,8 +17,16 @@ struct PaArgs {
     float* lse;
     float* ws_o;     // [2 CTAs][MT][HD]
     float2* ws_ml;   // [2 CTAs][MT]
+    struct PaJoin* ws_join;  // [CTAs]
     float scale_log2;
     int window, group;
+};
+
+// A unit that starts in a CTA's share and ends in another's, for the join:
+// its parts are this CTA's second slot and the first slots of the CTAs up to
+// `last` (below 0: this CTA starts no such unit).
+struct __align__(16) PaJoin {
+    int32_t last, row0, m0, rows, head, pad[3];  // rows from m0 on of the sequence whose rows start at row0; kv head
 };
 
 // What the walk needs of one sequence.
@@ -42,36 +50,44 @@ DF_DEV PaSeq pa_seq(const PaArgs& A, int s, int mt) {
     return q;
 }
 
-// Warp-wide: the line's length, and the share of a CTA.
-DF_DEV int64_t pa_total(const PaArgs& A, int mt, int lane) {
-    int64_t t = 0;
+// The line: the units' tiles in order (sequence, row tile, key/value head),
+// each unit led by `ov` places without a tile, which stand for what it costs a
+// CTA to end one unit and begin another, so that shares of equal length take
+// equal time.  ov is 0 where most CTAs hold a tile or two: there a place
+// without a tile would be an idle CTA.
+struct PaCur {
+    PaSeq q;
+    int s, u, tile;  // tile `tile` of unit `u` of sequence `s`
+    int ov;
+    int64_t left;  // places of the CTA's share from here on (0: none)
+};
+// This CTA's share (warp-wide); `chunk`: the places of a share.
+DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int64_t& chunk) {
+    int64_t tiles = 0, units = 0, w0 = 0, u0 = 0;
     for (int s = lane; s < A.R.n_seqs; s += 32) {
         const PaSeq q = pa_seq(A, s, mt);
-        t += (int64_t)q.ntiles * q.nunits;
+        const int64_t w = (int64_t)q.ntiles * q.nunits;
+        if (s < 32) w0 = w, u0 = q.nunits;
+        tiles += w;
+        units += q.nunits;
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    return t;
-}
-// Tiles before sequence `upto` (warp-wide).
-DF_DEV int64_t pa_before(const PaArgs& A, int mt, int lane, int upto) {
-    int64_t t = 0;
-    for (int s = lane; s < upto; s += 32) {
-        const PaSeq q = pa_seq(A, s, mt);
-        t += (int64_t)q.ntiles * q.nunits;
+    for (int o = 16; o > 0; o >>= 1) {
+        tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+        units += __shfl_xor_sync(0xffffffffu, units, o);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    return t;
-}
-// The sequence that holds tile t of the line, and the tiles before it.
-DF_DEV int pa_find(const PaArgs& A, int mt, int lane, int64_t t, int64_t& before) {
+    PaCur c{};
+    c.ov = tiles > 2 * (int64_t)gridDim.x ? ovh : 0;
+    const int64_t total = tiles + c.ov * units;
+    chunk = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t t = (int64_t)blockIdx.x * chunk;
+    if (t >= total) return c;
     int64_t run = 0;
     for (int s0 = 0; s0 < A.R.n_seqs; s0 += 32) {
-        int64_t w = 0;
-        if (s0 + lane < A.R.n_seqs) {
+        int64_t w = s0 == 0 ? w0 + c.ov * u0 : 0;
+        if (s0 > 0 && s0 + lane < A.R.n_seqs) {
             const PaSeq q = pa_seq(A, s0 + lane, mt);
-            w = (int64_t)q.ntiles * q.nunits;
+            w = (int64_t)(q.ntiles + c.ov) * q.nunits;
         }
         int64_t in = w;
 #pragma unroll
@@ -82,26 +98,33 @@ DF_DEV int pa_find(const PaArgs& A, int mt, int lane, int64_t t, int64_t& before
         const uint32_t hit = __ballot_sync(0xffffffffu, run + in > t);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            before = run + __shfl_sync(0xffffffffu, in - w, l);
-            return s0 + l;
+            const int64_t x = t - (run + __shfl_sync(0xffffffffu, in - w, l));
+            c.s = s0 + l;
+            c.q = pa_seq(A, c.s, mt);
+            const int per = c.q.ntiles + c.ov;
+            c.u = (int)(x / per);
+            const int v = (int)(x - (int64_t)c.u * per);
+            c.left = min(chunk, total - t);
+            if (v < c.ov)
+                c.left = max(c.left - (c.ov - v), (int64_t)0);
+            else
+                c.tile = v - c.ov;
+            return c;
         }
         run += __shfl_sync(0xffffffffu, in, 31);
     }
-    before = run;
-    return A.R.n_seqs;
+    return c;
 }
-
-// A place on the line: tile `tile` of unit `u` of sequence `s`.
-struct PaCur {
-    PaSeq q;
-    int s, u, tile;
-    int64_t left;  // tiles of the CTA's share from here on
-};
 DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c) {
     --c.left;
     if (++c.tile < c.q.ntiles) return;
     c.tile = 0;
-    if (++c.u < c.q.nunits || c.left <= 0) return;
+    c.left -= c.ov;
+    if (c.left <= 0) {
+        c.left = 0;
+        return;
+    }
+    if (++c.u < c.q.nunits) return;
     c.u = 0;
     do {
         if (++c.s >= A.R.n_seqs) {  // (never, while the lengths stay as they were counted)
@@ -110,6 +133,16 @@ DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c) {
         }
         c.q = pa_seq(A, c.s, mt);
     } while (c.q.nunits == 0);
+}
+// The entry of a unit that begins in this CTA's share and has `rest` tiles after it.
+DF_DEV PaJoin pa_join_entry(const PaCur& c, int rt, int mt, int rows, int head, int rest, int64_t chunk) {
+    PaJoin e{};
+    e.last = (int)(blockIdx.x + (rest + chunk - 1) / chunk);
+    e.row0 = c.q.row0;
+    e.m0 = rt * mt;
+    e.rows = rows;
+    e.head = head;
+    return e;
 }
 
 DF_DEV void cp16(uint32_t dst, const void* src, uint32_t bytes) {
