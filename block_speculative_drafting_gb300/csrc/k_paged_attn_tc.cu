@@ -26,8 +26,8 @@
 // keys, 10-13 values, each into a ring of slots, one tile each, in the 128-byte
 // swizzle.  16-bit loaders copy 16-byte
 // chunks asynchronously (the slot's barrier counts them as they land); e4m3
-// loaders hold two tiles in registers and write their codes' f16 values
-// (exact).  The MMA warps order those writes before their reads of them (a proxy
+// loaders copy codes to places of their own and write their f16 values (exact)
+// into the slots.  The MMA warps order those writes before their reads of them (a proxy
 // fence after the barrier).  The
 // page of a key is looked up a tile before it is needed.
 //
@@ -39,8 +39,6 @@
 // Every wait is bounded (1 s of %globaltimer).  A role whose wait expires stops;
 // the softmax then walks its remaining units without waiting and leaves NaN in
 // their rows.
-#include <type_traits>
-
 #include "kernels.cuh"
 #include "paged_attn.cuh"
 #include "tc.cuh"
@@ -61,10 +59,13 @@ struct PtShape {
     static constexpr int kThreads = kPtLoad * 32 + 2 * kLoaders;
     static constexpr int KPW = kPaTile / kLoadWarps;  // keys of a loader warp: one a lane
     static constexpr int kItem = kPaTile * HD * 2;    // a slot: a tile's keys or values in 16 bits
-    static constexpr int kSlots = HD == 128 ? 3 : 6;  // of the keys, and as many of the values
+    static constexpr int kSlots = (E8 ? 2 : 3) * (128 / HD);  // of the keys, and as many of the values
+    // e4m3: half tiles of codes on their way, 16 bytes a place, each place copied and read by one thread
+    static constexpr int kRaw = E8 ? 4 * (128 / HD) : 0, kRawLd = KPW * HD / 16 / 64;
+    static constexpr int kRawBytes = kRaw * kRawLd * 16 * 2 * kLoaders;
     static constexpr bool kSplitP = !E8;
     static constexpr int kCtl = 13 * 1024;
-    static constexpr size_t kSmem = 1024 /*alignment*/ + kCtl + 2 * (size_t)kSlots * kItem;
+    static constexpr size_t kSmem = 1024 /*alignment*/ + kCtl + 2 * (size_t)kSlots * kItem + kRawBytes;
     // tensor memory: two S / P buffers, O, Q
     static constexpr int kColS = 0, kColO = 256, kColQ = 384, kCols = 512;
 };
@@ -253,17 +254,20 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
             });
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
-            constexpr int CH = HD / 16, RPI = 32 / CH, LD = S::KPW / RPI, kHeld = 2;
-            uint4 raw[kHeld][LD];
+            constexpr int CH = HD / 16, RPI = 32 / CH, LD = S::kRawLd;  // copies of a lane a half tile
             const int ch = lane % CH;
-            // item `item` out of raw[b]: a chunk's 16 codes as 32 bytes of f16
-            auto write = [&](int item, const uint4 (&x)[LD]) -> bool {
-                if (!wait_empty(item)) return false;
-                unsigned char* dst = slots + (item % S::kSlots) * S::kItem;
+            unsigned char* raw = ring + 2 * S::kSlots * S::kItem + (threadIdx.x - kPtLoad * 32) * 16;
+            constexpr int kPlace = 2 * S::kLoaders * 16;  // from one of a thread's places to the next
+            // a half tile's codes as f16, 32 bytes a place
+            auto write = [&](int half) -> bool {
+                const int tile = half >> 1, slot = tile % S::kSlots;
+                if ((half & 1) == 0 && !wait_empty(tile)) return false;
+                unsigned char* dst = slots + slot * S::kItem;
 #pragma unroll
                 for (int i = 0; i < LD; ++i) {
-                    const int key = lw * S::KPW + i * RPI + lane / CH;
-                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    const int key = lw * S::KPW + ((half & 1) * LD + i) * RPI + lane / CH;
+                    const uint4 x = *reinterpret_cast<const uint4*>(raw + ((half % S::kRaw) * LD + i) * kPlace);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                     uint32_t y[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -274,33 +278,35 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                     const bool flip = ch >= CH / 2;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int half = flip ? 1 - j : j, chunk = 2 * ch + half;
-                        const uint4 v = half ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
+                        const int up = flip ? 1 - j : j, chunk = 2 * ch + up;
+                        const uint4 v = up ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
                         *reinterpret_cast<uint4*>(dst + (chunk >> 3) * (kPaTile * 128) + at_swz(key, chunk & 7)) = v;
                     }
                 }
-                mbar_arrive(&ctl.full[side][item % S::kSlots]);
+                if (half & 1) mbar_arrive(&ctl.full[side][slot]);
                 return true;
             };
-            // registers need fixed places: the b-th of every two tiles goes to raw[b]
-            auto step = [&](auto B, const unsigned char* rows) -> bool {
-                constexpr int b = decltype(B)::value;
-                if (n >= kHeld && !write(n - kHeld, raw[b])) return false;
+            walk([&](const unsigned char* rows) -> bool {
 #pragma unroll
-                for (int i = 0; i < LD; ++i) {
-                    const int r = i * RPI + lane / CH;
-                    const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(rows), r);
-                    raw[b][i] = p ? ldg_stream_v4(reinterpret_cast<const unsigned char*>(p) + 16 * ch)
-                                  : make_uint4(0u, 0u, 0u, 0u);
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int half = 2 * n + hf;
+#pragma unroll
+                    for (int i = 0; i < LD; ++i) {
+                        const int r = (hf * LD + i) * RPI + lane / CH;
+                        const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(rows), r);
+                        const void* src = p ? reinterpret_cast<const unsigned char*>(p) + 16 * ch : A.C.k;
+                        cp16(smem_addr(raw) + ((half % S::kRaw) * LD + i) * kPlace, src, p ? 16 : 0);
+                    }
+                    cp_commit();
+                    cp_wait<S::kRaw - 1>();
+                    if (half >= S::kRaw - 1 && !write(half - (S::kRaw - 1))) return false;
                 }
                 ++n;
                 return true;
-            };
-            walk([&](const unsigned char* row) -> bool {
-                return n & 1 ? step(std::integral_constant<int, 1>{}, row) : step(std::integral_constant<int, 0>{}, row);
             });
-            for (int i = max(0, n - kHeld); i < n; ++i)
-                if (!(i & 1 ? write(i, raw[1]) : write(i, raw[0]))) break;
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            for (int half = max(0, 2 * n - (S::kRaw - 1)); half < 2 * n; ++half)
+                if (!write(half)) break;
         }
     } else if (warp >= kPtQk) {
         // ------------------------------------------------------------ MMAs
