@@ -3,7 +3,6 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdflash.so")
@@ -78,14 +77,7 @@ class Rotation(C.Structure):
     _fields_ = [("inv_freq", _VP), ("rotary", C.c_int32), ("interleaved", C.c_int32), ("scale", C.c_float)]
 
 
-# The same layouts for packing in one go (native alignment: the C compiler's own).
-PAGED_CACHE = struct.Struct("@PPiiiiq6qPP")
-PAGED_ROWS = struct.Struct("@iiqPPPq")
-HEAD_ROWS = struct.Struct("@Piiqq")
-ROTATION = struct.Struct("@Piif0P")
-
-# descriptors: a packed bytes object or byref of the structure
-_PC = _PR = _PH = _VP
+_PC, _PR, _PH = C.POINTER(PagedCache), C.POINTER(PagedRows), C.POINTER(HeadRows)
 _SIGS = {
     "dflash_init": (C.c_int, [C.POINTER(Geometry), C.POINTER(Weights), C.c_int, _VP, C.POINTER(_VP)]),
     "dflash_free": (None, [_VP]),
@@ -120,7 +112,7 @@ _SIGS = {
                                          _VP, _VP, _VP]),
     "dflash_attention_noalloc": (C.c_int, [_VP, C.POINTER(_VP), C.c_int32, C.c_int32, C.POINTER(C.c_int64),
                                            C.c_int32, _VP, _VP, _VP]),
-    "dflash_paged_append": (C.c_int, [_PC, _PR, _PH, _PH, _PH, _PH, _VP, _VP, C.c_float, _VP, _VP]),
+    "dflash_paged_append": (C.c_int, [_PC, _PR, _PH, _PH, _PH, _PH, _VP, _VP, C.c_float, C.POINTER(Rotation), _VP]),
     "dflash_paged_attention": (C.c_int, [_PC, _PR, _PH, _PH, _VP, C.c_float, C.c_int32, _VP, C.c_int64, _VP]),
     "dflash_paged_attention_workspace": (C.c_int64, [_PC, C.c_int32, C.c_int64, C.c_int32]),
     "dflash_verify": (C.c_int, [_VP, C.c_int32, C.c_int64, _VP, C.c_int64, _VP, _VP, _VP, _VP, _VP, C.c_int32,

@@ -3,13 +3,15 @@
 Usage: python -m block_speculative_drafting_gb300.csrc.build [--verbose]
 Each .cu compiles on its own thread; the objects link into
 block_speculative_drafting_gb300/libdflash.so (CUDA runtime linked
-statically, so the library loads without a GPU).
+statically, so the library loads without a GPU).  binding.c, the compiled half
+of target.py, becomes a Python extension beside it.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +19,7 @@ PKG = os.path.dirname(HERE)
 ROOT = os.path.dirname(PKG)
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdflash.so")
+BINDING = os.path.join(PKG, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["api.cu", "k_quant.cu", "k_gemm.cu", "k_layer.cu", "k_stream.cu", "k_tc.cu", "k_tc_pair.cu",
            "k_attn_tc.cu", "ops.cu", "k_paged_append.cu", "k_paged_attn.cu", "k_paged_attn_tc.cu",
            "k_verify.cu"]
@@ -57,8 +60,19 @@ def build(verbose: bool = False, force: bool = False) -> str:
                 sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
+    def compile_binding() -> None:
+        src = os.path.join(HERE, "binding.c")
+        if force or _needs(BINDING, [src] + headers):
+            cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", sysconfig.get_path("include"), src, "-o",
+                   BINDING]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"{cmd[0]} failed on binding.c:\n{r.stdout}\n{r.stderr}")
+
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        bound = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        bound.result()
     if force or _needs(LIB, objs):
         cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", LIB, *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -15,12 +15,12 @@
 // whole is written out at once; a shared one leaves (m, l, O) per part in the
 // workspace, and a second small kernel joins the parts.
 //
-// In a CTA, 8 warps form KG key groups of RW row warps.  A warp holds 16 rows
-// (m16n8k16 MMAs: scores from K by ldmatrix, P from the scores' registers,
-// values by transposed ldmatrix).  A group's RW warps share its stages (16 RW
-// keys and values, each warp copies 16 of both with 16-byte asynchronous
-// copies) and meet once a stage; groups run on their own and meet once a unit.
-// A warp finds the pages of its next stage's keys while it copies this one's.
+// In a CTA, each of 8 warps takes 16 of a tile's 128 keys against the unit's (at
+// most 16) rows on its own: m16n8k16 MMAs (scores from K by ldmatrix, P from
+// the scores' registers, values by transposed ldmatrix), its own reference and
+// sum, its own ring of stages filled by 16-byte asynchronous copies.  The warps
+// meet once a unit, to join.  The page of a key is looked up a stage before
+// its copy.  Units of more rows go to the tcgen05 kernel (k_paged_attn_tc.cu).
 //
 // Masking.  Keys that no row may see (past the end, pages not held) are not
 // read: their slots are zero-filled and a bit mask sends their scores to -inf.
@@ -61,21 +61,20 @@ DF_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_
 }
 // BF: MMAs and cache in bf16 (else f16).  E8: an e4m3 cache; its codes become
 // f16 exactly, and a query row is brought into f16 by a power of two.
-template <bool BF, bool E8, int HD, int RW>
+// P goes through the MMAs as hi + lo pairs, so that they add no rounding of
+// their own to the output's: two more MMAs a value fragment, which the memory
+// leaves time for.
+constexpr int kPaM = 16, kPaKeys = 16;  // rows of a unit's tile, keys of a warp's stage
+template <bool BF, bool E8, int HD>
 struct PaShape {
-    static constexpr int KG = kPaWarps / RW, SK = 16 * RW, MT = 16 * RW;
     static constexpr int RB = HD * (E8 ? 1 : 2);  // bytes of a key row
     static constexpr int CH = RB / 16;            // its 16-byte chunks
-    static constexpr int kStage = 2 * SK * RB;    // a group's stage: keys, then values
-    static constexpr int kRound = KG * kStage;
+    static constexpr int kStage = 2 * kPaKeys * RB;  // a warp's stage: keys, then values
+    static constexpr int kRound = kPaWarps * kStage;
     static constexpr int NST = 196608 / kRound < 6 ? 196608 / kRound : 6;
-    static constexpr int NF = HD / 8;             // output fragments of a warp
-    static constexpr int kMerge = KG > 1 ? KG / 2 * MT * HD * 4 : 0;
+    static constexpr int NF = HD / 8;  // output fragments of a warp
+    static constexpr int kMerge = kPaWarps / 2 * kPaM * HD * 4;
     static constexpr size_t kSmem = (size_t)NST * kRound + kMerge;
-    // P as hi + lo pairs: the MMAs then add no rounding of their own to the
-    // output's.  Two more MMAs a value fragment: free while copies are awaited
-    // (one row warp a key), not with many row warps on the same keys.
-    static constexpr bool kSplitP = RW <= 2;
 };
 
 // byte offset of chunk c of key row r, so that eight rows' chunks of one column sit in different banks
@@ -84,16 +83,15 @@ DF_DEV uint32_t pa_off(int r, int c) {
     return (uint32_t)(r * CH * 16 + ((CH >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
 }
 
-template <bool BF, bool E8, int HD, int RW>
+template <bool BF, bool E8, int HD>
 __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_constant__ PaArgs A) {
-    using S = PaShape<BF, E8, HD, RW>;
-    constexpr int NST = S::NST, CH = S::CH, MT = S::MT, NF = S::NF, KG = S::KG;
+    using S = PaShape<BF, E8, HD>;
+    constexpr int NST = S::NST, CH = S::CH, MT = kPaM, NF = S::NF, KG = kPaWarps;
     extern __shared__ __align__(128) unsigned char sm[];
-    __shared__ uint32_t vbits[kPaWarps][NST];  // a stage's valid keys, by copying warp
+    __shared__ uint32_t vbits[kPaWarps][NST];  // a stage's valid keys
     __shared__ float2 ml[KG][MT];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    const int kg = warp / RW, wr = warp % RW;
-    const uint32_t base = smem_addr(sm) + kg * NST * S::kStage;
+    const uint32_t base = smem_addr(sm) + warp * NST * S::kStage;
     pdl_wait();
     pdl_trigger();
 
@@ -113,7 +111,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
     Look ahead{-1, 0, 0};
     auto look = [&](const PaCur& c) -> Look {
         Look k{-1, 0, c.u % A.C.kv_heads};
-        const int key = c.q.lo + c.tile * kPaTile + kg * S::SK + wr * 16 + (lane & 15);
+        const int key = c.q.lo + c.tile * kPaTile + warp * kPaKeys + (lane & 15);
         if (key >= 0 && key < c.q.hi) {
             const int idx = div_by(A.R.page, key);
             k.slot = key - idx * A.R.page.d;
@@ -140,19 +138,13 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
             for (int i = 0; i < 32 / RPI; ++i) {
                 const int r = i * RPI + lane / CH, c = lane % CH;
                 const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(now), r);
-                const uint32_t dst = st + (r >> 4) * (S::SK * S::RB) + pa_off<CH>(wr * 16 + (r & 15), c);
+                const uint32_t dst = st + (r >> 4) * (kPaKeys * S::RB) + pa_off<CH>(r & 15, c);
                 const void* src = p ? reinterpret_cast<const unsigned char*>(p) + 16 * c : A.C.k;
                 cp16(dst, src, p ? 16 : 0);
             }
             stage_put = stage_put + 1 == NST ? 0 : stage_put + 1;
         }
         cp_commit();
-    };
-    auto group_sync = [&]() {
-        if constexpr (RW == 1)
-            __syncwarp();
-        else
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * RW) : "memory");
     };
 #pragma unroll
     for (int i = 0; i < NST - 1; ++i) copy();
@@ -171,7 +163,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
         float rf[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int m = wr * 16 + gq + 8 * e;
+            const int m = gq + 8 * e;
             const bool in = m < mvalid;
             const int mm = rt * MT + m, r = mm / A.group, hq = h * A.group + mm % A.group;
             pos[e] = in ? sq.p0 + r : -1;
@@ -243,19 +235,14 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
         int done = tile0;  // tiles of the unit behind us
         do {
             cp_wait<NST - 2>();
-            group_sync();
+            __syncwarp();
             copy();
             const uint32_t st = base + stage * S::kStage;
-            const uint32_t sv = st + S::SK * S::RB;
-            const int key0 = sq.lo + cur.tile * kPaTile + kg * S::SK;
-            constexpr int KB = S::SK < 32 ? S::SK : 32;  // keys of one softmax step
-#pragma unroll 1
-            for (int kb = 0; kb < S::SK; kb += KB) {
-                constexpr int NT = KB / 8;
-                uint32_t bits = vbits[kg * RW + kb / 16][stage];
-                if constexpr (KB == 32) bits |= vbits[kg * RW + kb / 16 + 1][stage] << 16;
-                if (bits == 0) continue;
-                const int kfirst = key0 + kb, klast = kfirst + KB - 1;
+            const uint32_t sv = st + kPaKeys * S::RB;
+            const int kfirst = sq.lo + cur.tile * kPaTile + warp * kPaKeys, klast = kfirst + kPaKeys - 1;
+            const uint32_t bits = vbits[warp][stage];
+            if (bits != 0) {
+                constexpr int NT = kPaKeys / 8;
                 float sc[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -267,7 +254,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             uint32_t b[4];
-                            ldsm4(b, st + pa_off<CH>(kb + n * 8 + (lane & 7), 4 * j + (lane >> 3)));
+                            ldsm4(b, st + pa_off<CH>(n * 8 + (lane & 7), 4 * j + (lane >> 3)));
                             mma16816<BF>(sc[n], qf[2 * j], b[0], b[1]);
                             mma16816<BF>(sc[n], qf[2 * j + 1], b[2], b[3]);
                         }
@@ -278,13 +265,13 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             uint32_t b[4];
-                            ldsm4(b, st + pa_off<CH>(kb + n * 8 + (lane & 7), 4 * j + (lane >> 3)));
+                            ldsm4(b, st + pa_off<CH>(n * 8 + (lane & 7), 4 * j + (lane >> 3)));
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 mma16816<false>(sc[n], qf[4 * j + i], e4m3x2_f16x2(b[i]), e4m3x2_f16x2(b[i] >> 16));
                         }
                 }
-                const bool full = bits == (KB == 32 ? 0xffffffffu : 0xffffu) && klast <= pmin && kfirst >= wtop;
+                const bool full = bits == 0xffffu && klast <= pmin && kfirst >= wtop;
                 // bit 4 n + e of `hid`: this thread's score sc[n][e] is not in its row's view
                 uint32_t hid = 0;
                 if (!full) {
@@ -337,11 +324,11 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
                 bool plain = true;
                 if (!full && (klast > pmin || kfirst < wtop)) {
                     uint32_t bad = 0;
-                    for (int i = lane; i < KB * CH; i += 32) {
+                    for (int i = lane; i < kPaKeys * CH; i += 32) {
                         uint32_t w[4];
                         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                     : "r"(sv + pa_off<CH>(kb + i / CH, i % CH)));
+                                     : "r"(sv + pa_off<CH>(i / CH, i % CH)));
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             if constexpr (E8) {
@@ -358,53 +345,46 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
                     plain = !__any_sync(0xffffffffu, bad != 0);
                 }
                 if (plain) {
+                    uint32_t ph[4], pl[4];
+                    constexpr bool PB = BF && !E8;
 #pragma unroll
-                    for (int k = 0; k < KB / 16; ++k) {
-                        uint32_t ph[4], pl[4];
-                        constexpr bool PB = BF && !E8;
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = sc[i >> 1][2 * (i & 1)], y = sc[i >> 1][2 * (i & 1) + 1];
+                        ph[i] = pack2<PB>(x, y);
+                        const float2 r = unpack2<PB>(ph[i]);
+                        pl[i] = pack2<PB>(x - r.x, y - r.y);
+                    }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float x = sc[2 * k + (i >> 1)][2 * (i & 1)], y = sc[2 * k + (i >> 1)][2 * (i & 1) + 1];
-                            ph[i] = pack2<PB>(x, y);
-                            if constexpr (S::kSplitP) {
-                                const float2 r = unpack2<PB>(ph[i]);
-                                pl[i] = pack2<PB>(x - r.x, y - r.y);
+                    for (int j = 0; j < CH / 2; ++j) {
+                        uint32_t b[4];
+                        ldsm4t(b, sv + pa_off<CH>(lane & 15, 2 * j + (lane >> 4)));
+                        if constexpr (!E8) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                mma16816<BF>(o[2 * j + i], ph, b[2 * i], b[2 * i + 1]);
+                                mma16816<BF>(o[2 * j + i], pl, b[2 * i], b[2 * i + 1]);
                             }
-                        }
+                        } else {
+                            // a register: two neighbouring columns of keys 2 tq, 2 tq + 1 -> even
+                            // columns to fragment 2 ch, odd ones to 2 ch + 1 (chunk ch)
 #pragma unroll
-                        for (int j = 0; j < CH / 2; ++j) {
-                            uint32_t b[4];
-                            ldsm4t(b, sv + pa_off<CH>(kb + 16 * k + (lane & 15), 2 * j + (lane >> 4)));
-                            if constexpr (!E8) {
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    mma16816<BF>(o[2 * j + i], ph, b[2 * i], b[2 * i + 1]);
-                                    if constexpr (S::kSplitP) mma16816<BF>(o[2 * j + i], pl, b[2 * i], b[2 * i + 1]);
-                                }
-                            } else {
-                                // a register: two neighbouring columns of keys 2 tq, 2 tq + 1 -> even
-                                // columns to fragment 2 ch, odd ones to 2 ch + 1 (chunk ch)
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const uint32_t x0 = __byte_perm(b[2 * i], 0, 0x3120),
-                                                   x1 = __byte_perm(b[2 * i + 1], 0, 0x3120);
-                                    const uint32_t e0 = e4m3x2_f16x2(x0), e1 = e4m3x2_f16x2(x1),
-                                                   d0 = e4m3x2_f16x2(x0 >> 16), d1 = e4m3x2_f16x2(x1 >> 16);
-                                    const int f = 2 * (2 * j + i);
-                                    mma16816<false>(o[f], ph, e0, e1);
-                                    mma16816<false>(o[f + 1], ph, d0, d1);
-                                    if constexpr (S::kSplitP) {
-                                        mma16816<false>(o[f], pl, e0, e1);
-                                        mma16816<false>(o[f + 1], pl, d0, d1);
-                                    }
-                                }
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t x0 = __byte_perm(b[2 * i], 0, 0x3120),
+                                               x1 = __byte_perm(b[2 * i + 1], 0, 0x3120);
+                                const uint32_t e0 = e4m3x2_f16x2(x0), e1 = e4m3x2_f16x2(x1),
+                                               d0 = e4m3x2_f16x2(x0 >> 16), d1 = e4m3x2_f16x2(x1 >> 16);
+                                const int f = 2 * (2 * j + i);
+                                mma16816<false>(o[f], ph, e0, e1);
+                                mma16816<false>(o[f + 1], ph, d0, d1);
+                                mma16816<false>(o[f], pl, e0, e1);
+                                mma16816<false>(o[f + 1], pl, d0, d1);
                             }
                         }
                     }
                 } else {
                     // key by key, the hidden ones left out
 #pragma unroll 1
-                    for (int kk = 0; kk < KB; ++kk) {
+                    for (int kk = 0; kk < kPaKeys; ++kk) {
                         const int n = kk >> 3, src = (lane & ~3) | ((kk & 7) >> 1);
                         float p[2];
                         bool out[2];
@@ -425,7 +405,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
                                 // the column of this thread's o[f][y] and o[f][2 + y]
                                 const int col = E8 ? 16 * (f >> 1) + 4 * tq + 2 * y + (f & 1) : 8 * f + 2 * tq + y;
                                 float val;
-                                const uint32_t at = sv + pa_off<CH>(kb + kk, col * (E8 ? 1 : 2) / 16) +
+                                const uint32_t at = sv + pa_off<CH>(kk, col * (E8 ? 1 : 2) / 16) +
                                                     (col * (E8 ? 1 : 2)) % 16;
                                 if constexpr (E8) {
                                     uint32_t w;
@@ -460,15 +440,15 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
         // a part of a shared unit: its start goes to the CTA's second slot, any other part to the first
         const int part = blockIdx.x * 2 + (tile0 == 0 ? 1 : 0);
         float big[2];
-        if constexpr (KG > 1) {
+        {
             if (tq == 0) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) ml[kg][wr * 16 + gq + 8 * e] = make_float2(m[e], l[e]);
+                for (int e = 0; e < 2; ++e) ml[warp][gq + 8 * e] = make_float2(m[e], l[e]);
             }
             __syncthreads();
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = wr * 16 + gq + 8 * e;
+                const int r = gq + 8 * e;
                 big[e] = -INFINITY;
 #pragma unroll
                 for (int g = 0; g < KG; ++g) big[e] = fmaxf(big[e], ml[g][r].x);
@@ -490,35 +470,33 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
             // the upper half of the groups hand their sums to the lower half
             float* mg = reinterpret_cast<float*>(sm + (size_t)NST * S::kRound);
             constexpr int H = KG / 2;
-            auto at = [&](int g, int i) { return mg + ((size_t)(g * RW + wr) * (NF * 4) + i) * 32 + lane; };
-            if (kg >= H) {
+            auto at = [&](int g, int i) { return mg + ((size_t)g * (NF * 4) + i) * 32 + lane; };
+            if (warp >= H) {
 #pragma unroll
-                for (int i = 0; i < NF * 4; ++i) *at(kg - H, i) = o[i / 4][i % 4];
+                for (int i = 0; i < NF * 4; ++i) *at(warp - H, i) = o[i / 4][i % 4];
             }
             __syncthreads();
-            if (kg < H) {
+            if (warp < H) {
 #pragma unroll
-                for (int i = 0; i < NF * 4; ++i) o[i / 4][i % 4] += *at(kg, i);
+                for (int i = 0; i < NF * 4; ++i) o[i / 4][i % 4] += *at(warp, i);
             }
-            if constexpr (H > 1) {
-                if (kg > 0 && kg < H) {
+            if (warp > 0 && warp < H) {
 #pragma unroll
-                    for (int i = 0; i < NF * 4; ++i) *at(kg, i) = o[i / 4][i % 4];
-                }
-                __syncthreads();
-                if (kg == 0) {
+                for (int i = 0; i < NF * 4; ++i) *at(warp, i) = o[i / 4][i % 4];
+            }
+            __syncthreads();
+            if (warp == 0) {
 #pragma unroll
-                    for (int g = 1; g < H; ++g)
+                for (int g = 1; g < H; ++g)
 #pragma unroll
-                        for (int i = 0; i < NF * 4; ++i) o[i / 4][i % 4] += *at(g, i);
-                }
+                    for (int i = 0; i < NF * 4; ++i) o[i / 4][i % 4] += *at(g, i);
             }
         }
-        if (kg == 0) {
+        if (warp == 0) {
             const float vs = E8 && A.C.v_scale != nullptr ? A.C.v_scale[h] : 1.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int mrow = wr * 16 + gq + 8 * e;
+                const int mrow = gq + 8 * e;
                 if (mrow >= mvalid) continue;
                 if (whole) {
                     const int mm = rt * MT + mrow, r = sq.row0 + mm / A.group, hq = h * A.group + mm % A.group;
@@ -626,12 +604,15 @@ __global__ void __launch_bounds__(kPaThreads) paged_join_kernel(const __grid_con
     }
 }
 
-// Rows a unit's tile holds, by what a sequence of average length brings: 16 or
-// 32 on the warp MMAs, beyond that the tcgen05 kernel's 64 or 128.
+// Rows a unit's tile holds, by what a sequence of average length brings: 16 on
+// the warp MMAs; beyond that the tcgen05 kernel's 64 or 128.  (A warp-MMA
+// kernel of 32 rows took 71.7 us where the tcgen05 kernel's 64 take 67.4, 32
+// sequences of 8 rows x 4 heads, and 12.6 against 14.7 us on one sequence of
+// 2048 keys; with 16 rows, 32 sequences, the warp MMAs take 58 us, tcgen05 64.)
 static int pa_tile_rows(int n_seqs, int64_t n_rows, int group) {
     const int64_t per = n_seqs > 0 ? (n_rows + n_seqs - 1) / n_seqs : 0;
     const int64_t m = per * group;
-    return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
+    return m <= kPaM ? kPaM : m <= 64 ? 64 : 128;
 }
 
 int64_t paged_attention_workspace(int hd, int n_seqs, int64_t n_rows, int heads, int kv_heads, int num_sms) {
@@ -639,29 +620,22 @@ int64_t paged_attention_workspace(int hd, int n_seqs, int64_t n_rows, int heads,
     return num_sms * (2 * mt * (hd * 4 + 8) + (int64_t)sizeof(PaJoin));
 }
 
-template <bool BF, bool E8, int HD, int RW>
+template <bool BF, bool E8, int HD>
 static int pa_launch(const PaArgs& A, int num_sms, cudaStream_t st) {
-    using S = PaShape<BF, E8, HD, RW>;
+    using S = PaShape<BF, E8, HD>;
     // the limit is a device's own: one record each
     static size_t limit[kMaxDevices] = {};
-    auto kern = paged_attn_kernel<BF, E8, HD, RW>;
+    auto kern = paged_attn_kernel<BF, E8, HD>;
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return (int)e;
     if (cudaError_t e = raise_smem_limit(kern, S::kSmem, &limit[dev])) return (int)e;
     return (int)launch(kern, dim3(num_sms), dim3(kPaThreads), S::kSmem, st, A);
 }
-template <bool BF, bool E8, int HD>
-static int pa_rw(const PaArgs& A, int mt, int num_sms, cudaStream_t st) {
-    return mt == 16 ? pa_launch<BF, E8, HD, 1>(A, num_sms, st) : pa_launch<BF, E8, HD, 2>(A, num_sms, st);
-}
-static int pa_warp(const PaArgs& A, int cache_dtype, int hd, int mt, int num_sms, cudaStream_t st) {
-    if (hd == 64)
-        return cache_dtype == kBF16  ? pa_rw<true, false, 64>(A, mt, num_sms, st)
-               : cache_dtype == kF16 ? pa_rw<false, false, 64>(A, mt, num_sms, st)
-                                     : pa_rw<false, true, 64>(A, mt, num_sms, st);
-    return cache_dtype == kBF16  ? pa_rw<true, false, 128>(A, mt, num_sms, st)
-           : cache_dtype == kF16 ? pa_rw<false, false, 128>(A, mt, num_sms, st)
-                                 : pa_rw<false, true, 128>(A, mt, num_sms, st);
+template <int HD>
+static int pa_type(const PaArgs& A, int cache_dtype, int num_sms, cudaStream_t st) {
+    return cache_dtype == kBF16  ? pa_launch<true, false, HD>(A, num_sms, st)
+           : cache_dtype == kF16 ? pa_launch<false, false, HD>(A, num_sms, st)
+                                 : pa_launch<false, true, HD>(A, num_sms, st);
 }
 
 int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& q,
@@ -674,8 +648,9 @@ int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRow
     A.ws_o = static_cast<float*>(ws);
     A.ws_ml = reinterpret_cast<float2*>(A.ws_o + 2 * (int64_t)num_sms * mt * hd);
     A.ws_join = reinterpret_cast<PaJoin*>(A.ws_ml + 2 * (int64_t)num_sms * mt);
-    const int e = mt > 32 ? paged_attention_tc(A, cache_dtype, hd, mt, num_sms, st)
-                          : pa_warp(A, cache_dtype, hd, mt, num_sms, st);
+    const int e = mt > kPaM ? paged_attention_tc(A, cache_dtype, hd, mt, num_sms, st)
+                  : hd == 64 ? pa_type<64>(A, cache_dtype, num_sms, st)
+                             : pa_type<128>(A, cache_dtype, num_sms, st);
     if (e != 0) return e;
     const dim3 grid(num_sms, mt / 16);
     const int e8 = cache_dtype == kE4M3;

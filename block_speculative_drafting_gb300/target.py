@@ -21,127 +21,50 @@ import numpy as np
 
 from . import _abi
 
-# The calls below run once a layer and step, so what they do on the host is kept to some ten microseconds: the C
-# descriptors are packed in one go, attributes are asked for once, the library and torch are looked up once.
-torch = None
-_lib = None
-_DTYPES: dict = {}
-_current_device = _raw_stream = None
+torch = _binding = _current_device = None
 
 
 def _init():
-    global torch, _lib, _current_device, _raw_stream
+    """torch, the library and the compiled half of this module (csrc/binding.c), on the first call."""
+    global torch, _binding, _current_device
     import torch as t
 
-    from . import lib
-    _lib = lib()
-    _DTYPES.update({t.float32: _abi.F32, t.bfloat16: _abi.BF16, t.float16: _abi.F16, t.float8_e4m3fn: _abi.E4M3})
+    from . import DFlashError, lib
+    try:
+        from . import _binding as b
+    except ImportError as e:
+        raise ImportError("the binding is not built; run __graft_entry__.build() or "
+                          "python -m block_speculative_drafting_gb300.csrc.build") from e
+    L = lib()
+    names = ("dflash_paged_append", "dflash_paged_attention", "dflash_paged_attention_workspace", "dflash_verify",
+             "dflash_verify_workspace", "dflash_last_error")
+    raw = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda d: t.cuda.current_stream(d).cuda_stream)
+    b.init(tuple(C.cast(getattr(L, n), C.c_void_p).value for n in names),
+           (t.float32, t.bfloat16, t.float16, t.float8_e4m3fn, t.float64, t.int32, t.uint32), DFlashError, t.empty_like, raw)
     _current_device = t.cuda.current_device
-    _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda d: t.cuda.current_stream(d).cuda_stream)
-    torch = t
+    torch, _binding = t, b
 
 
 def _check(rc: int) -> int:
     if rc < 0:
-        from . import DFlashError
-        raise DFlashError(rc, _lib.dflash_last_error(None).decode())
+        from . import DFlashError, lib
+        raise DFlashError(rc, lib().dflash_last_error(None).decode())
     return rc
 
 
-def _refuse(msg: str):
-    from . import DFlashError
-    raise DFlashError(_abi.DFLASH_EINVAL, msg)
-
-
-def _direct(dev: int, stream) -> bool:
-    """Whether a call can run where it stands: on the current device, on its current stream."""
-    if dev < 0:
-        _refuse("tensors have to be on a CUDA device")
-    return stream is None and dev == _current_device()
-
-
 @contextlib.contextmanager
-def _moved(dev: int, stream):
+def _at(dev: int, stream):
     """The call's device and stream made current.  (What a call allocates belongs to the stream that is current, so
     that it is not dealt out again before that stream is done with it.)"""
+    if dev < 0:
+        from . import DFlashError
+        raise DFlashError(_abi.DFLASH_EINVAL, "tensors have to be on a CUDA device")
     with torch.cuda.device(dev):
         if stream is None:
             yield
         else:
             with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev)):
                 yield
-
-
-def _same_device(dev: int, *tensors):
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            _refuse(f"a tensor of shape {tuple(t.shape)} is on {t.device}, not on cuda:{dev}")
-
-
-def _vector(t, name: str, n: int, dtype) -> int:
-    """Pointer of a contiguous vector of n elements (None: 0)."""
-    if t is None:
-        return 0
-    if t.dtype is not dtype or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
-        _refuse(f"{name} has to be a contiguous vector of {n} elements of {dtype}, got {tuple(t.shape)} of {t.dtype}")
-    return t.data_ptr()
-
-
-def _head_rows(t, name: str, n: int, hd: int, written: bool = False) -> bytes:
-    """A [n][heads][hd] tensor as a dflash_head_rows (a type it has no code for: -1, which the library refuses)."""
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != n or shape[2] != hd:
-        _refuse(f"{name} has to be [{n}][heads][{hd}], got {tuple(shape)}")
-    h = shape[1]
-    sr, sh, sc = t.stride()
-    if sc != 1:
-        _refuse(f"{name} needs contiguous columns")
-    if n <= 1:  # the stride of a dimension of one element is anything
-        sr = 0
-    elif written and sr == 0:
-        _refuse(f"{name} is written and may not be an expanded tensor")
-    if h <= 1:
-        sh = 0
-    elif written and sh == 0:
-        _refuse(f"{name} is written and may not be an expanded tensor")
-    return _HEAD_ROWS(t.data_ptr(), _DTYPES.get(t.dtype, -1), h, sr, sh)
-
-
-_HEAD_ROWS, _PAGED_CACHE, _PAGED_ROWS = _abi.HEAD_ROWS.pack, _abi.PAGED_CACHE.pack, _abi.PAGED_ROWS.pack
-
-
-def _cache(k, v, shape, k_scale, v_scale, written: bool = False) -> bytes:
-    """The two cache tensors, k of the given shape, as a dflash_paged_cache."""
-    if len(shape) != 4 or v.shape != shape or v.dtype is not k.dtype:
-        _refuse("k_cache and v_cache have to be [pages][page_size][kv_heads][head_dim] of one shape and type, got "
-                f"{tuple(shape)} of {k.dtype} and {tuple(v.shape)} of {v.dtype}")
-    n, page, heads, hd = shape
-    k0, k1, k2, k3 = k.stride()
-    v0, v1, v2, v3 = v.stride()
-    if k3 != 1 or v3 != 1:
-        _refuse("k_cache and v_cache need contiguous columns")
-    if n <= 1 or page <= 1 or heads <= 1:  # the stride of a dimension of one element is anything
-        k0, v0 = (0, 0) if n <= 1 else (k0, v0)
-        k1, v1 = (0, 0) if page <= 1 else (k1, v1)
-        k2, v2 = (0, 0) if heads <= 1 else (k2, v2)
-    if written and not (k0 and k1 and k2 and v0 and v1 and v2) and (
-            n > 1 and not (k0 and v0) or page > 1 and not (k1 and v1) or heads > 1 and not (k2 and v2)):
-        _refuse("k_cache and v_cache are written and may not be expanded tensors")
-    ks = vs = 0
-    if k_scale is not None or v_scale is not None:
-        ks = _vector(k_scale, "k_scale", heads, torch.float32)
-        vs = _vector(v_scale, "v_scale", heads, torch.float32)
-    return _PAGED_CACHE(k.data_ptr(), v.data_ptr(), _DTYPES.get(k.dtype, -1), heads, hd, page, n, k0, k1, k2, v0, v1,
-                        v2, ks, vs)
-
-
-def _rows(table, kv_len, row_start, n_rows: int) -> bytes:
-    i32, shape = torch.int32, table.shape
-    if table.dtype is not i32 or len(shape) != 2 or (shape[1] > 1 and table.stride(1) != 1):
-        _refuse(f"table has to be int32 [sequences][pages] with contiguous rows, got {tuple(shape)} of {table.dtype}")
-    n, width = shape
-    return _PAGED_ROWS(n, width, n_rows, 0 if row_start is None else _vector(row_start, "row_start", n + 1, i32),
-                       _vector(kv_len, "kv_len", n, i32), table.data_ptr(), table.stride(0) if n > 1 else width)
 
 
 def rope_inv_freq(rotary: int, theta: float = 1e6, scaling: str | None = None, factor: float = 1.0,
@@ -198,41 +121,13 @@ def paged_append(k_cache, v_cache, k, v, table, kv_len, *, row_start=None, q=Non
     """
     if torch is None:
         _init()
+    args = (k_cache, v_cache, k, v, table, kv_len, row_start, q, q_out, inv_freq, interleaved, rope_scale, q_norm, k_norm,
+            eps, k_scale, v_scale)
     dev = k_cache.get_device()
-    if not _direct(dev, stream):
-        with _moved(dev, stream):
-            return paged_append(k_cache, v_cache, k, v, table, kv_len, row_start=row_start, q=q, q_out=q_out,
-                                inv_freq=inv_freq, interleaved=interleaved, rope_scale=rope_scale, q_norm=q_norm,
-                                k_norm=k_norm, eps=eps, k_scale=k_scale, v_scale=v_scale)
-    _same_device(dev, v_cache, k, v, table, kv_len, row_start, q, q_out, inv_freq, q_norm, k_norm, k_scale, v_scale)
-    shape, n = k_cache.shape, k.shape[0] if k.dim() else 0
-    cache = _cache(k_cache, v_cache, shape, k_scale, v_scale, True)
-    kv_heads, hd = shape[2], shape[3]
-    kr, vr = _head_rows(k, "k", n, hd), _head_rows(v, "v", n, hd)
-    qr = qo = rot = None
-    if inv_freq is not None:
-        f = inv_freq.numel()
-        rot = _abi.ROTATION.pack(_vector(inv_freq, "inv_freq", f, torch.float64), 2 * f, 1 if interleaved else 0,
-                                 rope_scale)
-    if q is not None:
-        qr = _head_rows(q, "q", n, hd)
-        if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        elif q_out.shape != q.shape:
-            _refuse(f"q_out has to be {tuple(q.shape)}, got {tuple(q_out.shape)}")
-        qo = _head_rows(q_out, "q_out", n, hd, True)
-    elif q_out is not None:
-        _refuse("q_out without q")
-    qn = kn = 0
-    if q_norm is not None:
-        qn = _vector(q_norm, "q_norm", hd, torch.float32)
-    if k_norm is not None:
-        kn = _vector(k_norm, "k_norm", hd, torch.float32)
-    rc = _lib.dflash_paged_append(cache, _rows(table, kv_len, row_start, n), kr, vr, qr, qo, qn, kn, eps, rot,
-                                  _raw_stream(dev))
-    if rc < 0:
-        _check(rc)
-    return q_out
+    if stream is not None or dev < 0 or dev != _current_device():
+        with _at(dev, stream):
+            return _binding.paged_append(*args)
+    return _binding.paged_append(*args)
 
 
 def paged_attention(q, k_cache, v_cache, table, kv_len, *, row_start=None, scale: float | None = None, window: int = 0,
@@ -251,49 +146,25 @@ def paged_attention(q, k_cache, v_cache, table, kv_len, *, row_start=None, scale
     """
     if torch is None:
         _init()
+    args = (q, k_cache, v_cache, table, kv_len, row_start, q.shape[-1] ** -0.5 if scale is None else scale, window, k_scale,
+            v_scale, out, lse, workspace)
     dev = q.get_device()
-    if not _direct(dev, stream):
-        with _moved(dev, stream):
-            return paged_attention(q, k_cache, v_cache, table, kv_len, row_start=row_start, scale=scale, window=window,
-                                   k_scale=k_scale, v_scale=v_scale, out=out, lse=lse, workspace=workspace)
-    _same_device(dev, k_cache, v_cache, table, kv_len, row_start, k_scale, v_scale, out, lse, workspace)
-    shape, qshape = k_cache.shape, q.shape
-    cache = _cache(k_cache, v_cache, shape, k_scale, v_scale)
-    if len(qshape) != 3:
-        _refuse(f"q has to be [rows][heads][head_dim], got {tuple(qshape)}")
-    n, heads, hd = qshape[0], qshape[1], shape[3]
-    qr, rows = _head_rows(q, "q", n, hd), _rows(table, kv_len, row_start, n)
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous()):
-        _refuse(f"lse has to be contiguous float32 [{n}][{heads}]")
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    elif out.shape != qshape:
-        _refuse(f"out has to be {tuple(qshape)}, got {tuple(out.shape)}")
-    if workspace is None:
-        need = _check(_lib.dflash_paged_attention_workspace(cache, table.shape[0], n, heads))
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    else:
-        if not workspace.is_contiguous():
-            _refuse("workspace has to be contiguous")
-        need = workspace.nbytes
-    rc = _lib.dflash_paged_attention(cache, rows, qr, _head_rows(out, "out", n, hd, True),
-                                     0 if lse is None else lse.data_ptr(), hd ** -0.5 if scale is None else scale,
-                                     window, workspace.data_ptr(), need, _raw_stream(dev))
-    if rc < 0:
-        _check(rc)
-    return out
+    if stream is not None or dev < 0 or dev != _current_device():
+        with _at(dev, stream):
+            return _binding.paged_attention(*args)
+    return _binding.paged_attention(*args)
 
 
 def paged_attention_workspace(q, k_cache, n_seqs: int) -> int:
     """Bytes of workspace that `paged_attention` needs for q's rows over n_seqs sequences."""
     if torch is None:
         _init()
-    dev = q.get_device()
-    if not _direct(dev, None):
-        with _moved(dev, None):
-            return paged_attention_workspace(q, k_cache, n_seqs)
-    cache = _cache(k_cache, k_cache, k_cache.shape, None, None)
-    return _check(_lib.dflash_paged_attention_workspace(cache, n_seqs, q.shape[0], q.shape[1]))
+    from . import lib
+    n, page, heads, hd = k_cache.shape
+    kind = {torch.bfloat16: _abi.BF16, torch.float16: _abi.F16, torch.float8_e4m3fn: _abi.E4M3}.get(k_cache.dtype, -1)
+    c = _abi.PagedCache(None, None, kind, heads, hd, page, 0)
+    with _at(q.get_device(), None):
+        return _check(lib().dflash_paged_attention_workspace(C.byref(c), n_seqs, q.shape[0], q.shape[1]))
 
 
 def verify_drafts(target_logits, draft_tokens, accept_u, sample_u, *, draft_logits=None, draft_start=None,
@@ -315,62 +186,16 @@ def verify_drafts(target_logits, draft_tokens, accept_u, sample_u, *, draft_logi
     """
     if torch is None:
         _init()
+    args = (target_logits, draft_tokens, accept_u, sample_u, draft_logits, draft_start, temperature, accepted, next_token,
+            prob, workspace)
     dev = target_logits.get_device()
-    if not _direct(dev, stream):
-        with _moved(dev, stream):
-            return verify_drafts(target_logits, draft_tokens, accept_u, sample_u, draft_logits=draft_logits,
-                                 draft_start=draft_start, temperature=temperature, accepted=accepted,
-                                 next_token=next_token, prob=prob, workspace=workspace)
-    _same_device(dev, draft_tokens, accept_u, sample_u, draft_logits, draft_start, temperature, accepted, next_token,
-                 prob, workspace)
-    f32, i32 = torch.float32, torch.int32
-    if target_logits.dim() != 2:
-        _refuse(f"target_logits has to be [rows][vocab], got {tuple(target_logits.shape)}")
-    n, d, (rows, vocab), (stride, one) = sample_u.numel(), draft_tokens.numel(), target_logits.shape, target_logits.stride()
-    if one != 1 and vocab > 1:
-        _refuse("target_logits needs contiguous rows")
-    if rows != n + d:
-        _refuse(f"{d} drafts of {n} sequences need {n + d} target rows, got {rows}")
-    if draft_tokens.dtype is not i32 and draft_tokens.dtype is not torch.uint32 or not draft_tokens.is_contiguous():
-        _refuse(f"draft_tokens has to be contiguous int32 or uint32, got {draft_tokens.dtype}")
-    dl, ds = None, 0
-    if draft_logits is not None:
-        if draft_logits.dtype is not f32 or draft_logits.shape[-1] != vocab or draft_logits.numel() != d * vocab:
-            _refuse(f"draft_logits has to be float32 [{d}][{vocab}], got {tuple(draft_logits.shape)}")
-        if draft_logits.dim() == 2 and (vocab == 1 or draft_logits.stride(1) == 1):
-            ds = draft_logits.stride(0) if d > 1 else vocab
-        elif draft_logits.is_contiguous():
-            ds = vocab
-        else:
-            _refuse("draft_logits needs contiguous rows (more than two dimensions: contiguous as a whole)")
-        dl = draft_logits.data_ptr()
-    if accepted is None:
-        accepted = torch.empty(n, dtype=i32, device=target_logits.device)
-    if next_token is None:
-        next_token = torch.empty_like(accepted)
-    if prob is None:
-        prob = torch.empty_like(accept_u, memory_format=torch.contiguous_format)
-    if workspace is None:
-        need = _check(_lib.dflash_verify_workspace(n, d, vocab))
-        workspace = torch.empty(need, dtype=torch.uint8, device=target_logits.device)
-    else:
-        if not workspace.is_contiguous():
-            _refuse("workspace has to be contiguous")
-        need = workspace.nbytes
-    rc = _lib.dflash_verify(
-        target_logits.data_ptr(), _DTYPES.get(target_logits.dtype, -1), stride if rows > 1 else vocab, dl, ds,
-        draft_tokens.data_ptr(), _vector(draft_start, "draft_start", n + 1, i32),
-        _vector(temperature, "temperature", n, f32), _vector(accept_u, "accept_u", d, f32),
-        _vector(sample_u, "sample_u", n, f32), n, d, vocab, _vector(accepted, "accepted", n, i32),
-        _vector(next_token, "next_token", n, i32), _vector(prob, "prob", d, f32), workspace.data_ptr(), need,
-        _raw_stream(dev))
-    if rc < 0:
-        _check(rc)
-    return accepted, next_token, prob
+    if stream is not None or dev < 0 or dev != _current_device():
+        with _at(dev, stream):
+            return _binding.verify_drafts(*args)
+    return _binding.verify_drafts(*args)
 
 
 def verify_workspace(n_seqs: int, n_drafts: int, vocab: int) -> int:
     """Bytes of workspace that `verify_drafts` needs on the current device."""
-    if torch is None:
-        _init()
-    return _check(_lib.dflash_verify_workspace(n_seqs, n_drafts, vocab))
+    from . import lib
+    return _check(lib().dflash_verify_workspace(n_seqs, n_drafts, vocab))

@@ -400,7 +400,7 @@ def test_append_in_place_queries():
 
 # --------------------------------------------------------------------------- attention
 def _check_attention(kind, src=None, hd=128, heads=4, kvh=2, page=16, rows=(1,), lens=(40,), window=0, uniform=False, bad=(),
-                     order="slot", extra=0, scale=None, seed=0, poison=None, spread=1.0, split_p=True, call=None):
+                     order="slot", extra=0, scale=None, seed=0, poison=None, spread=1.0):
     torch, dfl = _torch(), _dfl()
     rng = np.random.default_rng(seed)
     T = _types()
@@ -436,7 +436,9 @@ def _check_attention(kind, src=None, hd=128, heads=4, kvh=2, page=16, rows=(1,),
     # a score's error: head_dim f32 additions, of partial sums up to |q| |k|
     norm = lambda x: np.linalg.norm(np.where(np.isfinite(x), x, 0.0), axis=-1).max()  # noqa: E731
     s_err = hd * 2.0 ** -24 * (hd ** -0.5 if scale is None else scale) * norm(f64(q)) * norm(k64) + 2.0 ** -20
-    p_err = s_err + (0.0 if split_p else HALF["f16" if kind == "e4m3" else kind])
+    # an 8-bit cache's P is one f16 where more than 16 rows share the keys, a hi + lo pair otherwise
+    one_p = kind == "e4m3" and -(-R // len(lens)) * (heads // kvh) > 16
+    p_err = s_err + (HALF["f16"] if one_p else 0.0)
     with np.errstate(all="ignore"):
         tol = HALF[src] * np.abs(ref) + TINY[src] + 2 * p_err * mag
         fine = np.isfinite(ref)
@@ -457,7 +459,7 @@ def _check_attention(kind, src=None, hd=128, heads=4, kvh=2, page=16, rows=(1,),
 def test_attention_types_and_tiles(kind, src, hd, group, rows):
     # one to ten tiles of 16 query rows a unit; two sequences of different lengths
     _check_attention(kind, src, hd=hd, heads=2 * group, kvh=2, rows=(rows, rows), lens=(rows + 3, 300), uniform=True,
-                     seed=group, split_p=group * rows <= 32)
+                     seed=group)
 
 
 @gpu
@@ -478,8 +480,7 @@ def test_attention_lengths(length):
 @pytest.mark.parametrize("window", [1, 7, 16, 100, 5000])
 @pytest.mark.parametrize("rows", [1, 6, 33])
 def test_attention_windows(window, rows):
-    _check_attention("bf16", rows=(rows, 2, rows), lens=(400, 2, rows), window=window, heads=4, kvh=1,
-                     split_p=4 * ((2 * rows + 2 + 2) // 3) <= 32)
+    _check_attention("bf16", rows=(rows, 2, rows), lens=(400, 2, rows), window=window, heads=4, kvh=1)
 
 
 @gpu
@@ -488,8 +489,7 @@ def test_attention_ragged_padded_and_bad_pages():
     # no page held, some not held, positions before 0, lengths past the table
     _check_attention("bf16", rows=(1, 2, 1), lens=(10, 100, 33), bad=((0, 0), (1, 1), (1, 3), (2, 2)), seed=2)
     _check_attention("f16", rows=(4, 2, 1, 1), lens=(2, 0, -7, 1), seed=3)
-    _check_attention("e4m3", "f16", rows=(5,), lens=(4000,), bad=tuple((0, i) for i in range(0, 250, 3)), window=900, seed=4,
-                     split_p=True)
+    _check_attention("e4m3", "f16", rows=(5,), lens=(4000,), bad=tuple((0, i) for i in range(0, 250, 3)), window=900, seed=4)
 
 
 @gpu
@@ -548,9 +548,9 @@ def test_attention_keeps_what_rows_may_not_see_out(kind):
         rk[int(table[1][p // 16]), p % 16, 1, 5] = 0x7f if kind == "e4m3" else float("nan")
 
     free.more = later
-    for hd, heads, kvh, rows in ((128, 4, 2, (2, 4)), (64, 16, 2, (1, 9)), (128, 2, 2, (3, 3))):
+    for hd, heads, kvh, rows in ((128, 4, 2, (2, 4)), (64, 16, 2, (1, 9)), (128, 2, 2, (3, 3)), (128, 32, 2, (3, 9))):
         _check_attention(kind, "f16" if kind == "e4m3" else kind, hd=hd, heads=heads, kvh=kvh, rows=rows, lens=(5, 130),
-                         poison=free, split_p=heads // kvh * max(rows) <= 32)
+                         poison=free)
     # a window's edge: keys that the first rows see and the last do not
     free.lo, free.more = (0, 100), lambda torch, kc, vc, table: (vc.view(torch.uint8) if kind == "e4m3" else vc)[
         int(table[1][101 // 16]), 101 % 16].fill_(0x7f if kind == "e4m3" else float("inf"))
@@ -578,7 +578,7 @@ def test_attention_splits_long_contexts():
     # one unit over many SMs (joined in order), and many units of several SMs each
     _check_attention("bf16", rows=(1,), lens=(9000,), heads=2, kvh=1, page=64, hd=64)
     _check_attention("f16", rows=(2, 1, 1), lens=(3000, 10, 4100), heads=8, kvh=2, page=32)
-    _check_attention("e4m3", "bf16", rows=(16,), lens=(5000,), heads=4, kvh=1, page=128, split_p=False)
+    _check_attention("e4m3", "bf16", rows=(16,), lens=(5000,), heads=4, kvh=1, page=128)
 
 
 @gpu
