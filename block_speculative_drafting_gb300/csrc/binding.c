@@ -21,7 +21,7 @@ enum { F32 = DFLASH_F32, BF16 = DFLASH_BF16, F16 = DFLASH_F16, E4M3 = DFLASH_E4M
 
 static PyObject *s_shape, *s_stride, *s_data_ptr, *s_dtype, *s_get_device, *s_new_empty, *kw_dtype;
 static PyObject* dtypes[DTYPES]; /* torch's, by the codes above */
-static PyObject *error_type, *empty_like, *raw_stream;
+static PyObject *error_type, *empty_like, *raw_stream, *raw_alloc, *raw_delete;
 static __typeof__(&dflash_paged_append) lib_append;
 static __typeof__(&dflash_paged_attention) lib_attention;
 static __typeof__(&dflash_paged_attention_workspace) lib_attention_workspace;
@@ -175,43 +175,49 @@ static int current_stream(int dev, void** out) {
     Py_DECREF(s);
     return PyErr_Occurred() ? -1 : 0;
 }
-/* like.new_empty(n) of like's type, or of dtypes[dtype] */
+/* like.new_empty(n, dtype=dtypes[dtype]) */
 static PyObject* new_empty(PyObject* like, int64_t n, int dtype) {
     PyObject* size = PyLong_FromLongLong(n);
     if (size == NULL) return NULL;
-    PyObject* args[3] = {like, size, dtype < DTYPES ? dtypes[dtype] : NULL};
-    PyObject* t = PyObject_VectorcallMethod(s_new_empty, args, 2 | PY_VECTORCALL_ARGUMENTS_OFFSET, dtype < DTYPES ? kw_dtype : NULL);
+    PyObject* args[3] = {like, size, dtypes[dtype]};
+    PyObject* t = PyObject_VectorcallMethod(s_new_empty, args, 2 | PY_VECTORCALL_ARGUMENTS_OFFSET, kw_dtype);
     Py_DECREF(size);
     return t;
 }
-/* The caller's workspace, or one of at least `need` bytes allocated like `like`: a new reference. */
-static PyObject* workspace_of(PyObject* given, PyObject* like, int dev, int64_t need, void** p, int64_t* bytes) {
+/* The caller's workspace, or `need` bytes of torch's allocator for the call's stream: given back as soon as the call
+ * is queued, they are dealt out again to work behind it on that stream alone. */
+typedef struct {
+    void* p;
+    int64_t bytes;
+    PyObject* own; /* the address to give back, or NULL */
+} Workspace;
+static int workspace_of(PyObject* given, int dev, void* stream, int64_t need, Workspace* w) {
     Tensor t;
     static const int size[DTYPES] = {4, 2, 2, 1, 8, 4, 4};
-    PyObject* w = given;
-    if (given == Py_None)
-        w = new_empty(like, (need + 3) / 4, F32);
-    else
-        Py_INCREF(w);
-    if (w == NULL) return NULL;
-    if (read_tensor(w, "workspace", dev, &t)) {
-        Py_DECREF(w);
-        return NULL;
+    w->own = NULL;
+    if (given != Py_None) {
+        if (read_tensor(given, "workspace", dev, &t)) return -1;
+        if (t.nd != 1 || t.stride[0] != 1) return refuse("workspace has to be a contiguous vector");
+        w->p = t.p;
+        w->bytes = (t.dtype < DTYPES ? size[t.dtype] : 1) * t.shape[0]; /* (uint8 is none of the types above) */
+        return 0;
     }
-    *p = t.p;
-    if (given == Py_None) {
-        *bytes = need;
-    } else {
-        /* (torch.uint8 is none of the types above: one byte) */
-        int64_t n = t.dtype < DTYPES ? size[t.dtype] : 1;
-        if (t.nd != 1 || t.stride[0] != 1) {
-            refuse("workspace has to be a contiguous vector");
-            Py_DECREF(w);
-            return NULL;
-        }
-        *bytes = n * t.shape[0];
-    }
-    return w;
+    w->own = PyObject_CallFunction(raw_alloc, "LK", (long long)need, (unsigned long long)(uintptr_t)stream);
+    if (w->own == NULL) return -1;
+    w->p = PyLong_AsVoidPtr(w->own);
+    w->bytes = need;
+    return PyErr_Occurred() ? -1 : 0;
+}
+/* Gives an allocated workspace back; keeps the error that is set, if one is. */
+static int workspace_end(Workspace* w) {
+    if (w->own == NULL) return 0;
+    PyObject* err = PyErr_GetRaisedException();
+    PyObject* x = PyObject_CallOneArg(raw_delete, w->own);
+    const int bad = x == NULL;
+    Py_XDECREF(x);
+    Py_CLEAR(w->own);
+    if (err != NULL) PyErr_SetRaisedException(err);
+    return bad ? -1 : 0;
 }
 
 /* k_cache, v_cache, k, v, table, kv_len, row_start, q, q_out, inv_freq, interleaved, rope_scale, q_norm, k_norm, eps,
@@ -285,7 +291,7 @@ static PyObject* paged_attention(PyObject* self, PyObject* const* a, Py_ssize_t 
     dflash_head_rows q, o;
     Tensor tq, to, tl;
     int dev = -1;
-    void *ws, *stream, *lse = NULL;
+    void *stream, *lse = NULL;
     if (read_cache(a[1], a[2], a[8], a[9], &dev, 0, &c) || read_tensor(a[0], "q", dev, &tq)) return NULL;
     const int64_t n = tq.shape[0], hd = c.head_dim;
     if (head_rows(&tq, "q", n, hd, &q) || read_rows(a[3], a[4], a[5], dev, n, &r)) return NULL;
@@ -314,19 +320,16 @@ static PyObject* paged_attention(PyObject* self, PyObject* const* a, Py_ssize_t 
     } else {
         Py_INCREF(out);
     }
-    int64_t bytes = 0;
-    PyObject* w = NULL;
+    Workspace w = {NULL, 0, NULL};
     int rc = -1;
     if (!read_tensor(out, "out", dev, &to) && !written(&to, "out") && !head_rows(&to, "out", n, hd, &o) &&
-        !current_stream(dev, &stream))
-        w = workspace_of(a[12], a[0], dev, need, &ws, &bytes);
-    if (w != NULL) {
+        !current_stream(dev, &stream) && !workspace_of(a[12], dev, stream, need, &w)) {
         Py_BEGIN_ALLOW_THREADS;
-        rc = lib_attention(&c, &r, &q, &o, lse, (float)scale, (int32_t)window, ws, bytes, stream);
+        rc = lib_attention(&c, &r, &q, &o, lse, (float)scale, (int32_t)window, w.p, w.bytes, stream);
         Py_END_ALLOW_THREADS;
-        Py_DECREF(w);
         rc = check(rc);
     }
+    rc |= workspace_end(&w);
     if (rc) {
         Py_DECREF(out);
         return NULL;
@@ -390,7 +393,7 @@ static PyObject* verify_drafts(PyObject* self, PyObject* const* a, Py_ssize_t na
             return NULL;
         }
     }
-    void *start, *temp, *au, *su, *acc, *nxt, *prob, *ws, *stream;
+    void *start, *temp, *au, *su, *acc, *nxt, *prob, *stream;
     if (a[2] == Py_None || vector(a[2], "accept_u", dev, d, F32, &au) || vector(a[3], "sample_u", dev, n, F32, &su) ||
         vector(a[5], "draft_start", dev, n + 1, I32, &start) || vector(a[6], "temperature", dev, n, F32, &temp)) {
         if (!PyErr_Occurred()) refuse("accept_u is None");
@@ -401,7 +404,7 @@ static PyObject* verify_drafts(PyObject* self, PyObject* const* a, Py_ssize_t na
     PyObject* o[3] = {a[7], a[8], a[9]};
     for (int i = 0; i < 3; ++i) {
         if (o[i] == Py_None)
-            o[i] = new_empty(a[3], i == 2 ? d : n, i == 2 ? OTHER : I32);
+            o[i] = i == 0 ? new_empty(a[3], n, I32) : PyObject_CallOneArg(empty_like, i == 1 ? o[0] : a[2]);
         else
             Py_INCREF(o[i]);
         if (o[i] == NULL) {
@@ -409,32 +412,31 @@ static PyObject* verify_drafts(PyObject* self, PyObject* const* a, Py_ssize_t na
             return NULL;
         }
     }
-    int64_t bytes = 0;
-    PyObject* w = NULL;
+    Workspace w = {NULL, 0, NULL};
     int rc = -1;
     if (!vector(o[0], "accepted", dev, n, I32, &acc) && !vector(o[1], "next_token", dev, n, I32, &nxt) &&
-        !vector(o[2], "prob", dev, d, F32, &prob) && !current_stream(dev, &stream))
-        w = workspace_of(a[10], a[3], dev, need, &ws, &bytes);
-    if (w != NULL) {
+        !vector(o[2], "prob", dev, d, F32, &prob) && !current_stream(dev, &stream) &&
+        !workspace_of(a[10], dev, stream, need, &w)) {
         Py_BEGIN_ALLOW_THREADS;
         rc = lib_verify(t.p, t.dtype, t.shape[0] > 1 ? t.stride[0] : vocab, a[4] != Py_None ? (const float*)dl.p : NULL, ds,
-                        tok.p, start, temp, au, su, (int32_t)n, d, vocab, acc, nxt, prob, ws, bytes, stream);
+                        tok.p, start, temp, au, su, (int32_t)n, d, vocab, acc, nxt, prob, w.p, w.bytes, stream);
         Py_END_ALLOW_THREADS;
-        Py_DECREF(w);
         rc = check(rc);
     }
+    rc |= workspace_end(&w);
     PyObject* res = rc ? NULL : PyTuple_Pack(3, o[0], o[1], o[2]);
     for (int i = 0; i < 3; ++i) Py_DECREF(o[i]);
     return res;
 }
 
-/* init(addresses of the six entry points, torch's dtypes by code, DFlashError, empty_like, raw stream of a device) */
+/* init(addresses of the six entry points, torch's dtypes by code, DFlashError, empty_like, the raw stream of a device,
+ * torch's allocation of (bytes, stream) and its release) */
 static PyObject* init(PyObject* self, PyObject* args) {
     (void)self;
     unsigned long long f[6];
-    PyObject *types, *err, *like, *raw;
-    if (!PyArg_ParseTuple(args, "(KKKKKK)O!OOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &PyTuple_Type, &types, &err, &like,
-                          &raw))
+    PyObject *types, *err, *like, *raw, *alloc, *dealloc;
+    if (!PyArg_ParseTuple(args, "(KKKKKK)O!OOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &PyTuple_Type, &types, &err,
+                          &like, &raw, &alloc, &dealloc))
         return NULL;
     if (PyTuple_GET_SIZE(types) != DTYPES) return PyErr_Format(PyExc_ValueError, "%d types", DTYPES);
     lib_append = (__typeof__(lib_append))(uintptr_t)f[0];
@@ -453,6 +455,10 @@ static PyObject* init(PyObject* self, PyObject* args) {
     Py_XSETREF(empty_like, like);
     Py_INCREF(raw);
     Py_XSETREF(raw_stream, raw);
+    Py_INCREF(alloc);
+    Py_XSETREF(raw_alloc, alloc);
+    Py_INCREF(dealloc);
+    Py_XSETREF(raw_delete, dealloc);
     Py_RETURN_NONE;
 }
 

@@ -38,9 +38,15 @@ def _init():
     L = lib()
     names = ("dflash_paged_append", "dflash_paged_attention", "dflash_paged_attention_workspace", "dflash_verify",
              "dflash_verify_workspace", "dflash_last_error")
+    # torch's own short ways, where it has them: every operator call costs microseconds here
     raw = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda d: t.cuda.current_stream(d).cuda_stream)
+    alloc = getattr(t._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+    free = getattr(t._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+    if alloc is None or free is None:
+        alloc, free = (lambda n, s: t.cuda.caching_allocator_alloc(n, None, s)), t.cuda.caching_allocator_delete
     b.init(tuple(C.cast(getattr(L, n), C.c_void_p).value for n in names),
-           (t.float32, t.bfloat16, t.float16, t.float8_e4m3fn, t.float64, t.int32, t.uint32), DFlashError, t.empty_like, raw)
+           (t.float32, t.bfloat16, t.float16, t.float8_e4m3fn, t.float64, t.int32, t.uint32), DFlashError, t.empty_like, raw,
+           alloc, free)
     _current_device = t.cuda.current_device
     torch, _binding = t, b
 
