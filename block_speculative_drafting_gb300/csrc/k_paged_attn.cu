@@ -267,8 +267,11 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
                             uint32_t b[4];
                             ldsm4(b, st + pa_off<CH>(n * 8 + (lane & 7), 4 * j + (lane >> 3)));
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                mma16816<false>(sc[n], qf[4 * j + i], e4m3x2_f16x2(b[i]), e4m3x2_f16x2(b[i] >> 16));
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t b0, b1;
+                                e4m3x4_f16x4(b[i], b0, b1);
+                                mma16816<false>(sc[n], qf[4 * j + i], b0, b1);
+                            }
                         }
                 }
                 const bool full = bits == 0xffffu && klast <= pmin && kfirst >= wtop;
@@ -371,8 +374,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
                             for (int i = 0; i < 2; ++i) {
                                 const uint32_t x0 = __byte_perm(b[2 * i], 0, 0x3120),
                                                x1 = __byte_perm(b[2 * i + 1], 0, 0x3120);
-                                const uint32_t e0 = e4m3x2_f16x2(x0), e1 = e4m3x2_f16x2(x1),
-                                               d0 = e4m3x2_f16x2(x0 >> 16), d1 = e4m3x2_f16x2(x1 >> 16);
+                                uint32_t e0, e1, d0, d1;
+                                e4m3x4_f16x4(x0, e0, d0);
+                                e4m3x4_f16x4(x1, e1, d1);
                                 const int f = 2 * (2 * j + i);
                                 mma16816<false>(o[f], ph, e0, e1);
                                 mma16816<false>(o[f + 1], ph, d0, d1);

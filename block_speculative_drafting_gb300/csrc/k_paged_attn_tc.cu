@@ -270,10 +270,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                     uint32_t y[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        y[2 * j] = e4m3x2_f16x2(w[j]);
-                        y[2 * j + 1] = e4m3x2_f16x2(w[j] >> 16);
-                    }
+                    for (int j = 0; j < 4; ++j) e4m3x4_f16x4(w[j], y[2 * j], y[2 * j + 1]);
                     // (lanes of the upper blocks write their halves in the other order: other banks)
                     const bool flip = ch >= CH / 2;
 #pragma unroll

@@ -165,6 +165,12 @@ DF_DEV uint32_t e4m3x2_f16x2(uint32_t codes) {
     asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(y) : "r"(codes));
     return y;
 }
+// four codes -> four f16
+DF_DEV void e4m3x4_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
+}
 // (a, b) -> a pair of 16-bit floats, and what the rounding left
 template <bool BF>
 DF_DEV uint32_t pack2(float a, float b) {
