@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
     pdl_wait();
     pdl_trigger();
 
-    int64_t chunk;
+    int chunk;
     PaCur cur = pa_share(A, MT, kPaOver, lane, chunk);
     if (threadIdx.x == 0) A.ws_join[blockIdx.x].last = -1;
     if (cur.left <= 0) return;

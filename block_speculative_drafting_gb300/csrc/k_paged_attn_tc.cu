@@ -132,7 +132,7 @@ DF_DEV bool finite16(uint32_t h) {
     return BF ? (h & 0x7f80u) != 0x7f80u : (h & 0x7c00u) != 0x7c00u;
 }
 // the part of a unit that a share holds: from c on
-DF_DEV int pt_tiles(const PaCur& c) { return (int)min((int64_t)(c.q.ntiles - c.tile), c.left); }
+DF_DEV int pt_tiles(const PaCur& c) { return min(c.q.ntiles - c.tile, c.left); }
 template <int MT>
 DF_DEV void pt_skip(const PaArgs& A, PaCur& c, int n) {
     c.left -= n - 1;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
     pdl_wait();
     pdl_trigger();
     // this CTA's share of the line
-    int64_t chunk;
+    int chunk;
     const PaCur cur = pa_share(A, MT, kPtOver, lane, chunk);
     if (threadIdx.x == 0) A.ws_join[blockIdx.x].last = -1;
 

@@ -8,7 +8,7 @@
 #include "../../include/dflash.h"
 #include "common.cuh"
 #include "kernels.cuh"
-#include "paged.cuh"
+#include "paged_attn.cuh"
 
 using namespace dflash;
 
@@ -204,6 +204,8 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_r
     if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(DFLASH_EINVAL, "scale %g", (double)scale);
     if (window < 0 || window > 1 << 30) return fail(DFLASH_EINVAL, "window %d", window);
     if (!al4(lse)) return fail(DFLASH_EINVAL, "lse needs 4-byte alignment");
+    if (!pa_line_fits(R, q->heads, cache->kv_heads))
+        return fail(DFLASH_EINVAL, "%d sequences of %d positions: too many tiles of keys", R.n_seqs, R.cap);
     if (R.n_rows == 0) return DFLASH_OK;
     int n = 0;
     TRY(sms(&n));

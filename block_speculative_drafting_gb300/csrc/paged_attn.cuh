@@ -54,59 +54,65 @@ DF_DEV PaSeq pa_seq(const PaArgs& A, int s, int mt) {
 // each unit led by `ov` places without a tile, which stand for what it costs a
 // CTA to end one unit and begin another, so that shares of equal length take
 // equal time.  ov is 0 where most CTAs hold a tile or two: there a place
-// without a tile would be an idle CTA.
+// without a tile would be an idle CTA.  (The line is shorter than 2^31: pa_line_fits.)
 struct PaCur {
     PaSeq q;
     int s, u, tile;  // tile `tile` of unit `u` of sequence `s`
     int ov;
-    int64_t left;  // places of the CTA's share from here on (0: none)
+    int left;  // places of the CTA's share from here on (0: none)
 };
 // This CTA's share (warp-wide); `chunk`: the places of a share.
-DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int64_t& chunk) {
-    int64_t tiles = 0, units = 0, w0 = 0, u0 = 0;
+DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
+    int64_t t64 = 0, v64 = 0;
+    int w0 = 0, u0 = 0;
     for (int s = lane; s < A.R.n_seqs; s += 32) {
         const PaSeq q = pa_seq(A, s, mt);
         const int64_t w = (int64_t)q.ntiles * q.nunits;
-        if (s < 32) w0 = w, u0 = q.nunits;
-        tiles += w;
-        units += q.nunits;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-        units += __shfl_xor_sync(0xffffffffu, units, o);
+        if (s < 32) w0 = (int)w, u0 = q.nunits;
+        t64 = min(t64 + w, 1ll << 40);
+        v64 = min(v64 + q.nunits, 1ll << 40);
     }
     PaCur c{};
-    c.ov = tiles > 2 * (int64_t)gridDim.x ? ovh : 0;
-    const int64_t total = tiles + c.ov * units;
-    chunk = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t t = (int64_t)blockIdx.x * chunk;
-    if (t >= total) return c;
-    int64_t run = 0;
+    chunk = 1;
+    // (row starts out of order can give sequences the same rows many times over: such a line has no end worth walking)
+    auto sum = [](int64_t x) {
+        return ((int64_t)__reduce_add_sync(0xffffffffu, (unsigned)(x >> 20)) << 20) +
+               __reduce_add_sync(0xffffffffu, (unsigned)(x & 0xfffff));
+    };
+    t64 = sum(t64);
+    v64 = sum(v64);
+    if (t64 + ovh * v64 >= 1ll << 31) return c;
+    const int tiles = (int)t64, units = (int)v64;
+    c.ov = tiles > 2 * (int)gridDim.x ? ovh : 0;
+    const int total = tiles + c.ov * units, grid = (int)gridDim.x;
+    chunk = total / grid + (total % grid != 0);
+    if ((int64_t)blockIdx.x * chunk >= total) return c;
+    const int t = (int)blockIdx.x * chunk;
+    int run = 0;
     for (int s0 = 0; s0 < A.R.n_seqs; s0 += 32) {
-        int64_t w = s0 == 0 ? w0 + c.ov * u0 : 0;
+        int w = s0 == 0 ? w0 + c.ov * u0 : 0;
         if (s0 > 0 && s0 + lane < A.R.n_seqs) {
             const PaSeq q = pa_seq(A, s0 + lane, mt);
-            w = (int64_t)(q.ntiles + c.ov) * q.nunits;
+            w = (q.ntiles + c.ov) * q.nunits;
         }
-        int64_t in = w;
+        int in = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, in, o);
+            const int y = __shfl_up_sync(0xffffffffu, in, o);
             if (lane >= o) in += y;
         }
         const uint32_t hit = __ballot_sync(0xffffffffu, run + in > t);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            const int64_t x = t - (run + __shfl_sync(0xffffffffu, in - w, l));
+            const int x = t - (run + __shfl_sync(0xffffffffu, in - w, l));
             c.s = s0 + l;
             c.q = pa_seq(A, c.s, mt);
             const int per = c.q.ntiles + c.ov;
-            c.u = (int)(x / per);
-            const int v = (int)(x - (int64_t)c.u * per);
+            c.u = x / per;
+            const int v = x - c.u * per;
             c.left = min(chunk, total - t);
             if (v < c.ov)
-                c.left = max(c.left - (c.ov - v), (int64_t)0);
+                c.left = max(c.left - (c.ov - v), 0);
             else
                 c.tile = v - c.ov;
             return c;
@@ -135,7 +141,7 @@ DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c) {
     } while (c.q.nunits == 0);
 }
 // The entry of a unit that begins in this CTA's share and has `rest` tiles after it.
-DF_DEV PaJoin pa_join_entry(const PaCur& c, int rt, int mt, int rows, int head, int rest, int64_t chunk) {
+DF_DEV PaJoin pa_join_entry(const PaCur& c, int rt, int mt, int rows, int head, int rest, int chunk) {
     PaJoin e{};
     e.last = (int)(blockIdx.x + (rest + chunk - 1) / chunk);
     e.row0 = c.q.row0;
@@ -190,6 +196,11 @@ DF_DEV float2 unpack2(uint32_t u) {
         return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
+// Whether the places of any line of such a call stay below 2^31.
+inline bool pa_line_fits(const PagedRows& R, int heads, int kv_heads) {
+    const double units = (double)R.n_rows * heads / 16 + (double)R.n_seqs * kv_heads;
+    return units * ((double)R.cap / kPaTile + 8) < 2147483648.0;
+}
 // The tcgen05 kernel (k_paged_attn_tc.cu): units of up to mt = 64 or 128 rows.
 int paged_attention_tc(const PaArgs& A, int cache_dtype, int hd, int mt, int num_sms, cudaStream_t st);
 

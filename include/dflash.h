@@ -596,7 +596,7 @@ DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash
  * values already): row at position p, query head h, key/value head h /
  * (heads / kv_heads):
  *   out = sum_j softmax_j(scale * q . k_j) v_j over the held positions j <= p
- *         (window w > 0: and j > p - w)
+ *         (window w > 0, up to 2^30: and j > p - w)
  *   lse = ln sum_j exp(scale * q . k_j)          f32 [n_rows][heads], or NULL
  * A row that sees nothing gets out = 0 and lse = -inf.  What positions outside
  * a row's view hold (infinities, NaN, freed pages) does not reach it.  q and
@@ -604,7 +604,9 @@ DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash
  * workspace: at least dflash_paged_attention_workspace bytes of device
  * memory, 16-byte aligned, needing no initial contents; calls that may
  * overlap need one each.
- * Errors: EINVAL, EGEOM, ECAPACITY (workspace too small), ECUDA.
+ * Errors: EINVAL (also where sequences x heads x positions of the table come
+ * to more than 2^31 tiles of 128 keys), EGEOM, ECAPACITY (workspace too small),
+ * ECUDA.
  */
 DFLASH_API int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_rows* rows,
                                       const dflash_head_rows* q, const dflash_head_rows* out, float* lse, float scale,

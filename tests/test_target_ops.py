@@ -132,6 +132,9 @@ def test_paged_attention_refuses_bad_arguments(lib):
                 dict(lse=4097), dict(out=_head_struct(2)), dict(q=_head_struct(5), out=_head_struct(5))]:
         assert call(**bad) == _abi.DFLASH_EINVAL, bad
     assert call(r=_rows_struct(n_rows=0)) == 0
+    # more tiles of keys than a 32-bit count: 2^16 sequences of 2^31 - 2^17 positions
+    wide = dict(n_seqs=1 << 16, n_rows=1 << 16, max_pages=(1 << 27) - (1 << 13), table_stride=1 << 27)
+    assert call(r=_rows_struct(**wide)) == _abi.DFLASH_EINVAL
 
 
 def test_verify_refuses_bad_arguments(lib):
