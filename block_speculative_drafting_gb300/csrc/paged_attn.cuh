@@ -69,8 +69,8 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
         const PaSeq q = pa_seq(A, s, mt);
         const int64_t w = (int64_t)q.ntiles * q.nunits;
         if (s < 32) w0 = (int)w, u0 = q.nunits;
-        t64 = min(t64 + w, 1ll << 40);
-        v64 = min(v64 + q.nunits, 1ll << 40);
+        t64 = min(t64 + w, (int64_t)1 << 40);
+        v64 = min(v64 + q.nunits, (int64_t)1 << 40);
     }
     PaCur c{};
     chunk = 1;
