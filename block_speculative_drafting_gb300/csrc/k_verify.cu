@@ -511,7 +511,7 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), s = blockIdx.x / kVpCluster;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // the inputs are final before the statistics kernel lets this one start
+    pdl_wait();
     int a, b;
     draft_range(A, s, a, b);
     const int d = b - a;
@@ -534,7 +534,6 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
                     l = side ? __ldg(A.draft + (int64_t)(a + i) * A.draft_stride + x)
                              : logit_at(A.target, A.target_dtype, (row0 + i) * A.target_stride + x);
             }
-            pdl_wait();
             if (side && i == d) continue;
             const VerifyStat t = row_stat(P, side ? nt + a + i : row0 + i, c, lane);
             if (lane == 0) {
@@ -567,7 +566,6 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
         __syncthreads();
         if (i0 + 32 > d) break;
     }
-    pdl_wait();
     const int acc = min(refused, d);
     const int64_t row = row0 + acc;
     const VerifyStat t = acc >= i0 ? stat[0][acc - i0] : row_stat(P, row, c, lane);
