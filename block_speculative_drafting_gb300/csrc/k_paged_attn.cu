@@ -112,11 +112,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
     auto look = [&](const PaCur& c) -> Look {
         Look k{-1, 0, c.u % A.C.kv_heads};
         const int key = c.q.lo + c.tile * kPaTile + warp * kPaKeys + (lane & 15);
-        if (key >= 0 && key < c.q.hi) {
-            const int idx = div_by(A.R.page, key);
-            k.slot = key - idx * A.R.page.d;
-            k.id = A.R.table[(int64_t)c.s * A.R.table_stride + idx];
-        }
+        if (key < c.q.hi) k.id = page_entry(A.R, c.s, key, k.slot);
         return k;
     };
     const unsigned char* tensor = lane < 16 ? A.C.k : A.C.v;
@@ -128,7 +124,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
         if (put.left > 0) {
             const uint32_t st = base + stage_put * S::kStage;
             const unsigned char* now =
-                ahead.id < 0 || ahead.id >= A.C.n_pages ? nullptr : tensor + ahead.id * sp + ahead.slot * ss + ahead.h * sh;
+                page_held(ahead.id, A.C.n_pages) ? tensor + ahead.id * sp + ahead.slot * ss + ahead.h * sh : nullptr;
             const uint32_t bits = __ballot_sync(0xffffffffu, now != nullptr) & 0xffffu;
             if (lane == 0) vbits[warp][stage_put] = bits;
             pa_next(A, MT, put);
@@ -139,7 +135,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
                 const int r = i * RPI + lane / CH, c = lane % CH;
                 const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(now), r);
                 const uint32_t dst = st + (r >> 4) * (kPaKeys * S::RB) + pa_off<CH>(r & 15, c);
-                const void* src = p ? reinterpret_cast<const unsigned char*>(p) + 16 * c : A.C.k;
+                const void* src = p ? reinterpret_cast<const unsigned char*>(p) + 16 * c : A.q.p;  // (nothing is read)
                 cp16(dst, src, p ? 16 : 0);
             }
             stage_put = stage_put + 1 == NST ? 0 : stage_put + 1;

@@ -24,12 +24,11 @@
 //
 // Warps: 0-3 softmax and epilogue, 4 the scores' MMAs, 5 the values', 6-9 load
 // keys, 10-13 values, each into a ring of slots, one tile each, in the 128-byte
-// swizzle.  16-bit loaders copy 16-byte
-// chunks asynchronously (the slot's barrier counts them as they land); e4m3
-// loaders copy codes to places of their own and write their f16 values (exact)
-// into the slots.  The MMA warps order those writes before their reads of them (a proxy
-// fence after the barrier).  The
-// page of a key is looked up a tile before it is needed.
+// swizzle.  16-bit loaders copy 16-byte chunks asynchronously (the slot's
+// barrier counts them as they land); e4m3 loaders copy codes to places of their
+// own and write their f16 values (exact) into the slots.  The MMA warps order
+// those writes before their reads of them (a proxy fence after the barrier).
+// The page of a key is looked up a tile before it is needed.
 //
 // Keys that no row sees are zeros behind a bit mask; keys that only some rows
 // see are masked a row at a time, and where such a tile's values are not all
@@ -205,16 +204,12 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
             k.h = c.u % A.C.kv_heads;
             k.id = -1;
             k.slot = 0;
-            if (key >= 0 && key < c.q.hi) {
-                const int idx = div_by(A.R.page, key);
-                k.slot = key - idx * A.R.page.d;
-                k.id = A.R.table[(int64_t)c.s * A.R.table_stride + idx];
-            }
+            if (key < c.q.hi) k.id = page_entry(A.R, c.s, key, k.slot);
             return k;
         };
         auto wait_empty = [&](int tile) -> bool {
             return tile < S::kSlots ||
-                   mbar_wait(&ctl.empty[side][tile % S::kSlots], ((tile / S::kSlots) - 1) & 1, kPtWait);
+                   __all_sync(0xffffffffu, mbar_wait(&ctl.empty[side][tile % S::kSlots], ((tile / S::kSlots) - 1) & 1, kPtWait));
         };
         // the tiles in order: emit(row) is called with a lane's key's row (null: not held)
         auto walk = [&](auto emit) {
@@ -222,9 +217,9 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
             Look ahead{-1, 0, 0};
             if (c.left > 0) ahead = look(c);
             while (c.left > 0) {
-                const unsigned char* row = ahead.id < 0 || ahead.id >= A.C.n_pages
-                                               ? nullptr
-                                               : tensor + ahead.id * sp + ahead.slot * ss + ahead.h * sh;
+                const unsigned char* row = page_held(ahead.id, A.C.n_pages)
+                                               ? tensor + ahead.id * sp + ahead.slot * ss + ahead.h * sh
+                                               : nullptr;
                 if (side == 0) {
                     const uint32_t b = __ballot_sync(0xffffffffu, row != nullptr);
                     if (lane == 0) ctl.bits[n % kPtBits][lw] = b;
@@ -243,7 +238,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                 for (int i = 0; i < S::KPW / RPI; ++i) {
                     const int r = i * RPI + lane / CH, ch = lane % CH;
                     const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(rows), r);
-                    const void* src = p ? reinterpret_cast<const unsigned char*>(p) + 16 * ch : A.C.k;
+                    const void* src = p ? reinterpret_cast<const unsigned char*>(p) + 16 * ch : A.q.p;  // (nothing is read)
                     cp16(dst + (ch >> 3) * (kPaTile * 128) + at_swz(lw * S::KPW + r, ch & 7), src, p ? 16 : 0);
                 }
                 // arrives once this thread's copies have landed
@@ -291,7 +286,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                     for (int i = 0; i < LD; ++i) {
                         const int r = (hf * LD + i) * RPI + lane / CH;
                         const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(rows), r);
-                        const void* src = p ? reinterpret_cast<const unsigned char*>(p) + 16 * ch : A.C.k;
+                        const void* src = p ? reinterpret_cast<const unsigned char*>(p) + 16 * ch : A.q.p;  // (nothing is read)
                         cp16(smem_addr(raw) + ((half % S::kRaw) * LD + i) * kPlace, src, p ? 16 : 0);
                     }
                     cp_commit();

@@ -27,7 +27,13 @@ inline FastDiv fast_div(int d) {
     while ((1ull << s) < (uint64_t)d) ++s;
     return {(uint32_t)((((1ull << s) - (uint64_t)d) << 32) / (uint64_t)d + 1), s, d};
 }
-DF_DEV int div_by(const FastDiv& f, int n) { return (int)((__umulhi((uint32_t)n, f.mul) + (uint32_t)n) >> f.shift); }
+// (the walk from rows to pages also runs on the host, for its tests)
+#define DF_HD __host__ __device__ __forceinline__
+DF_HD int lowest(int a, int b) { return a < b ? a : b; }
+DF_HD int highest(int a, int b) { return a > b ? a : b; }
+DF_HD int div_by(const FastDiv& f, int n) {
+    return (int)(((uint32_t)(((uint64_t)(uint32_t)n * f.mul) >> 32) + (uint32_t)n) >> f.shift);
+}
 
 struct PagedCache {
     unsigned char *k, *v;
@@ -50,17 +56,17 @@ struct HeadRows {
 };
 
 // Rows [a, b) of sequence s, inside [0, n_rows] whatever the array holds.
-DF_DEV void rows_of(const PagedRows& R, int s, int& a, int& b) {
+DF_HD void rows_of(const PagedRows& R, int s, int& a, int& b) {
     if (R.row_start == nullptr) {
         a = s * R.per;
         b = a + R.per;
     } else {
-        a = min(max(R.row_start[s], 0), R.n_rows);
-        b = min(max(R.row_start[s + 1], a), R.n_rows);
+        a = lowest(highest(R.row_start[s], 0), R.n_rows);
+        b = lowest(highest(R.row_start[s + 1], a), R.n_rows);
     }
 }
 // The sequence that holds row r, or -1: the last whose start is at most r.
-DF_DEV int seq_of(const PagedRows& R, int r) {
+DF_HD int seq_of(const PagedRows& R, int r) {
     if (R.row_start == nullptr) return R.per > 0 ? r / R.per : -1;
     int lo = 0, hi = R.n_seqs;  // row_start[lo] <= r is not known for lo = 0
     while (hi - lo > 1) {
@@ -74,13 +80,19 @@ DF_DEV int seq_of(const PagedRows& R, int r) {
     rows_of(R, lo, a, b);
     return r >= a && r < b ? lo : -1;
 }
-// The page of position p of sequence s, or -1 where it is not held.
-DF_DEV int64_t page_of(const PagedRows& R, int64_t n_pages, int s, int p, int& slot) {
+// The table's entry for position p of sequence s, -1 outside the table.
+DF_HD int page_entry(const PagedRows& R, int s, int p, int& slot) {
+    slot = 0;
     if (p < 0 || p >= R.cap) return -1;
     const int idx = div_by(R.page, p);
     slot = p - idx * R.page.d;
-    const int64_t id = R.table[(int64_t)s * R.table_stride + idx];
-    return id >= 0 && id < n_pages ? id : -1;
+    return R.table[(int64_t)s * R.table_stride + idx];
+}
+DF_HD bool page_held(int id, int64_t n_pages) { return id >= 0 && id < n_pages; }
+// The page of position p of sequence s, or -1 where it is not held.
+DF_HD int64_t page_of(const PagedRows& R, int64_t n_pages, int s, int p, int& slot) {
+    const int id = page_entry(R, s, p, slot);
+    return page_held(id, n_pages) ? id : -1;
 }
 
 // ---- launchers (0 = queued fine, else a cudaError_t)

@@ -188,7 +188,8 @@ def verify_drafts(target_logits, draft_tokens, accept_u, sample_u, *, draft_logi
     temperature    float32 [sequences], 0: greedy; None: 1 for all
     A draft stays while accept_u * q(draft) < p(draft); the next token comes from max(p - q, 0) of the first refused
     draft's row, or from p of the last row, at the running sum that passes sample_u.  prob is min(1, p / q).  A row
-    without any probability yields token -1.  Sequences are refused or served alike: include/dflash.h, dflash_verify.
+    without any probability yields token -1.  Outputs and workspace may be given (`verify_workspace`); masked logits,
+    drafts outside the vocabulary and bad starts: include/dflash.h, dflash_verify.
     """
     if torch is None:
         _init()

@@ -112,7 +112,8 @@ def test_paged_append_refuses_bad_arguments(lib):
     calls = [dict(c=None), dict(r=None), dict(k=None), dict(v=None), dict(qo=None), dict(q=None),
              dict(k=_head_struct(3)), dict(v=_head_struct(2, data=4104)), dict(k=_head_struct(2, row_stride=130)),
              dict(q=_head_struct(3), qo=_head_struct(3)), dict(qo=_head_struct(6)), dict(qo=_head_struct(4, dtype=2)),
-             dict(q=_head_struct(4, dtype=3)), dict(qn=4100), dict(kn=4096, eps=-1.0), dict(kn=4096, eps=float("nan"))]
+             dict(q=_head_struct(4, dtype=3)), dict(v=_head_struct(2, dtype=2)), dict(qn=4100), dict(kn=4096, eps=-1.0),
+             dict(kn=4096, eps=float("nan"))]
     for bad in calls + [dict(rot=x) for x in bad_rot]:
         assert call(**bad) == _abi.DFLASH_EINVAL, bad
     assert call(r=_rows_struct(n_rows=0)) == 0  # nothing to do, nothing launched
@@ -603,6 +604,47 @@ def test_attention_offsets_past_32_bits():
     assert np.array_equal(c[ids[498 // 64] - (n_pages - 8), 498 % 64], f64(k)[0])
     ref, _, mag, _ = O.paged_attention(f64(q), c, c, [list(ids - (n_pages - 8))], [500])
     assert (np.abs(f64(out) - ref) <= HALF["bf16"] * np.abs(ref) + 1e-4 * mag).all()
+
+
+@gpu
+def test_attention_many_heads_of_one_and_an_empty_cache():
+    # more query heads of a key/value head than rows of any tile
+    _check_attention("bf16", heads=160, kvh=1, rows=(1, 1), lens=(70, 300), uniform=True)
+    _check_attention("e4m3", "f16", hd=64, heads=200, kvh=1, rows=(2,), lens=(129,), uniform=True)
+    torch, dfl = _torch(), _dfl()
+    for heads in (4, 40):  # no page at all
+        kc = torch.empty(0, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+        q = torch.ones(2, heads, 64, dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros(2, heads, device="cuda")
+        for table in ([[0, -1], [5, 2 ** 31 - 1]], [[], []]):
+            t = torch.tensor(table, dtype=torch.int32, device="cuda")
+            out = dfl.paged_attention(q, kc, kc, t, _i32(torch, [20, 0]), lse=lse)
+            assert (out == 0).all() and (lse == -float("inf")).all()
+            dfl.paged_append(kc, kc, q[:, :2], q[:, :2], t, _i32(torch, [20, 0]))
+
+
+@gpu
+def test_passes_on_two_streams_at_once():
+    torch, dfl = _torch(), _dfl()
+    states = [_pass_state(torch, dfl, seed) for seed in (1, 2)]
+    want = [_pass(dfl, st) for st in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    for _ in range(30):
+        got = []
+        for st, s in zip(states, streams):
+            with torch.cuda.stream(s):
+                got.append(_pass(dfl, st))
+        torch.cuda.synchronize()
+        for (y, v), (y2, v2) in zip(want, got):
+            assert torch.equal(y, y2) and all(torch.equal(a, b) for a, b in zip(v, v2))
+    # a stream by its handle, the default one's included
+    for handle in (streams[0].cuda_stream, 0, torch.cuda.default_stream().cuda_stream):
+        y = dfl.paged_attention(states[0]["q"], states[0]["kc"], states[0]["vc"], states[0]["table"], states[0]["lens"],
+                                row_start=states[0]["start"], stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(y, dfl.paged_attention(states[0]["q"], states[0]["kc"], states[0]["vc"], states[0]["table"],
+                                                  states[0]["lens"], row_start=states[0]["start"]))
 
 
 @gpu
