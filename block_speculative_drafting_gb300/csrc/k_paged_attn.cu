@@ -296,11 +296,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
                     mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
                     mx[e] *= c[e];
                 }
-                const bool move = mx[0] > m[0] + kPaLazy || mx[1] > m[1] + kPaLazy;
+                constexpr float under = kPaUnder<BF && !E8>;
+                const bool move = mx[0] > m[0] + (kPaLazy + under) || mx[1] > m[1] + (kPaLazy + under);
                 if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float to = mx[e] > m[e] + kPaLazy ? mx[e] : m[e];
+                        const float to = mx[e] > m[e] + (kPaLazy + under) ? mx[e] - under : m[e];
                         const float f = to == m[e] ? 1.f : pa_exp2(m[e] - to);
                         m[e] = to;
                         l[e] *= f;

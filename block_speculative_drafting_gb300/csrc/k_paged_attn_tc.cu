@@ -8,8 +8,8 @@
 // owns the row's tensor-memory lane, written over S as the A operand of
 // O += P V (V as stored, the MN-major B operand; O in tensor memory).  Two S
 // buffers: the next tile's scores are multiplied while this tile's softmax
-// runs.  m moves only where a row's maximum passes it by kPaLazy; O is then
-// rescaled in place.  A 16-bit cache's P is a hi + lo pair (the products then
+// runs.  m moves only where a row's maximum passes it by some powers of two; O
+// is then rescaled in place.  A 16-bit cache's P is a hi + lo pair (the products then
 // add no rounding of their own to the output's; the tensor pipe has the time:
 // a tile's MMAs take 0.8 us, its 64 KB 1.4 us of this SM's share of the
 // memory); an e4m3 cache's, whose tile is half the bytes, is one f16 (2^-12
@@ -501,8 +501,9 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                     }
                     mx *= cs;
                 }
-                if (__any_sync(0xffffffffu, mx > m + kPaLazy)) {
-                    const float to = mx > m + kPaLazy ? mx : m;
+                constexpr float under = kPaUnder<PB>;
+                if (__any_sync(0xffffffffu, mx > m + (kPaLazy + under))) {
+                    const float to = mx > m + (kPaLazy + under) ? mx - under : m;
                     const float f = to == m ? 1.f : pa_exp2(m - to);
                     m = to;
                     l *= f;

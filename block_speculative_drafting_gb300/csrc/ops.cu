@@ -201,6 +201,8 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_r
     TRY(check_heads(out, "out", q->heads, 1, R.n_rows, &O));
     if (q->dtype == DFLASH_F32 || out->dtype != q->dtype || (cache->dtype != DFLASH_E4M3 && q->dtype != cache->dtype))
         return fail(DFLASH_EINVAL, "q and out need the cache's type (BF16 or F16 for an E4M3 cache)");
+    if (q->data == out->data && R.n_rows > 0 && (q->row_stride != out->row_stride || q->head_stride != out->head_stride))
+        return fail(DFLASH_EINVAL, "out in q's place needs q's strides");
     if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(DFLASH_EINVAL, "scale %g", (double)scale);
     if (window < 0 || window > 1 << 30) return fail(DFLASH_EINVAL, "window %d", window);
     if (!al4(lse)) return fail(DFLASH_EINVAL, "lse needs 4-byte alignment");

@@ -8,7 +8,12 @@
 namespace dflash {
 
 constexpr int kPaTile = 128;     // keys a CTA takes at once: 16 a warp
-constexpr float kPaLazy = 8.f;   // log2 units a score may pass the reference before a rescale
+// A row's reference m: its largest score in log2 units less kPaUnder when m is set, moved only where a score passes
+// that by more than kPaLazy.  P = 2^(score - m) in f16 loses bits below 2^-14: set 7 under the maximum (P is then at
+// most 2^15) it loses none that weigh 2^-21 of the largest.  (bf16 has f32's exponents, and values near f32's end.)
+template <bool BF>
+constexpr float kPaUnder = BF ? 0.f : 7.f;
+constexpr float kPaLazy = 8.f;
 
 struct PaArgs {
     PagedCache C;

@@ -145,6 +145,7 @@ def paged_attention(q, k_cache, v_cache, table, kv_len, *, row_start=None, scale
                reads key/value head h / (heads / kv_heads)
     scale      of the scores; None: head_dim ** -0.5
     window     > 0: the row at position p sees the positions p - window + 1 .. p; 0: all up to p
+    out        where the result goes (default: a new tensor like q; q itself is allowed)
     lse        float32 [rows][heads] to fill with ln sum exp of the row's scores (-inf: the row sees nothing)
     workspace  uint8 tensor of `paged_attention_workspace` bytes for callers that may not allocate (calls that may
                overlap need one each); None: allocated for the call

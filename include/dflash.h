@@ -508,8 +508,8 @@ DFLASH_API int dflash_attention_noalloc(dflash_model* model, dflash_seq* const* 
  * Rules (EINVAL / EGEOM): dtype DFLASH_BF16, DFLASH_F16 or DFLASH_E4M3;
  * head_dim 64 or 128; kv_heads >= 1; page_size 1 .. 65536; n_pages >= 0; bases
  * and strides multiples of 16 bytes, strides >= 0.
- * k_scale, v_scale (E4M3 only, both or neither; NULL: 1): one positive f32 a
- * head on the device; an element is its code times the head's scale.
+ * k_scale, v_scale (E4M3 only, both or neither; NULL: 1): one positive, normal
+ * f32 a head on the device; an element is its code times the head's scale.
  */
 typedef struct {
     void* k;
@@ -581,9 +581,9 @@ typedef struct {
  * norm(x) = x / sqrt(mean(x^2) + eps) * gain over a head, with f32 gains
  * q_norm, k_norm [head_dim] on the device (NULL: no norm).  rotation NULL: no
  * rotation.  q NULL: keys and values alone.  q, k and v have one type; q_out
- * may be q itself, or of another type.  A row whose position is not held is not written to the
- * cache (its q' is written).  A table that maps two of the call's rows to one
- * slot leaves either row's elements there.
+ * may be q itself, or of another type.  A row whose position is not held is
+ * not written to the cache (its q' is written).  A table that maps two of the
+ * call's rows to one slot leaves either row's elements there.
  * Errors: EINVAL, EGEOM, ECUDA.
  */
 DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_rows* rows,
@@ -600,7 +600,8 @@ DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash
  *   lse = ln sum_j exp(scale * q . k_j)          f32 [n_rows][heads], or NULL
  * A row that sees nothing gets out = 0 and lse = -inf.  What positions outside
  * a row's view hold (infinities, NaN, freed pages) does not reach it.  q and
- * out have one type: the cache's, or BF16 / F16 for an E4M3 cache.
+ * out have one type: the cache's, or BF16 / F16 for an E4M3 cache; out may be
+ * q itself.
  * workspace: at least dflash_paged_attention_workspace bytes of device
  * memory, 16-byte aligned, needing no initial contents; calls that may
  * overlap need one each.

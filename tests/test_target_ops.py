@@ -607,6 +607,45 @@ def test_attention_offsets_past_32_bits():
 
 
 @gpu
+@pytest.mark.parametrize("kind,src", [("bf16", "bf16"), ("f16", "f16"), ("e4m3", "f16"), ("e4m3", "bf16")])
+@pytest.mark.parametrize("rows", [1, 6, 20])
+def test_attention_small_weights_in_sum(kind, src, rows):
+    """One key far above thousands of equal ones that carry all of the output: weights of 2^-17.6, which a 16-bit float
+    with five exponent bits holds to 7 bits alone, still come to their sum."""
+    torch, dfl = _torch(), _dfl()
+    T = _types()
+    n, hd, heads = 4096, 64, 4
+    q = torch.zeros(rows, heads, hd, device="cuda", dtype=T[src])
+    q[:, :, 3] = 1.0
+    kc = torch.zeros(n // 16, 16, 1, hd, device="cuda")
+    kc[0, 0, 0, 3] = 16.0
+    vc = 1.0 + torch.arange(hd, device="cuda").float().remainder(8).expand(n // 16, 16, 1, hd) / 8
+    vc = vc.clone()
+    vc[0, 0] = 0.0
+    kc, vc = kc.to(T[kind]), vc.to(T[kind])
+    table, scale = torch.arange(n // 16, device="cuda", dtype=torch.int32)[None], 12.2107 / 16
+    out = dfl.paged_attention(q, kc, vc, table, _i32(torch, [n]), scale=scale)
+    ref, _, mag, _ = O.paged_attention(f64(q), f64(kc), f64(vc), table.tolist(), [n], None, scale, 0)
+    # scores: one product (exact), scaled: 2^-23 of 17.6 twice at most; one f16 P: half a step of it
+    one_p = kind == "e4m3" and rows * heads > 16
+    p_err = 2.0 ** -22 * 18 + 2.0 ** -20 + (HALF["f16"] if one_p else 0.0)
+    assert (np.abs(f64(out) - ref) <= HALF[src] * np.abs(ref) + 2 * p_err * mag).all()
+
+
+@gpu
+def test_attention_out_in_place_of_q():
+    torch, dfl = _torch(), _dfl()
+    for heads in (4, 32):  # the warps' kernel, and the tensor memory's
+        q = torch.randn(9, heads, 64, device="cuda", dtype=torch.bfloat16)
+        kc, vc = (torch.randn(30, 16, 2, 64, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+        args = (kc, vc, torch.arange(30, device="cuda", dtype=torch.int32).reshape(3, 10), _i32(torch, [160, 3, 77]))
+        want = dfl.paged_attention(q, *args)
+        assert dfl.paged_attention(q, *args, out=q) is q and torch.equal(q, want)
+        with pytest.raises(dfl.DFlashError, match="strides"):
+            dfl.paged_attention(q, *args, out=q.flatten().as_strided((9, heads, 64), (64, 9 * 64, 1)))
+
+
+@gpu
 def test_attention_many_heads_of_one_and_an_empty_cache():
     # more query heads of a key/value head than rows of any tile
     _check_attention("bf16", heads=160, kvh=1, rows=(1, 1), lens=(70, 300), uniform=True)
