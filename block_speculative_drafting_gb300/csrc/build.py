@@ -1,14 +1,16 @@
-"""Build libdflash.so for sm_103a with nvcc (no cmake, no torch extension).
+"""Build libdflash.so for sm_103a with nvcc (no cmake, no torch in it).
 
 Usage: python -m block_speculative_drafting_gb300.csrc.build [--verbose]
 Each .cu compiles on its own thread; the objects link into
 block_speculative_drafting_gb300/libdflash.so (CUDA runtime linked
-statically, so the library loads without a GPU).  binding.c, the compiled half
-of target.py, becomes a Python extension beside it.
+statically, so the library loads without a GPU).  binding.cpp, the compiled half
+of target.py, becomes a Python extension beside it, against the installed torch.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -61,13 +63,17 @@ def build(verbose: bool = False, force: bool = False) -> str:
         return obj
 
     def compile_binding() -> None:
-        src = os.path.join(HERE, "binding.c")
+        src = os.path.join(HERE, "binding.cpp")
         if force or _needs(BINDING, [src] + headers):
-            cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", sysconfig.get_path("include"), src, "-o",
-                   BINDING]
+            torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+            cuda = os.path.dirname(os.path.dirname(shutil.which(nvcc()) or "/usr/local/cuda/bin/nvcc"))
+            cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+                   "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(cuda, "include"),
+                   "-isystem", sysconfig.get_path("include"), src, "-o", BINDING, "-L" + os.path.join(torch, "lib"),
+                   "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath," + os.path.join(torch, "lib")]
             r = subprocess.run(cmd, capture_output=True, text=True)
             if r.returncode != 0:
-                raise RuntimeError(f"{cmd[0]} failed on binding.c:\n{r.stdout}\n{r.stderr}")
+                raise RuntimeError(f"{cmd[0]} failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
 
     with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
         bound = ex.submit(compile_binding)

@@ -13,7 +13,6 @@ be captured into a CUDA graph; outputs and workspaces that it allocates then bel
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import math
 
@@ -21,12 +20,12 @@ import numpy as np
 
 from . import _abi
 
-torch = _binding = _current_device = None
+torch = _binding = None
 
 
 def _init():
-    """torch, the library and the compiled half of this module (csrc/binding.c), on the first call."""
-    global torch, _binding, _current_device
+    """torch, the library and the compiled half of this module (csrc/binding.cpp), on the first call."""
+    global torch, _binding
     import torch as t
 
     from . import DFlashError, lib
@@ -38,16 +37,8 @@ def _init():
     L = lib()
     names = ("dflash_paged_append", "dflash_paged_attention", "dflash_paged_attention_workspace", "dflash_verify",
              "dflash_verify_workspace", "dflash_last_error")
-    # torch's own short ways, where it has them: every operator call costs microseconds here
-    raw = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda d: t.cuda.current_stream(d).cuda_stream)
-    alloc = getattr(t._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
-    free = getattr(t._C, "_cuda_cudaCachingAllocator_raw_delete", None)
-    if alloc is None or free is None:
-        alloc, free = (lambda n, s: t.cuda.caching_allocator_alloc(n, None, s)), t.cuda.caching_allocator_delete
-    b.init(tuple(C.cast(getattr(L, n), C.c_void_p).value for n in names),
-           (t.float32, t.bfloat16, t.float16, t.float8_e4m3fn, t.float64, t.int32, t.uint32), DFlashError, t.empty_like, raw,
-           alloc, free)
-    _current_device = t.cuda.current_device
+    b.init(tuple(C.cast(getattr(L, n), C.c_void_p).value for n in names), DFlashError,
+           t.cuda.OutOfMemoryError)
     torch, _binding = t, b
 
 
@@ -56,21 +47,6 @@ def _check(rc: int) -> int:
         from . import DFlashError, lib
         raise DFlashError(rc, lib().dflash_last_error(None).decode())
     return rc
-
-
-@contextlib.contextmanager
-def _at(dev: int, stream):
-    """The call's device and stream made current.  (What a call allocates belongs to the stream that is current, so
-    that it is not dealt out again before that stream is done with it.)"""
-    if dev < 0:
-        from . import DFlashError
-        raise DFlashError(_abi.DFLASH_EINVAL, "tensors have to be on a CUDA device")
-    with torch.cuda.device(dev):
-        if stream is None:
-            yield
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev)):
-                yield
 
 
 def rope_inv_freq(rotary: int, theta: float = 1e6, scaling: str | None = None, factor: float = 1.0,
@@ -120,20 +96,15 @@ def paged_append(k_cache, v_cache, k, v, table, kv_len, *, row_start=None, q=Non
     kv_len            int32 [sequences]: tokens in each sequence's cache with its new rows in; row i of its r rows
                       stands at position kv_len - r + i
     row_start         int32 [sequences + 1]: each sequence's rows; None: equally many
-    q_out             where the queries go (default: a new tensor like q; q itself is allowed)
+    q_out             where the queries go (default: a new, contiguous tensor of q's shape and type; q itself is allowed)
     inv_freq          float64 [rotary / 2] (`rope_inv_freq`); None: no rotation.  Pairs are columns (i, i + rotary/2),
                       or (2i, 2i + 1) when interleaved; columns from `rotary` on stay
     q_norm, k_norm    float32 [head_dim] gains of an RMS norm before the rotation; None: none
     """
     if torch is None:
         _init()
-    args = (k_cache, v_cache, k, v, table, kv_len, row_start, q, q_out, inv_freq, interleaved, rope_scale, q_norm, k_norm,
-            eps, k_scale, v_scale)
-    dev = k_cache.get_device()
-    if stream is not None or dev < 0 or dev != _current_device():
-        with _at(dev, stream):
-            return _binding.paged_append(*args)
-    return _binding.paged_append(*args)
+    return _binding.paged_append(k_cache, v_cache, k, v, table, kv_len, row_start, q, q_out, inv_freq, interleaved,
+                                 rope_scale, q_norm, k_norm, eps, k_scale, v_scale, stream)
 
 
 def paged_attention(q, k_cache, v_cache, table, kv_len, *, row_start=None, scale: float | None = None, window: int = 0,
@@ -145,7 +116,7 @@ def paged_attention(q, k_cache, v_cache, table, kv_len, *, row_start=None, scale
                reads key/value head h / (heads / kv_heads)
     scale      of the scores; None: head_dim ** -0.5
     window     > 0: the row at position p sees the positions p - window + 1 .. p; 0: all up to p
-    out        where the result goes (default: a new tensor like q; q itself is allowed)
+    out        where the result goes (default: a new, contiguous tensor of q's shape and type; q itself is allowed)
     lse        float32 [rows][heads] to fill with ln sum exp of the row's scores (-inf: the row sees nothing)
     workspace  uint8 tensor of `paged_attention_workspace` bytes for callers that may not allocate (calls that may
                overlap need one each); None: allocated for the call
@@ -153,13 +124,8 @@ def paged_attention(q, k_cache, v_cache, table, kv_len, *, row_start=None, scale
     """
     if torch is None:
         _init()
-    args = (q, k_cache, v_cache, table, kv_len, row_start, q.shape[-1] ** -0.5 if scale is None else scale, window, k_scale,
-            v_scale, out, lse, workspace)
-    dev = q.get_device()
-    if stream is not None or dev < 0 or dev != _current_device():
-        with _at(dev, stream):
-            return _binding.paged_attention(*args)
-    return _binding.paged_attention(*args)
+    return _binding.paged_attention(q, k_cache, v_cache, table, kv_len, row_start, scale, window, k_scale, v_scale, out,
+                                    lse, workspace, stream)
 
 
 def paged_attention_workspace(q, k_cache, n_seqs: int) -> int:
@@ -170,7 +136,10 @@ def paged_attention_workspace(q, k_cache, n_seqs: int) -> int:
     n, page, heads, hd = k_cache.shape
     kind = {torch.bfloat16: _abi.BF16, torch.float16: _abi.F16, torch.float8_e4m3fn: _abi.E4M3}.get(k_cache.dtype, -1)
     c = _abi.PagedCache(None, None, kind, heads, hd, page, 0)
-    with _at(q.get_device(), None):
+    if not q.is_cuda:
+        from . import DFlashError
+        raise DFlashError(_abi.DFLASH_EINVAL, "tensors have to be on a CUDA device")
+    with torch.cuda.device(q.get_device()):
         return _check(lib().dflash_paged_attention_workspace(C.byref(c), n_seqs, q.shape[0], q.shape[1]))
 
 
@@ -194,13 +163,8 @@ def verify_drafts(target_logits, draft_tokens, accept_u, sample_u, *, draft_logi
     """
     if torch is None:
         _init()
-    args = (target_logits, draft_tokens, accept_u, sample_u, draft_logits, draft_start, temperature, accepted, next_token,
-            prob, workspace)
-    dev = target_logits.get_device()
-    if stream is not None or dev < 0 or dev != _current_device():
-        with _at(dev, stream):
-            return _binding.verify_drafts(*args)
-    return _binding.verify_drafts(*args)
+    return _binding.verify_drafts(target_logits, draft_tokens, accept_u, sample_u, draft_logits, draft_start, temperature,
+                                  accepted, next_token, prob, workspace, stream)
 
 
 def verify_workspace(n_seqs: int, n_drafts: int, vocab: int) -> int:
