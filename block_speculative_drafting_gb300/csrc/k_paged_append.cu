@@ -11,6 +11,11 @@
 // lanes that use them: head_dim / 8 lanes hold a head, eight columns (16 bytes
 // of a 16-bit type) a lane, the same columns of every head, so that a lane
 // keeps its eight sines and cosines in registers over all heads.
+//
+// Memory bound where rows are many: 8192 rows of 32 query and 8 key/value heads
+// of 128, bf16, half of each rotated: 39.7 us, 5.1 TB/s (75 % of a copy).  512
+// rows with head norms into an e4m3 cache: 8.5 us, the chain of a row's norms
+// and rotations; one row: 4.5 us, launch and lookups.
 #include "kernels.cuh"
 #include "paged.cuh"
 
@@ -262,7 +267,8 @@ int paged_append(const PagedCache& C, int cache_dtype, int hd, const PagedRows& 
                  const Rotation& rot, int num_sms, cudaStream_t st) {
     const int qd = q.heads > 0 ? qo.dtype : k.dtype;
     auto kern = hd == 64 ? append_kernel<64>(k.dtype, qd, cache_dtype) : append_kernel<128>(k.dtype, qd, cache_dtype);
-    // more warps a row while that leaves the SMs under a third of their warps
+    // more warps a row while that leaves the SMs under a third of their warps (512 rows: one warp a row 12.7 us, four
+    // 8.5, eight 10.2; one row: one warp 6.7 us, eight 4.5)
     int wl = 0;
     while (wl < 3 && ((int64_t)R.n_rows << (wl + 1)) <= (int64_t)num_sms * 20) ++wl;
     const int64_t warps = (int64_t)R.n_rows << wl;

@@ -35,6 +35,11 @@
 // finite (0 times an infinity would not be 0), those elements are taken out of
 // the tile and added to the rows that see them.
 //
+// Per tile 1.37 us with a bf16 cache, the memory's rate (19 blocks over 16384 keys x
+// 8 heads: 189 us, 6.8 TB/s), 1.27 us with an e4m3 one, 0.35 of it the codes' way
+// through shared memory.  A unit's end and the next one's beginning take 4.1 and
+// 6.7 us, start, epilogue and join of a call 13.
+//
 // Every wait is bounded (1 s of %globaltimer).  A role whose wait expires stops;
 // the softmax then walks its remaining units without waiting and leaves NaN in
 // their rows.
@@ -48,7 +53,8 @@ constexpr int kPtM = 128;
 constexpr int kPtSoft = 128;  // softmax threads: warps 0-3
 constexpr int kPtQk = kPtSoft / 32, kPtPv = kPtQk + 1, kPtLoad = kPtPv + 1;  // warps
 constexpr uint64_t kPtWait = 1000000000ull;
-constexpr int kPtOver = 4;   // tiles' time that a unit's end and the next one's beginning take
+// tiles' time that a unit's end and the next one's beginning take (32 blocks over a bf16 cache: 0 81.7 us, 2 73.3, 4 71.1)
+constexpr int kPtOver = 4;
 constexpr int kPtBits = 16;  // tiles whose key masks are kept: more than the loaders can be ahead of the softmax
 
 template <bool BF, bool E8, int HD>

@@ -21,7 +21,10 @@
 // few (two lanes a clock and SM: 64-bit sums in every warp took 30 us of a
 // 40 us call).  The drafts' p and q are formed in 64 bits, a lane a draft.
 //
-// Memory bound: the logits, once (the re-read row comes out of L2).
+// Memory bound: the logits, once (the re-read row comes out of L2).  32 blocks of
+// up to 16 drafts, 151936 bf16 logits against f32 ones: 88 us, of which the
+// statistics 55 (5.5 TB/s, 81 % of a copy) and the picking kernel 22 and its
+// launch; one block 17 us, greedy 7.5, most of it latency.
 #include <cooperative_groups.h>
 
 #include "kernels.cuh"

@@ -16,6 +16,9 @@ definition; RMSNorm's unit RMS and RoPE's norm preservation and relative
 position property; the page's own ``top_k`` example; a closed form of the
 head path; SiLU identities.  The end-to-end block has no printed values on
 the pages: its composition is pinned only through those parts.
+
+``oracle.target`` restates the operators of the target's verification pass
+from their formulas.
 """
 from . import quant  # noqa: F401
 from .drafter import (OracleModel, OracleSeq, Matrix, argmax_first, attention, block, inv_freq,  # noqa: F401
