@@ -28,6 +28,10 @@
 // barrier counts them as they land); e4m3 loaders copy codes to places of their
 // own and write their f16 values (exact) into the slots.  The MMA warps order
 // those writes before their reads of them (a proxy fence after the barrier).
+// A unit's queries are fetched by the softmax warps as the unit before ends, with
+// an e4m3 cache by four more warps: 3 us less a unit (32 blocks 73.8 -> 66.6 us);
+// a 16-bit cache's softmax needs the registers that those warps would take (71
+// -> 75 us).
 // The page of a key is looked up a tile before it is needed.
 //
 // Keys that no row sees are zeros behind a bit mask; keys that only some rows
@@ -61,7 +65,8 @@ template <bool BF, bool E8, int HD>
 struct PtShape {
     static constexpr int kLoadWarps = 4;  // of the keys, and as many of the values
     static constexpr int kLoaders = kLoadWarps * 32;
-    static constexpr int kThreads = kPtLoad * 32 + 2 * kLoaders;
+    static constexpr int kQueryWarps = E8 ? 4 : 0;
+    static constexpr int kThreads = (kPtLoad + kQueryWarps) * 32 + 2 * kLoaders;
     static constexpr int KPW = kPaTile / kLoadWarps;  // keys of a loader warp: one a lane
     static constexpr int kItem = kPaTile * HD * 2;    // a slot: a tile's keys or values in 16 bits
     static constexpr int kSlots = (E8 ? 2 : 3) * (128 / HD);  // of the keys, and as many of the values
@@ -69,7 +74,7 @@ struct PtShape {
     static constexpr int kRaw = E8 ? 4 * (128 / HD) : 0, kRawLd = KPW * HD / 16 / 64;
     static constexpr int kRawBytes = kRaw * kRawLd * 16 * 2 * kLoaders;
     static constexpr bool kSplitP = !E8;
-    static constexpr int kCtl = 13 * 1024;
+    static constexpr int kCtl = 15 * 1024;
     static constexpr size_t kSmem = 1024 /*alignment*/ + kCtl + 2 * (size_t)kSlots * kItem + kRawBytes;
     // tensor memory: two S / P buffers, O, Q
     static constexpr int kColS = 0, kColO = 256, kColQ = 384, kCols = 512;
@@ -78,11 +83,12 @@ struct PtShape {
 struct PtCtl {
     // a slot's data written / its MMAs done; a tile's scores in S; its P in
     // place of them (a barrier a buffer: a thread may be a tile ahead of
-    // another); its P V added; a unit's Q in place
-    uint64_t full[2][6], empty[2][6], s_full[2], p_full[2], o_done[2], q_full, fin[2];
+    // another); its P V added; a unit's Q in place, its last scores multiplied
+    uint64_t full[2][6], empty[2][6], s_full[2], p_full[2], o_done[2], q_full, q_free, fin[2];
     uint32_t tmem;
     uint32_t bits[kPtBits][4];  // a tile's valid keys
     uint32_t bad[4];            // keys whose values are not all finite
+    float rf[4][kPtM];          // what the queries of a unit (and the three after it) were scaled down by
     float2 ml[kPtM];            // a unit's row references and sums, for the join of a row's two lanes
     alignas(16) float xo[2][64][20];        // sixteen columns of the upper lanes' outputs on their way to the lower ones
 };
@@ -145,6 +151,69 @@ DF_DEV void pt_skip(const PaArgs& A, PaCur& c, int n) {
     pa_next(A, MT, c);
 }
 
+// A unit's queries to tensor memory at `to` (row t % MT of the unit), after `free` has waited for it.  An 8-bit cache's
+// warps of queries: a bf16 row is brought into f16 by a power of two, left in ctl.rf, its halves read for their largest
+// element and then again (registers).
+template <bool E8, int HD, int MT, class F>
+DF_DEV bool pt_queries(const PaArgs& A, PtCtl& ctl, const PaCur& c, int unit, int t, uint32_t to, F free) {
+    constexpr int kHalves = E8 ? 2 : 1, NX = HD / 8 / kHalves;
+    const int h = c.u % A.C.kv_heads, mm = (c.u / A.C.kv_heads) * MT + t % MT;
+    const bool in = mm < c.q.rows * A.group;
+    const int row = c.q.row0 + mm / A.group, hq = h * A.group + mm % A.group;
+    const unsigned char* qp = A.q.p + (int64_t)row * A.q.rs + (int64_t)hq * A.q.hs;
+    uint4 x[NX];
+    uint32_t (&w)[4 * NX] = *reinterpret_cast<uint32_t(*)[4 * NX]>(x);
+    auto load = [&](int half) {
+#pragma unroll
+        for (int j = 0; j < NX; ++j)
+            x[j] = in ? *reinterpret_cast<const uint4*>(qp + 16 * (half * NX + j)) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    float rf = 1.f, down = 1.f;
+    if constexpr (!E8) {
+        load(0);
+    } else if (A.q.dtype == kBF16) {
+        float mx = 0.f;
+#pragma unroll 1
+        for (int half = 0; half < kHalves; ++half) {
+            load(half);
+#pragma unroll
+            for (int j = 0; j < 4 * NX; ++j) {
+                const float2 f = unpack2<true>(w[j]);
+                mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+        }
+        // times 2^-x, the largest in [1, 2): what f16 cannot hold of the row then is under 2^-25 of that
+        if (mx > 0.f && mx < INFINITY) {
+            const int e = min(max(ilogbf(mx), -120), 120);
+            down = ldexpf(1.f, -e);
+            rf = ldexpf(1.f, e);
+        }
+    }
+    if (!free()) return false;
+    at_fence_after();
+    if constexpr (E8) ctl.rf[unit & 3][t] = rf;
+#pragma unroll 1
+    for (int half = 0; half < kHalves; ++half) {
+        if constexpr (E8) {
+            load(half);
+            if (A.q.dtype == kBF16) {
+#pragma unroll
+                for (int j = 0; j < 4 * NX; ++j) {
+                    const float2 f = unpack2<true>(w[j]);
+                    w[j] = pack2<false>(f.x * down, f.y * down);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * NX; i += 16)
+            pt_st16(to + 4 * NX * half + i, *reinterpret_cast<const uint32_t(*)[16]>(w + i));
+    }
+    at_wait_st();
+    at_fence_before();
+    mbar_arrive(&ctl.q_full);
+    return true;
+}
+
 // MT: rows of a unit's tile, 64 (each query on two lanes) or 128
 template <bool BF, bool E8, int HD, int MT>
 __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
@@ -171,6 +240,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
         mbar_init(&ctl.o_done[0], 1);
         mbar_init(&ctl.o_done[1], 1);
         mbar_init(&ctl.q_full, kPtSoft);
+        mbar_init(&ctl.q_free, 1);
         mbar_init(&ctl.fin[0], 1);
         mbar_init(&ctl.fin[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -192,7 +262,20 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
     const PaCur cur = pa_share(A, MT, kPtOver, lane, chunk);
     if (threadIdx.x == 0) A.ws_join[blockIdx.x].last = -1;
 
-    if (warp >= kPtLoad) {
+    if (S::kQueryWarps > 0 && warp >= kPtLoad + 2 * S::kLoadWarps) {
+        // ------------------------------------------------------------ queries (an e4m3 cache's)
+        const int t = (warp & 3) * 32 + lane;
+        int unit = 0;
+        for (PaCur c = cur; c.left > 0; ++unit) {
+            // (the unit before has multiplied its last scores)
+            auto free = [&]() {
+                return unit == 0 || __all_sync(0xffffffffu, mbar_wait(&ctl.q_free, (unit - 1) & 1, kPtWait));
+            };
+            if (!pt_queries<E8, HD, MT>(A, ctl, c, unit, t, tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kColQ, free))
+                break;
+            pt_skip<MT>(A, c, pt_tiles(c));
+        }
+    } else if (warp >= kPtLoad) {
         // ------------------------------------------------------------ loads
         const int side = (warp - kPtLoad) / S::kLoadWarps, lw = (warp - kPtLoad) % S::kLoadWarps;  // 0 keys, 1 values
         unsigned char* slots = ring + side * S::kSlots * S::kItem;
@@ -343,6 +426,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                     pt_commit(on, &ctl.s_full[tg & 1]);
                     if (on) mbar_arrive(&ctl.s_full[tg & 1]);
                 }
+                if (S::kQueryWarps > 0) pt_commit(on, &ctl.q_free);
             } else {
                 constexpr uint32_t idO = at_idesc(kPtM, HD, true) | kType;
                 const uint64_t dv0 = at_desc(smem_addr(ring) + S::kSlots * S::kItem, kPaTile * 128);
@@ -377,49 +461,14 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
         constexpr int NC = 4 / D;         // 32-key chunks of a lane
         const int t = threadIdx.x, r = t % MT, copy = t / MT;  // this lane's row of the unit, and its share of the keys
         const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
-        // A unit's queries to tensor memory; returns what this lane's row was scaled down by.
-        auto queries = [&](const PaCur& c) -> float {
-            const int h = c.u % A.C.kv_heads, mm = (c.u / A.C.kv_heads) * MT + r;
-            const bool in = mm < c.q.rows * A.group;
-            const int row = c.q.row0 + mm / A.group, hq = h * A.group + mm % A.group;
-            float rf = 1.f, down = 1.f;
-            const unsigned char* qp = A.q.p + (int64_t)row * A.q.rs + (int64_t)hq * A.q.hs;
-            uint4 x[HD / 8];
-#pragma unroll
-            for (int j = 0; j < HD / 8; ++j)
-                x[j] = in ? *reinterpret_cast<const uint4*>(qp + 16 * j) : make_uint4(0u, 0u, 0u, 0u);
-            uint32_t (&w)[HD / 2] = *reinterpret_cast<uint32_t(*)[HD / 2]>(x);
-            if (E8 && A.q.dtype == kBF16) {
-                float mx = 0.f;
-#pragma unroll
-                for (int j = 0; j < HD / 2; ++j) {
-                    const float2 f = unpack2<true>(w[j]);
-                    mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-                }
-                // times 2^-x, the largest in [1, 2): what f16 cannot hold of the row then is under 2^-25 of that
-                if (mx > 0.f && mx < INFINITY) {
-                    const int e = min(max(ilogbf(mx), -120), 120);
-                    down = ldexpf(1.f, -e);
-                    rf = ldexpf(1.f, e);
-                }
-#pragma unroll
-                for (int j = 0; j < HD / 2; ++j) {
-                    const float2 f = unpack2<true>(w[j]);
-                    w[j] = pack2<false>(f.x * down, f.y * down);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < HD / 32; ++i)
-                pt_st16(lane_addr + S::kColQ + 16 * i, *reinterpret_cast<const uint32_t(*)[16]>(w + 16 * i));
-            at_wait_st();
-            at_fence_before();
-            mbar_arrive(&ctl.q_full);
-            return rf;
-        };
         bool ok = true;
-        int tg = 0;
+        int tg = 0, unit = 0;  // tiles, units so far
         PaCur c = cur;
-        float rf_next = c.left > 0 ? queries(c) : 1.f;
+        auto queries = [&]() {  // (where no warps of their own bring them)
+            if (S::kQueryWarps == 0 && c.left > 0)
+                pt_queries<E8, HD, MT>(A, ctl, c, unit, t, lane_addr + S::kColQ, []() { return true; });
+        };
+        queries();
         while (c.left > 0) {
             const PaSeq sq = c.q;
             const int u = c.u, tile0 = c.tile, tiles = pt_tiles(c);
@@ -431,7 +480,6 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
             const int wlo = A.window > 0 ? pos - A.window + 1 : 0;
             const int pmin = sq.p0 + (rt * MT) / A.group, pmax = sq.p0 + (rt * MT + mvalid - 1) / A.group;
             const int wtop = A.window > 0 ? pmax - A.window + 1 : 0;
-            const float rf = rf_next;
             {
                 // O cleared (the unit before has read it)
                 const uint32_t zero[16] = {};
@@ -440,7 +488,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                 at_wait_st();
             }
             const float ks = E8 && A.C.k_scale != nullptr ? A.C.k_scale[h] : 1.f;
-            const float cs = fminf(fmaxf(A.scale_log2 * ks * rf, 1e-37f), 3e38f);
+            float cs = 0.f;
 
             float m = -INFINITY, l = 0.f;
             for (int i = 0; i < tiles; ++i, ++tg) {
@@ -456,6 +504,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                 }
                 if (!ok) continue;
                 at_fence_after();
+                if (i == 0) cs = fminf(fmaxf(A.scale_log2 * ks * (E8 ? ctl.rf[unit & 3][t] : 1.f), 1e-37f), 3e38f);
                 const uint32_t* bits = ctl.bits[tg % kPtBits];
                 const bool full = !edge && (bits[0] & bits[1] & bits[2] & bits[3]) == 0xffffffffu;
                 // this row's view of 32 keys
@@ -534,8 +583,8 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                     unsigned char* vt = ring + (S::kSlots + tg % S::kSlots) * S::kItem;
                     bool bad = false;
                     const bool got = ok && mbar_wait(&ctl.full[1][tg % S::kSlots], (tg / S::kSlots) & 1, kPtWait);
-#pragma unroll 1
-                    for (int x = 0; got && x < HD / 8; ++x) {
+#pragma unroll 4
+                    for (int x = 0; x < (got ? HD / 8 : 0); ++x) {
                         const uint4 y = *reinterpret_cast<const uint4*>(vt + (x >> 3) * (kPaTile * 128) + at_swz(t, x & 7));
                         const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -641,7 +690,8 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
             // the next unit's queries, whose scores may then be multiplied while this one's outputs are written
             // (its last scores have been read: Q is free)
             pt_skip<MT>(A, c, tiles);
-            if (c.left > 0) rf_next = queries(c);
+            ++unit;
+            queries();
             ok = __all_sync(0xffffffffu, ok && mbar_wait(&ctl.o_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1, kPtWait));
             at_fence_after();
             if (!ok) l = NAN;

@@ -633,6 +633,15 @@ def test_attention_small_weights_in_sum(kind, src, rows):
 
 
 @gpu
+@pytest.mark.parametrize("kind,src", [("bf16", "bf16"), ("f16", "f16"), ("e4m3", "bf16")])
+@pytest.mark.parametrize("rows", [4, 16, 32])
+def test_attention_many_units_of_several_tiles(kind, src, rows):
+    # three units and more a CTA, none of them a single tile: what a CTA hands from unit to unit
+    lens = tuple(260 + 13 * i for i in range(30))
+    _check_attention(kind, src, hd=64, heads=64, kvh=16, rows=(rows,) * 30, lens=lens, uniform=True, seed=rows)
+
+
+@gpu
 def test_attention_out_in_place_of_q():
     torch, dfl = _torch(), _dfl()
     for heads in (4, 32):  # the warps' kernel, and the tensor memory's
