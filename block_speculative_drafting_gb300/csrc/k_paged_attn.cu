@@ -616,7 +616,8 @@ __global__ void __launch_bounds__(kPaThreads) paged_join_kernel(const __grid_con
 // the warp MMAs; beyond that the tcgen05 kernel's 64 or 128.  (A warp-MMA
 // kernel of 32 rows took 71.7 us where the tcgen05 kernel's 64 take 67.4, 32
 // sequences of 8 rows x 4 heads, and 12.6 against 14.7 us on one sequence of
-// 2048 keys; with 16 rows, 32 sequences, the warp MMAs take 58 us, tcgen05 64.)
+// 2048 keys; with 16 rows, 32 sequences, the warp MMAs take 58 us, tcgen05 64.
+// 64 rows in a tile of 128: 41.0 for 40.1 us, one block over 32768 keys.)
 static int pa_tile_rows(int n_seqs, int64_t n_rows, int group) {
     const int64_t per = n_seqs > 0 ? (n_rows + n_seqs - 1) / n_seqs : 0;
     const int64_t m = per * group;

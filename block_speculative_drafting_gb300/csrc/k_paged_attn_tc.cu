@@ -40,9 +40,10 @@
 // the tile and added to the rows that see them.
 //
 // Per tile 1.37 us with a bf16 cache, the memory's rate (19 blocks over 16384 keys x
-// 8 heads: 189 us, 6.8 TB/s), 1.27 us with an e4m3 one, 0.35 of it the codes' way
-// through shared memory.  A unit's end and the next one's beginning take 4.1 and
-// 6.7 us, start, epilogue and join of a call 13.
+// 8 heads: 187 us, 6.8 TB/s), 1.27 us with an e4m3 one (178 us), 0.35 of it the codes'
+// way through shared memory.  A unit's end and the next one's beginning take about
+// 4 us, of which a tile that some rows see in part 2 and the outputs 2; start,
+// epilogue and join of a call 13.
 //
 // Every wait is bounded (1 s of %globaltimer).  A role whose wait expires stops;
 // the softmax then walks its remaining units without waiting and leaves NaN in

@@ -24,7 +24,7 @@
 // Memory bound: the logits, once (the re-read row comes out of L2).  32 blocks of
 // up to 16 drafts, 151936 bf16 logits against f32 ones: 88 us, of which the
 // statistics 55 (5.5 TB/s, 81 % of a copy) and the picking kernel 22 and its
-// launch; one block 17 us, greedy 7.5, most of it latency.
+// launch; one block 16 us, greedy 6.7, most of it latency.
 #include <cooperative_groups.h>
 
 #include "kernels.cuh"
@@ -685,11 +685,13 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
     if (sampled) cl.sync();  // no CTA leaves while its sums may be read
 }
 
-// Parts of a row: of up to 32K entries, and where there are few rows as many
-// as give a few CTAs an SM, of 4K entries at least.
+// Parts of a row: of up to 32K entries and at least 4K.  Where 32K entries a part leave all CTAs resident at once (four
+// an SM), as many as give two CTAs an SM (3 blocks of 16 rows against f32 logits: 24.9 us, with 16 CTAs an SM 29.2; one
+// block 16.1, 18.2); beyond, 16 CTAs an SM, whose last wave is the shorter (4 blocks: 29.5, with 32K entries a part
+// 31.2).
 static int verify_parts(int64_t rows, int64_t vocab, int num_sms) {
-    const int64_t want = (16 * (int64_t)num_sms + rows - 1) / (rows > 0 ? rows : 1);
-    const int64_t most = (vocab + 4095) / 4096, least = (vocab + 32767) / 32768;
+    const int64_t most = (vocab + 4095) / 4096, least = (vocab + 32767) / 32768, n = rows > 0 ? rows : 1;
+    const int64_t want = ((least * n <= 4 * (int64_t)num_sms ? 2 : 16) * (int64_t)num_sms + n - 1) / n;
     const int64_t p = want < least ? least : want;
     return (int)(p > most ? most : p);
 }
@@ -723,7 +725,8 @@ int verify(const VerifyArgs& A, void* ws, int num_sms, cudaStream_t st) {
     P.parts = verify_parts(rows, A.vocab, num_sms);
     if (cudaError_t e = launch(verify_stats_kernel, dim3((unsigned)(rows * P.parts)), dim3(kVsThreads), 0, st, P))
         return (int)e;
-    // 32 warps a CTA while every CTA has an SM to itself, else 16 (two CTAs an SM)
+    // 32 warps a CTA while every CTA has an SM to itself (one block: 18.2 us, with 16 warps 19.9), else 16, two CTAs an
+    // SM (32 blocks: 87.5 us, with 32 warps 94.3)
     return A.n_seqs * kVpCluster <= num_sms ? launch_pick<32>(P, st) : launch_pick<16>(P, st);
 }
 
