@@ -138,6 +138,21 @@ def test_paged_attention_refuses_bad_arguments(lib):
     assert call(r=_rows_struct(**wide)) == _abi.DFLASH_EINVAL
 
 
+def test_binding_refuses_tensors_of_the_host_and_other_objects(lib):
+    torch, dfl = pytest.importorskip("torch"), _dfl()
+    x, i = torch.zeros(2, 16, 2, 64), torch.zeros(2, 2, dtype=torch.int32)
+    refused = [lambda: dfl.paged_append(x, x, x[0], x[0], i, i[0]), lambda: dfl.paged_attention(x[0], x, x, i, i[0]),
+               lambda: dfl.verify_drafts(x[0, 0], i[0, :1], x[0, 0, 0, :1], x[0, 0, 0, :1]),
+               lambda: dfl.paged_attention_workspace(x[0], x, 2)]
+    for call in refused:
+        with pytest.raises(dfl.DFlashError, match="CUDA device"):
+            call()
+    for call in (lambda: dfl.paged_append(None, x, x, x, i, i), lambda: dfl.paged_attention([1.0], x, x, i, i),
+                 lambda: dfl.verify_drafts(3, i, x, x)):
+        with pytest.raises(TypeError, match="has to be a tensor"):
+            call()
+
+
 def test_verify_refuses_bad_arguments(lib):
     from block_speculative_drafting_gb300 import _abi
     good = dict(target=4096, dtype=0, stride=100, dl=None, ds=100, tok=4096, start=None, temp=None, au=4096, su=4096,
@@ -639,6 +654,54 @@ def test_attention_many_units_of_several_tiles(kind, src, rows):
     # three units and more a CTA, none of them a single tile: what a CTA hands from unit to unit
     lens = tuple(260 + 13 * i for i in range(30))
     _check_attention(kind, src, hd=64, heads=64, kvh=16, rows=(rows,) * 30, lens=lens, uniform=True, seed=rows)
+
+
+@gpu
+def test_passes_from_two_threads_at_once():
+    import threading
+    torch, dfl = _torch(), _dfl()
+    states = [_pass_state(torch, dfl, seed) for seed in (3, 4)]
+    want = [_pass(dfl, st) for st in states]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(st, expect):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                y, v = _pass(dfl, st)
+                if not (torch.equal(y, expect[0]) and all(torch.equal(a, b) for a, b in zip(v, expect[1]))):
+                    wrong.append(1)
+
+    threads = [threading.Thread(target=work, args=x) for x in zip(states, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+@gpu
+def test_calls_keep_no_reference_to_their_arguments():
+    import sys
+    torch, dfl = _torch(), _dfl()
+    st = _pass_state(torch, dfl)
+    out, lse = torch.empty_like(st["q"]), torch.empty(12, 8, device="cuda")
+    keep = dict(st, out=out, lse=lse)
+    before = {k: sys.getrefcount(v) for k, v in keep.items()}
+    for scale in (1.0, -1.0):  # served, refused
+        for _ in range(5):
+            try:
+                dfl.paged_append(st["kc"], st["vc"], st["k"], st["v"], st["table"], st["lens"], row_start=st["start"],
+                                 q=st["q"], q_out=out, inv_freq=st["f"], eps=scale, rope_scale=1.0)
+                y = dfl.paged_attention(out, st["kc"], st["vc"], st["table"], st["lens"], row_start=st["start"],
+                                        scale=scale, out=out, lse=lse)
+                assert y is out
+                del y
+            except dfl.DFlashError:
+                assert scale < 0
+    made = dfl.paged_attention(st["q"], st["kc"], st["vc"], st["table"], st["lens"], row_start=st["start"])
+    assert sys.getrefcount(made) == 2
+    assert {k: sys.getrefcount(v) for k, v in keep.items()} == before
 
 
 @gpu
