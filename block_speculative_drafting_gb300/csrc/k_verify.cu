@@ -498,6 +498,11 @@ struct Left {
     }
 };
 
+// A CTA's shared memory may be written from its cluster only once it runs: every CTA says so as it starts, and none
+// writes before all have (the wait falls into the statistics' time).
+DF_DEV void cluster_started() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+DF_DEV void cluster_wait_started() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+
 template <int WARPS>
 __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
     verify_pick_kernel(const __grid_constant__ VerifyParams P) {
@@ -514,6 +519,7 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), s = blockIdx.x / kVpCluster;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    cluster_started();
     pdl_wait();
     int a, b;
     draft_range(A, s, a, b);
@@ -575,6 +581,7 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
     int token = t.max == -INFINITY ? -1 : t.tag;
     bool writes = rank == 0 && threadIdx.x == 0;
     const bool sampled = !c.greedy() && t.max > -INFINITY;
+    cluster_wait_started();
     if (sampled) {
         writes = false;
         Left L;
@@ -682,7 +689,7 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
         A.accepted[s] = acc;
         A.next_tok[s] = token;
     }
-    if (sampled) cl.sync();  // no CTA leaves while its sums may be read
+    // (a CTA's sums are written before the last meeting and read by itself alone: none has to wait to leave)
 }
 
 // Parts of a row: of up to 32K entries and at least 4K.  Where 32K entries a part leave all CTAs resident at once (four
