@@ -92,28 +92,41 @@ struct VerifyParams {
     int parts;
 };
 
-DF_DEV void draft_range(const VerifyArgs& A, int s, int& a, int& b) {
+// A start as it is read: inside [0, n_drafts], and not before any start ahead of it, so that the sequences' drafts are
+// apart and in order whatever the array holds.
+DF_DEV int draft_start_at(const VerifyArgs& A, int j) { return min(max(A.draft_start[j], 0), A.n_drafts); }
+// Drafts [a, b) of sequence s.  By a warp.
+DF_DEV void draft_range(const VerifyArgs& A, int s, int lane, int& a, int& b) {
     if (A.draft_start == nullptr) {
         a = s * A.per;
         b = a + A.per;
-    } else {
-        a = min(max(A.draft_start[s], 0), A.n_drafts);
-        b = min(max(A.draft_start[s + 1], a), A.n_drafts);
+        return;
     }
+    int m = 0;
+    for (int j = lane; j <= s; j += 32) m = max(m, draft_start_at(A, j));
+    a = __reduce_max_sync(0xffffffffu, m);
+    b = max(draft_start_at(A, s + 1), a);
 }
-// The last sequence whose drafts (shift 0) or target rows (shift 1) start at
-// or before entry i; -1 where no sequence holds it.  By a warp, 32 starts at once.
+// The sequence that holds draft (shift 0) or target row (shift 1) i, or -1: the last whose drafts or target rows start
+// at or before it, unless they end there.  By a warp, 32 starts at once.
 DF_DEV int verify_seq(const VerifyArgs& A, int i, int shift, int lane) {
     if (A.draft_start == nullptr) return i / (A.per + shift);
-    int s = -1;
-    for (int b = 0; b < A.n_seqs; b += 32) {
+    int run = 0;  // the largest start so far
+    for (int b = 0; b <= A.n_seqs; b += 32) {
         const int j = b + lane;
-        s += __popc(__ballot_sync(0xffffffffu, j < A.n_seqs && A.draft_start[j] + shift * j <= i));
+        int at = j <= A.n_seqs ? draft_start_at(A, j) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at = max(at, y);
+        }
+        at = max(at, run);
+        // (starts ascend from here on: the first one past row i ends the search; sequence j has target rows at + j ..)
+        const uint32_t past = __ballot_sync(0xffffffffu, j <= A.n_seqs && (int64_t)at + shift * (int64_t)j > i);
+        if (past != 0) return b + __ffs(past) - 2;
+        run = __shfl_sync(0xffffffffu, at, 31);
     }
-    if (s < 0) return -1;
-    int a, e;
-    draft_range(A, s, a, e);
-    return i >= a + shift * s && i < e + shift * (s + 1) ? s : -1;
+    return -1;
 }
 
 // c = log2(e) / T as hi + lo, lo > 0 (so that -inf * lo is -inf); hi = 0
@@ -522,7 +535,7 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
     cluster_started();
     pdl_wait();
     int a, b;
-    draft_range(A, s, a, b);
+    draft_range(A, s, lane, a, b);
     const int d = b - a;
     const Scale c = scale_of(A, s);
     const bool drawn = A.draft != nullptr && !c.greedy();  // q is the drafter's distribution, not one token

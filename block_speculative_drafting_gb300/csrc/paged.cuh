@@ -55,30 +55,45 @@ struct HeadRows {
     int dtype, heads;
 };
 
-// Rows [a, b) of sequence s, inside [0, n_rows] whatever the array holds.
+// A row start as it is read: inside [0, n_rows], and not before any start ahead of it (the largest so far counts), so
+// that the sequences' rows are apart and in order whatever the array holds.  On the device the two walks below are a
+// warp's: 32 starts at once, every lane with the same s or r and the same answer.
+DF_HD int row_start_at(const PagedRows& R, int j) { return lowest(highest(R.row_start[j], 0), R.n_rows); }
+#ifdef __CUDA_ARCH__
+constexpr int kWalk = 32;
+DF_DEV int walk_lane() { return (int)(threadIdx.x & 31); }
+DF_DEV int walk_max(int x) {
+    for (int o = 16; o > 0; o >>= 1) x = highest(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+DF_DEV int walk_first(bool x) { return __ffs(__ballot_sync(0xffffffffu, x)) - 1; }  // the first lane with x, or -1
+#else
+constexpr int kWalk = 1;
+inline int walk_lane() { return 0; }
+inline int walk_max(int x) { return x; }
+inline int walk_first(bool x) { return x ? 0 : -1; }
+#endif
+// Rows [a, b) of sequence s.
 DF_HD void rows_of(const PagedRows& R, int s, int& a, int& b) {
     if (R.row_start == nullptr) {
         a = s * R.per;
         b = a + R.per;
-    } else {
-        a = lowest(highest(R.row_start[s], 0), R.n_rows);
-        b = lowest(highest(R.row_start[s + 1], a), R.n_rows);
+        return;
     }
+    int m = 0;
+    for (int j = walk_lane(); j <= s; j += kWalk) m = highest(m, row_start_at(R, j));
+    a = walk_max(m);
+    b = highest(row_start_at(R, s + 1), a);
 }
-// The sequence that holds row r, or -1: the last whose start is at most r.
+// The sequence that holds row r, or -1: the one before the first start past r.
 DF_HD int seq_of(const PagedRows& R, int r) {
     if (R.row_start == nullptr) return R.per > 0 ? r / R.per : -1;
-    int lo = 0, hi = R.n_seqs;  // row_start[lo] <= r is not known for lo = 0
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (R.row_start[mid] <= r)
-            lo = mid;
-        else
-            hi = mid;
+    for (int j0 = 0; j0 <= R.n_seqs; j0 += kWalk) {
+        const int j = j0 + walk_lane();
+        const int past = walk_first(j <= R.n_seqs && row_start_at(R, j) > r);
+        if (past >= 0) return j0 + past - 1;
     }
-    int a, b;
-    rows_of(R, lo, a, b);
-    return r >= a && r < b ? lo : -1;
+    return -1;
 }
 // The table's entry for position p of sequence s, -1 outside the table.
 DF_HD int page_entry(const PagedRows& R, int s, int p, int& slot) {

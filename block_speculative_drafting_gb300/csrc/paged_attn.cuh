@@ -41,11 +41,11 @@ struct PaSeq {
     int ntiles, nunits;
 };
 
-DF_DEV PaSeq pa_seq(const PaArgs& A, int s, int mt) {
+// of sequence s with rows [a, b)
+DF_DEV PaSeq pa_seq(const PaArgs& A, int s, int a, int b, int mt) {
     PaSeq q;
-    int b;
-    rows_of(A.R, s, q.row0, b);
-    q.rows = b - q.row0;
+    q.row0 = a;
+    q.rows = b - a;
     const int len = A.R.kv_len[s];
     q.p0 = max(len, -1) - q.rows;  // a length below 0 reads as -1: no position of any row is held
     q.hi = min(max(len, 0), A.R.cap);
@@ -66,27 +66,52 @@ struct PaCur {
     int ov;
     int left;  // places of the CTA's share from here on (0: none)
 };
+// The end of sequence s's rows, which start at a.
+DF_DEV int pa_rows_end(const PaArgs& A, int s, int a) {
+    return A.R.row_start == nullptr ? a + A.R.per : max(row_start_at(A.R, s + 1), a);
+}
+// Rows [a, b) of sequence s0 + lane (warp-wide; none past the last sequence); `from`: where sequence s0's start.
+DF_DEV void pa_rows_of_lane(const PaArgs& A, int s0, int from, int lane, int& a, int& b) {
+    const int s = min(s0 + lane, A.R.n_seqs - 1);
+    if (A.R.row_start == nullptr) {
+        a = s * A.R.per;
+        b = a + A.R.per;
+    } else {
+        b = max(row_start_at(A.R, s + 1), from);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, b, o);
+            if (lane >= o) b = max(b, y);
+        }
+        a = __shfl_up_sync(0xffffffffu, b, 1);
+        if (lane == 0) a = from;
+    }
+}
 // This CTA's share (warp-wide); `chunk`: the places of a share.
 DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
     int64_t t64 = 0, v64 = 0;
     int w0 = 0, u0 = 0;
-    for (int s = lane; s < A.R.n_seqs; s += 32) {
-        const PaSeq q = pa_seq(A, s, mt);
+    const int first = A.R.row_start == nullptr ? 0 : row_start_at(A.R, 0);
+    for (int s0 = 0, from = first; s0 < A.R.n_seqs; s0 += 32) {
+        int a, b;
+        pa_rows_of_lane(A, s0, from, lane, a, b);
+        from = __shfl_sync(0xffffffffu, b, 31);
+        if (s0 + lane >= A.R.n_seqs) continue;
+        const PaSeq q = pa_seq(A, s0 + lane, a, b, mt);
         const int64_t w = (int64_t)q.ntiles * q.nunits;
-        if (s < 32) w0 = (int)w, u0 = q.nunits;
+        if (s0 == 0) w0 = (int)w, u0 = q.nunits;
         t64 = min(t64 + w, (int64_t)1 << 40);
         v64 = min(v64 + q.nunits, (int64_t)1 << 40);
     }
     PaCur c{};
     chunk = 1;
-    // (row starts out of order can give sequences the same rows many times over: such a line has no end worth walking)
     auto sum = [](int64_t x) {
         return ((int64_t)__reduce_add_sync(0xffffffffu, (unsigned)(x >> 20)) << 20) +
                __reduce_add_sync(0xffffffffu, (unsigned)(x & 0xfffff));
     };
     t64 = sum(t64);
     v64 = sum(v64);
-    if (t64 + ovh * v64 >= 1ll << 31) return c;
+    if (t64 + ovh * v64 >= 1ll << 31) return c;  // (never: pa_line_fits)
     const int tiles = (int)t64, units = (int)v64;
     c.ov = tiles > 2 * (int)gridDim.x ? ovh : 0;
     const int total = tiles + c.ov * units, grid = (int)gridDim.x;
@@ -94,11 +119,13 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
     if ((int64_t)blockIdx.x * chunk >= total) return c;
     const int t = (int)blockIdx.x * chunk;
     int run = 0;
-    for (int s0 = 0; s0 < A.R.n_seqs; s0 += 32) {
-        int w = s0 == 0 ? w0 + c.ov * u0 : 0;
-        if (s0 > 0 && s0 + lane < A.R.n_seqs) {
-            const PaSeq q = pa_seq(A, s0 + lane, mt);
-            w = (q.ntiles + c.ov) * q.nunits;
+    for (int s0 = 0, from = first; s0 < A.R.n_seqs; s0 += 32) {
+        int w = w0 + c.ov * u0, a, b;
+        pa_rows_of_lane(A, s0, from, lane, a, b);
+        from = __shfl_sync(0xffffffffu, b, 31);
+        if (s0 > 0) {
+            const PaSeq q = pa_seq(A, min(s0 + lane, A.R.n_seqs - 1), a, b, mt);
+            w = s0 + lane < A.R.n_seqs ? (q.ntiles + c.ov) * q.nunits : 0;
         }
         int in = w;
 #pragma unroll
@@ -111,7 +138,7 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
             const int l = __ffs(hit) - 1;
             const int x = t - (run + __shfl_sync(0xffffffffu, in - w, l));
             c.s = s0 + l;
-            c.q = pa_seq(A, c.s, mt);
+            c.q = pa_seq(A, c.s, __shfl_sync(0xffffffffu, a, l), __shfl_sync(0xffffffffu, b, l), mt);
             const int per = c.q.ntiles + c.ov;
             c.u = x / per;
             const int v = x - c.u * per;
@@ -142,7 +169,8 @@ DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c) {
             c.left = 0;
             return;
         }
-        c.q = pa_seq(A, c.s, mt);
+        const int a = c.q.row0 + c.q.rows;
+        c.q = pa_seq(A, c.s, a, pa_rows_end(A, c.s, a), mt);
     } while (c.q.nunits == 0);
 }
 // The entry of a unit that begins in this CTA's share and has `rest` tiles after it.

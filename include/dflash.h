@@ -535,8 +535,8 @@ typedef struct {
  * n_rows < 2^24.
  * Not held: positions below 0 or from max_pages * page_size on, and positions
  * whose page id lies outside [0, n_pages).  row_start is read clamped to
- * [0, n_rows] and to ascending order; rows outside every sequence are left as
- * they were.
+ * [0, n_rows], a start before one ahead of it in the array as that one (so that
+ * no row has two sequences); rows outside every sequence are left as they were.
  */
 typedef struct {
     int32_t n_seqs;
@@ -642,8 +642,8 @@ DFLASH_API int64_t dflash_paged_attention_workspace(const dflash_paged_cache* ca
  * [n_drafts] rows of f32, target_stride / draft_stride elements apart, vocab
  * contiguous logits each; draft_tok u32 [n_drafts] (dflash_block's logits and
  * draft_tok fit as they are).  accepted, next_tok int32 [n_seqs], prob f32
- * [n_drafts] or NULL.  draft_start is read clamped to [0, n_drafts] and to
- * ascending order; entries of no sequence are left as they were.  n_drafts +
+ * [n_drafts] or NULL.  draft_start is read as row_start is, clamped to [0,
+ * n_drafts]; entries of no sequence are left as they were.  n_drafts +
  * n_seqs < 2^24, vocab < 2^30.
  * workspace: at least dflash_verify_workspace bytes, as for the attention.
  * Errors: EINVAL, ECAPACITY (workspace too small), ECUDA.

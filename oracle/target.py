@@ -10,16 +10,12 @@ import numpy as np
 
 
 def rows_of(n_seqs: int, n_rows: int, row_start=None):
-    """[(sequence, first row, rows)]: clamped to the call's rows and to ascending order."""
+    """[(sequence, first row, rows)]: starts clamped to the call's rows, and none before one ahead of it."""
     if row_start is None:
         per = n_rows // n_seqs if n_seqs else 0
         return [(s, s * per, per) for s in range(n_seqs)]
-    out = []
-    for s in range(n_seqs):
-        a = min(max(int(row_start[s]), 0), n_rows)
-        b = min(max(int(row_start[s + 1]), a), n_rows)
-        out.append((s, a, b - a))
-    return out
+    at = np.maximum.accumulate(np.clip(np.asarray(row_start, np.int64)[:n_seqs + 1], 0, n_rows))
+    return [(s, int(at[s]), int(at[s + 1] - at[s])) for s in range(n_seqs)]
 
 
 def slot_of(table_row, page_size: int, n_pages: int, p: int):
