@@ -126,3 +126,173 @@ def test_verify_of_many_short_sequences_in_clusters_that_start_late():
         assert acc.tolist() == [0] * n
         assert all(g == x for g, (_, x, margin) in zip(got, res) if margin > 1e-5)
         torch.cuda.synchronize()
+
+
+def _define(torch, target, tok, au, su, draft=None, T=1.0):
+    """One draft a sequence (none: tok None), verified by the definition in 64 bits: (kept, token, how far the numbers are
+    from where the answer changes, relative to what is compared, what is left in all)."""
+    soft = lambda x: torch.softmax(x.double() / T, -1)  # noqa: E731
+    n = su.shape[0]
+    rows = target.view(n, -1, target.shape[-1])
+    kept = torch.ones(n, dtype=torch.bool, device="cuda")
+    near = torch.full((n,), np.inf, dtype=torch.float64, device="cuda")
+    rest = soft(rows[:, -1])
+    if tok is not None:
+        p, i = soft(rows[:, 0]), torch.arange(n, device="cuda")
+        q = torch.zeros_like(p).scatter_(1, tok.long()[:, None], 1.0) if draft is None else soft(draft)
+        px, uq = p[i, tok.long()], au.double() * q[i, tok.long()]
+        kept, near = uq < px, (uq - px).abs() / torch.maximum(uq, px)
+        rest = torch.where(kept[:, None], rest, (p - q).clamp(min=0))
+    c = torch.cumsum(rest, -1)
+    whole = c[:, -1:]
+    want = su.double()[:, None] * whole
+    token = (c <= want).sum(-1)
+    near = torch.minimum(near, ((c - want).abs().amin(-1)) / whole[:, 0])
+    return kept, token, near, whole[:, 0]
+
+
+def _compare(torch, got, want):
+    """(accepted, token) against _define's, wherever 64 bits decide: p and q there are off by their exponentials' and
+    divisions' few 2^-53 and the exponents' 2^-53 of up to 40, 4e-15 in all, of what is left."""
+    kept, token, near, whole = want
+    sure = near > torch.maximum(4e-15 / whole, torch.full_like(whole, 1e-12))
+    acc, nxt = got[0].bool(), got[1].long()
+    assert torch.equal(acc[sure], kept[sure]) and torch.equal(nxt[sure], token[sure])
+    return int(sure.sum())
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["float32", "bfloat16"])
+@pytest.mark.parametrize("noise", [0.7, 0.1, 0.01, 0.001, None])
+def test_verify_draws_the_definitions_token(kind, noise):
+    """Hundreds of refused drafts over a whole vocabulary, of drafters from far to very near the target (what is left to
+    draw from is the refused mass, 0.3 down to 0.0003), and drafts that were chosen: every token is the definition's."""
+    torch, dfl = _torch(), _dfl()
+    n, V, T, sure, total, left = 256, 151936, float(np.float32(0.8)), 0, 0, []
+    for seed in range(2):
+        g = torch.Generator("cuda").manual_seed(seed)
+        t = (2.5 * torch.randn(2 * n, V, device="cuda", generator=g)).to(getattr(torch, kind))
+        first = t[0::2].float()
+        d = None if noise is None else first + noise * torch.randn(n, V, device="cuda", generator=g)
+        # a draft that the drafter likes better than the target does (chosen: a likely one), refused by a large number
+        tok = (first if d is None else d.softmax(-1) - first.softmax(-1)).argmax(-1).int()
+        au = torch.full((n,), 1 - 2.0 ** -24, device="cuda")
+        su = torch.rand(n, device="cuda", generator=g)
+        got = dfl.verify_drafts(t, tok, au, su, draft_logits=d, temperature=torch.full((n,), T, device="cuda"))
+        want = _define(torch, t, tok, au, su, d, T)
+        sure, total, left = sure + _compare(torch, got, want), total + n, left + want[3].tolist()
+        assert not want[0].any()
+    assert sure > 0.99 * total
+    if noise is not None:
+        assert 0.1 * noise < np.median(left) < noise
+
+
+def _at_borders(torch, rest, least):
+    """For every row a number in [0, 1) of 32 bits right at a border of the row's running sums: as near as it can be and
+    still more than `least` of the whole away."""
+    c = torch.cumsum(rest, -1)
+    whole = c[:, -1:]
+    share = c / whole
+    u = share.float()
+    away = ((u.double() * whole - c).abs() / whole).masked_fill((u >= 1) | (u <= 0), np.inf)
+    away = away.masked_fill(away < least, np.inf)
+    return u.gather(1, away.argmin(-1, keepdim=True))[:, 0]
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("V", [1000, 151936, 700001])
+@pytest.mark.parametrize("drawn", [None, False, True])
+def test_verify_draws_at_the_borders(kind, V, drawn):
+    """Numbers within 1e-9 to 1e-12 of a border of the running sums, where sums of 32-bit weights do not decide."""
+    torch, dfl = _torch(), _dfl()
+    T = float(np.float32(0.9))
+    for n, seed in ((3, 0), (30, 1)):
+        g = torch.Generator("cuda").manual_seed(seed)
+        t = (2 * torch.randn(n * (1 if drawn is None else 2), V, device="cuda", generator=g)).to(getattr(torch, kind))
+        su, au = torch.zeros(n, device="cuda"), torch.full((n,), 1 - 2.0 ** -24, device="cuda")
+        temps = torch.full((n,), T, device="cuda")
+        soft = lambda x: torch.softmax(x.double() / T, -1)  # noqa: E731
+        d = tok = None
+        if drawn is None:
+            rest = soft(t)
+            tok_in, au_in = torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, device="cuda")
+        else:
+            first = t[0::2].float()
+            if drawn:
+                d = first + 0.3 * torch.randn(n, V, device="cuda", generator=g)
+                q = soft(d)
+                tok = (q - soft(first)).argmax(-1).int()
+            else:
+                tok = first.argmax(-1).int()
+                q = torch.zeros(n, V, dtype=torch.float64, device="cuda").scatter_(1, tok.long()[:, None], 1.0)
+            rest = (soft(first) - q).clamp(min=0)
+            tok_in, au_in = tok, au
+        su = _at_borders(torch, rest, 2e-12)
+        got = dfl.verify_drafts(t, tok_in, au_in, su, draft_logits=d, temperature=temps)
+        want = _define(torch, t, tok, au, su, d, T)
+        acc = (torch.ones(n, device="cuda") if drawn is None else got[0], got[1])
+        assert _compare(torch, acc, want) == n
+
+
+@gpu
+@pytest.mark.parametrize("drawn", [False, True])
+def test_verify_decides_drafts_at_the_border(drawn):
+    """Numbers within 1e-8 to 1e-12 of p / q: kept or refused as 64 bits say."""
+    torch, dfl = _torch(), _dfl()
+    n, V, T = 64, 50000, float(np.float32(0.7))
+    g = torch.Generator("cuda").manual_seed(0)
+    t = 2 * torch.randn(2 * n, V, device="cuda", generator=g)
+    first = t[0::2]
+    d = first + 0.5 * torch.randn(n, V, device="cuda", generator=g) if drawn else None
+    p = torch.softmax(first.double() / T, -1)
+    q = torch.softmax(d.double() / T, -1) if drawn else torch.ones_like(p)
+    ratio = p / q
+    u = ratio.float()
+    away = ((u.double() - ratio).abs() / ratio).masked_fill((u >= 1) | (u < 1e-6), np.inf)
+    away = away.masked_fill(away < 1e-12, np.inf)
+    tok = away.argmin(-1).int()
+    au = u.gather(1, tok.long()[:, None])[:, 0]
+    assert away.amin(-1).max() < 2e-8
+    got = dfl.verify_drafts(t, tok, au, torch.rand(n, device="cuda", generator=g), draft_logits=d,
+                            temperature=torch.full((n,), T, device="cuda"))
+    want = _define(torch, t, tok, au, torch.rand(n, device="cuda", generator=g), d, T)
+    assert torch.equal(got[0].bool(), want[0]) and 0 < got[0].sum() < n
+    # probabilities: 32-bit sums of exponentials, within 2^-20
+    px = (p / q).gather(1, tok.long()[:, None])[:, 0].clamp(max=1)
+    assert ((got[2].double() - px).abs() <= 2.0 ** -20 * px).all()
+
+
+@gpu
+def test_verify_of_the_smallest_numbers_and_sharp_temperatures():
+    torch, dfl = _torch(), _dfl()
+    inf = float("inf")
+    none, empty = torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, device="cuda")
+    # a number of 0 takes the first entry with any probability in 64 bits: masked and vanishing ones come first
+    t = torch.full((4, 3000), -inf, device="cuda")
+    t[:, 2000] = 10.0
+    t[0, 700], t[1, 700], t[2, 700], t[3, 700] = -500.0, -800.0, 9.0, -30.0
+    _, nxt, _ = dfl.verify_drafts(t, none, empty, torch.zeros(4, device="cuda"))
+    assert nxt.tolist() == [700, 2000, 700, 700]
+    # after a refusal: the first entry that the target likes better, however little of either there is
+    t = torch.full((2, 3000), -inf, device="cuda")
+    t[:, 5], t[:, 40], t[:, 1000], t[:, 2000] = -59.0, -70.0, 3.0, 2.9
+    d = t[:1].clone()
+    d[0, 1000], d[0, 5], d[0, 40] = 3.5, -59.0, -75.0
+    acc, nxt, _ = dfl.verify_drafts(t, _i32(torch, [1000]), torch.full((1,), 1 - 2.0 ** -24, device="cuda"),
+                                    torch.zeros(1, device="cuda"), draft_logits=d)
+    p, q = torch.softmax(t[0].double(), -1), torch.softmax(d[0].double(), -1)
+    assert acc.tolist() == [0] and nxt.tolist() == [int((p > q).nonzero()[0])]
+    # exponents past the 32-bit form's range, and at its end
+    g = torch.Generator("cuda").manual_seed(0)
+    for T in (1e-2, 3e-3, 1e-3, 1e-5, 1e-9):
+        T = float(np.float32(T))
+        t = (3 * torch.randn(40, 5000, device="cuda", generator=g)).to(torch.bfloat16)
+        t[:, 3000] = t[:, 17] = t.amax(-1)  # (several entries share what there is)
+        su = torch.rand(40, device="cuda", generator=g)
+        _, nxt, _ = dfl.verify_drafts(t, none, empty, su, temperature=torch.full((40,), T, device="cuda"))
+        x = t.double()
+        c = torch.cumsum(torch.softmax((x - x.amax(-1, keepdim=True)) / T, -1), -1)
+        want = su.double()[:, None] * c[:, -1:]
+        sure = (c - want).abs().amin(-1) > 1e-12
+        assert torch.equal(nxt.long()[sure], (c <= want).sum(-1)[sure]) and sure.sum() > 35
