@@ -33,7 +33,9 @@
 // A key that some rows see and others do not (the new rows among themselves, a
 // window's edge) is masked per row; P is then 0 there, and 0 times an infinite
 // or NaN value would not be, so such stages look for non-finite values and,
-// where there are any, add P V row by row with the hidden keys left out.
+// where there are any, add P V row by row with the hidden keys left out.  What
+// an infinite value that every row sees makes of the products, the join's kernel
+// mends (pa_odd_row).
 #include "kernels.cuh"
 #include "paged_attn.cuh"
 
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
 
     int chunk;
     PaCur cur = pa_share(A, MT, kPaOver, lane, chunk);
-    if (threadIdx.x == 0) A.ws_join[blockIdx.x].last = -1;
+    if (threadIdx.x == 0) A.ws_join[blockIdx.x].last = -1, A.ws_odd[blockIdx.x] = 0;
     if (cur.left <= 0) return;
 
     // ---------------------------------------------------------------- copies
@@ -511,11 +513,13 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
                     const float inv = l[e] == 0.f ? 0.f : vs / l[e];
                     unsigned char* p = A.out.p + (int64_t)r * A.out.rs + (int64_t)hq * A.out.hs;
                     const bool ob = A.out.dtype == kBF16;
+                    bool odd = false;
 #pragma unroll
                     for (int f = 0; f < NF; f += E8 ? 2 : 1) {
                         auto w2 = [&](int col, float x, float y) {
                             *reinterpret_cast<uint32_t*>(p + col * 2) =
                                 ob ? pack2<true>(x * inv, y * inv) : pack2<false>(x * inv, y * inv);
+                            if constexpr (!E8) odd |= x != x || y != y;
                         };
                         if constexpr (E8) {
                             w2(8 * f + 4 * tq, o[f][2 * e], o[f + 1][2 * e]);
@@ -523,6 +527,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
                         } else {
                             w2(8 * f + 2 * tq, o[f][2 * e], o[f][2 * e + 1]);
                         }
+                    }
+                    if (!E8 && odd && pa_weighs(l[e])) {  // (columns of the other lanes' too: they wrote NaN, or will mark it)
+                        pa_mark_odd<BF>(p, HD);
+                        A.ws_odd[blockIdx.x] = 1;
                     }
                     if (A.lse != nullptr && tq == 0)
                         A.lse[(int64_t)r * A.q.heads + hq] =
@@ -544,27 +552,85 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
     }
 }
 
+// Row r, head hq of the output: NaN that is kept apart becomes the sum of the column's values that are not finite over
+// the keys in the row's view.  By a warp; in little code, which all calls carry and few run (with its loops unrolled and a
+// form for each type it took 6 us of a call's 40, one block over 32768 keys, though nothing of it ran).
+template <int HD>
+DF_DEV void pa_odd_row(const PaArgs& A, int r, int hq) {
+    constexpr int V = HD / 32;  // columns a lane
+    const int lane = threadIdx.x & 31, h = hq / A.group;
+    const bool bf = A.out.dtype == kBF16;
+    const uint32_t top = bf ? 0x7f807f80u : 0x7c007c00u, mark = bf ? kPaOdd<true> : kPaOdd<false>;
+    uint16_t* out = reinterpret_cast<uint16_t*>(A.out.p + (int64_t)r * A.out.rs + (int64_t)hq * A.out.hs) + V * lane;
+    uint32_t which = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) which |= (uint32_t)(out[i] == mark) << i;
+    if (!__any_sync(0xffffffffu, which)) return;
+    const int s = seq_of(A.R, r);
+    if (s < 0) return;
+    int a, b;
+    rows_of(A.R, s, a, b);
+    const int pos = pa_seq(A, s, a, b, kPaM).p0 + r - a;
+    float sum[V] = {};
+#pragma unroll 1
+    for (int j0 = A.window > 0 ? max(0, pos - A.window + 1) : 0; j0 <= pos && j0 < A.R.cap; j0 += 32) {
+        int slot = 0;
+        const int64_t page = j0 + lane <= pos ? page_of(A.R, A.C.n_pages, s, j0 + lane, slot) : -1;
+        const int64_t at = page < 0 ? -1 : page * A.C.vs[0] + slot * A.C.vs[1] + h * A.C.vs[2];
+        const int64_t key = page * A.C.ks[0] + slot * A.C.ks[1] + h * A.C.ks[2];
+        bool odd = false;
+        if (page >= 0) {
+#pragma unroll 2
+            for (int c = 0; c < HD / 2; ++c) {
+                const uint32_t x = ~reinterpret_cast<const uint32_t*>(A.C.v + at)[c] & top;
+                odd |= (x & 0xffffu) == 0 || x < 0x10000u;
+            }
+        }
+#pragma unroll 1
+        for (uint32_t found = __ballot_sync(0xffffffffu, odd); found != 0; found &= found - 1) {
+            const int l = __ffs(found) - 1;
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(A.C.v + __shfl_sync(0xffffffffu, at, l)) + V * lane;
+            const uint16_t* k = reinterpret_cast<const uint16_t*>(A.C.k + __shfl_sync(0xffffffffu, key, l)) + V * lane;
+            // (the row's weights are finite: with a key that is not, the score was -inf)
+            bool fine = true;
+#pragma unroll
+            for (int i = 0; i < V; ++i) fine &= (~k[i] & top & 0xffffu) != 0;
+            const float times = __all_sync(0xffffffffu, fine) ? 1.f : 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if ((~v[i] & top & 0xffffu) == 0)
+                    sum[i] += times * (v[i] & ~top & 0x7fffu ? NAN : v[i] & 0x8000u ? -INFINITY : INFINITY);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if ((which >> i) & 1u)
+            out[i] = (uint16_t)(sum[i] == 0.f || sum[i] != sum[i] ? 0x7fffu : (top & 0xffffu) | (sum[i] < 0.f ? 0x8000u : 0u));
+}
 // The shared units' parts joined: CTA (c, y) takes rows 16 y .. of the unit that
 // starts in share c and ends in another, a warp a row.
 template <int HD>
 __global__ void __launch_bounds__(kPaThreads) paged_join_kernel(const __grid_constant__ PaArgs A, int mt, int e8) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
+    const int odd = A.ws_odd[blockIdx.x];
+    bool any = false;
     const PaJoin e = A.ws_join[blockIdx.x];
     const int c0 = blockIdx.x, c1 = e.last, h = e.head;
-    if (c1 <= c0) return;
+    if (c1 > c0) {
 #pragma unroll 1
     for (int mrow = 16 * blockIdx.y + warp; mrow < min(e.rows, 16 * (int)blockIdx.y + 16); mrow += kPaWarps) {
     const int mm = e.m0 + mrow, row = e.row0 + mm / A.group, hq = h * A.group + mm % A.group;
     constexpr int V = HD / 32;  // columns a lane
     float m = -INFINITY, l = 0.f, o[V] = {};
-    // parts in order, 32 references and sums at a time, 16 outputs in flight
+    // parts in order, 32 references and sums at a time, 8 outputs in flight (16 are more code: 40.3 -> 42.6 us, one block
+    // over 32768 keys)
     for (int b = c0; b <= c1; b += 32) {
         const int n = min(32, c1 - b + 1);
         float2 x = make_float2(-INFINITY, 0.f);
         auto slot = [&](int c) { return (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * mt + mrow; };
         if (lane < n) x = A.ws_ml[slot(b + lane)];
-        constexpr int U = 16;
+        constexpr int U = 8;
         float y[U][V];
         auto load = [&](int k0) {
 #pragma unroll
@@ -609,6 +675,28 @@ __global__ void __launch_bounds__(kPaThreads) paged_join_kernel(const __grid_con
     if (A.lse != nullptr && lane == 0)
         A.lse[(int64_t)row * A.q.heads + hq] =
             l == 0.f ? -INFINITY : (m == -INFINITY ? l : (m + log2f(l)) * 0.69314718056f);
+    if (!e8 && pa_weighs(l)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (o[i] != o[i]) {
+                reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(A.out.dtype == kBF16 ? kPaOdd<true> : kPaOdd<false>);
+                any = true;
+            }
+    }
+    }
+    }
+    // this warp's joined rows with NaN that is kept apart, then all of the call's where the share's whole units have some
+    // (rows that others join and see to themselves among them: both write the same)
+    any = __any_sync(0xffffffffu, any);
+    if (!any && odd == 0) return;
+    const uint32_t joined = any ? min(16, e.rows - 16 * (int)blockIdx.y) : 0,
+                   all = odd != 0 ? (uint32_t)A.R.n_rows * A.q.heads : 0;  // (under 2^31: check_heads)
+#pragma unroll 1
+    for (uint32_t i = warp; i < 16 + all; i += kPaWarps) {
+        if (i < 16 && i >= joined) continue;
+        // rows of a unit are group by group, rows of the call heads by heads
+        const uint32_t per = i < 16 ? A.group : A.q.heads, at = i < 16 ? e.m0 + 16 * blockIdx.y + i : i - 16, r = at / per;
+        pa_odd_row<HD>(A, (int)r + (i < 16 ? e.row0 : 0), (int)(at - r * per) + (i < 16 ? h * A.group : 0));
     }
 }
 
@@ -626,7 +714,7 @@ static int pa_tile_rows(int n_seqs, int64_t n_rows, int group) {
 
 int64_t paged_attention_workspace(int hd, int n_seqs, int64_t n_rows, int heads, int kv_heads, int num_sms) {
     const int64_t mt = pa_tile_rows(n_seqs, n_rows, heads / kv_heads);
-    return num_sms * (2 * mt * (hd * 4 + 8) + (int64_t)sizeof(PaJoin));
+    return num_sms * (2 * mt * (hd * 4 + 8) + (int64_t)sizeof(PaJoin) + (int64_t)sizeof(int32_t));
 }
 
 template <bool BF, bool E8, int HD>
@@ -657,6 +745,7 @@ int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRow
     A.ws_o = static_cast<float*>(ws);
     A.ws_ml = reinterpret_cast<float2*>(A.ws_o + 2 * (int64_t)num_sms * mt * hd);
     A.ws_join = reinterpret_cast<PaJoin*>(A.ws_ml + 2 * (int64_t)num_sms * mt);
+    A.ws_odd = reinterpret_cast<int32_t*>(A.ws_join + num_sms);
     const int e = mt > kPaM ? paged_attention_tc(A, cache_dtype, hd, mt, num_sms, st)
                   : hd == 64 ? pa_type<64>(A, cache_dtype, num_sms, st)
                              : pa_type<128>(A, cache_dtype, num_sms, st);

@@ -58,8 +58,6 @@ constexpr int kPtM = 128;
 constexpr int kPtSoft = 128;  // softmax threads: warps 0-3
 constexpr int kPtQk = kPtSoft / 32, kPtPv = kPtQk + 1, kPtLoad = kPtPv + 1;  // warps
 constexpr uint64_t kPtWait = 1000000000ull;
-// tiles' time that a unit's end and the next one's beginning take (32 blocks over a bf16 cache: 0 81.7 us, 2 73.3, 4 71.1)
-constexpr int kPtOver = 4;
 constexpr int kPtBits = 16;  // tiles whose key masks are kept: more than the loaders can be ahead of the softmax
 
 template <bool BF, bool E8, int HD>
@@ -138,10 +136,6 @@ DF_DEV bool pt_soft_or(bool v) {
         : "r"((uint32_t)v), "n"(kPtSoft)
         : "memory");
     return r != 0;
-}
-template <bool BF>
-DF_DEV bool finite16(uint32_t h) {
-    return BF ? (h & 0x7f80u) != 0x7f80u : (h & 0x7c00u) != 0x7c00u;
 }
 // the part of a unit that a share holds: from c on
 DF_DEV int pt_tiles(const PaCur& c) { return min(c.q.ntiles - c.tile, c.left); }
@@ -261,7 +255,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
     // this CTA's share of the line
     int chunk;
     const PaCur cur = pa_share(A, MT, kPtOver, lane, chunk);
-    if (threadIdx.x == 0) A.ws_join[blockIdx.x].last = -1;
+    if (threadIdx.x == 0) A.ws_join[blockIdx.x].last = -1, A.ws_odd[blockIdx.x] = 0;
 
     if (S::kQueryWarps > 0 && warp >= kPtLoad + 2 * S::kLoadWarps) {
         // ------------------------------------------------------------ queries (an e4m3 cache's)
@@ -711,6 +705,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
             unsigned char* op = A.out.p + (int64_t)row * A.out.rs + (int64_t)hq * A.out.hs;
             float* wp = A.ws_o + ((int64_t)part * MT + r) * HD;
             const bool ob = A.out.dtype == kBF16;
+            bool odd = false;
 #pragma unroll 1
             for (int x = 0; x < HD; x += 16) {
                 float o[16];
@@ -742,6 +737,10 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                     for (int j = 0; j < 8; ++j)
                         w[j] = ob ? pack2<true>(o[2 * j] * inv, o[2 * j + 1] * inv)
                                   : pack2<false>(o[2 * j] * inv, o[2 * j + 1] * inv);
+                    if constexpr (!E8) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) odd |= o[j] != o[j];
+                    }
                     *reinterpret_cast<uint4*>(op + 2 * x) = make_uint4(w[0], w[1], w[2], w[3]);
                     *reinterpret_cast<uint4*>(op + 2 * x + 16) = make_uint4(w[4], w[5], w[6], w[7]);
                 } else {
@@ -749,6 +748,10 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                     for (int j = 0; j < 16; j += 4)
                         *reinterpret_cast<float4*>(wp + x + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                 }
+            }
+            if (!E8 && odd && pa_weighs(l)) {
+                pa_mark_odd<BF>(op, HD);
+                A.ws_odd[blockIdx.x] = 1;
             }
             if (in && copy == 0) {
                 if (!whole)

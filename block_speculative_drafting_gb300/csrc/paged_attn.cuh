@@ -23,6 +23,7 @@ struct PaArgs {
     float* ws_o;     // [2 CTAs][MT][HD]
     float2* ws_ml;   // [2 CTAs][MT]
     struct PaJoin* ws_join;  // [CTAs]
+    int32_t* ws_odd;         // [CTAs]: outputs of the CTA's whole units wait for pa_odd_row
     float scale_log2;
     int window, group;
 };
@@ -31,7 +32,7 @@ struct PaArgs {
 // its parts are this CTA's second slot and the first slots of the CTAs up to
 // `last` (below 0: this CTA starts no such unit).
 struct __align__(16) PaJoin {
-    int32_t last, row0, m0, rows, head, pad[3];  // rows from m0 on of the sequence whose rows start at row0; kv head
+    int32_t last, row0, m0, rows, head, seq, pad[2];  // rows from m0 on of sequence seq, whose rows start at row0; kv head
 };
 
 // What the walk needs of one sequence.
@@ -181,6 +182,7 @@ DF_DEV PaJoin pa_join_entry(const PaCur& c, int rt, int mt, int rows, int head, 
     e.m0 = rt * mt;
     e.rows = rows;
     e.head = head;
+    e.seq = c.s;
     return e;
 }
 
@@ -229,11 +231,36 @@ DF_DEV float2 unpack2(uint32_t u) {
         return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
+// A value that is infinite, at a key in a row's view, makes that column of the row infinite (NaN where both signs meet, or
+// where the key's weight is 0 because its score is -inf).  The products do not see to that: a weight goes in as a hi + lo
+// pair, whose lo may be 0 or below, a row on two lanes multiplies the other lane's keys by 0, and a moved reference may
+// multiply by 0.  All of these give NaN, so outputs that are NaN though the row's weights are not are kept apart by a NaN of
+// their own (FMA gives 0x7fff) until the join's kernel looks over the row's keys for values that are not finite (pa_odd_row).
+template <bool BF>
+constexpr uint32_t kPaOdd = BF ? 0x7fc1u : 0x7e01u;
+template <bool BF>
+DF_DEV bool finite16(uint32_t h) {
+    return BF ? (h & 0x7f80u) != 0x7f80u : (h & 0x7c00u) != 0x7c00u;
+}
+// whether a sum of weights is one (not 0, NaN or infinite)
+DF_DEV bool pa_weighs(float l) { return l > 0.f && l < INFINITY; }
+// An output row's NaN made the one kept apart, by one thread.
+template <bool BF>
+DF_DEV void pa_mark_odd(unsigned char* row, int hd) {
+    uint16_t* x = reinterpret_cast<uint16_t*>(row);
+#pragma unroll 1
+    for (int d = 0; d < hd; ++d)
+        if ((x[d] & 0x7fffu) > (BF ? 0x7f80u : 0x7c00u)) x[d] = (uint16_t)kPaOdd<BF>;
+}
+
 // Whether the places of any line of such a call stay below 2^31.
 inline bool pa_line_fits(const PagedRows& R, int heads, int kv_heads) {
     const double units = (double)R.n_rows * heads / 16 + (double)R.n_seqs * kv_heads;
     return units * ((double)R.cap / kPaTile + 8) < 2147483648.0;
 }
+// tiles' time that a unit's end and the next one's beginning take in the tcgen05 kernel (32 blocks over a
+// bf16 cache: 0 81.7 us, 2 73.3, 4 71.1)
+constexpr int kPtOver = 4;
 // The tcgen05 kernel (k_paged_attn_tc.cu): units of up to mt = 64 or 128 rows.
 int paged_attention_tc(const PaArgs& A, int cache_dtype, int hd, int mt, int num_sms, cudaStream_t st);
 

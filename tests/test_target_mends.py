@@ -296,3 +296,60 @@ def test_verify_of_the_smallest_numbers_and_sharp_temperatures():
         want = su.double()[:, None] * c[:, -1:]
         sure = (c - want).abs().amin(-1) > 1e-12
         assert torch.equal(nxt.long()[sure], (c <= want).sum(-1)[sure]) and sure.sum() > 35
+
+
+# --------------------------------------------------------------------------- attention
+def _odd_values(torch, kc, vc, table):
+    """Values that are not finite at keys that every row sees, early in each sequence: +inf; both signs in one column and
+    in two; NaN beside an infinity; an infinity at a key that is not finite itself (the score is -inf for half of the rows,
+    +inf for the others); most of a row; and sequences without any."""
+    inf, page = float("inf"), kc.shape[1]
+    for s in range(len(table)):
+        at = lambda p: (int(table[s][p // page]), p % page)  # noqa: E731
+        (p0, s0), (p1, s1) = at(3), at(40)
+        h = s % kc.shape[2]
+        kind = s % 7
+        if kind == 1:
+            vc[p0, s0, h, 1] = inf
+        elif kind == 2:
+            vc[p0, s0, h, 2], vc[p1, s1, h, 2], vc[p1, s1, h, 9], vc[p0, s0, h, 33] = inf, -inf, -inf, inf
+        elif kind == 3:
+            vc[p0, s0, h, 4], vc[p1, s1, h, 4], vc[p0, s0, h, 5] = float("nan"), inf, -inf
+        elif kind == 4:
+            vc[p1, s1, h, 6], vc[p0, s0, h, 7], kc[p1, s1, h, 5] = inf, -inf, inf
+        elif kind == 5:
+            vc[p0, s0, h, ::2] = -inf
+        elif kind == 6:
+            vc[p1, s1, h, 60:] = inf
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows,heads,kvh", [(1, 2, 2), (3, 4, 1), (10, 8, 2), (16, 16, 2)])  # 1, 12, 40, 128 rows a unit
+@pytest.mark.parametrize("n,lens,window", [(7, 2000, 0), (7, 700, 690), (80, 200, 0)])  # units split over SMs, and whole ones
+def test_attention_of_values_that_are_not_finite(kind, hd, rows, heads, kvh, n, lens, window):
+    from test_target_ops import _check_attention
+    _check_attention(kind, hd=hd, heads=heads, kvh=kvh, rows=(rows,) * n, lens=tuple(lens + 5 * i for i in range(n)),
+                     window=window, poison=_odd_values, seed=rows)
+
+
+@gpu
+@pytest.mark.parametrize("rows,heads", [(1, 2), (12, 8)])
+def test_attention_of_an_infinity_before_the_reference_moves(rows, heads):
+    """An infinite value whose weight vanishes against a later key's is infinite all the same; what overflows stays NaN or
+    infinite, and other rows, heads and columns keep their bits."""
+    torch, dfl = _torch(), _dfl()
+    rng = np.random.default_rng(0)
+    kc = torch.from_numpy(rng.standard_normal((64, 16, 1, 64)).astype(np.float32)).cuda().to(torch.bfloat16)
+    vc = torch.from_numpy(rng.standard_normal((64, 16, 1, 64)).astype(np.float32)).cuda().to(torch.bfloat16)
+    q = torch.from_numpy(rng.standard_normal((rows, heads, 64)).astype(np.float32)).cuda().to(torch.bfloat16)
+    q[..., 0] = 8.0
+    kc[60, 0, 0, 0] = 256.0  # the score there is 256 above the others': 369 in powers of two
+    args = (_i32(torch, np.arange(64)[None]), _i32(torch, [1024]))
+    want = dfl.paged_attention(q, kc, vc, *args)
+    vc[2, 5, 0, 7] = float("-inf")
+    got = dfl.paged_attention(q, kc, vc, *args)
+    assert (got[..., 7] == float("-inf")).all()
+    got[..., 7] = want[..., 7]
+    assert torch.equal(got, want) and torch.isfinite(want).all()
