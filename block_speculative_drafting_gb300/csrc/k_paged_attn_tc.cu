@@ -9,11 +9,12 @@
 // O += P V (V as stored, the MN-major B operand; O in tensor memory).  Two S
 // buffers: the next tile's scores are multiplied while this tile's softmax
 // runs.  m moves only where a row's maximum passes it by some powers of two; O
-// is then rescaled in place.  A 16-bit cache's P is a hi + lo pair (the products then
-// add no rounding of their own to the output's; the tensor pipe has the time:
-// a tile's MMAs take 0.8 us, its 64 KB 1.4 us of this SM's share of the
-// memory); an e4m3 cache's, whose tile is half the bytes, is one f16 (2^-12
-// relative, under a bf16 output's 2^-9).
+// is then rescaled in place.  P is a hi + lo pair (the products then add no
+// rounding of their own to the output's; with a 16-bit cache the tensor pipe has the
+// time: a tile's MMAs take 0.8 us, its 64 KB 1.4 us of this SM's share of the
+// memory).  Only bf16 outputs over an e4m3 cache take P as one f16: off by 2^-11 of
+// each key's part at most, an eighth of the output's own 2^-8, where the pair costs
+// 17 % (32 blocks 65.5 -> 76.5 us: the softmax's registers and conversions).
 //
 // An MMA of M 128 costs what it costs with fewer rows, so a unit of up to 64
 // rows holds every query twice: lanes r and r + 64 take the lower and the upper
@@ -60,6 +61,7 @@ constexpr int kPtQk = kPtSoft / 32, kPtPv = kPtQk + 1, kPtLoad = kPtPv + 1;  // 
 constexpr uint64_t kPtWait = 1000000000ull;
 constexpr int kPtBits = 16;  // tiles whose key masks are kept: more than the loaders can be ahead of the softmax
 
+// BF: queries and outputs in bf16 (else f16), and a 16-bit cache with them; E8: an e4m3 cache
 template <bool BF, bool E8, int HD>
 struct PtShape {
     static constexpr int kLoadWarps = 4;  // of the keys, and as many of the values
@@ -72,7 +74,7 @@ struct PtShape {
     // e4m3: half tiles of codes on their way, 16 bytes a place, each place copied and read by one thread
     static constexpr int kRaw = E8 ? 4 * (128 / HD) : 0, kRawLd = KPW * HD / 16 / 64;
     static constexpr int kRawBytes = kRaw * kRawLd * 16 * 2 * kLoaders;
-    static constexpr bool kSplitP = !E8;
+    static constexpr bool kSplitP = !E8 || !BF;
     static constexpr int kCtl = 15 * 1024;
     static constexpr size_t kSmem = 1024 /*alignment*/ + kCtl + 2 * (size_t)kSlots * kItem + kRawBytes;
     // tensor memory: two S / P buffers, O, Q
@@ -149,7 +151,7 @@ DF_DEV void pt_skip(const PaArgs& A, PaCur& c, int n) {
 // A unit's queries to tensor memory at `to` (row t % MT of the unit), after `free` has waited for it.  An 8-bit cache's
 // warps of queries: a bf16 row is brought into f16 by a power of two, left in ctl.rf, its halves read for their largest
 // element and then again (registers).
-template <bool E8, int HD, int MT, class F>
+template <bool BF, bool E8, int HD, int MT, class F>
 DF_DEV bool pt_queries(const PaArgs& A, PtCtl& ctl, const PaCur& c, int unit, int t, uint32_t to, F free) {
     constexpr int kHalves = E8 ? 2 : 1, NX = HD / 8 / kHalves;
     const int h = c.u % A.C.kv_heads, mm = (c.u / A.C.kv_heads) * MT + t % MT;
@@ -166,7 +168,7 @@ DF_DEV bool pt_queries(const PaArgs& A, PtCtl& ctl, const PaCur& c, int unit, in
     float rf = 1.f, down = 1.f;
     if constexpr (!E8) {
         load(0);
-    } else if (A.q.dtype == kBF16) {
+    } else if constexpr (BF) {
         float mx = 0.f;
 #pragma unroll 1
         for (int half = 0; half < kHalves; ++half) {
@@ -191,7 +193,7 @@ DF_DEV bool pt_queries(const PaArgs& A, PtCtl& ctl, const PaCur& c, int unit, in
     for (int half = 0; half < kHalves; ++half) {
         if constexpr (E8) {
             load(half);
-            if (A.q.dtype == kBF16) {
+            if constexpr (BF) {
 #pragma unroll
                 for (int j = 0; j < 4 * NX; ++j) {
                     const float2 f = unpack2<true>(w[j]);
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
             auto free = [&]() {
                 return unit == 0 || __all_sync(0xffffffffu, mbar_wait(&ctl.q_free, (unit - 1) & 1, kPtWait));
             };
-            if (!pt_queries<E8, HD, MT>(A, ctl, c, unit, t, tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kColQ, free))
+            if (!pt_queries<BF, E8, HD, MT>(A, ctl, c, unit, t, tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kColQ, free))
                 break;
             pt_skip<MT>(A, c, pt_tiles(c));
         }
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
         PaCur c = cur;
         auto queries = [&]() {  // (where no warps of their own bring them)
             if (S::kQueryWarps == 0 && c.left > 0)
-                pt_queries<E8, HD, MT>(A, ctl, c, unit, t, lane_addr + S::kColQ, []() { return true; });
+                pt_queries<BF, E8, HD, MT>(A, ctl, c, unit, t, lane_addr + S::kColQ, []() { return true; });
         };
         queries();
         while (c.left > 0) {
@@ -704,7 +706,6 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
             const float inv = l == 0.f ? 0.f : vs / l;
             unsigned char* op = A.out.p + (int64_t)row * A.out.rs + (int64_t)hq * A.out.hs;
             float* wp = A.ws_o + ((int64_t)part * MT + r) * HD;
-            const bool ob = A.out.dtype == kBF16;
             bool odd = false;
 #pragma unroll 1
             for (int x = 0; x < HD; x += 16) {
@@ -735,8 +736,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                     uint32_t w[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        w[j] = ob ? pack2<true>(o[2 * j] * inv, o[2 * j + 1] * inv)
-                                  : pack2<false>(o[2 * j] * inv, o[2 * j + 1] * inv);
+                        w[j] = pack2<BF>(o[2 * j] * inv, o[2 * j + 1] * inv);
                     if constexpr (!E8) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) odd |= o[j] != o[j];
@@ -785,6 +785,7 @@ template <int HD, int MT>
 static int pt_type(const PaArgs& A, int cache_dtype, int num_sms, cudaStream_t st) {
     return cache_dtype == kBF16  ? pt_launch<true, false, HD, MT>(A, num_sms, st)
            : cache_dtype == kF16 ? pt_launch<false, false, HD, MT>(A, num_sms, st)
+           : A.q.dtype == kBF16 ? pt_launch<true, true, HD, MT>(A, num_sms, st)
                                  : pt_launch<false, true, HD, MT>(A, num_sms, st);
 }
 

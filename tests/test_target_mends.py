@@ -353,3 +353,26 @@ def test_attention_of_an_infinity_before_the_reference_moves(rows, heads):
     assert (got[..., 7] == float("-inf")).all()
     got[..., 7] = want[..., 7]
     assert torch.equal(got, want) and torch.isfinite(want).all()
+
+
+@gpu
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows,heads,kvh", [(5, 8, 2), (16, 8, 2), (16, 16, 2)])  # 20, 64 and 128 rows a unit
+@pytest.mark.parametrize("lens", [300, 3000])
+def test_attention_of_f16_blocks_over_an_8_bit_cache_rounds_once(hd, rows, heads, kvh, lens):
+    """f16 queries over an e4m3 cache: weights add no rounding of their own, however many rows share the keys.  Every key but
+    one in 64 weighs 65.03125 / 128 of those, which one f16 takes for 65 or 65.0625, 2^-11 off; all values are 1.875, and
+    so is the result, to 2^-18 before its one rounding."""
+    torch, dfl = _torch(), _dfl()
+    page, n = 16, lens // 16 + 1
+    scale = float(np.log(128 / 65.03125))
+    q = torch.zeros(rows, heads, hd, device="cuda", dtype=torch.float16)
+    q[..., 3] = 1.0
+    kc = torch.zeros(n, page, kvh, hd, device="cuda")
+    kc[..., 3] = -1.0
+    kc[::4, 0, :, 3] = 0.0
+    vc = torch.full_like(kc, 1.875)
+    kc, vc = kc.to(torch.float8_e4m3fn), vc.to(torch.float8_e4m3fn)
+    out = dfl.paged_attention(q, kc, vc, torch.arange(n, device="cuda", dtype=torch.int32)[None], _i32(torch, [lens]),
+                              scale=scale)
+    assert (out == 1.875).all(), out.float().unique()
