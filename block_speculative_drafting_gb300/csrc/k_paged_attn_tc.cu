@@ -226,7 +226,8 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * S::kSlots; ++i) {
-            mbar_init(&ctl.full[i & 1][i >> 1], S::kLoaders);
+            // (16-bit keys' copies arrive by themselves; their warps arrive beside them for the key masks)
+            mbar_init(&ctl.full[i & 1][i >> 1], S::kLoaders + (!E8 && (i & 1) == 0 ? S::kLoadWarps : 0));
             mbar_init(&ctl.empty[i & 1][i >> 1], 1);
         }
         // (the commit, and an arrival of the MMA thread's own that orders the key masks)
@@ -330,6 +331,8 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                 // arrives once this thread's copies have landed
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_addr(&ctl.full[side][n % S::kSlots]))
                              : "memory");
+                // (that follows the copies alone: the tile's key mask, written by this lane, takes an arrival of its own)
+                if (side == 0 && lane == 0) mbar_arrive(&ctl.full[0][n % S::kSlots]);
                 ++n;
                 return true;
             });

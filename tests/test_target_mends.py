@@ -376,3 +376,25 @@ def test_attention_of_f16_blocks_over_an_8_bit_cache_rounds_once(hd, rows, heads
     out = dfl.paged_attention(q, kc, vc, torch.arange(n, device="cuda", dtype=torch.int32)[None], _i32(torch, [lens]),
                               scale=scale)
     assert (out == 1.875).all(), out.float().unique()
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_attention_of_blocks_keeps_every_tiles_key_mask(kind):
+    """Blocks over contexts with a third of their pages not held: each tile's keys have a mask of their own, which the
+    loaders write while tiles before it are worked on.  Right once, and the same bits in every repetition."""
+    torch, dfl = _torch(), _dfl()
+    from test_target_ops import _check_attention, _types
+    bad = tuple((s, i) for s in range(3) for i in range((s + 1) % 3, 60, 3))
+    _check_attention(kind, heads=8, kvh=2, rows=(9, 16, 5), lens=(950, 970, 955), bad=bad, seed=7)
+    rng = np.random.default_rng(3)
+    n, pages, width = 24, 2000, 80
+    table = rng.integers(0, pages, (n, width)).astype(np.int32)
+    table[rng.random((n, width)) < 0.33] = -1
+    kc, vc = (torch.randn(pages, 16, 2, 128, device="cuda").to(_types()[kind]) for _ in range(2))
+    q = torch.randn(n * 16, 8, 128, device="cuda").to(_types()[kind])
+    args = (kc, vc, _i32(torch, table), _i32(torch, rng.integers(900, 1280, n)))
+    want = dfl.paged_attention(q, *args)
+    assert torch.isfinite(want).all()
+    for _ in range(50):
+        assert torch.equal(dfl.paged_attention(q, *args), want)
