@@ -146,14 +146,9 @@ DF_DEV void head_loop(const HeadLoop& H, const float (&co)[8], const float (&si)
             }
             if (h < H.heads) {
                 if (H.scale != nullptr) {
-                    // the rounded quotient by the reciprocal and one correction from the remainder (a quotient
-                    // that is clamped or not finite has none)
-                    const float sc = H.scale[h], inv = __frcp_rn(sc);
+                    const float sc = H.scale[h];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float y = x[j] * inv;
-                        x[j] = fabsf(y) < 1024.f ? fmaf(fmaf(-y, sc, x[j]), inv, y) : y;
-                    }
+                    for (int j = 0; j < 8; ++j) x[j] = __fdiv_rn(x[j], sc);
                 }
                 store8<OUT>(to, x);
             }

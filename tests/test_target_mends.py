@@ -298,6 +298,34 @@ def test_verify_of_the_smallest_numbers_and_sharp_temperatures():
         assert torch.equal(nxt.long()[sure], (c <= want).sum(-1)[sure]) and sure.sum() > 35
 
 
+# --------------------------------------------------------------------------- append
+@gpu
+@pytest.mark.parametrize("src", ["float32", "bfloat16"])
+def test_append_rounds_the_quotient(src):
+    """An 8-bit cache's codes are those of the f32 quotient x / scale, rounded once each: values around every step of the
+    codes and far beyond, scales over f32's range."""
+    torch, dfl = _torch(), _dfl()
+    rng = np.random.default_rng(0)
+    scales = np.array([1.0, 0.1, 3.0, 1 / 3, 2.0 ** -126, 2.0 ** 126, 3.3e38, 0.07, 1e-10, 448.0, 1e20, 7e-7], np.float32)
+    rows, kvh, hd = 64, len(scales), 128
+    code = np.frombuffer(np.arange(256, dtype=np.uint8).tobytes(), np.uint8)
+    steps = torch.from_numpy(code.copy()).view(torch.float8_e4m3fn).float().numpy()
+    steps = np.sort(steps[np.isfinite(steps)])
+    mids = np.concatenate((steps, (steps[1:] + steps[:-1]) / 2, [1e4, -1e9, 0.0]))
+    x = (rng.choice(mids, (rows, kvh, hd)) * (1 + rng.integers(-2, 3, (rows, kvh, hd)) * 2.0 ** -23)).astype(np.float32)
+    with np.errstate(all="ignore"):
+        x = (x * scales[:, None]).astype(np.float32)
+        x[~np.isfinite(x)] = 3.4e38
+        x = torch.from_numpy(x).to(getattr(torch, src))
+        want = torch.from_numpy(np.clip(x.float().numpy() / scales[:, None], -448, 448)).to(torch.float8_e4m3fn)
+    kc = torch.zeros(rows, 1, kvh, hd, device="cuda").to(torch.float8_e4m3fn)
+    vc, sc = kc.clone(), torch.from_numpy(scales).cuda()
+    dfl.paged_append(kc, vc, x.cuda(), x.cuda(), torch.arange(rows, device="cuda", dtype=torch.int32)[None],
+                     _i32(torch, [rows]), k_scale=sc, v_scale=sc)
+    for c in (kc, vc):
+        assert torch.equal(c.view(torch.uint8)[:, 0].cpu(), want.view(torch.uint8))
+
+
 # --------------------------------------------------------------------------- attention
 def _odd_values(torch, kc, vc, table):
     """Values that are not finite at keys that every row sees, early in each sequence: +inf; both signs in one column and
