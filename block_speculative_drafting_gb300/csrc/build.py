@@ -22,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdflash.so")
 BINDING = os.path.join(PKG, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+BOUND_FOR = os.path.join(BUILD, "binding.txt")
 SOURCES = ["api.cu", "k_quant.cu", "k_gemm.cu", "k_layer.cu", "k_stream.cu", "k_tc.cu", "k_tc_pair.cu",
            "k_attn_tc.cu", "ops.cu", "k_paged_append.cu", "k_paged_attn.cu", "k_paged_attn_tc.cu",
            "k_verify.cu"]
@@ -44,6 +45,14 @@ def _needs(out: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _text(path: str):
+    try:
+        with open(path) as f:
+            return f.read()
+    except FileNotFoundError:
+        return None
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(HERE, f) for f in os.listdir(HERE) if f.endswith((".cuh", ".h"))]
@@ -64,16 +73,21 @@ def build(verbose: bool = False, force: bool = False) -> str:
 
     def compile_binding() -> None:
         src = os.path.join(HERE, "binding.cpp")
-        if force or _needs(BINDING, [src] + headers):
-            torch = os.path.dirname(importlib.util.find_spec("torch").origin)
-            cuda = os.path.dirname(os.path.dirname(shutil.which(nvcc()) or "/usr/local/cuda/bin/nvcc"))
-            cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-                   "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(cuda, "include"),
-                   "-isystem", sysconfig.get_path("include"), src, "-o", BINDING, "-L" + os.path.join(torch, "lib"),
-                   "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath," + os.path.join(torch, "lib")]
+        torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+        cuda = os.path.dirname(os.path.dirname(shutil.which(nvcc()) or "/usr/local/cuda/bin/nvcc"))
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+               "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(cuda, "include"),
+               "-isystem", sysconfig.get_path("include"), src, "-o", BINDING, "-L" + os.path.join(torch, "lib"),
+               "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath," + os.path.join(torch, "lib")]
+        # what it was built for: another torch has another ABI, and neither its name nor file times say so
+        with open(os.path.join(torch, "version.py")) as f:
+            made_for = "\n".join(cmd) + "\n" + f.read()
+        if force or _needs(BINDING, [src] + headers) or _text(BOUND_FOR) != made_for:
             r = subprocess.run(cmd, capture_output=True, text=True)
             if r.returncode != 0:
                 raise RuntimeError(f"{cmd[0]} failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+            with open(BOUND_FOR, "w") as f:
+                f.write(made_for)
 
     with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
         bound = ex.submit(compile_binding)

@@ -32,8 +32,8 @@ def _init():
     try:
         from . import _binding as b
     except ImportError as e:
-        raise ImportError("the binding is not built; run __graft_entry__.build() or "
-                          "python -m block_speculative_drafting_gb300.csrc.build") from e
+        raise ImportError(f"the binding is not built, or not for this torch; run __graft_entry__.build() or "
+                          f"python -m block_speculative_drafting_gb300.csrc.build ({e})") from e
     L = lib()
     names = ("dflash_paged_append", "dflash_paged_attention", "dflash_paged_attention_workspace", "dflash_verify",
              "dflash_verify_workspace", "dflash_last_error")

@@ -426,3 +426,37 @@ def test_attention_of_blocks_keeps_every_tiles_key_mask(kind):
     assert torch.isfinite(want).all()
     for _ in range(50):
         assert torch.equal(dfl.paged_attention(q, *args), want)
+
+
+# --------------------------------------------------------------------------- the build
+def test_binding_is_built_again_for_another_torch(tmp_path, monkeypatch):
+    """A torch of another version, or at another place, has the extension compiled again; the same one does not."""
+    import importlib.util
+    from block_speculative_drafting_gb300.csrc import build as B
+    B.build()
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        return type("R", (), dict(returncode=0, stdout="", stderr=""))()
+
+    monkeypatch.setattr(B.subprocess, "run", run)
+    monkeypatch.setattr(B, "BOUND_FOR", str(tmp_path / "binding.txt"))
+    monkeypatch.setattr(B, "_needs", lambda out, deps: False)
+    B.build()
+    assert len(ran) == 1 and ran[0][-1].startswith("-Wl,-rpath,") and B.BINDING in ran[0]  # not known what it was built for
+    B.build()
+    assert len(ran) == 1
+    old = tmp_path / "torch"
+    old.mkdir()
+    (old / "__init__.py").write_text("")
+    (old / "version.py").write_text("__version__ = '0.0'\n")
+    spec = importlib.util.spec_from_file_location("torch", old / "__init__.py")
+    monkeypatch.setattr(B.importlib.util, "find_spec", lambda name: spec)
+    B.build()
+    assert len(ran) == 2
+    B.build()
+    assert len(ran) == 2
+    (old / "version.py").write_text("__version__ = '0.1'\n")
+    B.build()
+    assert len(ran) == 3
