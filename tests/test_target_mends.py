@@ -460,3 +460,174 @@ def test_binding_is_built_again_for_another_torch(tmp_path, monkeypatch):
     (old / "version.py").write_text("__version__ = '0.1'\n")
     B.build()
     assert len(ran) == 3
+
+
+# --------------------------------------------------------------------------- refusals, one change from a call that is served
+def _good(torch):
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+    i32 = lambda x: _i32(torch, x)  # noqa: E731
+    append = dict(k_cache=z(6, 16, 2, 64), v_cache=z(6, 16, 2, 64), k=z(4, 2, 64), v=z(4, 2, 64), table=i32([[0, 1], [2, 3]]),
+                  kv_len=i32([20, 30]), row_start=i32([0, 2, 4]), q=z(4, 4, 64), q_out=z(4, 4, 64),
+                  inv_freq=z(32, dtype=torch.float64), q_norm=z(64, dtype=torch.float32), k_norm=z(64, dtype=torch.float32))
+    attention = dict(q=z(4, 4, 64), k_cache=z(6, 16, 2, 64), v_cache=z(6, 16, 2, 64), table=i32([[0, 1], [2, 3]]),
+                     kv_len=i32([20, 30]), row_start=i32([0, 2, 4]), out=z(4, 4, 64), lse=z(4, 4, dtype=torch.float32),
+                     workspace=z(1 << 24, dtype=torch.uint8))
+    verify = dict(target_logits=z(6, 50), draft_tokens=i32([1, 2, 3, 4]), accept_u=z(4, dtype=torch.float32),
+                  sample_u=z(2, dtype=torch.float32), draft_logits=z(4, 50, dtype=torch.float32), draft_start=i32([0, 1, 4]),
+                  temperature=z(2, dtype=torch.float32), accepted=i32([0, 0]), next_token=i32([0, 0]),
+                  prob=z(4, dtype=torch.float32), workspace=z(1 << 24, dtype=torch.uint8))
+    return dict(paged_append=append, paged_attention=attention, verify_drafts=verify)
+
+
+_SHIFTED = lambda x: x.new_zeros(x.numel() + 1)[1:].view(x.shape)  # noqa: E731  (a base off its alignment)
+_WIDE = lambda x: x.new_zeros(*x.shape[:-1], 2 * x.shape[-1])[..., ::2]  # noqa: E731  (columns two apart)
+_E4M3 = lambda x: x.new_zeros(x.shape, dtype=__import__("torch").float8_e4m3fn)  # noqa: E731
+_SCALES = dict(k_cache=_E4M3, v_cache=_E4M3, k_scale="f2", v_scale="f2")
+REFUSALS = [
+    # call, changes (None: left out; text: a type, or a float vector's length), message
+    ("paged_append", dict(k=lambda x: x.cpu()), "k is not on the call's CUDA device"),
+    ("paged_append", dict(table=lambda x: x.cpu()), "table is not on the call's CUDA device"),
+    ("paged_append", dict(inv_freq=lambda x: x.cpu()), "inv_freq is not on the call's CUDA device"),
+    ("paged_append", dict(k_cache=lambda x: x[None], v_cache=lambda x: x[None]), "k_cache has 5 dimensions"),
+    ("paged_append", dict(v_cache=lambda x: x.half()), "of one type"),
+    ("paged_append", dict(v_cache=lambda x: x[:, :8]), "differ in shape"),
+    ("paged_append", dict(v_cache=lambda x: x[:5]), "differ in shape"),
+    ("paged_append", dict(k_cache=_WIDE), "contiguous columns"),
+    ("paged_append", dict(v_cache=_WIDE), "contiguous columns"),
+    ("paged_append", dict(k_cache=lambda x: x[:1].expand_as(x)), "k_cache is written"),
+    ("paged_append", dict(v_cache=lambda x: x[:, :, :1].expand_as(x)), "v_cache is written"),
+    ("paged_append", dict(k_cache=_SHIFTED), "16-byte alignment"),
+    ("paged_append", dict(k_cache=lambda x: x.new_zeros(6, 16, 2, 65)[..., :64]), "cache strides"),
+    ("paged_append", dict(k_cache="double", v_cache="double"), "cache dtype"),
+    ("paged_append", dict(k_cache=lambda x: x[..., :32], v_cache=lambda x: x[..., :32], k=lambda x: x[..., :32],
+                          v=lambda x: x[..., :32], q=lambda x: x[..., :32], q_out=lambda x: x[..., :32], q_norm=None,
+                          k_norm=None, inv_freq=None), "head_dim 32"),
+    ("paged_append", dict(k=lambda x: x[:, :1]), "k has 1 heads"),
+    ("paged_append", dict(k=lambda x: x[..., :32]), "k has to be"),
+    ("paged_append", dict(k=_WIDE), "k has to be"),
+    ("paged_append", dict(k=_SHIFTED), "k: base and strides"),
+    ("paged_append", dict(v=lambda x: x[:3]), "v has to be"),
+    ("paged_append", dict(v="float32"), "one type"),
+    ("paged_append", dict(k="double", v="double", q="double"), "k dtype"),
+    ("paged_append", dict(table="int64"), "table has to be int32"),
+    ("paged_append", dict(table=lambda x: x[0]), "table has to be int32"),
+    ("paged_append", dict(table=_WIDE), "table has to be int32"),
+    ("paged_append", dict(kv_len="int64"), "kv_len has to be"),
+    ("paged_append", dict(kv_len=lambda x: x[:1]), "kv_len has to be"),
+    ("paged_append", dict(kv_len=_WIDE), "kv_len has to be"),
+    ("paged_append", dict(row_start=lambda x: x[:2]), "row_start has to be"),
+    ("paged_append", dict(row_start="int64"), "row_start has to be"),
+    ("paged_append", dict(row_start=None, k=lambda x: x[:3], v=lambda x: x[:3], q=lambda x: x[:3], q_out=lambda x: x[:3]),
+     "do not divide"),
+    ("paged_append", dict(q=None), "q_out without q"),
+    ("paged_append", dict(q=lambda x: x[:, :3], q_out=lambda x: x[:, :3]), "q has 3 heads"),
+    ("paged_append", dict(q=lambda x: x[:3]), "q has to be"),
+    ("paged_append", dict(q_out=lambda x: x[:3]), "q_out has to be"),
+    ("paged_append", dict(q_out=lambda x: x[:, :2]), "q_out has 2 heads"),
+    ("paged_append", dict(q_out=lambda x: x[:1].expand_as(x)), "q_out is written"),
+    ("paged_append", dict(q_out="double"), "q_out dtype"),
+    ("paged_append", dict(q_norm=lambda x: x[:32]), "q_norm has to be"),
+    ("paged_append", dict(k_norm="bfloat16"), "k_norm has to be"),
+    ("paged_append", dict(k_norm=_SHIFTED), "16-byte alignment"),
+    ("paged_append", dict(inv_freq="float32"), "inv_freq has to be"),
+    ("paged_append", dict(inv_freq=_WIDE), "inv_freq has to be"),
+    ("paged_append", dict(inv_freq=lambda x: x[:7]), "rotary 14"),
+    ("paged_append", dict(inv_freq=lambda x: x.repeat(2)), "rotary 128"),
+    ("paged_append", dict(k_scale="f2", v_scale="f2"), "scales need an E4M3 cache"),
+    ("paged_append", {**_SCALES, "v_scale": None}, "come together"),
+    ("paged_append", {**_SCALES, "k_scale": "f3"}, "k_scale has to be"),
+    ("paged_append", {**_SCALES, "v_scale": lambda x: __import__("torch").zeros(2, device="cuda").double()}, "v_scale has to be"),
+    ("paged_attention", dict(q="float16"), "need the cache's type"),
+    ("paged_attention", dict(q="float32", out="float32"), "need the cache's type"),
+    ("paged_attention", dict(q=_WIDE), "q has to be"),
+    ("paged_attention", dict(q=lambda x: x[:, :3], out=lambda x: x[:, :3], lse=lambda x: x[:, :3].contiguous()), "heads 3"),
+    ("paged_attention", dict(k_cache=lambda x: x[:, :, :1]), "differ in shape"),
+    ("paged_attention", dict(v_cache=lambda x: x.cpu()), "v_cache is not on the call's CUDA device"),
+    ("paged_attention", dict(table=lambda x: x.t()), "table has to be int32"),
+    ("paged_attention", dict(kv_len=None), "kv_len is None"),
+    ("paged_attention", dict(row_start=lambda x: x[:2]), "row_start has to be"),
+    ("paged_attention", dict(out=lambda x: x[:3]), "out has to be"),
+    ("paged_attention", dict(out=lambda x: x[:, :2]), "out has 2 heads"),
+    ("paged_attention", dict(out="float16"), "need the cache's type"),
+    ("paged_attention", dict(out=lambda x: x[:, :1].expand_as(x)), "out is written"),
+    ("paged_attention", dict(out=_SHIFTED), "out: base and strides"),
+    ("paged_attention", dict(lse=lambda x: x[:, :3]), "lse has to be"),
+    ("paged_attention", dict(lse=lambda x: x[:3]), "lse has to be"),
+    ("paged_attention", dict(lse=lambda x: x.t()), "lse has to be"),
+    ("paged_attention", dict(lse="double"), "lse has to be"),
+    ("paged_attention", dict(lse=lambda x: x[:1].expand_as(x)), "lse has to be"),
+    ("paged_attention", dict(workspace=lambda x: x[:64]), "workspace of 64 bytes"),
+    ("paged_attention", dict(workspace=lambda x: x[::2]), "workspace has to be"),
+    ("paged_attention", dict(workspace=lambda x: x[8:]), "not 16-byte aligned"),
+    ("paged_attention", dict(workspace=lambda x: x.cpu()), "workspace is not on the call's CUDA device"),
+    ("paged_attention", dict(window=lambda x: -1), "window -1"),
+    ("paged_attention", dict(window=lambda x: 1 << 40), "window"),
+    ("paged_attention", dict(scale=lambda x: float("nan")), "scale"),
+    ("verify_drafts", dict(target_logits=lambda x: x[:5]), "need 6 target rows, got 5"),
+    ("verify_drafts", dict(target_logits=lambda x: x[0]), "target_logits has to be"),
+    ("verify_drafts", dict(target_logits=_WIDE), "target_logits has to be"),
+    ("verify_drafts", dict(target_logits="double"), "target dtype"),
+    ("verify_drafts", dict(target_logits=lambda x: x[:1].expand_as(x)), "row stride"),
+    ("verify_drafts", dict(draft_tokens="int64"), "draft_tokens has to be"),
+    ("verify_drafts", dict(draft_tokens=_WIDE), "draft_tokens has to be"),
+    ("verify_drafts", dict(draft_tokens=lambda x: x.cpu()), "draft_tokens is not on the call's CUDA device"),
+    ("verify_drafts", dict(accept_u=None), "accept_u is None"),
+    ("verify_drafts", dict(accept_u=lambda x: x[:3]), "accept_u has to be"),
+    ("verify_drafts", dict(accept_u="double"), "accept_u has to be"),
+    ("verify_drafts", dict(sample_u=lambda x: x[None]), "sample_u has to be"),
+    ("verify_drafts", dict(sample_u=_WIDE), "sample_u has to be"),
+    ("verify_drafts", dict(draft_logits=lambda x: x[:, :49]), "draft_logits has to be"),
+    ("verify_drafts", dict(draft_logits=lambda x: x[:3]), "draft_logits has to be"),
+    ("verify_drafts", dict(draft_logits="bfloat16"), "draft_logits has to be"),
+    ("verify_drafts", dict(draft_logits=_WIDE), "draft_logits has to be"),
+    ("verify_drafts", dict(draft_logits=lambda x: x.new_zeros(3, 2, 50)[:2].transpose(0, 1)), "draft_logits has to be"),
+    ("verify_drafts", dict(draft_logits=lambda x: x[:1].expand_as(x)), "row stride"),
+    ("verify_drafts", dict(draft_start=lambda x: x[:2]), "draft_start has to be"),
+    ("verify_drafts", dict(draft_start="int64"), "draft_start has to be"),
+    ("verify_drafts", dict(temperature=lambda x: x[:1]), "temperature has to be"),
+    ("verify_drafts", dict(temperature="double"), "temperature has to be"),
+    ("verify_drafts", dict(accepted="int64"), "accepted has to be"),
+    ("verify_drafts", dict(accepted=lambda x: x[:1].expand(2)), "accepted has to be"),
+    ("verify_drafts", dict(next_token=lambda x: x[:1]), "next_token has to be"),
+    ("verify_drafts", dict(prob=lambda x: x[:3]), "prob has to be"),
+    ("verify_drafts", dict(prob=lambda x: x[:1].expand(4)), "prob has to be"),
+    ("verify_drafts", dict(workspace=lambda x: x[:16]), "workspace of 16 bytes"),
+    ("verify_drafts", dict(workspace=lambda x: x[8:]), "not 16-byte aligned"),
+]
+
+
+@gpu
+@pytest.mark.parametrize("name", ["paged_append", "paged_attention", "verify_drafts"])
+def test_calls_one_change_from_the_refused_ones_are_served(name):
+    torch, dfl = _torch(), _dfl()
+    getattr(dfl, name)(**_good(torch)[name])
+    if name != "verify_drafts":
+        args = _good(torch)[name]
+        sc = dict(k_scale=torch.ones(2, device="cuda"), v_scale=torch.ones(2, device="cuda"))
+        getattr(dfl, name)(**{**args, "k_cache": _E4M3(args["k_cache"]), "v_cache": _E4M3(args["v_cache"]), **sc})
+    torch.cuda.synchronize()
+
+
+@gpu
+@pytest.mark.parametrize("name,changes,message", REFUSALS, ids=[f"{i}-{r[0]}-{r[2][:24]}" for i, r in enumerate(REFUSALS)])
+def test_calls_refused_for_one_thing(name, changes, message):
+    """Each by its own check and in its words, and nothing is launched or written."""
+    torch, dfl = _torch(), _dfl()
+    args = _good(torch)[name]
+    outs = [k for k in ("k_cache", "v_cache", "q_out", "out", "lse", "accepted", "next_token", "prob") if k in args]
+    before = {k: args[k].clone() for k in outs}
+    call = dict(args)
+    for key, how in changes.items():
+        if how is None:
+            call[key] = None
+        elif isinstance(how, str) and how[0] == "f" and how[1:].isdigit():
+            call[key] = torch.ones(int(how[1:]), device="cuda")
+        elif isinstance(how, str):
+            call[key] = args[key].to(getattr(torch, how))
+        else:
+            call[key] = how(args.get(key))
+    with pytest.raises(dfl.DFlashError) as e:
+        getattr(dfl, name)(**call)
+    assert message in str(e.value) and e.value.code in (dfl._abi.DFLASH_EINVAL, dfl._abi.DFLASH_EGEOM, dfl._abi.DFLASH_ECAPACITY)
+    torch.cuda.synchronize()
+    assert all(torch.equal(args[k], before[k]) for k in outs)
