@@ -531,28 +531,16 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                     for (int j = 4; j < 32; ++j) a[j & 3] = fmaxf(a[j & 3], v[j]);
                     return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
                 };
-                // (64 scores stay in registers; 128 are read twice)
-                constexpr bool kKeep = NC <= 1;
-                float v[kKeep ? 32 * NC : 32];
+                // (a lane's 64 or 128 scores are read twice, 32 at a time: more of them do not fit the registers)
+                float v[32];
                 float mx = -INFINITY;
                 if (warp_in) {
-                    if constexpr (kKeep) {
-#pragma unroll
-                        for (int q = 0; q < NC; ++q) scores(q, v + 32 * q);
-                        at_wait_ld();
-#pragma unroll
-                        for (int q = 0; q < NC; ++q) {
-                            hide(q, v + 32 * q);
-                            mx = fmaxf(mx, largest(v + 32 * q));
-                        }
-                    } else {
 #pragma unroll 1
-                        for (int q = 0; q < NC; ++q) {
-                            scores(q, v);
-                            at_wait_ld();
-                            hide(q, v);
-                            mx = fmaxf(mx, largest(v));
-                        }
+                    for (int q = 0; q < NC; ++q) {
+                        scores(q, v);
+                        at_wait_ld();
+                        hide(q, v);
+                        mx = fmaxf(mx, largest(v));
                     }
                     mx *= cs;
                 }
@@ -654,17 +642,12 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                         pt_st16(mine + 32 * q, hi);
                         if constexpr (S::kSplitP) pt_st16(mine + 32 * q + 16, lo);
                     };
-                    if constexpr (kKeep) {
-#pragma unroll
-                        for (int q = 0; q < NC; ++q) weights(q, v + 32 * q);
-                    } else {
 #pragma unroll 1
-                        for (int q = 0; q < NC; ++q) {
-                            scores(q, v);
-                            at_wait_ld();
-                            hide(q, v);
-                            weights(q, v);
-                        }
+                    for (int q = 0; q < NC; ++q) {
+                        scores(q, v);
+                        at_wait_ld();
+                        hide(q, v);
+                        weights(q, v);
                     }
                     l = (ls[0] + ls[1]) + (ls[2] + ls[3]);
                     // the keys of the row's other lane
