@@ -555,8 +555,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(const __grid_
 // Row r, head hq of the output: NaN that is kept apart becomes the sum of the column's values that are not finite over
 // the keys in the row's view.  By a warp; in little code, which all calls carry and few run (with its loops unrolled and a
 // form for each type it took 6 us of a call's 40, one block over 32768 keys, though nothing of it ran).
+// `mine`: this warp has joined the row; else rows that are joined are left alone, which their own warps may not have
+// written yet (what the buffer held before may look like that NaN).
 template <int HD>
-DF_DEV void pa_odd_row(const PaArgs& A, int r, int hq) {
+DF_DEV void pa_odd_row(const PaArgs& A, int r, int hq, bool mine) {
     constexpr int V = HD / 32;  // columns a lane
     const int lane = threadIdx.x & 31, h = hq / A.group;
     const bool bf = A.out.dtype == kBF16;
@@ -570,6 +572,16 @@ DF_DEV void pa_odd_row(const PaArgs& A, int r, int hq) {
     if (s < 0) return;
     int a, b;
     rows_of(A.R, s, a, b);
+    if (!mine) {
+        const int mm = (r - a) * A.group + hq % A.group;
+        bool joined = false;
+#pragma unroll 1
+        for (int c = lane; c < (int)gridDim.x; c += 32) {
+            const PaJoin e = A.ws_join[c];
+            joined |= e.last > c && e.seq == s && e.head == h && mm >= e.m0 && mm - e.m0 < e.rows;
+        }
+        if (__any_sync(0xffffffffu, joined)) return;
+    }
     const int pos = pa_seq(A, s, a, b, kPaM).p0 + r - a;
     float sum[V] = {};
 #pragma unroll 1
@@ -686,7 +698,7 @@ __global__ void __launch_bounds__(kPaThreads) paged_join_kernel(const __grid_con
     }
     }
     // this warp's joined rows with NaN that is kept apart, then all of the call's where the share's whole units have some
-    // (rows that others join and see to themselves among them: both write the same)
+    // (other shares' too, where they have some: both write the same)
     any = __any_sync(0xffffffffu, any);
     if (!any && odd == 0) return;
     const uint32_t joined = any ? min(16, e.rows - 16 * (int)blockIdx.y) : 0,
@@ -696,7 +708,7 @@ __global__ void __launch_bounds__(kPaThreads) paged_join_kernel(const __grid_con
         if (i < 16 && i >= joined) continue;
         // rows of a unit are group by group, rows of the call heads by heads
         const uint32_t per = i < 16 ? A.group : A.q.heads, at = i < 16 ? e.m0 + 16 * blockIdx.y + i : i - 16, r = at / per;
-        pa_odd_row<HD>(A, (int)r + (i < 16 ? e.row0 : 0), (int)(at - r * per) + (i < 16 ? h * A.group : 0));
+        pa_odd_row<HD>(A, (int)r + (i < 16 ? e.row0 : 0), (int)(at - r * per) + (i < 16 ? h * A.group : 0), i < 16);
     }
 }
 

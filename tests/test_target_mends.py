@@ -631,3 +631,35 @@ def test_calls_refused_for_one_thing(name, changes, message):
     assert message in str(e.value) and e.value.code in (dfl._abi.DFLASH_EINVAL, dfl._abi.DFLASH_EGEOM, dfl._abi.DFLASH_ECAPACITY)
     torch.cuda.synchronize()
     assert all(torch.equal(args[k], before[k]) for k in outs)
+
+
+@gpu
+@pytest.mark.parametrize("kind,mark", [("bf16", 0x7fc1), ("f16", 0x7e01)])
+@pytest.mark.parametrize("rows,heads", [(1, 4), (16, 8)])
+def test_attention_does_not_take_what_the_output_held_for_its_own(kind, mark, rows, heads):
+    """Whatever NaN the output's buffer held before: split and whole units among one another, values that are not finite
+    in some; the same bits as in a fresh buffer, and rows of no sequence keep theirs."""
+    torch, dfl = _torch(), _dfl()
+    from test_target_ops import _types
+    rng = np.random.default_rng(5)
+    lens = [150 + 3 * i for i in range(60)] + [9000, 4000]
+    need = [-(-x // 16) for x in lens]
+    table = np.full((len(lens), max(need)), -1, np.int32)
+    ids = rng.permutation(sum(need))
+    for s, m in enumerate(need):
+        table[s, :m], ids = ids[:m], ids[m:]
+    kc, vc = (torch.from_numpy(rng.standard_normal((sum(need), 16, 2, 64)).astype(np.float32)).cuda().to(_types()[kind])
+              for _ in range(2))
+    _odd_values(torch, kc, vc, table)
+    n = rows * len(lens)
+    q = torch.from_numpy(rng.standard_normal((n + 3, heads, 64)).astype(np.float32)).cuda().to(_types()[kind])
+    args = (kc, vc, _i32(torch, table), _i32(torch, lens))
+    start = _i32(torch, np.arange(len(lens) + 1) * rows)
+    want = dfl.paged_attention(q, *args, row_start=start, out=torch.zeros_like(q))
+    for _ in range(20):
+        out = torch.zeros_like(q)
+        out.view(torch.int16).fill_(mark)
+        dfl.paged_attention(q, *args, row_start=start, out=out)
+        assert torch.equal(out.view(torch.int16)[:n], want.view(torch.int16)[:n])
+        assert (out.view(torch.int16)[n:] == mark).all()
+    assert not torch.isfinite(want).all() and torch.isfinite(want).any()
