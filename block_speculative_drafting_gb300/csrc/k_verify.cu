@@ -10,20 +10,22 @@
 // the cluster's warps sum what is left of equal parts of the vocabulary, and the
 // CTA in which the running sum passes the given number's share of the whole finds
 // the part and the entry.  That kernel runs once through its code, so its code is
-// kept small (rolled loops): what it waits for most is instructions.
+// kept small (rolled loops, one copy of each part): what it waits for most is
+// instructions, and code that does not run costs it time as well (without the exact
+// form's, one block 17.6 -> 16.9 us).
 //
 // Arithmetic.  A softmax sum of the statistics is a tree of f32 additions of
 // exponentials within 2^-22 each; c is a pair (hi, lo), so that its rounding does
 // not tilt the distribution, and R is an integer, so that moving a sum to another
-// reference is exact and x c - R is rounded once: off by 2^-18 at most, of which
-// prob keeps about 2^-23.  A draft whose number lies within that of p / q, and a
+// reference is exact and x c - R is rounded once: off by 2^-18 at most (prob was
+// seen within 2^-21 of its value).  A draft whose number lies within that of p / q, and a
 // token whose share of the whole lies within the 32-bit form's bound of a border
 // (below), are decided again in 64 bits: every decision is the definition's.
 //
 // Memory bound: the logits, once (the re-read row comes out of L2).  32 blocks of
-// up to 16 drafts, 151936 bf16 logits against f32 ones: 81 us, of which the
+// up to 16 drafts, 151936 bf16 logits against f32 ones: 80 us, of which the
 // statistics 55 (5.5 TB/s, 81 % of a copy) and the picking kernel the rest; one
-// block 17.9 us, 13.8 of chosen drafts, greedy 6.8, most of it latency.
+// block 17.6 us, 13.7 of chosen drafts, greedy 6.7, most of it latency.
 #include <cooperative_groups.h>
 
 #include "kernels.cuh"
@@ -72,6 +74,7 @@ DF_DEV void draft_range(const VerifyArgs& A, int s, int lane, int& a, int& b) {
         return;
     }
     int m = 0;
+#pragma unroll 1
     for (int j = lane; j <= s; j += 32) m = max(m, draft_start_at(A, j));
     a = __reduce_max_sync(0xffffffffu, m);
     b = max(draft_start_at(A, s + 1), a);
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(kVsThreads, 4) verify_stats_kernel(const __gri
 
 // A row's parts joined (warp-wide, every lane gets the answer).  A row with a
 // careful part is careful as a whole.
-DF_DEV VerifyStat row_stat(const VerifyParams& P, int64_t row, Scale c, int lane) {
+__device__ __noinline__ VerifyStat row_stat(const VerifyParams& P, int64_t row, Scale c, int lane) {
     const VerifyStat* st = P.stats + row * P.parts;
     VerifyStat r{0.f, kRefNone, -INFINITY, 0};
     if (c.greedy()) {
@@ -358,12 +361,14 @@ DF_DEV VerifyStat row_stat(const VerifyParams& P, int64_t row, Scale c, int lane
         auto join = [&](float m, int arg) {
             if (m > r.max || (m == r.max && arg < r.tag)) r.max = m, r.tag = arg;
         };
+#pragma unroll 1
         for (int i = lane; i < P.parts; i += 32) join(st[i].max, st[i].tag);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             join(__shfl_xor_sync(0xffffffffu, r.max, o), __shfl_xor_sync(0xffffffffu, r.tag, o));
         return r;
     }
+#pragma unroll 1
     for (int i = lane; i < P.parts; i += 32) {
         const VerifyStat x = st[i];
         const float to = fmaxf(r.ref, x.ref);
@@ -381,15 +386,14 @@ DF_DEV VerifyStat row_stat(const VerifyParams& P, int64_t row, Scale c, int lane
     } else {
         // in 64 bits: every part's sum to the row's largest logit
         double sum = 0.0;
+#pragma unroll 1
         for (int i = lane; i < P.parts; i += 32) {
             const VerifyStat x = st[i];
             if (x.sum == 0.f) continue;
-            double f = 1.0;
-            if (!x.tag)
-                f = exp2((double)x.ref - (double)r.max * c.wide());
-            else if (x.max != r.max)
-                f = exp2(((double)x.max - (double)r.max) * c.wide());
-            sum += (double)x.sum * f;
+            // (an infinite largest logit has nothing but itself)
+            const double by = x.tag ? x.max == r.max ? 0.0 : ((double)x.max - (double)r.max) * c.wide()
+                                    : (double)x.ref - (double)r.max * c.wide();
+            sum += (double)x.sum * exp2(by);
         }
         r.sum = (float)sum;
     }
@@ -870,6 +874,7 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
         const int n = min(32, d + 1 - i0);  // rows of the round, the one after the last draft among them
         float u = 0.f;
         if (warp == 0 && i0 + lane < d) u = __ldg(A.accept_u + a + i0 + lane);
+#pragma unroll 1
         for (int j = warp; j < (drawn ? 2 : 1) * n; j += WARPS) {
             const int i = i0 + j % n, side = j / n;
             float l = -INFINITY;
