@@ -436,7 +436,7 @@ DF_DEV float weight_any(float x, const VerifyStat& r, Scale c) {
 //
 // 2^z by a table of 2^(i / 128) and a polynomial (P. T. P. Tang, "Table-driven implementation of the exponential function
 // in IEEE floating-point arithmetic", ACM TOMS 15, 1989), first in 32 bits: z = x c to the nearest 128th, the remainder
-// r, |r| <= 2^-8 + 2^-10, exact but for 2^-33; the table, normalised by the row's sum as the statistics have it, rounded to
+// r, |r| <= 2^-8 + 2^-10, by two roundings; the table, normalised by the row's sum as the statistics have it, rounded to
 // 2^-32; 257 (2^r - 1) + 3 in f32, whose 32 bits from 2.0 to 4.0 are 0x40400000 2^r (257 = 0x40400000 / 2^22), rounded to
 // 2^-31; their product in 64 bits.  Together under kVpEps.  The pass also sums the rows themselves, whose statistics are
 // off by about 2^-20: with g = sum of (p' - q'), p' and q' as computed, p - q is p' - q' - g q' (of p' + ..), where a
@@ -445,11 +445,13 @@ DF_DEV float weight_any(float x, const VerifyStat& r, Scale c) {
 // The entry's distance from both of its borders is compared with the bound that all this gives.  Where it is within the
 // bound, or the exponents are past that form's range, the row is gone through again with exponents in 64 bits, table and
 // polynomial in 64-bit fixed point, and p and q by exactly normalised sums: the definition in 64 bits, with sums that do
-// not round.  Of 2048 refused rows over 151936 entries: none where a third of the mass is refused, 13 at 5 %, 229 at
+// not round.  Of 2048 refused rows over 151936 entries: none where a third of the mass is refused, 13 at 5 %, 238 at
 // 0.05 %; 108 us more for one sequence.  (Weights of 22 bits, in sums of 48, drew another token in up to 7 % of such rows;
 // one pass in 64-bit floats would take 0.6 ms: two lanes of them a clock and SM.)
 constexpr int kVpSteps = 128;
-constexpr float kVpEps = 1.05e-9f;  // 2.25 2^-31: 1 + 1/2 + 2 (1/4 ln 2) + 2 / 2^2.5 of it, as above
+// 2.7 2^-31: the last rounding 1, the table 1/2, r's two 2 (1/2 ln 2 past 2^-8), the polynomial's two 2 / 2^2.5 of it
+// (c's own error is every entry's, and goes with the normaliser)
+constexpr float kVpEps = 1.26e-9f;
 constexpr long long kVpOne = 1ll << 60;
 constexpr float kVpMagic = 98304.f;  // 1.5 * 2^16: a sum with it is rounded to 128ths
 constexpr uint32_t kVpZero = 0x47C00000;  // its bits
@@ -909,9 +911,10 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
                                 wq = !drawn ? 1.f : other ? weight_any(lq, g, c) : 0.f, sq = drawn && g.max > -INFINITY ? g.sum : 1.f;
                     const float p = wp * sq, uq = u * (wq * sp);
                     refuse = !(uq < p);
-                    // (a weight's exponent, rounded twice, may be 2^-23 of it off; weights under f32's range count as 0)
-                    const float far = fabsf(lp * c.hi - (t.tag ? t.max * c.hi : t.ref)) +
-                                      (other ? fabsf(lq * c.hi - (g.tag ? g.max * c.hi : g.ref)) : 0.f);
+                    // (a weight's exponent, rounded twice, may be 2^-23 of it off, and so may those of the sums, which
+                    // the low part of c can move; weights under f32's range count as 0)
+                    const float far = fabsf(lp * c.hi - (t.tag ? t.max * c.hi : t.ref)) + fabsf(t.max * c.lo) +
+                                      (other ? fabsf(lq * c.hi - (g.tag ? g.max * c.hi : g.ref)) + fabsf(g.max * c.lo) : 0.f);
                     unsure = some && (!drawn || other) &&
                              fabsf(uq - p) <= fmaf(fmaf(fminf(far, 300.f), 3e-7f, tol), fmaxf(uq, p), 1e-35f * (sp * sq));
                 }
@@ -1020,7 +1023,7 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
             Sums x{};
             if (lane < kVpCluster) x = ctas[lane];
             Picked k;
-            k.g = L.mode == 2 && !exact ? warp_sum(x.g) : 0;
+            k.g = L.mode == 2 && !exact ? warp_sum(x.g) : 0;  // (under 2^42, or nothing below counts)
             const long long own = left_of(x, k.g);
             k.whole = warp_sum(own);
             // (the whole part of u times the whole; of nothing, nothing)
@@ -1043,7 +1046,8 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
             __syncthreads();
             continue;
         }
-        if (!exact && k.whole <= 0) {  // (about nothing: the exact form says what)
+        // (about nothing, or normalisers further off than what `tie` takes for agreeing: the exact form says what)
+        if (!exact && (k.whole <= 0 || llabs(k.g) >= 1ll << 42)) {
             exact = true;
             __syncthreads();
             continue;
@@ -1100,7 +1104,7 @@ __global__ void __cluster_dims__(kVpCluster, 1, 1) __launch_bounds__(WARPS * 32)
                     if (L.mode == 2)
                         off = eps * ((float)k.whole + 4.f * 4294967296.f * (float)sum.q) +
                               2.1f * g * (3.7252903e-9f * (float)sum.tie) + entries * (4.f + 1.5e-8f * g) + 65536.f;
-                    sure = at >= 0 && (float)below > off && (float)above > off && g < 4.3980465e12f /* 2^42 */;
+                    sure = at >= 0 && (float)below > off && (float)above > off;
                     if (exact || sure) {
                         A.accepted[s] = acc;
                         A.next_tok[s] = first + (at < 0 ? last : at);

@@ -634,10 +634,12 @@ DFLASH_API int64_t dflash_paged_attention_workspace(const dflash_paged_cache* ca
  *   prob[i]  min(1, p_i(x_i) / q_i(x_i)) of every draft
  * T <= 0 (or NaN) is greedy: p_i is all at the target's largest logit (the
  * lowest index among equals), q_i all at x_i, and the token is that largest
- * one.  accept_u, sample_u: f32 in [0, 1).  Logits of -inf, and NaN, count as
- * probability 0; at +inf the row's +inf entries share it all.  A row with no
- * probability at all refuses its draft and yields token -1.  A draft outside
- * the vocabulary is refused.
+ * one.  accept_u, sample_u: f32 in [0, 1).  Which drafts are kept, and the
+ * token, are what 64 bits make of this, also right at a border (of a sample_u
+ * that is 0 or at least 2^-40); prob is within 2^-20.  Logits of -inf, and NaN,
+ * count as probability 0; at +inf the row's +inf entries share it all.  A row
+ * with no probability at all refuses its draft and yields token -1.  A draft
+ * outside the vocabulary is refused.
  * target [n_drafts + n_seqs] rows of f32, BF16 or F16, draft_logits
  * [n_drafts] rows of f32, target_stride / draft_stride elements apart, vocab
  * contiguous logits each; draft_tok u32 [n_drafts] (dflash_block's logits and
