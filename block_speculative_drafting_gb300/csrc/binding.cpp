@@ -101,6 +101,8 @@ struct Tensor {
             // (the stride of a dimension of one element is anything)
             stride[i] = shape[i] > 1 ? t.stride(i) : i == nd - 1 ? 1 : 0;
         }
+        if (t.numel() == 0)  // (and so are all of a tensor without elements)
+            for (int64_t i = nd - 1, s = 1; i >= 0; s *= shape[i] > 1 ? shape[i] : 1, --i) stride[i] = s;
         dtype = type_of(t.scalar_type());
         p = t.data_ptr();
     }

@@ -663,3 +663,27 @@ def test_attention_does_not_take_what_the_output_held_for_its_own(kind, mark, ro
         assert torch.equal(out.view(torch.int16)[:n], want.view(torch.int16)[:n])
         assert (out.view(torch.int16)[n:] == mark).all()
     assert not torch.isfinite(want).all() and torch.isfinite(want).any()
+
+
+@gpu
+def test_calls_without_rows_take_any_strides():
+    """Tensors without elements have whatever strides they came with (those of an empty numpy array are 0)."""
+    torch, dfl = _torch(), _dfl()
+    good = _good(torch)
+    none = lambda *s, dtype=torch.bfloat16: torch.empty(1, dtype=dtype, device="cuda").as_strided((0, *s), (0,) * (len(s) + 1))  # noqa: E731
+    a = good["paged_append"]
+    start = _i32(torch, [0, 0, 0])
+    q = dfl.paged_append(**{**a, "k": none(2, 64), "v": none(2, 64), "q": none(4, 64), "q_out": None, "row_start": start})
+    assert q.shape == (0, 4, 64)
+    b = good["paged_attention"]
+    y = dfl.paged_attention(**{**b, "q": none(4, 64), "out": None, "lse": none(4, dtype=torch.float32), "row_start": start})
+    assert y.shape == (0, 4, 64)
+    no_pages = none(16, 2, 64)
+    y = dfl.paged_attention(b["q"], no_pages, no_pages, b["table"], b["kv_len"], row_start=b["row_start"])
+    assert (y == 0).all()
+    f32 = torch.float32
+    t = torch.randn(2, 50, device="cuda")
+    acc, nxt, prob = dfl.verify_drafts(t, none(dtype=torch.int32), none(dtype=f32), torch.full((2,), 0.5, device="cuda"),
+                                       draft_logits=none(50, dtype=f32), draft_start=start)
+    res, _ = O.verify(f64(t), [], [], [0.5, 0.5])
+    assert acc.tolist() == [0, 0] and nxt.tolist() == [r[1] for r in res] and prob.shape == (0,)
