@@ -581,7 +581,7 @@ typedef struct {
  * norm(x) = x / sqrt(mean(x^2) + eps) * gain over a head, with f32 gains
  * q_norm, k_norm [head_dim] on the device (NULL: no norm).  rotation NULL: no
  * rotation.  q NULL: keys and values alone.  q, k and v have one type; q_out
- * may be q itself, or of another type.  A row whose position is not held is
+ * may be q itself, or apart from it and of another type.  A row whose position is not held is
  * not written to the cache (its q' is written).  A table that maps two of the
  * call's rows to one slot leaves either row's elements there.
  * Errors: EINVAL, EGEOM, ECUDA.
@@ -598,10 +598,10 @@ DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash
  *   out = sum_j softmax_j(scale * q . k_j) v_j over the held positions j <= p
  *         (window w > 0, up to 2^30: and j > p - w)
  *   lse = ln sum_j exp(scale * q . k_j)          f32 [n_rows][heads], or NULL
- * A row that sees nothing gets out = 0 and lse = -inf.  What positions outside
- * a row's view hold (infinities, NaN, freed pages) does not reach it.  q and
- * out have one type: the cache's, or BF16 / F16 for an E4M3 cache; out may be
- * q itself.
+ * A row that sees nothing, or finite values at scores of -inf alone, gets out =
+ * 0 and lse = -inf.  What positions outside a row's view hold (infinities, NaN,
+ * freed pages) does not reach it.  q and out have one type: the cache's, or BF16
+ * / F16 for an E4M3 cache; out may be q itself, or has to be apart from it.
  * workspace: at least dflash_paged_attention_workspace bytes of device
  * memory, 16-byte aligned, needing no initial contents; calls that may
  * overlap need one each.

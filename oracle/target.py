@@ -100,6 +100,8 @@ def paged_attention(q, k_cache, v_cache, table, kv_len, row_start=None, scale=No
                 with np.errstate(all="ignore"):
                     sc = scale * (kk @ q[a + i, h])
                     m = sc.max()
+                    if m == -np.inf:  # scores of -inf alone: nothing to weigh
+                        continue
                     e = np.exp(sc - m)
                     out[a + i, h] = (e / e.sum()) @ vv
                     mag[a + i, h] = (e / e.sum()) @ np.abs(vv)

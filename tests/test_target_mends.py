@@ -687,3 +687,27 @@ def test_calls_without_rows_take_any_strides():
                                        draft_logits=none(50, dtype=f32), draft_start=start)
     res, _ = O.verify(f64(t), [], [], [0.5, 0.5])
     assert acc.tolist() == [0, 0] and nxt.tolist() == [r[1] for r in res] and prob.shape == (0,)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,heads", [(1, 4), (12, 8)])
+def test_attention_of_scores_that_are_all_minus_infinity(kind, rows, heads):
+    """Rows of which every score is -inf weigh nothing: 0, and -inf; those beside them that see another key do."""
+    torch, dfl = _torch(), _dfl()
+    from test_target_ops import _types
+    rng = np.random.default_rng(2)
+    kc, vc = (torch.from_numpy(rng.standard_normal((4, 16, 1, 64)).astype(np.float32)).cuda().to(_types()[kind])
+              for _ in range(2))
+    q = torch.from_numpy(rng.standard_normal((2 * rows, heads, 64)).astype(np.float32)).cuda().to(_types()[kind])
+    q[..., 7] = -1.0
+    kc[0, :, 0, 7] = float("inf")  # the first page's keys: scores of -inf for every row
+    table, lens = [[0, 1], [0, 2]], [16, 30]
+    lse = torch.zeros(2 * rows, heads, device="cuda")
+    out = dfl.paged_attention(q, kc, vc, _i32(torch, table), _i32(torch, lens), lse=lse)
+    ref, rl, mag, _ = O.paged_attention(f64(q), f64(kc), f64(vc), table, lens)
+    assert (out[:rows] == 0).all() and (lse[:rows] == -float("inf")).all()
+    assert (np.abs(f64(out) - ref) <= 2.0 ** -8 * np.abs(ref) + 1e-3 * mag).all()
+    got = f64(lse)
+    some = np.isfinite(rl)
+    assert np.array_equal(np.isneginf(got), np.isneginf(rl)) and np.abs(got[some] - rl[some]).max() < 1e-3
