@@ -14,7 +14,7 @@
 //
 // Memory bound where rows are many: 8192 rows of 32 query and 8 key/value heads
 // of 128, bf16, half of each rotated: 39.7 us, 5.1 TB/s (75 % of a copy).  512
-// rows with head norms into an e4m3 cache: 8.5 us, the chain of a row's norms
+// rows with head norms into an e4m3 cache: 9.0 us, the chain of a row's norms
 // and rotations; one row: 4.5 us, launch and lookups.
 #include "kernels.cuh"
 #include "paged.cuh"

@@ -17,7 +17,9 @@ constexpr int kF32 = 0, kBF16 = 1, kF16 = 2, kE4M3 = 3;
 constexpr int kMaxDevices = 64;
 
 // Division of 0 <= n < 2^31 by a fixed d: one high product, one addition and
-// a shift (a page size is any number, and every key row divides by it).
+// a shift (T. Granlund and P. L. Montgomery, "Division by invariant integers using
+// multiplication", PLDI 1994; a page size is any number, and every key row divides
+// by it).
 struct FastDiv {
     uint32_t mul, shift;
     int d;
