@@ -697,18 +697,33 @@ __global__ void __launch_bounds__(kPaThreads) paged_join_kernel(const __grid_con
     }
     }
     }
-    // this warp's joined rows with NaN that is kept apart, then all of the call's where the share's whole units have some
-    // (other shares' too, where they have some: both write the same)
+    // this warp's joined rows with NaN that is kept apart; then, where the share's whole units have some, all of the call's
+    // rows, dealt out over the warps of all such shares
     any = __any_sync(0xffffffffu, any);
     if (!any && odd == 0) return;
-    const uint32_t joined = any ? min(16, e.rows - 16 * (int)blockIdx.y) : 0,
-                   all = odd != 0 ? (uint32_t)A.R.n_rows * A.q.heads : 0;  // (under 2^31: check_heads)
+    uint32_t shares = 0, before = 0;
 #pragma unroll 1
-    for (uint32_t i = warp; i < 16 + all; i += kPaWarps) {
-        if (i < 16 && i >= joined) continue;
+    for (int c0 = 0; c0 < (int)gridDim.x; c0 += 32) {
+        const uint32_t w = __ballot_sync(0xffffffffu, c0 + lane < (int)gridDim.x && A.ws_odd[c0 + lane] != 0);
+        shares += __popc(w);
+        before += __popc(c0 + 32 <= (int)blockIdx.x ? w : c0 > (int)blockIdx.x ? 0u : w & ((1u << (blockIdx.x - c0)) - 1));
+    }
+    const uint32_t joined = any ? min(16, e.rows - 16 * (int)blockIdx.y) : 0,
+                   all = odd != 0 ? (uint32_t)A.R.n_rows * A.q.heads : 0,  // (under 2^31: check_heads)
+                   by = shares * gridDim.y * kPaWarps;
+    uint32_t i = warp;
+    bool mine = true;
+#pragma unroll 1
+    for (;;) {
+        if (mine && i >= joined) {
+            mine = false;
+            i = (before * gridDim.y + blockIdx.y) * kPaWarps + warp;
+        }
+        if (!mine && i >= all) break;
         // rows of a unit are group by group, rows of the call heads by heads
-        const uint32_t per = i < 16 ? A.group : A.q.heads, at = i < 16 ? e.m0 + 16 * blockIdx.y + i : i - 16, r = at / per;
-        pa_odd_row<HD>(A, (int)r + (i < 16 ? e.row0 : 0), (int)(at - r * per) + (i < 16 ? h * A.group : 0), i < 16);
+        const uint32_t per = mine ? A.group : A.q.heads, at = mine ? e.m0 + 16 * blockIdx.y + i : i, r = at / per;
+        pa_odd_row<HD>(A, (int)r + (mine ? e.row0 : 0), (int)(at - r * per) + (mine ? h * A.group : 0), mine);
+        i += mine ? kPaWarps : by;
     }
 }
 
