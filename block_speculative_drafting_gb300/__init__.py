@@ -11,7 +11,8 @@ ones numpy arrays; calls run on torch's current stream unless given one.
     logits, tokens = model.block([seq], [anchor_tok], [anchor_pos], block_len)
 
 The target's own pass over a drafted block (target.py): paged_append,
-paged_attention and verify_drafts.
+paged_attention and verify_drafts; its cache kept small, in 4 bits or cut back
+to its heaviest tokens: paged_read, paged_key_weights and paged_evict.
 """
 from __future__ import annotations
 
@@ -21,8 +22,9 @@ import numpy as np
 
 from . import _abi
 from ._abi import QUANT_F32, QUANT_Q4G32, MAT_FC, MAT_HEAD, mat_layer  # noqa: F401
-from .target import (paged_append, paged_attention, paged_attention_workspace, rope_inv_freq,  # noqa: F401
-                     verify_drafts, verify_workspace)
+from .target import (paged_append, paged_attention, paged_attention_workspace, paged_evict,  # noqa: F401
+                     paged_evict_workspace, paged_key_weights, paged_read, rope_inv_freq, verify_drafts,
+                     verify_workspace)
 
 _lib = None
 

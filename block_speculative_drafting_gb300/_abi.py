@@ -52,7 +52,7 @@ class Weights(C.Structure):
 
 
 # element types of the target's verification pass
-F32, BF16, F16, E4M3 = 0, 1, 2, 3
+F32, BF16, F16, E4M3, E2M1 = 0, 1, 2, 3, 4
 
 _VP = C.c_void_p
 
@@ -60,7 +60,8 @@ _VP = C.c_void_p
 class PagedCache(C.Structure):
     _fields_ = [("k", _VP), ("v", _VP), ("dtype", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
                 ("page_size", C.c_int32), ("n_pages", C.c_int64), ("k_strides", C.c_int64 * 3),
-                ("v_strides", C.c_int64 * 3), ("k_scale", _VP), ("v_scale", _VP)]
+                ("v_strides", C.c_int64 * 3), ("k_scale", _VP), ("v_scale", _VP), ("k_block", _VP), ("v_block", _VP),
+                ("k_block_strides", C.c_int64 * 3), ("v_block_strides", C.c_int64 * 3)]
 
 
 class PagedRows(C.Structure):
@@ -75,6 +76,10 @@ class HeadRows(C.Structure):
 
 class Rotation(C.Structure):
     _fields_ = [("inv_freq", _VP), ("rotary", C.c_int32), ("interleaved", C.c_int32), ("scale", C.c_float)]
+
+
+class KeyWeights(C.Structure):
+    _fields_ = [("data", _VP), ("positions", C.c_int64), ("seq_stride", C.c_int64), ("head_stride", C.c_int64)]
 
 
 _PC, _PR, _PH = C.POINTER(PagedCache), C.POINTER(PagedRows), C.POINTER(HeadRows)
@@ -115,6 +120,13 @@ _SIGS = {
     "dflash_paged_append": (C.c_int, [_PC, _PR, _PH, _PH, _PH, _PH, _VP, _VP, C.c_float, C.POINTER(Rotation), _VP]),
     "dflash_paged_attention": (C.c_int, [_PC, _PR, _PH, _PH, _VP, C.c_float, C.c_int32, _VP, C.c_int64, _VP]),
     "dflash_paged_attention_workspace": (C.c_int64, [_PC, C.c_int32, C.c_int64, C.c_int32]),
+    "dflash_paged_append_at": (C.c_int, [_PC, _PR, _PH, _PH, _PH, _PH, _VP, _VP, C.c_float, C.POINTER(Rotation), _VP,
+                                         _VP]),
+    "dflash_paged_read": (C.c_int, [_PC, _PR, _PH, _PH, _VP]),
+    "dflash_paged_key_weights": (C.c_int, [_PC, _PR, _PH, _VP, C.c_float, C.c_int32, C.POINTER(KeyWeights), _VP]),
+    "dflash_paged_evict": (C.c_int, [_PC, _PR, C.c_int32, C.c_int32, C.c_int32, C.POINTER(KeyWeights),
+                                     C.POINTER(KeyWeights), _VP, _VP, _VP, _VP, C.c_int64, _VP]),
+    "dflash_paged_evict_workspace": (C.c_int64, [C.c_int32, C.c_int32, C.c_int32, C.c_int32]),
     "dflash_verify": (C.c_int, [_VP, C.c_int32, C.c_int64, _VP, C.c_int64, _VP, _VP, _VP, _VP, _VP, C.c_int32,
                                 C.c_int64, C.c_int64, _VP, _VP, _VP, _VP, C.c_int64, _VP]),
     "dflash_verify_workspace": (C.c_int64, [C.c_int32, C.c_int64, C.c_int64]),

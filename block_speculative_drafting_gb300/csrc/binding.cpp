@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -25,10 +26,14 @@
 
 namespace {
 
-enum { F32 = DFLASH_F32, BF16 = DFLASH_BF16, F16 = DFLASH_F16, E4M3 = DFLASH_E4M3, F64, I32, U32, OTHER };
+enum { F32 = DFLASH_F32, BF16 = DFLASH_BF16, F16 = DFLASH_F16, E4M3 = DFLASH_E4M3, E2M1 = DFLASH_E2M1, F64 = 64, I32, U32, U8, OTHER };
 
 PyObject *error_type, *memory_error;  // DFlashError, torch's OutOfMemoryError
-decltype(&dflash_paged_append) lib_append;
+decltype(&dflash_paged_append_at) lib_append;
+decltype(&dflash_paged_read) lib_read;
+decltype(&dflash_paged_key_weights) lib_key_weights;
+decltype(&dflash_paged_evict) lib_evict;
+decltype(&dflash_paged_evict_workspace) lib_evict_workspace;
 decltype(&dflash_paged_attention) lib_attention;
 decltype(&dflash_paged_attention_workspace) lib_attention_workspace;
 decltype(&dflash_verify) lib_verify;
@@ -83,6 +88,8 @@ int type_of(at::ScalarType t) {
         case at::kDouble: return F64;
         case at::kInt: return I32;
         case at::kUInt32: return U32;
+        case at::kByte: return U8;
+        case at::ScalarType::Float4_e2m1fn_x2: return E2M1;
         default: return OTHER;
     }
 }
@@ -194,9 +201,23 @@ dflash_head_rows head_rows(const Tensor& t, const char* name, int64_t n, int64_t
     if (t.shape[1] > INT32_MAX) refuse("%s has %lld heads", name, (long long)t.shape[1]);
     return {t.p, t.dtype, (int32_t)t.shape[1], t.stride[0], t.stride[1]};
 }
+// A 4-bit cache's block scales, one an e4m3 byte for 16 columns.
+void read_blocks(const Call& call, PyObject* o, const char* name, const dflash_paged_cache& c, bool writes, void** p,
+                 int64_t (&strides)[3]) {
+    if (o == Py_None) refuse("a 4-bit cache needs %s", name);
+    const Tensor t = call.read(o, name);
+    if (t.nd != 4 || t.dtype != E4M3 || t.shape[0] != c.n_pages || t.shape[1] != c.page_size ||
+        t.shape[2] != c.kv_heads || t.shape[3] != c.head_dim / 16 || t.stride[3] != 1)
+        refuse("%s has to be float8_e4m3fn [%lld][%d][%d][%d] with contiguous blocks", name, (long long)c.n_pages,
+               (int)c.page_size, (int)c.kv_heads, (int)c.head_dim / 16);
+    if (writes) t.written(name);
+    *p = t.p;
+    for (int i = 0; i < 3; ++i) strides[i] = t.stride[i];
+}
+// v None: a call that reads keys alone (the values' fields are then the keys').
 dflash_paged_cache read_cache(const Call& call, PyObject* k, PyObject* v, PyObject* k_scale, PyObject* v_scale,
-                              bool writes) {
-    const Tensor tk = call.read(k, "k_cache"), tv = call.read(v, "v_cache");
+                              PyObject* k_block, PyObject* v_block, bool writes) {
+    const Tensor tk = call.read(k, "k_cache"), tv = v == Py_None ? tk : call.read(v, "v_cache");
     if (tk.nd != 4 || tv.nd != 4 || tk.dtype != tv.dtype)
         refuse("k_cache and v_cache have to be [pages][page_size][kv_heads][head_dim] of one type");
     for (int i = 0; i < 4; ++i)
@@ -204,21 +225,28 @@ dflash_paged_cache read_cache(const Call& call, PyObject* k, PyObject* v, PyObje
     if (tk.stride[3] != 1 || tv.stride[3] != 1) refuse("k_cache and v_cache need contiguous columns");
     if (writes) tk.written("k_cache"), tv.written("v_cache");
     for (int i = 1; i < 4; ++i)
-        if (tk.shape[i] > INT32_MAX) refuse("a cache dimension is too large");
+        if (tk.shape[i] > INT32_MAX / 2) refuse("a cache dimension is too large");
     dflash_paged_cache c{};
     c.k = tk.p;
     c.v = tv.p;
-    c.dtype = tk.dtype;
+    c.dtype = tk.dtype == U8 ? E2M1 : tk.dtype;
     c.n_pages = tk.shape[0];
     c.page_size = (int32_t)tk.shape[1];
     c.kv_heads = (int32_t)tk.shape[2];
-    c.head_dim = (int32_t)tk.shape[3];
+    c.head_dim = (int32_t)tk.shape[3] * (c.dtype == E2M1 ? 2 : 1);
     for (int i = 0; i < 3; ++i) {
         c.k_strides[i] = tk.stride[i];
         c.v_strides[i] = tv.stride[i];
     }
     c.k_scale = static_cast<const float*>(call.vector(k_scale, "k_scale", c.kv_heads, F32));
-    c.v_scale = static_cast<const float*>(call.vector(v_scale, "v_scale", c.kv_heads, F32));
+    c.v_scale = v == Py_None ? c.k_scale : static_cast<const float*>(call.vector(v_scale, "v_scale", c.kv_heads, F32));
+    if (c.dtype == E2M1) {
+        read_blocks(call, k_block, "k_block", c, writes, &c.k_block, c.k_block_strides);
+        read_blocks(call, v == Py_None ? k_block : v_block, v == Py_None ? "k_block" : "v_block", c, writes, &c.v_block,
+                    c.v_block_strides);
+    } else if (k_block != Py_None || v_block != Py_None) {
+        refuse("block scales need a 4-bit cache");
+    }
     return c;
 }
 dflash_paged_rows read_rows(const Call& call, PyObject* table, PyObject* kv_len, PyObject* row_start, int64_t n_rows) {
@@ -242,18 +270,19 @@ bool arguments(Py_ssize_t got, Py_ssize_t want) {
 }
 
 // k_cache, v_cache, k, v, table, kv_len, row_start, q, q_out, inv_freq, interleaved, rope_scale, q_norm, k_norm, eps,
-// k_scale, v_scale, stream
+// k_scale, v_scale, stream, k_block, v_block, evicted
 PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t na) {
-    if (!arguments(na, 18)) return nullptr;
+    if (!arguments(na, 21)) return nullptr;
     return entry([&]() -> PyObject* {
         const Call call(tensor(a[0], "k_cache"), a[17]);
-        const dflash_paged_cache c = read_cache(call, a[0], a[1], a[15], a[16], true);
+        const dflash_paged_cache c = read_cache(call, a[0], a[1], a[15], a[16], a[18], a[19], true);
         const Tensor tk = call.read(a[2], "k"), tv = call.read(a[3], "v");
         const int64_t n = tk.shape[0], hd = c.head_dim;
         const dflash_head_rows k = head_rows(tk, "k", n, hd), v = head_rows(tv, "v", n, hd);
         const dflash_paged_rows r = read_rows(call, a[4], a[5], a[6], n);
         const float* qn = static_cast<const float*>(call.vector(a[12], "q_norm", hd, F32));
         const float* kn = static_cast<const float*>(call.vector(a[13], "k_norm", hd, F32));
+        const auto* evicted = static_cast<const int32_t*>(call.vector(a[20], "evicted", r.n_seqs, I32));
         dflash_rotation rot{};
         const bool rotates = a[9] != Py_None, with_q = a[7] != Py_None;
         if (rotates) {
@@ -280,35 +309,43 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t na) {
         }
         checked(unlocked([&] {
             return lib_append(&c, &r, &k, &v, with_q ? &q : nullptr, with_q ? &qo : nullptr, qn, kn, eps,
-                              rotates ? &rot : nullptr, call.stream);
+                              rotates ? &rot : nullptr, evicted, call.stream);
         }));
         return made.defined() ? THPVariable_Wrap(std::move(made)) : kept(a[8]);
     });
 }
 
-// q, k_cache, v_cache, table, kv_len, row_start, scale, window, k_scale, v_scale, out, lse, workspace, stream
+// The scale of the scores: None is head_dim ** -0.5.
+double scale_of(PyObject* o, int64_t hd) { return o == Py_None ? std::pow((double)hd, -0.5) : number(o); }
+int32_t window_of(PyObject* o) {
+    const long window = PyLong_AsLong(o);
+    if (PyErr_Occurred()) throw PythonError{};
+    if (window < 0 || window > INT32_MAX) refuse("window %ld", window);
+    return (int32_t)window;
+}
+float* read_lse(const Call& call, PyObject* o, int64_t n, int heads) {
+    const Tensor t = call.read(o, "lse");
+    if (t.nd != 2 || t.dtype != F32 || t.shape[0] != n || t.shape[1] != heads || t.stride[1] != 1 ||
+        (n > 1 && t.stride[0] != heads))
+        refuse("lse has to be contiguous float32 [%lld][%d]", (long long)n, heads);
+    return static_cast<float*>(t.p);
+}
+
+// q, k_cache, v_cache, table, kv_len, row_start, scale, window, k_scale, v_scale, out, lse, workspace, stream, k_block,
+// v_block
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t na) {
-    if (!arguments(na, 14)) return nullptr;
+    if (!arguments(na, 16)) return nullptr;
     return entry([&]() -> PyObject* {
         const at::Tensor& qt = tensor(a[0], "q");
         const Call call(qt, a[13]);
-        const dflash_paged_cache c = read_cache(call, a[1], a[2], a[8], a[9], false);
+        const dflash_paged_cache c = read_cache(call, a[1], a[2], a[8], a[9], a[14], a[15], false);
         const Tensor tq(qt, "q", call.dev);
         const int64_t n = tq.shape[0], hd = c.head_dim;
         const dflash_head_rows q = head_rows(tq, "q", n, hd);
         const dflash_paged_rows r = read_rows(call, a[3], a[4], a[5], n);
-        const double scale = a[6] == Py_None ? std::pow((double)hd, -0.5) : number(a[6]);
-        const long window = PyLong_AsLong(a[7]);
-        if (PyErr_Occurred()) throw PythonError{};
-        if (window < 0 || window > INT32_MAX) refuse("window %ld", window);
-        float* lse = nullptr;
-        if (a[11] != Py_None) {
-            const Tensor t = call.read(a[11], "lse");
-            if (t.nd != 2 || t.dtype != F32 || t.shape[0] != n || t.shape[1] != q.heads || t.stride[1] != 1 ||
-                (n > 1 && t.stride[0] != q.heads))
-                refuse("lse has to be contiguous float32 [%lld][%d]", (long long)n, (int)q.heads);
-            lse = static_cast<float*>(t.p);
-        }
+        const double scale = scale_of(a[6], hd);
+        const int32_t window = window_of(a[7]);
+        float* lse = a[11] == Py_None ? nullptr : read_lse(call, a[11], n, q.heads);
         const int64_t need = checked(lib_attention_workspace(&c, r.n_seqs, n, q.heads));
         at::Tensor made;
         if (a[10] == Py_None) made = call.make(qt.sizes(), qt.scalar_type());
@@ -317,9 +354,122 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t na) {
         const dflash_head_rows o = head_rows(to, "out", n, hd);
         const Workspace w(call, a[12], need);
         checked(unlocked([&] {
-            return lib_attention(&c, &r, &q, &o, lse, (float)scale, (int32_t)window, w.p, w.bytes, call.stream);
+            return lib_attention(&c, &r, &q, &o, lse, (float)scale, window, w.p, w.bytes, call.stream);
         }));
         return made.defined() ? THPVariable_Wrap(std::move(made)) : kept(a[10]);
+    });
+}
+
+// k_cache, v_cache, table, kv_len, rows, row_start, k_scale, v_scale, k_block, v_block, dtype's name, k_out, v_out, stream
+PyObject* paged_read(PyObject*, PyObject* const* a, Py_ssize_t na) {
+    if (!arguments(na, 14)) return nullptr;
+    return entry([&]() -> PyObject* {
+        const Call call(tensor(a[0], "k_cache"), a[13]);
+        const dflash_paged_cache c = read_cache(call, a[0], a[1], a[6], a[7], a[8], a[9], false);
+        const long long n = PyLong_AsLongLong(a[4]);
+        if (PyErr_Occurred()) throw PythonError{};
+        if (n < 0 || n >= 1 << 24) refuse("rows %lld", n);
+        const dflash_paged_rows r = read_rows(call, a[2], a[3], a[5], n);
+        at::ScalarType type = at::kBFloat16;
+        if (a[10] != Py_None) {
+            if (!THPDtype_Check(a[10])) {
+                PyErr_Format(PyExc_TypeError, "dtype has to be a torch.dtype, not %s", Py_TYPE(a[10])->tp_name);
+                throw PythonError{};
+            }
+            type = reinterpret_cast<THPDtype*>(a[10])->scalar_type;
+        } else if (c.dtype == F16) {
+            type = at::kHalf;
+        }
+        at::Tensor made[2];
+        dflash_head_rows out[2];
+        static const char* const names[2] = {"k_out", "v_out"};
+        if (type != at::kFloat && type != at::kBFloat16 && type != at::kHalf)
+            refuse("dtype is not float32, bfloat16 or float16");
+        for (int i = 0; i < 2; ++i) {
+            if (a[11 + i] == Py_None) made[i] = call.make({n, c.kv_heads, c.head_dim}, type);
+            const Tensor t(a[11 + i] == Py_None ? made[i] : tensor(a[11 + i], names[i]), names[i], call.dev);
+            t.written(names[i]);
+            if (a[10] != Py_None && t.dtype != type_of(type)) refuse("%s is not of the dtype asked for", names[i]);
+            out[i] = head_rows(t, names[i], n, c.head_dim);
+        }
+        checked(unlocked([&] { return lib_read(&c, &r, &out[0], &out[1], call.stream); }));
+        PyObject* res = PyTuple_New(2);
+        for (int i = 0; res != nullptr && i < 2; ++i) {
+            PyObject* x = made[i].defined() ? THPVariable_Wrap(std::move(made[i])) : kept(a[11 + i]);
+            if (x == nullptr) Py_CLEAR(res);
+            if (res != nullptr) PyTuple_SET_ITEM(res, i, x);
+        }
+        return res;
+    });
+}
+
+// float32 [sequences][kv_heads][positions] with contiguous positions
+dflash_key_weights read_weights(const Call& call, PyObject* o, const char* name, const dflash_paged_rows& r,
+                                const dflash_paged_cache& c, bool writes) {
+    const Tensor t = call.read(o, name);
+    if (t.nd != 3 || t.dtype != F32 || t.shape[0] != r.n_seqs || t.shape[1] != c.kv_heads || t.stride[2] != 1)
+        refuse("%s has to be float32 [%d][%d][positions] with contiguous positions", name, (int)r.n_seqs, (int)c.kv_heads);
+    if (writes) t.written(name);
+    return {static_cast<float*>(t.p), t.shape[2], t.stride[0], t.stride[1]};
+}
+
+// weights, q, k_cache, table, kv_len, lse, row_start, scale, window, k_scale, k_block, stream
+PyObject* paged_key_weights(PyObject*, PyObject* const* a, Py_ssize_t na) {
+    if (!arguments(na, 12)) return nullptr;
+    return entry([&]() -> PyObject* {
+        const at::Tensor& qt = tensor(a[1], "q");
+        const Call call(qt, a[11]);
+        const dflash_paged_cache c = read_cache(call, a[2], Py_None, a[9], Py_None, a[10], Py_None, false);
+        const Tensor tq(qt, "q", call.dev);
+        const int64_t n = tq.shape[0], hd = c.head_dim;
+        const dflash_head_rows q = head_rows(tq, "q", n, hd);
+        const dflash_paged_rows r = read_rows(call, a[3], a[4], a[6], n);
+        const double scale = scale_of(a[7], hd);
+        const int32_t window = window_of(a[8]);
+        const float* lse = read_lse(call, a[5], n, q.heads);
+        const dflash_key_weights w = read_weights(call, a[0], "weights", r, c, true);
+        checked(unlocked([&] { return lib_key_weights(&c, &r, &q, lse, (float)scale, window, &w, call.stream); }));
+        return kept(a[0]);
+    });
+}
+
+int32_t whole(PyObject* o, const char* name) {
+    const long x = PyLong_AsLong(o);
+    if (PyErr_Occurred()) throw PythonError{};
+    if (x < 0 || x > INT32_MAX) refuse("%s %ld", name, x);
+    return (int32_t)x;
+}
+// k_cache, v_cache, weights, table, kv_len, keep, first, recent, k_block, v_block, weights_out, new_len, kept, evicted,
+// workspace, stream
+PyObject* paged_evict(PyObject*, PyObject* const* a, Py_ssize_t na) {
+    if (!arguments(na, 16)) return nullptr;
+    return entry([&]() -> PyObject* {
+        const Call call(tensor(a[0], "k_cache"), a[15]);
+        const dflash_paged_cache c = read_cache(call, a[0], a[1], Py_None, Py_None, a[8], a[9], true);
+        const dflash_paged_rows r = read_rows(call, a[3], a[4], Py_None, 0);
+        const int32_t keep = whole(a[5], "keep"), first = whole(a[6], "first"), recent = whole(a[7], "recent");
+        const bool aside = a[10] != Py_None && a[10] != a[2];
+        const dflash_key_weights w = read_weights(call, a[2], "weights", r, c, !aside);
+        const dflash_key_weights o = aside ? read_weights(call, a[10], "weights_out", r, c, true) : w;
+        int32_t* kept_slots = nullptr;
+        if (a[12] != Py_None) {
+            const Tensor t = call.read(a[12], "kept");
+            if (t.nd != 3 || t.dtype != I32 || t.shape[0] != r.n_seqs || t.shape[1] != c.kv_heads || t.shape[2] != keep ||
+                (keep > 1 && t.stride[2] != 1) || (c.kv_heads > 1 && t.stride[1] != keep) ||
+                (r.n_seqs > 1 && t.stride[0] != (int64_t)c.kv_heads * keep))
+                refuse("kept has to be contiguous int32 [%d][%d][%d]", (int)r.n_seqs, (int)c.kv_heads, (int)keep);
+            kept_slots = static_cast<int32_t*>(t.p);
+        }
+        auto* evicted = static_cast<int32_t*>(call.vector(a[13], "evicted", r.n_seqs, I32));
+        const int64_t need = checked(lib_evict_workspace(r.n_seqs, c.kv_heads, keep, kept_slots == nullptr));
+        at::Tensor made;
+        if (a[11] == Py_None) made = call.make({r.n_seqs}, at::kInt);
+        auto* new_len = static_cast<int32_t*>(a[11] == Py_None ? made.data_ptr() : call.vector(a[11], "new_len", r.n_seqs, I32));
+        const Workspace ws(call, a[14], need);
+        checked(unlocked([&] {
+            return lib_evict(&c, &r, keep, first, recent, &w, &o, new_len, kept_slots, evicted, ws.p, ws.bytes, call.stream);
+        }));
+        return made.defined() ? THPVariable_Wrap(std::move(made)) : kept(a[11]);
     });
 }
 
@@ -403,17 +553,23 @@ PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t na) {
     });
 }
 
-// init(addresses of the six entry points, DFlashError, torch's OutOfMemoryError)
+// init(addresses of the entry points, DFlashError, torch's OutOfMemoryError)
 PyObject* init(PyObject*, PyObject* args) {
-    unsigned long long f[6];
+    unsigned long long f[10];
     PyObject *err, *memory;
-    if (!PyArg_ParseTuple(args, "(KKKKKK)OO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &err, &memory)) return nullptr;
+    if (!PyArg_ParseTuple(args, "(KKKKKKKKKK)OO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9],
+                          &err, &memory))
+        return nullptr;
     lib_append = reinterpret_cast<decltype(lib_append)>((uintptr_t)f[0]);
     lib_attention = reinterpret_cast<decltype(lib_attention)>((uintptr_t)f[1]);
     lib_attention_workspace = reinterpret_cast<decltype(lib_attention_workspace)>((uintptr_t)f[2]);
     lib_verify = reinterpret_cast<decltype(lib_verify)>((uintptr_t)f[3]);
     lib_verify_workspace = reinterpret_cast<decltype(lib_verify_workspace)>((uintptr_t)f[4]);
     lib_last_error = reinterpret_cast<decltype(lib_last_error)>((uintptr_t)f[5]);
+    lib_read = reinterpret_cast<decltype(lib_read)>((uintptr_t)f[6]);
+    lib_key_weights = reinterpret_cast<decltype(lib_key_weights)>((uintptr_t)f[7]);
+    lib_evict = reinterpret_cast<decltype(lib_evict)>((uintptr_t)f[8]);
+    lib_evict_workspace = reinterpret_cast<decltype(lib_evict_workspace)>((uintptr_t)f[9]);
     Py_INCREF(err);
     Py_XSETREF(error_type, err);
     Py_INCREF(memory);
@@ -427,6 +583,9 @@ PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
 PyMethodDef methods[] = {{"init", init, METH_VARARGS, nullptr},
                          {"paged_append", fast(paged_append), METH_FASTCALL, nullptr},
                          {"paged_attention", fast(paged_attention), METH_FASTCALL, nullptr},
+                         {"paged_read", fast(paged_read), METH_FASTCALL, nullptr},
+                         {"paged_key_weights", fast(paged_key_weights), METH_FASTCALL, nullptr},
+                         {"paged_evict", fast(paged_evict), METH_FASTCALL, nullptr},
                          {"verify_drafts", fast(verify_drafts), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

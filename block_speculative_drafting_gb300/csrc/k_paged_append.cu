@@ -17,7 +17,7 @@
 // rows with head norms into an e4m3 cache: 9.0 us, the chain of a row's norms
 // and rotations; one row: 4.5 us, launch and lookups.
 #include "kernels.cuh"
-#include "paged.cuh"
+#include "paged_attn.cuh"
 
 namespace dflash {
 
@@ -51,6 +51,37 @@ struct Raw8 {
         }
     }
 };
+
+// Eight values of a 4-bit cache's row, in units of the head's scale: with the eight of the neighbouring lane they are a
+// block of 16.  s = e4m3(min(max |x| / 6, 448)), codes e2m1(x / s) (nearest, ties to even, clamped to +-6; the
+// conversions and the division round as IEEE's do).  A NaN makes its block's scale NaN, and so all that the block stands for; a
+// block whose scale rounds to 0 is 0.  The even lane writes the scale.
+DF_DEV void store8_e2m1(unsigned char* p, unsigned char* block, const float (&x)[8], bool in, int c) {
+    float m = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        m = fmaxf(m, fabsf(x[i]));
+        nan |= x[i] != x[i];
+    }
+    if (nan) m = NAN;
+    const float o = __shfl_xor_sync(0xffffffffu, m, 1);
+    m = m != m || o != o ? NAN : fmaxf(m, o);
+    const float q = __fdiv_rn(m, 6.f);
+    const uint32_t s8 = m != m ? 0x7fu : __nv_cvt_float_to_fp8(fminf(q, 448.f), __NV_SATFINITE, __NV_E4M3);
+    const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s8, __NV_E4M3)));
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = s > 0.f ? __fdiv_rn(x[i], s) : 0.f;
+    uint32_t w;
+    asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
+        : "=r"(w)
+        : "f"(u[0]), "f"(u[1]), "f"(u[2]), "f"(u[3]), "f"(u[4]), "f"(u[5]), "f"(u[6]), "f"(u[7]));
+    if (!in) return;
+    *reinterpret_cast<uint32_t*>(p) = w;
+    if ((c & 1) == 0) *block = (unsigned char)s8;
+}
 
 // Eight values as type DT, rounded to nearest even.
 template <int DT>
@@ -93,6 +124,8 @@ struct HeadLoop {
     int64_t from_step, to_step;  // bytes to the next round's head
     int first, step, heads, rounds;
     const float *gain, *scale;  // the norm's gain (columns 8 c ..), the cache's scales by head; null: none
+    unsigned char* block;       // a 4-bit cache: where the first head's scale of the lane's block goes
+    int64_t block_step;         // bytes to the next round's
     float eps;
     bool rotates, turned, interleaved;
     int other;  // the lane with the other columns of the pairs
@@ -103,6 +136,7 @@ DF_DEV void head_loop(const HeadLoop& H, const float (&co)[8], const float (&si)
     Raw8<IN> next[AHEAD];
     const unsigned char* from = H.from;
     unsigned char* to = H.to;
+    [[maybe_unused]] unsigned char* block = H.block;
     int h = H.first;
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
@@ -144,15 +178,19 @@ DF_DEV void head_loop(const HeadLoop& H, const float (&co)[8], const float (&si)
                     }
                 }
             }
-            if (h < H.heads) {
+            if (OUT == kE2M1 || h < H.heads) {
                 if (H.scale != nullptr) {
-                    const float sc = H.scale[h];
+                    const float sc = H.scale[min(h, H.heads - 1)];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) x[j] = __fdiv_rn(x[j], sc);
                 }
-                store8<OUT>(to, x);
+                if constexpr (OUT == kE2M1)  // (all lanes: pairs of them share a block)
+                    store8_e2m1(to, block, x, h < H.heads, threadIdx.x & (L - 1));
+                else
+                    store8<OUT>(to, x);
             }
             h += H.step;
+            if constexpr (OUT == kE2M1) block += H.block_step;
             from += H.from_step;
             to += H.to_step;
         }
@@ -165,7 +203,7 @@ __global__ void __launch_bounds__(kApWarps * 32, 4)
                         const __grid_constant__ HeadRows k, const __grid_constant__ HeadRows v,
                         const __grid_constant__ HeadRows q, const __grid_constant__ HeadRows qo,
                         const float* __restrict__ q_norm, const float* __restrict__ k_norm, float eps,
-                        const __grid_constant__ Rotation rot, int warps_log2) {
+                        const __grid_constant__ Rotation rot, const int32_t* __restrict__ evicted, int warps_log2) {
     constexpr int L = HD / 8;     // lanes of a head
     constexpr int HPW = 32 / L;   // heads a warp holds at once
     __shared__ float2 turns_of[kApWarps][HD / 2];
@@ -181,6 +219,7 @@ __global__ void __launch_bounds__(kApWarps * 32, 4)
     const int64_t pos64 = (int64_t)R.kv_len[s] - (b - a) + (row - a);
     int slot = 0;
     const int64_t page = page_of(R, C.n_pages, s, (int)max(pos64, (int64_t)-1), slot);
+    const int64_t turn64 = evicted != nullptr ? pos64 + evicted[s] : pos64;  // the token's place in its sequence
     // column 8 c + i becomes x co[i] + y si[i], y the other column of its pair
     const bool turned = 8 * c < rot.rotary;
     const int half = rot.rotary / 16;  // lanes between the columns of a pair (pairs (i, i + rotary / 2))
@@ -188,7 +227,7 @@ __global__ void __launch_bounds__(kApWarps * 32, 4)
     float co[8], si[8];
     if (rot.rotary > 0) {
         for (int i = lane; i < rot.rotary / 2; i += 32) {
-            const double t = (double)pos64 * rot.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+            const double t = (double)turn64 * rot.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
             float sn, cn;
             sincospif(2.f * (float)(t - rint(t)), &sn, &cn);
             turns_of[warp][i] = make_float2(cn * rot.scale, sn * rot.scale);
@@ -210,13 +249,14 @@ __global__ void __launch_bounds__(kApWarps * 32, 4)
     H.other = other;
     H.step = HPW << warps_log2;
     H.first = share * HPW + lane / L;
-    const auto bytes = [](int dtype) { return dtype == kF32 ? 4 : dtype == kE4M3 ? 1 : 2; };
+    // bytes of this lane's columns before its own (8 c of them)
+    const auto before = [c](int dtype) { return dtype == kE2M1 ? 4 * c : 8 * c * (dtype == kF32 ? 4 : dtype == kE4M3 ? 1 : 2); };
     auto set = [&](const HeadRows& src, unsigned char* to, int64_t hs, int out) {
         H.heads = src.heads;
         H.rounds = (src.heads - share * HPW + H.step - 1) / H.step;
-        H.from = src.p + (int64_t)row * src.rs + H.first * src.hs + 8 * c * bytes(IN);
+        H.from = src.p + (int64_t)row * src.rs + H.first * src.hs + before(IN);
         H.from_step = H.step * src.hs;
-        H.to = to + H.first * hs + 8 * c * bytes(out);
+        H.to = to + H.first * hs + before(out);
         H.to_step = H.step * hs;
     };
     if (q.heads > 0) {
@@ -233,16 +273,125 @@ __global__ void __launch_bounds__(kApWarps * 32, 4)
         set(side == 0 ? k : v, (side == 0 ? C.k : C.v) + page * st[0] + slot * st[1], st[2], OUT);
         H.gain = side == 0 && k_norm != nullptr ? k_norm + 8 * c : nullptr;
         H.scale = side == 0 ? C.k_scale : C.v_scale;
+        if constexpr (OUT == kE2M1) {
+            const int64_t* bt = side == 0 ? C.kbs : C.vbs;
+            H.block = (side == 0 ? C.kb : C.vb) + page * bt[0] + slot * bt[1] + H.first * bt[2] + c / 2;
+            H.block_step = H.step * bt[2];
+        }
         H.rotates = side == 0 && rot.rotary > 0;
         head_loop<HD, IN, OUT>(H, co, si);
     }
+}
+
+// ---------------------------------------------------------------- rows read back
+// A cache's rows as values: 16 columns a lane and round (16 bytes of codes at most from an 8-bit cache, 8 from a 4-bit
+// one), warps over the call's rows as in the append.  Code times block scale is exact, the head's scale rounds in 32
+// bits, and the output's type once.  Positions that are not held read as zeros.
+template <int HD, int CD, int OUT>
+__global__ void __launch_bounds__(kApWarps * 32)
+    paged_read_kernel(const __grid_constant__ PagedCache C, const __grid_constant__ PagedRows R,
+                      const __grid_constant__ HeadRows ko, const __grid_constant__ HeadRows vo, int warps_log2) {
+    constexpr int L = HD / 16;   // lanes of a head
+    constexpr int HPW = 32 / L;  // heads a warp holds at once
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % L;
+    const int64_t id = (int64_t)blockIdx.x * kApWarps + warp;
+    const int row = (int)(id >> warps_log2), share = (int)(id & ((1 << warps_log2) - 1));
+    pdl_wait();
+    pdl_trigger();
+    const int s = row < R.n_rows ? seq_of(R, row) : -1;
+    if (s < 0) return;
+    int a, b;
+    rows_of(R, s, a, b);
+    const int64_t pos64 = (int64_t)R.kv_len[s] - (b - a) + (row - a);
+    int slot = 0;
+    const int64_t page = page_of(R, C.n_pages, s, (int)max(pos64, (int64_t)-1), slot);
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+        const HeadRows& O = side == 0 ? ko : vo;
+        if (O.p == nullptr) continue;
+        const unsigned char* from = (side == 0 ? C.k : C.v) + max(page, (int64_t)0) * (side == 0 ? C.ks[0] : C.vs[0]) +
+                                    slot * (side == 0 ? C.ks[1] : C.vs[1]);
+        const int64_t hs = side == 0 ? C.ks[2] : C.vs[2];
+        const float* scale = side == 0 ? C.k_scale : C.v_scale;
+#pragma unroll 2
+        for (int h = share * HPW + lane / L; h < C.kv_heads; h += HPW << warps_log2) {
+            float x[2][8] = {};
+            if (page >= 0) {
+                const unsigned char* p = from + h * hs;
+                const float sc = scale != nullptr ? scale[h] : 1.f;
+                if constexpr (CD == kBF16 || CD == kF16) {
+                    Raw8<CD> r[2];
+                    r[0].load(p + 32 * c);
+                    r[1].load(p + 32 * c + 16);
+                    r[0].values(x[0]);
+                    r[1].values(x[1]);
+                } else {
+                    uint32_t y[8];
+                    float f = sc;
+                    if constexpr (CD == kE4M3) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(p + 16 * c);
+                        e4m3x4_f16x4(w.x, y[0], y[1]);
+                        e4m3x4_f16x4(w.y, y[2], y[3]);
+                        e4m3x4_f16x4(w.z, y[4], y[5]);
+                        e4m3x4_f16x4(w.w, y[6], y[7]);
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2*>(p + 8 * c);
+                        const unsigned char* bl = side == 0 ? C.kb + page * C.kbs[0] + slot * C.kbs[1] + h * C.kbs[2]
+                                                            : C.vb + page * C.vbs[0] + slot * C.vbs[1] + h * C.vbs[2];
+                        const uint32_t s2 = __byte_perm(e4m3x2_f16x2(bl[c]), 0, 0x1010);
+                        uint32_t z[4];
+                        e2m1x8_f16x8(w.x, z);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) y[i] = mul_f16x2(z[i], s2);
+                        e2m1x8_f16x8(w.y, z);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) y[4 + i] = mul_f16x2(z[i], s2);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 v = unpack2<false>(y[i]);
+                        x[i >> 2][2 * (i & 3)] = v.x * f;
+                        x[i >> 2][2 * (i & 3) + 1] = v.y * f;
+                    }
+                }
+            }
+            constexpr int E = OUT == kF32 ? 4 : 2;
+            unsigned char* to = O.p + (int64_t)row * O.rs + h * O.hs + 16 * c * E;
+            store8<OUT>(to, x[0]);
+            store8<OUT>(to + 8 * E, x[1]);
+        }
+    }
+}
+template <int HD, int CD>
+static auto read_kernel(int out) {
+    return out == kBF16  ? paged_read_kernel<HD, CD, kBF16>
+           : out == kF16 ? paged_read_kernel<HD, CD, kF16>
+                         : paged_read_kernel<HD, CD, kF32>;
+}
+template <int HD>
+static auto read_kernel(int cd, int out) {
+    return cd == kBF16   ? read_kernel<HD, kBF16>(out)
+           : cd == kF16  ? read_kernel<HD, kF16>(out)
+           : cd == kE4M3 ? read_kernel<HD, kE4M3>(out)
+                         : read_kernel<HD, kE2M1>(out);
+}
+int paged_read(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& ko, const HeadRows& vo,
+               int num_sms, cudaStream_t st) {
+    const int out = ko.p != nullptr ? ko.dtype : vo.dtype;
+    auto kern = hd == 64 ? read_kernel<64>(cache_dtype, out) : read_kernel<128>(cache_dtype, out);
+    int wl = 0;
+    while (wl < 3 && ((int64_t)R.n_rows << (wl + 1)) <= (int64_t)num_sms * 20) ++wl;
+    const int64_t warps = (int64_t)R.n_rows << wl;
+    return (int)launch(kern, dim3((unsigned)((warps + kApWarps - 1) / kApWarps)), dim3(kApWarps * 32), 0, st, C, R, ko,
+                       vo, wl);
 }
 
 template <int HD, int IN, int QO>
 static auto append_kernel(int out) {
     return out == kBF16  ? paged_append_kernel<HD, IN, QO, kBF16>
            : out == kF16 ? paged_append_kernel<HD, IN, QO, kF16>
-                         : paged_append_kernel<HD, IN, QO, kE4M3>;
+           : out == kE4M3 ? paged_append_kernel<HD, IN, QO, kE4M3>
+                         : paged_append_kernel<HD, IN, QO, kE2M1>;
 }
 template <int HD, int IN>
 static auto append_kernel(int qo, int out) {
@@ -259,7 +408,7 @@ static auto append_kernel(int in, int qo, int out) {
 
 int paged_append(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& k, const HeadRows& v,
                  const HeadRows& q, const HeadRows& qo, const float* q_norm, const float* k_norm, float eps,
-                 const Rotation& rot, int num_sms, cudaStream_t st) {
+                 const Rotation& rot, const int32_t* evicted, int num_sms, cudaStream_t st) {
     const int qd = q.heads > 0 ? qo.dtype : k.dtype;
     auto kern = hd == 64 ? append_kernel<64>(k.dtype, qd, cache_dtype) : append_kernel<128>(k.dtype, qd, cache_dtype);
     // more warps a row while that leaves the SMs under a third of their warps (512 rows: one warp a row 12.7 us, four
@@ -268,7 +417,7 @@ int paged_append(const PagedCache& C, int cache_dtype, int hd, const PagedRows& 
     while (wl < 3 && ((int64_t)R.n_rows << (wl + 1)) <= (int64_t)num_sms * 20) ++wl;
     const int64_t warps = (int64_t)R.n_rows << wl;
     return (int)launch(kern, dim3((unsigned)((warps + kApWarps - 1) / kApWarps)), dim3(kApWarps * 32), 0, st, C,
-                       R, k, v, q, qo, q_norm, k_norm, eps, rot, wl);
+                       R, k, v, q, qo, q_norm, k_norm, eps, rot, evicted, wl);
 }
 
 }  // namespace dflash

@@ -733,14 +733,15 @@ __global__ void __launch_bounds__(kPaThreads) paged_join_kernel(const __grid_con
 // sequences of 8 rows x 4 heads, and 12.6 against 14.7 us on one sequence of
 // 2048 keys; with 16 rows, 32 sequences, the warp MMAs take 58 us, tcgen05 64.
 // 64 rows in a tile of 128: 41.0 for 40.1 us, one block over 32768 keys.)
-static int pa_tile_rows(int n_seqs, int64_t n_rows, int group) {
+static int pa_tile_rows(int cache_dtype, int n_seqs, int64_t n_rows, int group) {
     const int64_t per = n_seqs > 0 ? (n_rows + n_seqs - 1) / n_seqs : 0;
     const int64_t m = per * group;
-    return m <= kPaM ? kPaM : m <= 64 ? 64 : 128;
+    return m <= kPaM && cache_dtype != kE2M1 ? kPaM : m <= 64 ? 64 : 128;
 }
 
-int64_t paged_attention_workspace(int hd, int n_seqs, int64_t n_rows, int heads, int kv_heads, int num_sms) {
-    const int64_t mt = pa_tile_rows(n_seqs, n_rows, heads / kv_heads);
+int64_t paged_attention_workspace(int cache_dtype, int hd, int n_seqs, int64_t n_rows, int heads, int kv_heads,
+                                  int num_sms) {
+    const int64_t mt = pa_tile_rows(cache_dtype, n_seqs, n_rows, heads / kv_heads);
     return num_sms * (2 * mt * (hd * 4 + 8) + (int64_t)sizeof(PaJoin) + (int64_t)sizeof(int32_t));
 }
 
@@ -768,7 +769,7 @@ int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRow
     A.C = C, A.R = R, A.q = q, A.out = out, A.lse = lse, A.window = window;
     A.scale_log2 = scale * 1.4426950408889634f;
     A.group = q.heads / C.kv_heads;
-    const int mt = pa_tile_rows(R.n_seqs, R.n_rows, A.group);
+    const int mt = pa_tile_rows(cache_dtype, R.n_seqs, R.n_rows, A.group);
     A.ws_o = static_cast<float*>(ws);
     A.ws_ml = reinterpret_cast<float2*>(A.ws_o + 2 * (int64_t)num_sms * mt * hd);
     A.ws_join = reinterpret_cast<PaJoin*>(A.ws_ml + 2 * (int64_t)num_sms * mt);
@@ -778,7 +779,7 @@ int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRow
                              : pa_type<128>(A, cache_dtype, num_sms, st);
     if (e != 0) return e;
     const dim3 grid(num_sms, mt / 16);
-    const int e8 = cache_dtype == kE4M3;
+    const int e8 = cache_dtype == kE4M3 || cache_dtype == kE2M1;
     return hd == 64 ? (int)launch(paged_join_kernel<64>, grid, dim3(kPaThreads), 0, st, A, mt, e8)
                     : (int)launch(paged_join_kernel<128>, grid, dim3(kPaThreads), 0, st, A, mt, e8);
 }

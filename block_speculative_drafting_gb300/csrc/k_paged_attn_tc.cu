@@ -61,9 +61,11 @@ constexpr int kPtQk = kPtSoft / 32, kPtPv = kPtQk + 1, kPtLoad = kPtPv + 1;  // 
 constexpr uint64_t kPtWait = 1000000000ull;
 constexpr int kPtBits = 16;  // tiles whose key masks are kept: more than the loaders can be ahead of the softmax
 
-// BF: queries and outputs in bf16 (else f16), and a 16-bit cache with them; E8: an e4m3 cache
-template <bool BF, bool E8, int HD>
+// BF: queries and outputs in bf16 (else f16), and a 16-bit cache with them; CB: bits of a cache's element, 16, 8
+// (e4m3) or 4 (e2m1)
+template <bool BF, int CB, int HD>
 struct PtShape {
+    static constexpr bool E8 = CB < 16;
     static constexpr int kLoadWarps = 4;  // of the keys, and as many of the values
     static constexpr int kLoaders = kLoadWarps * 32;
     static constexpr int kQueryWarps = E8 ? 4 : 0;
@@ -71,9 +73,12 @@ struct PtShape {
     static constexpr int KPW = kPaTile / kLoadWarps;  // keys of a loader warp: one a lane
     static constexpr int kItem = kPaTile * HD * 2;    // a slot: a tile's keys or values in 16 bits
     static constexpr int kSlots = (E8 ? 2 : 3) * (128 / HD);  // of the keys, and as many of the values
-    // e4m3: half tiles of codes on their way, 16 bytes a place, each place copied and read by one thread
-    static constexpr int kRaw = E8 ? 4 * (128 / HD) : 0, kRawLd = KPW * HD / 16 / 64;
-    static constexpr int kRawBytes = kRaw * kRawLd * 16 * 2 * kLoaders;
+    // codes: half tiles on their way, 16 bytes a place, each place copied and read by one thread; beside a place of e2m1
+    // codes the four bytes of the row's block scales that hold its two
+    static constexpr int kRawCh = HD * CB / 128;  // places of a row
+    static constexpr int kRaw = E8 ? 4 * (128 / HD) * 8 / CB : 0, kRawLd = KPW * kRawCh / 64;
+    static constexpr int kRawCodes = kRaw * kRawLd * 16 * 2 * kLoaders;
+    static constexpr int kRawBytes = kRawCodes + (CB == 4 ? kRawCodes / 4 : 0);
     static constexpr bool kSplitP = !E8 || !BF;
     static constexpr int kCtl = 15 * 1024;
     static constexpr size_t kSmem = 1024 /*alignment*/ + kCtl + 2 * (size_t)kSlots * kItem + kRawBytes;
@@ -151,8 +156,9 @@ DF_DEV void pt_skip(const PaArgs& A, PaCur& c, int n) {
 // A unit's queries to tensor memory at `to` (row t % MT of the unit), after `free` has waited for it.  An 8-bit cache's
 // warps of queries: a bf16 row is brought into f16 by a power of two, left in ctl.rf, its halves read for their largest
 // element and then again (registers).
-template <bool BF, bool E8, int HD, int MT, class F>
+template <bool BF, int CB, int HD, int MT, class F>
 DF_DEV bool pt_queries(const PaArgs& A, PtCtl& ctl, const PaCur& c, int unit, int t, uint32_t to, F free) {
+    constexpr bool E8 = CB < 16;
     constexpr int kHalves = E8 ? 2 : 1, NX = HD / 8 / kHalves;
     const int h = c.u % A.C.kv_heads, mm = (c.u / A.C.kv_heads) * MT + t % MT;
     const bool in = mm < c.q.rows * A.group;
@@ -212,10 +218,11 @@ DF_DEV bool pt_queries(const PaArgs& A, PtCtl& ctl, const PaCur& c, int unit, in
 }
 
 // MT: rows of a unit's tile, 64 (each query on two lanes) or 128
-template <bool BF, bool E8, int HD, int MT>
-__global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
+template <bool BF, int CB, int HD, int MT>
+__global__ void __launch_bounds__((PtShape<BF, CB, HD>::kThreads), 1)
     paged_attn_tc_kernel(const __grid_constant__ PaArgs A) {
-    using S = PtShape<BF, E8, HD>;
+    using S = PtShape<BF, CB, HD>;
+    constexpr bool E8 = S::E8;
     constexpr bool PB = BF && !E8;  // the MMAs' type: bf16, or f16
     extern __shared__ __align__(1024) unsigned char sm_raw[];
     unsigned char* sm = sm_raw + ((1024 - (smem_addr(sm_raw) & 1023)) & 1023);
@@ -269,7 +276,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
             auto free = [&]() {
                 return unit == 0 || __all_sync(0xffffffffu, mbar_wait(&ctl.q_free, (unit - 1) & 1, kPtWait));
             };
-            if (!pt_queries<BF, E8, HD, MT>(A, ctl, c, unit, t, tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kColQ, free))
+            if (!pt_queries<BF, CB, HD, MT>(A, ctl, c, unit, t, tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kColQ, free))
                 break;
             pt_skip<MT>(A, c, pt_tiles(c));
         }
@@ -298,27 +305,31 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
             return tile < S::kSlots ||
                    __all_sync(0xffffffffu, mbar_wait(&ctl.empty[side][tile % S::kSlots], ((tile / S::kSlots) - 1) & 1, kPtWait));
         };
-        // the tiles in order: emit(row) is called with a lane's key's row (null: not held)
+        // the tiles in order: emit(row, blocks) is called with a lane's key's row and its block scales (null: not held)
         auto walk = [&](auto emit) {
             PaCur c = cur;
             Look ahead{-1, 0, 0};
             if (c.left > 0) ahead = look(c);
             while (c.left > 0) {
-                const unsigned char* row = page_held(ahead.id, A.C.n_pages)
-                                               ? tensor + ahead.id * sp + ahead.slot * ss + ahead.h * sh
-                                               : nullptr;
+                const unsigned char *row = nullptr, *blocks = nullptr;
+                if (page_held(ahead.id, A.C.n_pages)) {
+                    row = tensor + ahead.id * sp + ahead.slot * ss + ahead.h * sh;
+                    if constexpr (CB == 4)
+                        blocks = (side ? A.C.vb : A.C.kb) + ahead.id * (side ? A.C.vbs[0] : A.C.kbs[0]) +
+                                 ahead.slot * (side ? A.C.vbs[1] : A.C.kbs[1]) + ahead.h * (side ? A.C.vbs[2] : A.C.kbs[2]);
+                }
                 if (side == 0) {
                     const uint32_t b = __ballot_sync(0xffffffffu, row != nullptr);
                     if (lane == 0) ctl.bits[n % kPtBits][lw] = b;
                 }
                 pa_next(A, MT, c);
                 if (c.left > 0) ahead = look(c);
-                if (!emit(row)) return;
+                if (!emit(row, blocks)) return;
             }
         };
         if constexpr (!E8) {
             constexpr int CH = HD / 8, RPI = 32 / CH;  // 16-byte chunks of a row, rows a copy instruction covers
-            walk([&](const unsigned char* rows) -> bool {
+            walk([&](const unsigned char* rows, const unsigned char*) -> bool {
                 if (!wait_empty(n)) return false;
                 const uint32_t dst = smem_addr(slots) + (n % S::kSlots) * S::kItem;
 #pragma unroll
@@ -338,11 +349,13 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
             });
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
-            constexpr int CH = HD / 16, RPI = 32 / CH, LD = S::kRawLd;  // copies of a lane a half tile
+            constexpr int CH = S::kRawCh, RPI = 32 / CH, LD = S::kRawLd;  // copies of a lane a half tile
             const int ch = lane % CH;
-            unsigned char* raw = ring + 2 * S::kSlots * S::kItem + (threadIdx.x - kPtLoad * 32) * 16;
+            const int self = threadIdx.x - kPtLoad * 32;
+            unsigned char* raw = ring + 2 * S::kSlots * S::kItem + self * 16;
+            unsigned char* raw_scale = ring + 2 * S::kSlots * S::kItem + S::kRawCodes + self * 4;
             constexpr int kPlace = 2 * S::kLoaders * 16;  // from one of a thread's places to the next
-            // a half tile's codes as f16, 32 bytes a place
+            // a half tile's codes as f16, 32 bytes a place (64 of e2m1 codes)
             auto write = [&](int half) -> bool {
                 const int tile = half >> 1, slot = tile % S::kSlots;
                 if ((half & 1) == 0 && !wait_empty(tile)) return false;
@@ -352,22 +365,43 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                     const int key = lw * S::KPW + ((half & 1) * LD + i) * RPI + lane / CH;
                     const uint4 x = *reinterpret_cast<const uint4*>(raw + ((half % S::kRaw) * LD + i) * kPlace);
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t y[8];
+                    if constexpr (CB == 4) {
+                        // a word: eight columns of one block, times the block's scale (exact: 2 bits times 4)
+                        const uint32_t sc = *reinterpret_cast<const uint32_t*>(
+                                                raw_scale + ((half % S::kRaw) * LD + i) * (kPlace / 4)) >>
+                                            ((2 * ch & 3) * 8);
+                        const uint32_t s2 = e4m3x2_f16x2(sc);
+                        // (places of the upper half write their chunks in another order: other banks)
+                        const int flip = ch >= CH / 2 ? 2 : 0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) e4m3x4_f16x4(w[j], y[2 * j], y[2 * j + 1]);
-                    // (lanes of the upper blocks write their halves in the other order: other banks)
-                    const bool flip = ch >= CH / 2;
+                        for (int j = 0; j < 4; ++j) {
+                            const int up = j ^ flip, chunk = 4 * ch + up;
+                            const uint32_t word = flip ? w[j ^ 2] : w[j];
+                            const uint32_t s1 = __byte_perm(s2, 0, (up >> 1) ? 0x3232 : 0x1010);
+                            uint32_t y[4];
+                            e2m1x8_f16x8(word, y);
+                            *reinterpret_cast<uint4*>(dst + (chunk >> 3) * (kPaTile * 128) + at_swz(key, chunk & 7)) =
+                                make_uint4(mul_f16x2(y[0], s1), mul_f16x2(y[1], s1), mul_f16x2(y[2], s1),
+                                           mul_f16x2(y[3], s1));
+                        }
+                    } else {
+                        uint32_t y[8];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int up = flip ? 1 - j : j, chunk = 2 * ch + up;
-                        const uint4 v = up ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
-                        *reinterpret_cast<uint4*>(dst + (chunk >> 3) * (kPaTile * 128) + at_swz(key, chunk & 7)) = v;
+                        for (int j = 0; j < 4; ++j) e4m3x4_f16x4(w[j], y[2 * j], y[2 * j + 1]);
+                        // (lanes of the upper blocks write their halves in the other order: other banks)
+                        const bool flip = ch >= CH / 2;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int up = flip ? 1 - j : j, chunk = 2 * ch + up;
+                            const uint4 v = up ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4*>(dst + (chunk >> 3) * (kPaTile * 128) + at_swz(key, chunk & 7)) = v;
+                        }
                     }
                 }
                 if (half & 1) mbar_arrive(&ctl.full[side][slot]);
                 return true;
             };
-            walk([&](const unsigned char* rows) -> bool {
+            walk([&](const unsigned char* rows, const unsigned char* blocks) -> bool {
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     const int half = 2 * n + hf;
@@ -377,6 +411,11 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
                         const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(rows), r);
                         const void* src = p ? reinterpret_cast<const unsigned char*>(p) + 16 * ch : A.q.p;  // (nothing is read)
                         cp16(smem_addr(raw) + ((half % S::kRaw) * LD + i) * kPlace, src, p ? 16 : 0);
+                        if constexpr (CB == 4) {
+                            const uint64_t b = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(blocks), r);
+                            const void* bs = b ? reinterpret_cast<const unsigned char*>(b) + (2 * ch & ~3) : A.q.p;
+                            cp4(smem_addr(raw_scale) + ((half % S::kRaw) * LD + i) * (kPlace / 4), bs, b ? 4 : 0);
+                        }
                     }
                     cp_commit();
                     cp_wait<S::kRaw - 1>();
@@ -466,7 +505,7 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
         PaCur c = cur;
         auto queries = [&]() {  // (where no warps of their own bring them)
             if (S::kQueryWarps == 0 && c.left > 0)
-                pt_queries<BF, E8, HD, MT>(A, ctl, c, unit, t, lane_addr + S::kColQ, []() { return true; });
+                pt_queries<BF, CB, HD, MT>(A, ctl, c, unit, t, lane_addr + S::kColQ, []() { return true; });
         };
         queries();
         while (c.left > 0) {
@@ -757,11 +796,11 @@ __global__ void __launch_bounds__((PtShape<BF, E8, HD>::kThreads), 1)
     }
 }
 
-template <bool BF, bool E8, int HD, int MT>
+template <bool BF, int CB, int HD, int MT>
 static int pt_launch(const PaArgs& A, int num_sms, cudaStream_t st) {
-    using S = PtShape<BF, E8, HD>;
+    using S = PtShape<BF, CB, HD>;
     static size_t limit[kMaxDevices] = {};
-    auto kern = paged_attn_tc_kernel<BF, E8, HD, MT>;
+    auto kern = paged_attn_tc_kernel<BF, CB, HD, MT>;
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return (int)e;
     if (cudaError_t e = raise_smem_limit(kern, S::kSmem, &limit[dev])) return (int)e;
@@ -769,10 +808,12 @@ static int pt_launch(const PaArgs& A, int num_sms, cudaStream_t st) {
 }
 template <int HD, int MT>
 static int pt_type(const PaArgs& A, int cache_dtype, int num_sms, cudaStream_t st) {
-    return cache_dtype == kBF16  ? pt_launch<true, false, HD, MT>(A, num_sms, st)
-           : cache_dtype == kF16 ? pt_launch<false, false, HD, MT>(A, num_sms, st)
-           : A.q.dtype == kBF16 ? pt_launch<true, true, HD, MT>(A, num_sms, st)
-                                 : pt_launch<false, true, HD, MT>(A, num_sms, st);
+    if (cache_dtype == kE2M1)
+        return A.q.dtype == kBF16 ? pt_launch<true, 4, HD, MT>(A, num_sms, st) : pt_launch<false, 4, HD, MT>(A, num_sms, st);
+    return cache_dtype == kBF16  ? pt_launch<true, 16, HD, MT>(A, num_sms, st)
+           : cache_dtype == kF16 ? pt_launch<false, 16, HD, MT>(A, num_sms, st)
+           : A.q.dtype == kBF16 ? pt_launch<true, 8, HD, MT>(A, num_sms, st)
+                                 : pt_launch<false, 8, HD, MT>(A, num_sms, st);
 }
 
 int paged_attention_tc(const PaArgs& A, int cache_dtype, int hd, int mt, int num_sms, cudaStream_t st) {

@@ -30,7 +30,8 @@ int launched(int e, const char* what) {
 }
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
-int64_t size_of(int dtype) { return dtype == DFLASH_F32 ? 4 : dtype == DFLASH_E4M3 ? 1 : 2; }
+// (of a 4-bit cache: of the two codes that its strides count)
+int64_t size_of(int dtype) { return dtype == DFLASH_F32 ? 4 : dtype == DFLASH_E4M3 || dtype == DFLASH_E2M1 ? 1 : 2; }
 
 // The current device's SM count (asked of the driver once a device).
 int sms(int* out) {
@@ -52,8 +53,8 @@ int sms(int* out) {
 
 int check_cache(const dflash_paged_cache* c, PagedCache* out) {
     if (c == nullptr) return fail(DFLASH_EINVAL, "cache is NULL");
-    if (c->dtype != DFLASH_BF16 && c->dtype != DFLASH_F16 && c->dtype != DFLASH_E4M3)
-        return fail(DFLASH_EINVAL, "cache dtype %d is not BF16, F16 or E4M3", c->dtype);
+    if (c->dtype != DFLASH_BF16 && c->dtype != DFLASH_F16 && c->dtype != DFLASH_E4M3 && c->dtype != DFLASH_E2M1)
+        return fail(DFLASH_EINVAL, "cache dtype %d is not BF16, F16, E4M3 or E2M1", c->dtype);
     if (c->head_dim != 64 && c->head_dim != 128)
         return fail(DFLASH_EGEOM, "head_dim %d is not 64 or 128", c->head_dim);
     if (c->kv_heads < 1 || c->kv_heads > 65536) return fail(DFLASH_EINVAL, "kv_heads %d", c->kv_heads);
@@ -63,7 +64,8 @@ int check_cache(const dflash_paged_cache* c, PagedCache* out) {
     if (!al16(c->k) || !al16(c->v)) return fail(DFLASH_EINVAL, "cache k and v need 16-byte alignment");
     if ((c->k_scale == nullptr) != (c->v_scale == nullptr))
         return fail(DFLASH_EINVAL, "k_scale and v_scale come together");
-    if (c->k_scale != nullptr && c->dtype != DFLASH_E4M3) return fail(DFLASH_EINVAL, "scales need an E4M3 cache");
+    if (c->k_scale != nullptr && c->dtype != DFLASH_E4M3 && c->dtype != DFLASH_E2M1)
+        return fail(DFLASH_EINVAL, "scales need an E4M3 cache or an E2M1 one");
     if (!al4(c->k_scale) || !al4(c->v_scale)) return fail(DFLASH_EINVAL, "scales need 4-byte alignment");
     const int64_t e = size_of(c->dtype);
     *out = PagedCache{};
@@ -79,6 +81,23 @@ int check_cache(const dflash_paged_cache* c, PagedCache* out) {
     out->v_scale = c->v_scale;
     out->n_pages = c->n_pages;
     out->kv_heads = c->kv_heads;
+    if (c->dtype == DFLASH_E2M1) {
+        const int64_t row = c->head_dim / 16;
+        const auto apart = [row](const void* p) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)row == 0; };
+        if (c->n_pages > 0 && (c->k_block == nullptr || c->v_block == nullptr))
+            return fail(DFLASH_EINVAL, "an E2M1 cache needs k_block and v_block");
+        bool ok = apart(c->k_block) && apart(c->v_block);
+        for (int i = 0; i < 3; ++i) {
+            out->kbs[i] = c->k_block_strides[i];
+            out->vbs[i] = c->v_block_strides[i];
+            ok = ok && out->kbs[i] >= 0 && out->vbs[i] >= 0 && out->kbs[i] % row == 0 && out->vbs[i] % row == 0;
+        }
+        if (!ok)
+            return fail(DFLASH_EINVAL, "block scales: base and strides must be multiples of %d bytes, strides not negative",
+                        (int)row);
+        out->kb = static_cast<unsigned char*>(c->k_block);
+        out->vb = static_cast<unsigned char*>(c->v_block);
+    }
     return DFLASH_OK;
 }
 
@@ -127,6 +146,16 @@ int check_heads(const dflash_head_rows* h, const char* name, int heads, int kv_h
     return DFLASH_OK;
 }
 
+int check_weights(const dflash_key_weights* w, const char* name, const PagedRows& R, KeyWeights* out) {
+    if (w == nullptr) return fail(DFLASH_EINVAL, "%s is NULL", name);
+    if ((w->data == nullptr && R.n_seqs > 0 && R.cap > 0) || !al4(w->data)) return fail(DFLASH_EINVAL, "%s data is NULL or not 4-byte aligned", name);
+    if (w->positions < R.cap)
+        return fail(DFLASH_EINVAL, "%s of %lld positions, the table names %d", name, (long long)w->positions, R.cap);
+    if (w->seq_stride < 0 || w->head_stride < 0) return fail(DFLASH_EINVAL, "%s: strides must not be negative", name);
+    *out = KeyWeights{w->data, w->seq_stride, w->head_stride};
+    return DFLASH_OK;
+}
+
 #define TRY(expr)                   \
     do {                            \
         const int e__ = (expr);     \
@@ -137,10 +166,10 @@ int check_heads(const dflash_head_rows* h, const char* name, int heads, int kv_h
 
 extern "C" {
 
-int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_rows* rows, const dflash_head_rows* k,
-                        const dflash_head_rows* v, const dflash_head_rows* q, const dflash_head_rows* q_out,
-                        const float* q_norm, const float* k_norm, float eps, const dflash_rotation* rotation,
-                        void* stream) {
+int dflash_paged_append_at(const dflash_paged_cache* cache, const dflash_paged_rows* rows, const dflash_head_rows* k,
+                           const dflash_head_rows* v, const dflash_head_rows* q, const dflash_head_rows* q_out,
+                           const float* q_norm, const float* k_norm, float eps, const dflash_rotation* rotation,
+                           const int32_t* evicted, void* stream) {
     PagedCache C;
     PagedRows R;
     HeadRows K, V, Q{}, QO{};
@@ -170,12 +199,110 @@ int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_rows
         if (!std::isfinite(rotation->scale)) return fail(DFLASH_EINVAL, "rotation scale %g", (double)rotation->scale);
         rot = Rotation{rotation->inv_freq, rotation->rotary, rotation->interleaved != 0, rotation->scale};
     }
+    if (!al4(evicted)) return fail(DFLASH_EINVAL, "evicted needs 4-byte alignment");
     if (R.n_rows == 0) return DFLASH_OK;
     int n = 0;
     TRY(sms(&n));
-    return launched(paged_append(C, cache->dtype, cache->head_dim, R, K, V, Q, QO, q_norm, k_norm, eps, rot, n,
+    return launched(paged_append(C, cache->dtype, cache->head_dim, R, K, V, Q, QO, q_norm, k_norm, eps, rot, evicted, n,
                                  static_cast<cudaStream_t>(stream)),
                     "dflash_paged_append");
+}
+
+int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_rows* rows, const dflash_head_rows* k,
+                        const dflash_head_rows* v, const dflash_head_rows* q, const dflash_head_rows* q_out,
+                        const float* q_norm, const float* k_norm, float eps, const dflash_rotation* rotation,
+                        void* stream) {
+    return dflash_paged_append_at(cache, rows, k, v, q, q_out, q_norm, k_norm, eps, rotation, nullptr, stream);
+}
+
+int dflash_paged_read(const dflash_paged_cache* cache, const dflash_paged_rows* rows, const dflash_head_rows* k_out,
+                      const dflash_head_rows* v_out, void* stream) {
+    PagedCache C;
+    PagedRows R;
+    HeadRows K{}, V{};
+    TRY(check_cache(cache, &C));
+    TRY(check_rows(rows, cache, &R));
+    if (k_out == nullptr && v_out == nullptr) return fail(DFLASH_EINVAL, "k_out and v_out are NULL");
+    if (k_out != nullptr) TRY(check_heads(k_out, "k_out", cache->kv_heads, 1, R.n_rows, &K));
+    if (v_out != nullptr) TRY(check_heads(v_out, "v_out", cache->kv_heads, 1, R.n_rows, &V));
+    if (k_out != nullptr && v_out != nullptr && k_out->dtype != v_out->dtype)
+        return fail(DFLASH_EINVAL, "k_out and v_out need one type");
+    if (R.n_rows == 0) return DFLASH_OK;
+    int n = 0;
+    TRY(sms(&n));
+    return launched(paged_read(C, cache->dtype, cache->head_dim, R, K, V, n, static_cast<cudaStream_t>(stream)),
+                    "dflash_paged_read");
+}
+
+int dflash_paged_key_weights(const dflash_paged_cache* cache, const dflash_paged_rows* rows, const dflash_head_rows* q,
+                             const float* lse, float scale, int32_t window, const dflash_key_weights* weights,
+                             void* stream) {
+    PagedCache C;
+    PagedRows R;
+    HeadRows Q;
+    KeyWeights W;
+    TRY(check_cache(cache, &C));
+    TRY(check_rows(rows, cache, &R));
+    TRY(check_heads(q, "q", 0, cache->kv_heads, R.n_rows, &Q));
+    if (q->dtype == DFLASH_F32 || (size_of(cache->dtype) == 2 && q->dtype != cache->dtype))
+        return fail(DFLASH_EINVAL, "q needs the cache's type (BF16 or F16 for an E4M3 or E2M1 cache)");
+    if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(DFLASH_EINVAL, "scale %g", (double)scale);
+    if (window < 0 || window > 1 << 30) return fail(DFLASH_EINVAL, "window %d", window);
+    if (!al4(lse) || (lse == nullptr && R.n_rows > 0)) return fail(DFLASH_EINVAL, "lse is NULL or not 4-byte aligned");
+    TRY(check_weights(weights, "weights", R, &W));
+    if (!pa_line_fits(R, q->heads, cache->kv_heads))
+        return fail(DFLASH_EINVAL, "%d sequences of %d positions: too many tiles of keys", R.n_seqs, R.cap);
+    if (R.n_rows == 0) return DFLASH_OK;
+    int n = 0;
+    TRY(sms(&n));
+    return launched(paged_key_weights(C, cache->dtype, cache->head_dim, R, Q, lse, scale, window, W, n,
+                                      static_cast<cudaStream_t>(stream)),
+                    "dflash_paged_key_weights");
+}
+
+int64_t dflash_paged_evict_workspace(int32_t n_seqs, int32_t kv_heads, int32_t keep, int32_t own_kept) {
+    if (n_seqs < 0 || n_seqs >= 1 << 24 || kv_heads < 1 || kv_heads > 65536 || keep < 1 ||
+        (int64_t)n_seqs * kv_heads > INT32_MAX / 16)
+        return fail(DFLASH_EINVAL, "n_seqs %d, kv_heads %d, keep %d", n_seqs, kv_heads, keep);
+    return paged_evict_workspace(n_seqs, kv_heads, keep, own_kept != 0);
+}
+
+int dflash_paged_evict(const dflash_paged_cache* cache, const dflash_paged_rows* seqs, int32_t keep, int32_t first,
+                       int32_t recent, const dflash_key_weights* weights, const dflash_key_weights* out,
+                       int32_t* new_len, int32_t* kept, int32_t* evicted, void* workspace, int64_t workspace_bytes,
+                       void* stream) {
+    EvictArgs A{};
+    TRY(check_cache(cache, &A.C));
+    TRY(check_rows(seqs, cache, &A.R));
+    if (A.R.n_rows != 0 || A.R.row_start != nullptr) return fail(DFLASH_EINVAL, "an eviction has no rows");
+    if (keep < 1 || first < 0 || recent < 0 || (int64_t)first + recent > keep)
+        return fail(DFLASH_EINVAL, "keep %d, first %d, recent %d", keep, first, recent);
+    const int64_t need = dflash_paged_evict_workspace(A.R.n_seqs, cache->kv_heads, keep, kept == nullptr);
+    if (need < 0) return (int)need;
+    if (A.R.n_seqs == 0) return DFLASH_OK;
+    if (A.R.kv_len == nullptr || (A.R.max_pages > 0 && A.R.table == nullptr))
+        return fail(DFLASH_EINVAL, "kv_len or table is NULL");
+    TRY(check_weights(weights, "weights", A.R, &A.in));
+    TRY(check_weights(out, "out", A.R, &A.out));
+    if (A.in.p == A.out.p && (A.in.ss != A.out.ss || A.in.hs != A.out.hs))
+        return fail(DFLASH_EINVAL, "out in weights' place needs its strides");
+    if (new_len == nullptr || !al4(new_len) || !al4(kept) || !al4(evicted))
+        return fail(DFLASH_EINVAL, "new_len is NULL, or new_len, kept or evicted not 4-byte aligned");
+    if (workspace == nullptr || !al16(workspace))
+        return fail(DFLASH_EINVAL, "workspace is NULL or not 16-byte aligned");
+    if (workspace_bytes < need)
+        return fail(DFLASH_ECAPACITY, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes,
+                    (long long)need);
+    int n = 0;
+    TRY(sms(&n));
+    A.keep = keep, A.first = first, A.recent = recent;
+    A.new_len = new_len, A.evicted = evicted;
+    A.lens = static_cast<int2*>(workspace);
+    A.kept = kept != nullptr ? kept
+                             : reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) +
+                                                          paged_evict_workspace(A.R.n_seqs, cache->kv_heads, keep, false));
+    return launched(paged_evict(A, cache->dtype, cache->head_dim, n, static_cast<cudaStream_t>(stream)),
+                    "dflash_paged_evict");
 }
 
 int64_t dflash_paged_attention_workspace(const dflash_paged_cache* cache, int32_t n_seqs, int64_t n_rows,
@@ -186,7 +313,7 @@ int64_t dflash_paged_attention_workspace(const dflash_paged_cache* cache, int32_
         return fail(DFLASH_EINVAL, "n_seqs %d, n_rows %lld, heads %d", n_seqs, (long long)n_rows, heads);
     int n = 0;
     TRY(sms(&n));
-    return paged_attention_workspace(cache->head_dim, n_seqs, n_rows, heads, cache->kv_heads, n);
+    return paged_attention_workspace(cache->dtype, cache->head_dim, n_seqs, n_rows, heads, cache->kv_heads, n);
 }
 
 int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_rows* rows, const dflash_head_rows* q,
@@ -199,8 +326,8 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_r
     TRY(check_rows(rows, cache, &R));
     TRY(check_heads(q, "q", 0, cache->kv_heads, R.n_rows, &Q));
     TRY(check_heads(out, "out", q->heads, 1, R.n_rows, &O));
-    if (q->dtype == DFLASH_F32 || out->dtype != q->dtype || (cache->dtype != DFLASH_E4M3 && q->dtype != cache->dtype))
-        return fail(DFLASH_EINVAL, "q and out need the cache's type (BF16 or F16 for an E4M3 cache)");
+    if (q->dtype == DFLASH_F32 || out->dtype != q->dtype || (size_of(cache->dtype) == 2 && q->dtype != cache->dtype))
+        return fail(DFLASH_EINVAL, "q and out need the cache's type (BF16 or F16 for an E4M3 or E2M1 cache)");
     if (q->data == out->data && R.n_rows > 0 && (q->row_stride != out->row_stride || q->head_stride != out->head_stride))
         return fail(DFLASH_EINVAL, "out in q's place needs q's strides");
     if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(DFLASH_EINVAL, "scale %g", (double)scale);
@@ -212,7 +339,7 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_r
     int n = 0;
     TRY(sms(&n));
     const int64_t need =
-        paged_attention_workspace(cache->head_dim, R.n_seqs, R.n_rows, q->heads, cache->kv_heads, n);
+        paged_attention_workspace(cache->dtype, cache->head_dim, R.n_seqs, R.n_rows, q->heads, cache->kv_heads, n);
     if (workspace == nullptr || !al16(workspace))
         return fail(DFLASH_EINVAL, "workspace is NULL or not 16-byte aligned");
     if (workspace_bytes < need)

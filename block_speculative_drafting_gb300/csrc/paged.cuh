@@ -11,8 +11,8 @@
 
 namespace dflash {
 
-// element types: the values of DFLASH_F32 .. DFLASH_E4M3
-constexpr int kF32 = 0, kBF16 = 1, kF16 = 2, kE4M3 = 3;
+// element types: the values of DFLASH_F32 .. DFLASH_E2M1
+constexpr int kF32 = 0, kBF16 = 1, kF16 = 2, kE4M3 = 3, kE2M1 = 4;
 
 constexpr int kMaxDevices = 64;
 
@@ -43,6 +43,9 @@ struct PagedCache {
     const float *k_scale, *v_scale;
     int64_t n_pages;
     int kv_heads;
+    // 4-bit caches: a row's block scales, one e4m3 byte for 16 columns
+    unsigned char *kb, *vb;
+    int64_t kbs[3], vbs[3];  // page, slot, head strides in bytes
 };
 struct PagedRows {
     int n_seqs, max_pages, per;  // per: rows of every sequence where row_start is null
@@ -120,9 +123,30 @@ struct Rotation {
 };
 int paged_append(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& k, const HeadRows& v,
                  const HeadRows& q, const HeadRows& qo, const float* q_norm, const float* k_norm, float eps,
-                 const Rotation& rot, int num_sms, cudaStream_t st);
+                 const Rotation& rot, const int32_t* evicted, int num_sms, cudaStream_t st);
+int paged_read(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& ko, const HeadRows& vo,
+               int num_sms, cudaStream_t st);
+// weights: [sequence][key/value head][position] f32, the strides of the first two in elements
+struct KeyWeights {
+    float* p;
+    int64_t ss, hs;
+};
+int paged_key_weights(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& q,
+                      const float* lse, float scale, int window, const KeyWeights& W, int num_sms, cudaStream_t st);
+struct EvictArgs {
+    PagedCache C;
+    PagedRows R;
+    KeyWeights in, out;
+    int keep, first, recent;
+    int32_t *new_len, *evicted;
+    int32_t* kept;   // [sequence][head][keep]: the slots that stay, -1 from the new length on
+    int2* lens;      // [sequence]: the length before and after
+};
+int64_t paged_evict_workspace(int n_seqs, int kv_heads, int keep, bool own_kept);
+int paged_evict(const EvictArgs& A, int cache_dtype, int hd, int num_sms, cudaStream_t st);
 
-int64_t paged_attention_workspace(int hd, int n_seqs, int64_t n_rows, int heads, int kv_heads, int num_sms);
+int64_t paged_attention_workspace(int cache_dtype, int hd, int n_seqs, int64_t n_rows, int heads, int kv_heads,
+                                  int num_sms);
 int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& q,
                     const HeadRows& out, float* lse, float scale, int window, void* ws, int num_sms, cudaStream_t st);
 

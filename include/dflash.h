@@ -482,6 +482,13 @@ DFLASH_API int dflash_attention_noalloc(dflash_model* model, dflash_seq* const* 
  *   dflash_paged_attention  its rows' attention over that cache
  *   dflash_verify           which drafts stay, and the token after them
  *
+ * and of keeping that cache small:
+ *
+ *   (a cache in 4 bits      DFLASH_E2M1, in all of the paged calls)
+ *   dflash_paged_read       rows of the cache as values
+ *   dflash_paged_key_weights  the attention weight that each key receives
+ *   dflash_paged_evict      a cache cut back to its heaviest tokens
+ *
  * (The pages leave the target to the engine around the drafter and have no
  * counterpart.)  They take no model: every buffer is the caller's device
  * memory, on the current device, and nothing is allocated or kept between
@@ -499,17 +506,27 @@ DFLASH_API int dflash_attention_noalloc(dflash_model* model, dflash_seq* const* 
 #define DFLASH_BF16 1
 #define DFLASH_F16 2
 #define DFLASH_E4M3 3 /* 8-bit float, 4 exponent bits, largest 448, no infinity */
+#define DFLASH_E2M1 4 /* 4-bit float: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives */
 
 /*
  * A paged key/value cache.  Slot t of page p of head h holds head_dim
  * contiguous elements at k + p * k_strides[0] + t * k_strides[1] + h *
  * k_strides[2] (elements; v likewise), so that [page][slot][head] and
  * [page][head][slot] are both served.
- * Rules (EINVAL / EGEOM): dtype DFLASH_BF16, DFLASH_F16 or DFLASH_E4M3;
- * head_dim 64 or 128; kv_heads >= 1; page_size 1 .. 65536; n_pages >= 0; bases
- * and strides multiples of 16 bytes, strides >= 0.
- * k_scale, v_scale (E4M3 only, both or neither; NULL: 1): one positive, normal
- * f32 a head on the device; an element is its code times the head's scale.
+ * Rules (EINVAL / EGEOM): dtype DFLASH_BF16, DFLASH_F16, DFLASH_E4M3 or
+ * DFLASH_E2M1; head_dim 64 or 128; kv_heads >= 1; page_size 1 .. 65536;
+ * n_pages >= 0; bases and strides multiples of 16 bytes, strides >= 0.
+ * k_scale, v_scale (E4M3 and E2M1, both or neither; NULL: 1): one positive,
+ * normal f32 a head on the device; an element is its code times the head's
+ * scale.
+ * E2M1: two codes a byte, the first of them in the lower four bits, so that a
+ * row is head_dim / 2 bytes, and the strides of k and v are in bytes.  16
+ * columns share a block scale, an e4m3 byte: column d of slot t of page p of
+ * head h has the byte k_block + p * k_block_strides[0] + t *
+ * k_block_strides[1] + h * k_block_strides[2] + d / 16, and an element is code
+ * * block scale * head's scale.  Bases and strides of the block scales are
+ * multiples of head_dim / 16 bytes, not negative.  (The fields from k_block on
+ * are read with dtype E2M1 alone.)
  */
 typedef struct {
     void* k;
@@ -523,6 +540,10 @@ typedef struct {
     int64_t v_strides[3];
     const float* k_scale; /* [kv_heads] */
     const float* v_scale; /* [kv_heads] */
+    void* k_block; /* E2M1: block scales */
+    void* v_block;
+    int64_t k_block_strides[3]; /* page, slot, head; in bytes */
+    int64_t v_block_strides[3];
 } dflash_paged_cache;
 
 /*
@@ -577,7 +598,11 @@ typedef struct {
 /*
  * Append the call's rows to the cache, rotated on the way: k' = rot_p(norm(k))
  * and v go to their slots in the cache's type (rounded to nearest; E4M3:
- * x / scale, clamped to +-448, NaN kept), q' = rot_p(norm(q)) to q_out.
+ * x / scale, clamped to +-448, NaN kept; E2M1: with t = x / the head's scale
+ * over a block of 16 columns, the block scale s is max |t| / 6 rounded to
+ * e4m3, clamped to 448, and a code t / s rounded to e2m1, ties to even, clamped to
+ * +-6; a NaN makes its block NaN, and a block whose s rounds to 0, all |t|
+ * below 6 * 2^-10, is 0), q' = rot_p(norm(q)) to q_out.
  * norm(x) = x / sqrt(mean(x^2) + eps) * gain over a head, with f32 gains
  * q_norm, k_norm [head_dim] on the device (NULL: no norm).  rotation NULL: no
  * rotation.  q NULL: keys and values alone.  q, k and v have one type; q_out
@@ -592,6 +617,27 @@ DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash
                                    const dflash_rotation* rotation, void* stream);
 
 /*
+ * dflash_paged_append for caches that dflash_paged_evict has shortened: the
+ * rows' slots are dflash_paged_append's, by kv_len, but a row of sequence s is
+ * rotated as the position of its slot + evicted[s] (int32 [n_seqs] on the
+ * device; NULL: 0).
+ */
+DFLASH_API int dflash_paged_append_at(const dflash_paged_cache* cache, const dflash_paged_rows* rows,
+                                      const dflash_head_rows* k, const dflash_head_rows* v, const dflash_head_rows* q,
+                                      const dflash_head_rows* q_out, const float* q_norm, const float* k_norm,
+                                      float eps, const dflash_rotation* rotation, const int32_t* evicted, void* stream);
+
+/*
+ * The keys and values that the cache holds for the call's rows, as values:
+ * code * block scale * head's scale (or the element itself), rounded to the
+ * output's type once.  k_out, v_out: kv_heads heads, one type; either may be
+ * NULL.  A row whose position is not held reads as zeros.
+ * Errors: EINVAL, EGEOM, ECUDA.
+ */
+DFLASH_API int dflash_paged_read(const dflash_paged_cache* cache, const dflash_paged_rows* rows,
+                                 const dflash_head_rows* k_out, const dflash_head_rows* v_out, void* stream);
+
+/*
  * Attention of the call's rows over the cache (which holds their own keys and
  * values already): row at position p, query head h, key/value head h /
  * (heads / kv_heads):
@@ -601,7 +647,7 @@ DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash
  * A row that sees nothing, or finite values at scores of -inf alone, gets out =
  * 0 and lse = -inf.  What positions outside a row's view hold (infinities, NaN,
  * freed pages) does not reach it.  q and out have one type: the cache's, or BF16
- * / F16 for an E4M3 cache; out may be q itself, or has to be apart from it.
+ * / F16 for an E4M3 or E2M1 cache; out may be q itself, or has to be apart from it.
  * workspace: at least dflash_paged_attention_workspace bytes of device
  * memory, 16-byte aligned, needing no initial contents; calls that may
  * overlap need one each.
@@ -617,6 +663,67 @@ DFLASH_API int dflash_paged_attention(const dflash_paged_cache* cache, const dfl
  * `n_seqs` sequences needs on the current device: >= 0, or an error. */
 DFLASH_API int64_t dflash_paged_attention_workspace(const dflash_paged_cache* cache, int32_t n_seqs, int64_t n_rows,
                                                     int32_t heads);
+
+/* A weight for each key that a cache holds: sequence s, key/value head h,
+ * position p at data + s * seq_stride + h * head_stride + p (f32 on the device;
+ * strides in elements, not negative), for positions 0 .. positions - 1, no fewer
+ * than the table names (max_pages * page_size). */
+typedef struct {
+    float* data;
+    int64_t positions;
+    int64_t seq_stride;
+    int64_t head_stride;
+} dflash_key_weights;
+
+/*
+ * The attention weight that each key receives from the call's rows, added to
+ * what earlier calls have left:
+ *   weights[s][h][j] += sum of exp(scale * q_i . k_j - lse_i) over the rows of
+ *   sequence s that see position j and the query heads i that share head h
+ * with rows, scale, window and lse those of the dflash_paged_attention call
+ * whose weights they are (lse f32 [n_rows][heads]; a row of lse -inf adds
+ * nothing).  The positions of the call's own rows start at 0, whatever weights
+ * held there; positions past the sequence's last token, those of sequences
+ * without rows and those that are not held are left as they were.  Sums run in
+ * 32 bits and in one order: equal calls give equal bits.  Only the cache's keys
+ * are read (v may be k).  weights of different sequences and heads are apart.
+ * Errors: EINVAL (also where sequences x heads x positions of the table come to
+ * more than 2^31 tiles of 128 keys), EGEOM, ECUDA.
+ */
+DFLASH_API int dflash_paged_key_weights(const dflash_paged_cache* cache, const dflash_paged_rows* rows,
+                                        const dflash_head_rows* q, const float* lse, float scale, int32_t window,
+                                        const dflash_key_weights* weights, void* stream);
+
+/*
+ * Cut caches back to `keep` tokens.  Of a sequence of L = kv_len[s] (at most
+ * max_pages * page_size) > keep tokens each key/value head keeps the `first`
+ * first ones, the `recent` last ones, and of those between them the keep -
+ * first - recent with the largest weights (equal ones: the lowest position; NaN
+ * counts as -inf).  They move, in order, to the positions 0 .. keep - 1 of the
+ * same pages, keys, values, block scales and weights alike; what stood behind
+ * them stays where it was.  Shorter sequences stay as they are.
+ *   seqs       n_seqs, max_pages, kv_len and table (n_rows 0, row_start NULL);
+ *              no two entries of the table that hold tokens name one page,
+ *              and k and v are apart
+ *   out        where the weights go: weights itself, or memory apart from it
+ *   new_len    int32 [n_seqs]: min(L, keep); may be kv_len itself
+ *   kept       int32 [n_seqs][kv_heads][keep] or NULL: the position that each
+ *              token of the new cache had (-1 from the new length on)
+ *   evicted    int32 [n_seqs] or NULL: grows by L - new_len, as
+ *              dflash_paged_append_at takes it
+ * A token moves from or to a position that is not held: its keys and values are
+ * not written.  keep >= 1, first and recent >= 0, first + recent <= keep.
+ * workspace: at least dflash_paged_evict_workspace bytes (own_kept: 1 where
+ * kept is NULL, else 0), as for the attention.
+ * Errors: EINVAL, EGEOM, ECAPACITY (workspace too small), ECUDA.
+ */
+DFLASH_API int dflash_paged_evict(const dflash_paged_cache* cache, const dflash_paged_rows* seqs, int32_t keep,
+                                  int32_t first, int32_t recent, const dflash_key_weights* weights,
+                                  const dflash_key_weights* out, int32_t* new_len, int32_t* kept, int32_t* evicted,
+                                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace a dflash_paged_evict call needs: >= 0, or an error. */
+DFLASH_API int64_t dflash_paged_evict_workspace(int32_t n_seqs, int32_t kv_heads, int32_t keep, int32_t own_kept);
 
 /*
  * Verify drafted tokens.  Sequence s has the drafts draft_start[s] ..

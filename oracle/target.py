@@ -1,5 +1,6 @@
 """The target's verification pass in plain float64: appending to a paged cache with the head norm and the rotation,
-attention of a pass's rows over that cache, and the verification of drafted tokens.
+attention of a pass's rows over that cache, and the verification of drafted tokens; and what keeps that cache small: the
+4-bit rounding, the weight that keys receive, and the choice of the tokens that stay.
 
 Everything goes row by row (or draft by draft) from the formulas, on numpy arrays; a row's attention takes only the
 keys in its view, so nothing outside it can reach the result.
@@ -68,6 +69,77 @@ def paged_append(k, v, q, table, kv_len, page_size, n_pages, row_start=None, inv
             if at is not None:
                 slots[at] = (kk, v[a + i])
     return slots, q_out, touched
+
+
+E2M1 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
+
+
+def round_e4m3(x):
+    """x >= 0 to the nearest e4m3 value (ties to even), at most 448; NaN stays."""
+    x = np.minimum(np.asarray(x, np.float64), 448.0)
+    _, e = np.frexp(np.where(x > 0, x, 1.0))
+    step = np.exp2(np.maximum(e - 1, -6) - 3.0)
+    return np.rint(x / step) * step
+
+
+def round_e2m1(x):
+    """x to the nearest e2m1 value (ties to the even code), clamped to +-6."""
+    x = np.asarray(x, np.float64)
+    d = np.abs(np.minimum(np.abs(x), 6.0)[..., None] - E2M1)
+    near = d == d.min(-1, keepdims=True)
+    even = near & (np.arange(8) % 2 == 0)
+    at = np.where(even.any(-1), np.argmax(even, -1), np.argmax(near, -1))
+    return np.where(np.isnan(x), np.nan, np.copysign(E2M1[at], x))
+
+
+def quantise_e2m1(t):
+    """t [..][16 b] in units of the head's scale -> (e2m1 values [..][16 b], block scales [..][b])."""
+    t = np.asarray(t, np.float64)
+    g = t.reshape(*t.shape[:-1], -1, 16)
+    s = round_e4m3(np.abs(g).max(-1) / 6)
+    with np.errstate(all="ignore"):
+        u = np.where(s[..., None] > 0, g / s[..., None], np.where(np.isnan(s[..., None]), np.nan, 0.0))
+    return round_e2m1(u).reshape(t.shape), s
+
+
+def paged_key_weights(weights, q, lse, k_cache, table, kv_len, row_start=None, scale=None, window=0):
+    """(weights after the call, the scores' magnitude each sum saw); k_cache [pages][page_size][kv_heads][hd]."""
+    q = np.asarray(q, np.float64)
+    n_pages, page_size, kvh, hd = k_cache.shape
+    g = q.shape[1] // kvh
+    scale = hd ** -0.5 if scale is None else scale
+    out, amp = np.array(weights, np.float64), np.zeros(weights.shape)
+    for s, a, n in rows_of(len(kv_len), len(q), row_start):
+        L = int(kv_len[s])
+        for j in range(min(L, len(table[s]) * page_size) if n else 0):
+            at = slot_of(table[s], page_size, n_pages, j)
+            if at is None:
+                continue
+            for h in range(kvh):
+                tot = 0.0
+                for i in range(n):
+                    p = L - n + i
+                    if j > p or (window and j <= p - window):
+                        continue
+                    for e in range(h * g, (h + 1) * g):
+                        if lse[a + i, e] == -np.inf:
+                            continue
+                        with np.errstate(all="ignore"):
+                            w = np.exp(scale * (q[a + i, e] @ k_cache[at[0], at[1], h]) - lse[a + i, e])
+                        tot += w
+                        amp[s, h, j] += w * scale * (np.abs(q[a + i, e]) @ np.abs(k_cache[at[0], at[1], h]))
+                out[s, h, j] = tot + (out[s, h, j] if j < L - n else 0.0)
+    return out, amp
+
+
+def kept_slots(w, length, keep, first, recent):
+    """The positions of one head's tokens that stay: the first, the recent, and the heaviest between (lowest first)."""
+    if length <= keep:
+        return list(range(length))
+    mid = range(first, length - recent)
+    weight = {j: -np.inf if np.isnan(w[j]) else float(w[j]) for j in mid}
+    best = sorted(mid, key=lambda j: (-weight[j], j))[:keep - first - recent]
+    return sorted(list(range(first)) + best + list(range(length - recent, length)))
 
 
 def paged_attention(q, k_cache, v_cache, table, kv_len, row_start=None, scale=None, window=0):
