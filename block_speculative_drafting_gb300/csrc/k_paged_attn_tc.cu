@@ -50,8 +50,7 @@
 // the softmax then walks its remaining units without waiting and leaves NaN in
 // their rows.
 #include "kernels.cuh"
-#include "paged_attn.cuh"
-#include "tc.cuh"
+#include "paged_tile.cuh"
 
 namespace dflash {
 
@@ -99,16 +98,6 @@ struct PtCtl {
     alignas(16) float xo[2][64][20];        // sixteen columns of the upper lanes' outputs on their way to the lower ones
 };
 
-DF_DEV void pt_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
 DF_DEV uint32_t pt_ld1(uint32_t taddr) {
     uint32_t r;
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
@@ -117,20 +106,12 @@ DF_DEV uint32_t pt_ld1(uint32_t taddr) {
 DF_DEV void pt_st16(uint32_t taddr, const uint32_t (&w)[16]) {
     at_st16(taddr, *reinterpret_cast<const float(*)[16]>(w));
 }
-// at_mma_ts, at_commit and mbar_arrive for the one lane with `on`, in code that the whole warp runs: the operands then
-// stay in uniform registers (issued under a divergent branch, each MMA took 60 ns to put together, twice its work)
+// at_mma_ts by the one lane with `on` (as pt_commit)
 DF_DEV void pt_mma(bool on, uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
         " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
         "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"((uint32_t)on)
-        : "memory");
-}
-DF_DEV void pt_commit(bool on, uint64_t* bar) {
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar)),
-        "r"((uint32_t)on)
         : "memory");
 }
 // named barrier 1: the softmax threads
@@ -364,39 +345,11 @@ __global__ void __launch_bounds__((PtShape<BF, CB, HD>::kThreads), 1)
                 for (int i = 0; i < LD; ++i) {
                     const int key = lw * S::KPW + ((half & 1) * LD + i) * RPI + lane / CH;
                     const uint4 x = *reinterpret_cast<const uint4*>(raw + ((half % S::kRaw) * LD + i) * kPlace);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    if constexpr (CB == 4) {
-                        // a word: eight columns of one block, times the block's scale (exact: 2 bits times 4)
-                        const uint32_t sc = *reinterpret_cast<const uint32_t*>(
-                                                raw_scale + ((half % S::kRaw) * LD + i) * (kPlace / 4)) >>
-                                            ((2 * ch & 3) * 8);
-                        const uint32_t s2 = e4m3x2_f16x2(sc);
-                        // (places of the upper half write their chunks in another order: other banks)
-                        const int flip = ch >= CH / 2 ? 2 : 0;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int up = j ^ flip, chunk = 4 * ch + up;
-                            const uint32_t word = flip ? w[j ^ 2] : w[j];
-                            const uint32_t s1 = __byte_perm(s2, 0, (up >> 1) ? 0x3232 : 0x1010);
-                            uint32_t y[4];
-                            e2m1x8_f16x8(word, y);
-                            *reinterpret_cast<uint4*>(dst + (chunk >> 3) * (kPaTile * 128) + at_swz(key, chunk & 7)) =
-                                make_uint4(mul_f16x2(y[0], s1), mul_f16x2(y[1], s1), mul_f16x2(y[2], s1),
-                                           mul_f16x2(y[3], s1));
-                        }
-                    } else {
-                        uint32_t y[8];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) e4m3x4_f16x4(w[j], y[2 * j], y[2 * j + 1]);
-                        // (lanes of the upper blocks write their halves in the other order: other banks)
-                        const bool flip = ch >= CH / 2;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int up = flip ? 1 - j : j, chunk = 2 * ch + up;
-                            const uint4 v = up ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
-                            *reinterpret_cast<uint4*>(dst + (chunk >> 3) * (kPaTile * 128) + at_swz(key, chunk & 7)) = v;
-                        }
-                    }
+                    uint32_t scales = 0;
+                    if constexpr (CB == 4)
+                        scales = *reinterpret_cast<const uint32_t*>(raw_scale + ((half % S::kRaw) * LD + i) * (kPlace / 4)) >>
+                                 ((2 * ch & 3) * 8);
+                    tile_place<CB, HD>(dst, key, ch, x, scales);
                 }
                 if (half & 1) mbar_arrive(&ctl.full[side][slot]);
                 return true;

@@ -68,17 +68,17 @@ struct PaCur {
     int left;  // places of the CTA's share from here on (0: none)
 };
 // The end of sequence s's rows, which start at a.
-DF_DEV int pa_rows_end(const PaArgs& A, int s, int a) {
-    return A.R.row_start == nullptr ? a + A.R.per : max(row_start_at(A.R, s + 1), a);
+DF_DEV int rows_end(const PagedRows& R, int s, int a) {
+    return R.row_start == nullptr ? a + R.per : max(row_start_at(R, s + 1), a);
 }
 // Rows [a, b) of sequence s0 + lane (warp-wide; none past the last sequence); `from`: where sequence s0's start.
-DF_DEV void pa_rows_of_lane(const PaArgs& A, int s0, int from, int lane, int& a, int& b) {
-    const int s = min(s0 + lane, A.R.n_seqs - 1);
-    if (A.R.row_start == nullptr) {
-        a = s * A.R.per;
-        b = a + A.R.per;
+DF_DEV void rows_of_lane(const PagedRows& R, int s0, int from, int lane, int& a, int& b) {
+    const int s = min(s0 + lane, R.n_seqs - 1);
+    if (R.row_start == nullptr) {
+        a = s * R.per;
+        b = a + R.per;
     } else {
-        b = max(row_start_at(A.R, s + 1), from);
+        b = max(row_start_at(R, s + 1), from);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, b, o);
@@ -95,7 +95,7 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
     const int first = A.R.row_start == nullptr ? 0 : row_start_at(A.R, 0);
     for (int s0 = 0, from = first; s0 < A.R.n_seqs; s0 += 32) {
         int a, b;
-        pa_rows_of_lane(A, s0, from, lane, a, b);
+        rows_of_lane(A.R, s0, from, lane, a, b);
         from = __shfl_sync(0xffffffffu, b, 31);
         if (s0 + lane >= A.R.n_seqs) continue;
         const PaSeq q = pa_seq(A, s0 + lane, a, b, mt);
@@ -122,7 +122,7 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
     int run = 0;
     for (int s0 = 0, from = first; s0 < A.R.n_seqs; s0 += 32) {
         int w = w0 + c.ov * u0, a, b;
-        pa_rows_of_lane(A, s0, from, lane, a, b);
+        rows_of_lane(A.R, s0, from, lane, a, b);
         from = __shfl_sync(0xffffffffu, b, 31);
         if (s0 > 0) {
             const PaSeq q = pa_seq(A, min(s0 + lane, A.R.n_seqs - 1), a, b, mt);
@@ -171,7 +171,7 @@ DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c) {
             return;
         }
         const int a = c.q.row0 + c.q.rows;
-        c.q = pa_seq(A, c.s, a, pa_rows_end(A, c.s, a), mt);
+        c.q = pa_seq(A, c.s, a, rows_end(A.R, c.s, a), mt);
     } while (c.q.nunits == 0);
 }
 // The entry of a unit that begins in this CTA's share and has `rest` tiles after it.
