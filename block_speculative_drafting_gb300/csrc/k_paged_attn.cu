@@ -732,11 +732,12 @@ __global__ void __launch_bounds__(kPaThreads) paged_join_kernel(const __grid_con
 // kernel of 32 rows took 71.7 us where the tcgen05 kernel's 64 take 67.4, 32
 // sequences of 8 rows x 4 heads, and 12.6 against 14.7 us on one sequence of
 // 2048 keys; with 16 rows, 32 sequences, the warp MMAs take 58 us, tcgen05 64.
-// 64 rows in a tile of 128: 41.0 for 40.1 us, one block over 32768 keys.)
+// 64 rows in a tile of 128: 41.0 for 40.1 us, one block over 32768 keys.  A 4-bit
+// cache's warps take 8 or 16.)
 static int pa_tile_rows(int cache_dtype, int n_seqs, int64_t n_rows, int group) {
     const int64_t per = n_seqs > 0 ? (n_rows + n_seqs - 1) / n_seqs : 0;
     const int64_t m = per * group;
-    return m <= kPaM && cache_dtype != kE2M1 ? kPaM : m <= 64 ? 64 : 128;
+    return cache_dtype == kE2M1 && m <= 8 ? 8 : m <= kPaM ? kPaM : m <= 64 ? 64 : 128;
 }
 
 int64_t paged_attention_workspace(int cache_dtype, int hd, int n_seqs, int64_t n_rows, int heads, int kv_heads,
@@ -774,11 +775,12 @@ int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRow
     A.ws_ml = reinterpret_cast<float2*>(A.ws_o + 2 * (int64_t)num_sms * mt * hd);
     A.ws_join = reinterpret_cast<PaJoin*>(A.ws_ml + 2 * (int64_t)num_sms * mt);
     A.ws_odd = reinterpret_cast<int32_t*>(A.ws_join + num_sms);
-    const int e = mt > kPaM ? paged_attention_tc(A, cache_dtype, hd, mt, num_sms, st)
+    const int e = mt > kPaM                ? paged_attention_tc(A, cache_dtype, hd, mt, num_sms, st)
+                  : cache_dtype == kE2M1 ? paged_attention4(A, hd, mt, num_sms, st)
                   : hd == 64 ? pa_type<64>(A, cache_dtype, num_sms, st)
                              : pa_type<128>(A, cache_dtype, num_sms, st);
     if (e != 0) return e;
-    const dim3 grid(num_sms, mt / 16);
+    const dim3 grid(num_sms, (mt + 15) / 16);
     const int e8 = cache_dtype == kE4M3 || cache_dtype == kE2M1;
     return hd == 64 ? (int)launch(paged_join_kernel<64>, grid, dim3(kPaThreads), 0, st, A, mt, e8)
                     : (int)launch(paged_join_kernel<128>, grid, dim3(kPaThreads), 0, st, A, mt, e8);

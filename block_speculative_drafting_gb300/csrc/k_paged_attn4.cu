@@ -1,0 +1,556 @@
+// Attention of few rows (one token a sequence, mostly) over a 4-bit paged cache.
+// The line of work, its cut into equal shares and the join of shared units are
+// k_paged_attn.cu's, in tiles of 32 keys: a tile is one warp's, and a CTA's warps
+// deal a unit's tiles out among them.
+//
+// A byte of this cache is two elements, so the elements' way through the
+// registers is what costs: at the memory's rate an SM would have 42 of them a
+// clock.  The products are therefore the other way round than
+// k_paged_attn.cu's: S^T = K Q^T and O^T = V^T P^T, with keys (or a value's
+// columns) as the 16 rows of an m16n8k16 MMA and the unit's rows as its 8
+// columns: half the MMAs, half the exponentials and half the output registers
+// where a unit has up to 8 rows (two such halves where it has up to 16).  Codes come by
+// ldmatrix, four bytes a lane: of a key row those are eight columns, two MMAs'
+// operands in any order that the queries follow; of values, transposed in
+// two-byte units, four columns of two keys each.  A code is converted by the
+// hardware (e2m1 pairs -> f16 pairs) and multiplied by its block's scale in
+// f16, exactly.  The weights go from rows of S^T to columns of P^T by movmatrix.
+//
+// P is one f16 for bf16 outputs, off by 2^-11 of each key's part at most, an
+// eighth of the output's own 2^-8, and a hi + lo pair for f16 outputs.
+//
+// Masking: as in k_paged_attn.cu.  Codes are finite, so a value that is not can
+// only be a block scale of NaN: where rows see different keys, such tiles add P V key by
+// key with the hidden ones left out.
+#include "kernels.cuh"
+#include "paged_attn.cuh"
+
+namespace dflash {
+
+// tiles' time that a unit's end and the next one's beginning take
+constexpr int kP4Over = 8;
+
+DF_DEV void p4_ldsm(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+DF_DEV void p4_ldsm_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+DF_DEV void p4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+DF_DEV uint32_t p4_transposed(uint32_t x) {  // an 8 x 8 matrix of 16-bit elements, two of a row a lane
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <int N>
+struct P4Words {
+    uint32_t w[N];
+};
+// N words of a row's (or two rows') block scales
+template <int N>
+DF_DEV P4Words<N> p4_scales(uint32_t addr) {
+    P4Words<N> r;
+    if constexpr (N == 4)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "r"(addr));
+    else if constexpr (N == 2)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "r"(addr));
+    else
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r.w[0]) : "r"(addr));
+    return r;
+}
+
+// PAIR: weights as a hi + lo pair; NT: eights of a unit's rows
+template <bool PAIR, int HD, int NT>
+struct P4Shape {
+    static constexpr int W = NT == 1 ? 16 : 12, kThreads = W * 32;
+    static constexpr int RB = HD / 2, CH = RB / 16, SB = HD / 16;  // a row's bytes, 16-byte chunks, block scales
+    static constexpr int kCodes = kP4Keys * RB, kScales = kP4Keys * SB;
+    static constexpr int kStage = 2 * (kCodes + kScales);  // a warp's stage: keys, values, their scales
+    static constexpr int NST = HD == 64 ? 4 : 2;
+    static constexpr int kRow = HD + 4;  // f32 of a row's sums on their way through shared memory (four apart: other banks)
+    static constexpr int kMerge = W * 8 * NT * kRow * 4;
+    static constexpr size_t kSmem = (size_t)W * NST * kStage + kMerge;
+};
+// byte offset of chunk c of code row r, so that eight rows' chunks of one column sit in different banks
+template <int CH>
+DF_DEV uint32_t p4_off(int r, int c) {
+    return (uint32_t)(r * CH * 16 + ((CH == 4 ? c ^ ((r >> 1) & 3) : c ^ ((r >> 2) & 1)) << 4));
+}
+
+template <bool PAIR, int HD, int NT>
+__global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
+    paged_attn4_kernel(const __grid_constant__ PaArgs A) {
+    using S = P4Shape<PAIR, HD, NT>;
+    constexpr int W = S::W, NST = S::NST, CH = S::CH, SB = S::SB, MT = 8 * NT, SW = SB / 4;
+    extern __shared__ __align__(128) unsigned char sm[];
+    __shared__ uint32_t vbits[W][NST];  // a stage's held keys
+    __shared__ float2 ml[2][W][MT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+    const uint32_t base = smem_addr(sm) + warp * NST * S::kStage;
+    float* merge = reinterpret_cast<float*>(sm + (size_t)W * NST * S::kStage);
+    pdl_wait();
+    pdl_trigger();
+
+    int chunk;
+    PaCur cur = pa_share<kP4Keys>(A, MT, kP4Over, lane, chunk);
+    if (threadIdx.x == 0) A.ws_join[blockIdx.x].last = -1, A.ws_odd[blockIdx.x] = 0;
+    if (cur.left <= 0) return;
+    // the part of a unit that the share holds, and the unit after it
+    auto tiles_of = [](const PaCur& c) { return min(c.q.ntiles - c.tile, c.left); };
+    auto skip = [&](PaCur& c, int n) {
+        c.left -= n - 1;
+        c.tile += n - 1;
+        pa_next<kP4Keys>(A, MT, c);
+    };
+
+    // ---------------------------------------------------------------- copies
+    // Lane l holds the place of a stage's key l; `ahead` belongs to the stage to copy next.
+    struct Look {
+        int id, slot, h;
+    };
+    PaCur put = cur;
+    int put_n = tiles_of(put), put_t = warp;  // this warp's tile among the unit's
+    auto settle = [&]() {  // to the next unit with a tile for this warp
+        while (put.left > 0 && put_t >= put_n) {
+            skip(put, put_n);
+            put_n = tiles_of(put);
+            put_t = warp;
+        }
+    };
+    auto look = [&]() -> Look {
+        Look k{-1, 0, put.u % A.C.kv_heads};
+        const int key = put.q.lo + (put.tile + put_t) * kP4Keys + lane;
+        if (key < put.q.hi) k.id = page_entry(A.R, put.s, key, k.slot);
+        return k;
+    };
+    Look ahead{-1, 0, 0};
+    settle();
+    if (put.left > 0) ahead = look();
+    int stage_put = 0;
+    auto copy = [&]() {
+        if (put.left > 0) {
+            const uint32_t st = base + stage_put * S::kStage;
+            const bool held = page_held(ahead.id, A.C.n_pages);
+            const int64_t id = held ? ahead.id : 0, slot = held ? ahead.slot : 0;
+            const unsigned char* kp = A.C.k + id * A.C.ks[0] + slot * A.C.ks[1] + ahead.h * A.C.ks[2];
+            const unsigned char* vp = A.C.v + id * A.C.vs[0] + slot * A.C.vs[1] + ahead.h * A.C.vs[2];
+            const unsigned char* kb = A.C.kb + id * A.C.kbs[0] + slot * A.C.kbs[1] + ahead.h * A.C.kbs[2];
+            const unsigned char* vb = A.C.vb + id * A.C.vbs[0] + slot * A.C.vbs[1] + ahead.h * A.C.vbs[2];
+            const uint32_t bits = __ballot_sync(0xffffffffu, held);
+            if (lane == 0) vbits[warp][stage_put] = bits;
+            put_t += W;
+            settle();
+            if (put.left > 0) ahead = look();
+            constexpr int RPI = 32 / CH;  // rows a copy instruction covers
+#pragma unroll
+            for (int i = 0; i < kP4Keys / RPI; ++i) {
+                const int r = i * RPI + lane / CH, c = lane % CH;
+                const uint64_t k = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(kp), r);
+                const uint64_t v = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(vp), r);
+                const uint32_t bytes = (bits >> r) & 1u ? 16 : 0;  // (else nothing is read)
+                cp16(st + p4_off<CH>(r, c), bytes ? reinterpret_cast<const unsigned char*>(k) + 16 * c : A.q.p, bytes);
+                cp16(st + S::kCodes + p4_off<CH>(r, c), bytes ? reinterpret_cast<const unsigned char*>(v) + 16 * c : A.q.p, bytes);
+            }
+            if constexpr (SB == 8) {
+                cp8(st + 2 * S::kCodes + lane * SB, held ? kb : A.q.p, held ? 8 : 0);
+                cp8(st + 2 * S::kCodes + S::kScales + lane * SB, held ? vb : A.q.p, held ? 8 : 0);
+            } else {
+                cp4(st + 2 * S::kCodes + lane * SB, held ? kb : A.q.p, held ? 4 : 0);
+                cp4(st + 2 * S::kCodes + S::kScales + lane * SB, held ? vb : A.q.p, held ? 4 : 0);
+            }
+            stage_put = stage_put + 1 == NST ? 0 : stage_put + 1;
+        }
+        cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i) copy();
+
+    int stage = 0, turn = 0;
+    while (cur.left > 0) {
+        // ------------------------------------------------------------ a unit
+        const PaCur unit = cur;
+        const PaSeq& sq = unit.q;
+        const int tiles = tiles_of(unit);
+        const int h = unit.u % A.C.kv_heads, rt = unit.u / A.C.kv_heads;
+        const int mvalid = min(MT, sq.rows * A.group - rt * MT);
+        // queries: of row gq (and gq + 8) columns 32 c + 8 tq .., in f16, by a power of two where they are bf16
+        uint4 qf[NT][CH];
+        float c[NT][2];  // scores of rows 2 tq, 2 tq + 1 in log2 units: S c; never 0, so that -inf stays -inf
+        const float ks = A.scale_log2 * (A.C.k_scale != nullptr ? A.C.k_scale[h] : 1.f);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int m = gq + 8 * n, mm = rt * MT + m, r = mm / A.group, hq = h * A.group + mm % A.group;
+            const bool in = m < mvalid;
+            const unsigned char* p = A.q.p + (int64_t)(sq.row0 + r) * A.q.rs + (int64_t)hq * A.q.hs;
+            const bool qb = A.q.dtype == kBF16;
+            float mx = 0.f;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                qf[n][j] = in ? *reinterpret_cast<const uint4*>(p + 64 * j + 16 * tq) : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t w[4] = {qf[n][j].x, qf[n][j].y, qf[n][j].z, qf[n][j].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack2<true>(w[i]);
+                    mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            float rf = 1.f;
+            if (qb) {
+                // a row times 2^-x, its largest element in [1, 2): what f16 cannot hold of it then is under 2^-25 of that
+                float down = 1.f;
+                if (mx > 0.f && mx < INFINITY) {
+                    const int x = min(max(ilogbf(mx), -120), 120);
+                    down = ldexpf(1.f, -x);
+                    rf = ldexpf(1.f, x);
+                }
+#pragma unroll
+                for (int j = 0; j < CH; ++j) {
+                    uint32_t w[4] = {qf[n][j].x, qf[n][j].y, qf[n][j].z, qf[n][j].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = unpack2<true>(w[i]);
+                        w[i] = pack2<false>(f.x * down, f.y * down);
+                    }
+                    qf[n][j] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                c[n][e] = fminf(fmaxf(ks * __shfl_sync(0xffffffffu, rf, 4 * (2 * tq + e)), 1e-37f), 3e38f);
+        }
+        // positions between which every row of the unit's tile sees every key
+        const int pmin = sq.p0 + (rt * MT) / A.group;
+        const int pmax = sq.p0 + (rt * MT + mvalid - 1) / A.group;
+        const int wtop = A.window > 0 ? pmax - A.window + 1 : 0;
+
+        float o[NT][CH][2][4];  // columns 32 c + 4 gq + 2 t + {0, 1} of rows 8 n + 2 tq + {0, 1}
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) m[n][e] = -INFINITY, l[n][e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[n][j][t][e] = 0.f;
+        }
+
+#pragma unroll 1
+        for (int t = warp; t < tiles; t += W) {
+            cp_wait<NST - 2>();
+            __syncwarp();
+            copy();
+            const uint32_t sk = base + stage * S::kStage, sv = sk + S::kCodes, bk = sk + 2 * S::kCodes, bv = bk + S::kScales;
+            const uint32_t bits = vbits[warp][stage];
+            const int kfirst = sq.lo + (unit.tile + t) * kP4Keys, klast = kfirst + kP4Keys - 1;
+            stage = stage + 1 == NST ? 0 : stage + 1;
+            if (bits == 0) continue;
+            // ---- scores: keys 16 k + gq (+ 8) of rows 2 tq, 2 tq + 1
+            float sc[2][NT][4];
+            const int lrow = ((lane >> 3) & 1) * 8 + (lane & 7), lch = lane >> 4;  // the row and chunk of this lane's ldmatrix address
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[k][n][e] = 0.f;
+                uint32_t s[2][2];  // the keys' scales of this lane's block of chunks 0, 1 and 2, 3
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const auto x = p4_scales<SW>(bk + (16 * k + gq + 8 * e) * SB);
+                    const uint32_t y = __byte_perm(x.w[0], x.w[SW - 1], tq & 2 ? (SW == 2 ? 0x7531 : 0x3131) : (SW == 2 ? 0x6420 : 0x2020));
+                    e4m3x4_f16x4(y, s[e][0], s[e][1]);
+                }
+#pragma unroll
+                for (int j = 0; j < CH; j += 2) {
+                    uint32_t r[4];
+                    p4_ldsm(r, sk + p4_off<CH>(16 * k + lrow, j + lch));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t a[4], b[4];
+                        e2m1x8_f16x8(r[2 * i], a);
+                        e2m1x8_f16x8(r[2 * i + 1], b);
+                        const uint32_t sa = __byte_perm(s[0][j >> 1], 0, i ? 0x3232 : 0x1010),
+                                       sb = __byte_perm(s[1][j >> 1], 0, i ? 0x3232 : 0x1010);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a[e] = mul_f16x2(a[e], sa), b[e] = mul_f16x2(b[e], sb);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const uint4& q = qf[n][j + i];
+                            p4_mma(sc[k][n], a[0], b[0], a[1], b[1], q.x, q.y);
+                            p4_mma(sc[k][n], a[2], b[2], a[3], b[3], q.z, q.w);
+                        }
+                    }
+                }
+            }
+            // ---- softmax
+            const bool full = bits == 0xffffffffu && klast <= pmin && kfirst >= wtop;
+            uint32_t hid = 0;  // bit 8 n + 4 k + e: sc[k][n][e] is not in its row's view
+            if (!full) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = 8 * n + 2 * tq + e, mm = rt * MT + row;
+                        const int pos = row < mvalid ? sq.p0 + mm / A.group : -1;
+                        const int wlo = A.window > 0 ? pos - A.window + 1 : 0;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const int kk = 16 * k + gq + 8 * y, key = kfirst + kk;
+                                if (!((bits >> kk) & 1u) || key > pos || key < wlo) {
+                                    sc[k][n][2 * y + e] = -INFINITY;
+                                    hid |= 1u << (8 * n + 4 * k + 2 * y + e);
+                                }
+                            }
+                    }
+            }
+            constexpr float over = kPaLazy + kPaUnder<false>;
+            float mx[NT][2];
+            bool move = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[n][e] = fmaxf(fmaxf(sc[0][n][e], sc[0][n][2 + e]), fmaxf(sc[1][n][e], sc[1][n][2 + e])) * c[n][e];
+                    move |= mx[n][e] > m[n][e] + over;
+                }
+            if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = mx[n][e];
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                        const float to = x > m[n][e] + over ? x - kPaUnder<false> : m[n][e];
+                        const float f = to == m[n][e] ? 1.f : pa_exp2(m[n][e] - to);
+                        m[n][e] = to;
+                        l[n][e] *= f;
+#pragma unroll
+                        for (int j = 0; j < CH; ++j)
+#pragma unroll
+                            for (int t2 = 0; t2 < 2; ++t2) o[n][j][t2][e] *= f, o[n][j][t2][2 + e] *= f;
+                    }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float mr = m[n][e] == -INFINITY ? 0.f : m[n][e];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            float& p = sc[k][n][2 * y + e];
+                            p = pa_exp2(fmaf(p, c[n][e], -mr));
+                            l[n][e] += p;
+                        }
+                }
+            // keys that some row of the tile sees and another does not: are their values' scales numbers?
+            if (!full && (klast > pmin || kfirst < wtop)) {
+                const auto x = p4_scales<SW>(bv + lane * SB);
+                bool nan = false;
+#pragma unroll
+                for (int i = 0; i < SW; ++i) nan |= (((x.w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+                if (__any_sync(0xffffffffu, nan)) {
+                    // key by key, the hidden ones left out
+#pragma unroll 1
+                    for (int kk = 0; kk < kP4Keys; ++kk) {
+                        const int src = 4 * (kk & 7) + tq, at = 4 * (kk >> 4) + 2 * ((kk >> 3) & 1);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            float p[2] = {0.f, 0.f};
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y)
+                                    if (4 * k + 2 * y == at) p[0] = sc[k][n][2 * y], p[1] = sc[k][n][2 * y + 1];
+                            p[0] = __shfl_sync(0xffffffffu, p[0], src);
+                            p[1] = __shfl_sync(0xffffffffu, p[1], src);
+                            const uint32_t hb = __shfl_sync(0xffffffffu, hid, src) >> (8 * n + at);
+#pragma unroll
+                            for (int j = 0; j < CH; ++j) {
+                                uint32_t w, b;
+                                asm volatile("ld.shared.u16 %0, [%1];" : "=r"(w) : "r"(sv + p4_off<CH>(kk, j) + 2 * gq));
+                                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(bv + kk * SB + 2 * j + (gq >> 2)));
+                                uint32_t v[4];
+                                e2m1x8_f16x8(w, v);
+                                const float s = unpack2<false>(e4m3x2_f16x2(b)).x;
+#pragma unroll
+                                for (int t2 = 0; t2 < 2; ++t2) {
+                                    const float2 f = unpack2<false>(v[t2]);
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e)
+                                        if (!((hb >> e) & 1u)) {
+                                            o[n][j][t2][e] = fmaf(p[e], f.x * s, o[n][j][t2][e]);
+                                            o[n][j][t2][2 + e] = fmaf(p[e], f.y * s, o[n][j][t2][2 + e]);
+                                        }
+                                }
+                            }
+                        }
+                    }
+                    continue;
+                }
+            }
+            // ---- values: O^T += V^T P^T
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t hi = pack2<false>(sc[k][n][2 * y], sc[k][n][2 * y + 1]);
+                        ph[n][y] = p4_transposed(hi);
+                        if constexpr (PAIR) {
+                            const float2 f = unpack2<false>(hi);
+                            pl[n][y] = p4_transposed(pack2<false>(sc[k][n][2 * y] - f.x, sc[k][n][2 * y + 1] - f.y));
+                        }
+                    }
+                uint32_t s[2][4];  // scales of keys 2 tq, 2 tq + 1 (and 8 on), of this lane's block of each chunk
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const auto x = p4_scales<2 * SW>(bv + (16 * k + 8 * y + 2 * tq) * SB);
+                    const uint32_t pick = gq & 4 ? (SW == 2 ? 0x7531 : 0x3131) : (SW == 2 ? 0x6420 : 0x2020);
+                    const uint32_t k0 = __byte_perm(x.w[0], x.w[SW - 1], pick), k1 = __byte_perm(x.w[SW], x.w[2 * SW - 1], pick);
+                    e4m3x4_f16x4(__byte_perm(k0, k1, 0x5140), s[y][0], s[y][1]);
+                    if constexpr (CH == 4) e4m3x4_f16x4(__byte_perm(k0, k1, 0x7362), s[y][2], s[y][3]);
+                }
+#pragma unroll
+                for (int j = 0; j < CH; j += 2) {
+                    uint32_t r[4];
+                    p4_ldsm_t(r, sv + p4_off<CH>(16 * k + lrow, j + lch));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t v[2][4];  // columns 0 .. 3 of keys 2 tq, 2 tq + 1 and of keys 8 on
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            uint32_t x[4];
+                            e2m1x8_f16x8(r[2 * i + y], x);
+                            const uint32_t sy = s[y][j + i];
+                            v[y][0] = mul_f16x2(__byte_perm(x[0], x[2], 0x5410), sy);
+                            v[y][1] = mul_f16x2(__byte_perm(x[0], x[2], 0x7632), sy);
+                            v[y][2] = mul_f16x2(__byte_perm(x[1], x[3], 0x5410), sy);
+                            v[y][3] = mul_f16x2(__byte_perm(x[1], x[3], 0x7632), sy);
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int t2 = 0; t2 < 2; ++t2) {
+                                p4_mma(o[n][j + i][t2], v[0][2 * t2], v[0][2 * t2 + 1], v[1][2 * t2], v[1][2 * t2 + 1], ph[n][0], ph[n][1]);
+                                if constexpr (PAIR)
+                                    p4_mma(o[n][j + i][t2], v[0][2 * t2], v[0][2 * t2 + 1], v[1][2 * t2], v[1][2 * t2 + 1], pl[n][0], pl[n][1]);
+                            }
+                    }
+                }
+            }
+        }
+
+        // ------------------------------------------------------------ the unit's end: the warps that had tiles join
+        const int active = min(W, tiles);
+        float2(&part)[W][MT] = ml[turn & 1];
+        ++turn;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+                if (gq == 0) part[warp][8 * n + 2 * tq + e] = make_float2(m[n][e], l[n][e]);
+            }
+        __syncthreads();
+        if (warp < active) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = 8 * n + 2 * tq + e;
+                    float big = -INFINITY;
+#pragma unroll 4
+                    for (int w = 0; w < active; ++w) big = fmaxf(big, part[w][row].x);
+                    const float f = m[n][e] == -INFINITY ? 1.f : pa_exp2(m[n][e] - big);
+                    float* to = merge + (size_t)(warp * MT + row) * S::kRow + 4 * gq;
+#pragma unroll
+                    for (int j = 0; j < CH; ++j)
+                        *reinterpret_cast<float4*>(to + 32 * j) = make_float4(o[n][j][0][e] * f, o[n][j][0][2 + e] * f,
+                                                                              o[n][j][1][e] * f, o[n][j][1][2 + e] * f);
+                }
+        }
+        __syncthreads();
+        const bool whole = unit.tile == 0 && tiles == sq.ntiles;
+        if (!whole && unit.tile == 0 && threadIdx.x == 0)
+            A.ws_join[blockIdx.x] = pa_join_entry(unit, rt, MT, mvalid, h, sq.ntiles - tiles, chunk);
+        // a part of a shared unit: its start goes to the CTA's second slot, any other part to the first
+        const int slot = blockIdx.x * 2 + (unit.tile == 0 ? 1 : 0);
+#pragma unroll 1
+        for (int i = threadIdx.x; i < mvalid * (HD / 4); i += S::kThreads) {
+            const int row = i / (HD / 4), col = 4 * (i % (HD / 4));
+            float big = -INFINITY, sum = 0.f;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int w = 0; w < active; ++w) big = fmaxf(big, part[w][row].x);
+#pragma unroll 4
+            for (int w = 0; w < active; ++w) {
+                const float2 x = part[w][row];
+                sum += x.x == -INFINITY ? x.y : x.y * pa_exp2(x.x - big);  // (a NaN sum without a maximum stays)
+                const float4 z = *reinterpret_cast<const float4*>(merge + (size_t)(w * MT + row) * S::kRow + col);
+                y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+            }
+            if (whole) {
+                const int mm = rt * MT + row, r = sq.row0 + mm / A.group, hq = h * A.group + mm % A.group;
+                const float inv = sum == 0.f ? 0.f : (A.C.v_scale != nullptr ? A.C.v_scale[h] : 1.f) / sum;
+                uint2 w;
+                if (A.out.dtype == kBF16)
+                    w = make_uint2(pack2<true>(y.x * inv, y.y * inv), pack2<true>(y.z * inv, y.w * inv));
+                else
+                    w = make_uint2(pack2<false>(y.x * inv, y.y * inv), pack2<false>(y.z * inv, y.w * inv));
+                *reinterpret_cast<uint2*>(A.out.p + (int64_t)r * A.out.rs + (int64_t)hq * A.out.hs + 2 * col) = w;
+                if (A.lse != nullptr && col == 0)
+                    A.lse[(int64_t)r * A.q.heads + hq] =
+                        sum == 0.f ? -INFINITY : (big == -INFINITY ? sum : (big + log2f(sum)) * 0.69314718056f);
+            } else {
+                *reinterpret_cast<float4*>(A.ws_o + ((int64_t)slot * MT + row) * HD + col) = y;
+                if (col == 0) A.ws_ml[(int64_t)slot * MT + row] = make_float2(big, sum);
+            }
+        }
+        skip(cur, tiles);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <bool PAIR, int HD, int NT>
+static int p4_launch(const PaArgs& A, int num_sms, cudaStream_t st) {
+    using S = P4Shape<PAIR, HD, NT>;
+    static size_t limit[kMaxDevices] = {};
+    auto kern = paged_attn4_kernel<PAIR, HD, NT>;
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return (int)e;
+    if (cudaError_t e = raise_smem_limit(kern, S::kSmem, &limit[dev])) return (int)e;
+    return (int)launch(kern, dim3(num_sms), dim3(S::kThreads), S::kSmem, st, A);
+}
+template <bool PAIR>
+static int p4_shape(const PaArgs& A, int hd, int mt, int num_sms, cudaStream_t st) {
+    if (mt == 8) return hd == 64 ? p4_launch<PAIR, 64, 1>(A, num_sms, st) : p4_launch<PAIR, 128, 1>(A, num_sms, st);
+    return hd == 64 ? p4_launch<PAIR, 64, 2>(A, num_sms, st) : p4_launch<PAIR, 128, 2>(A, num_sms, st);
+}
+int paged_attention4(const PaArgs& A, int hd, int mt, int num_sms, cudaStream_t st) {
+    return A.out.dtype == kF16 ? p4_shape<true>(A, hd, mt, num_sms, st) : p4_shape<false>(A, hd, mt, num_sms, st);
+}
+
+}  // namespace dflash

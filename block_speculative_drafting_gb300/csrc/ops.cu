@@ -250,7 +250,7 @@ int dflash_paged_key_weights(const dflash_paged_cache* cache, const dflash_paged
     if (window < 0 || window > 1 << 30) return fail(DFLASH_EINVAL, "window %d", window);
     if (!al4(lse) || (lse == nullptr && R.n_rows > 0)) return fail(DFLASH_EINVAL, "lse is NULL or not 4-byte aligned");
     TRY(check_weights(weights, "weights", R, &W));
-    if (!pa_line_fits(R, q->heads, cache->kv_heads))
+    if (!pa_line_fits(R, q->heads, cache->kv_heads, cache->dtype))
         return fail(DFLASH_EINVAL, "%d sequences of %d positions: too many tiles of keys", R.n_seqs, R.cap);
     if (R.n_rows == 0) return DFLASH_OK;
     int n = 0;
@@ -333,7 +333,7 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_r
     if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(DFLASH_EINVAL, "scale %g", (double)scale);
     if (window < 0 || window > 1 << 30) return fail(DFLASH_EINVAL, "window %d", window);
     if (!al4(lse)) return fail(DFLASH_EINVAL, "lse needs 4-byte alignment");
-    if (!pa_line_fits(R, q->heads, cache->kv_heads))
+    if (!pa_line_fits(R, q->heads, cache->kv_heads, cache->dtype))
         return fail(DFLASH_EINVAL, "%d sequences of %d positions: too many tiles of keys", R.n_seqs, R.cap);
     if (R.n_rows == 0) return DFLASH_OK;
     int n = 0;

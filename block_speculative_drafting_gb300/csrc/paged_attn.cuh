@@ -8,6 +8,7 @@
 namespace dflash {
 
 constexpr int kPaTile = 128;     // keys a CTA takes at once: 16 a warp
+constexpr int kP4Keys = 32;      // keys a warp takes at once of a 4-bit cache
 // A row's reference m: its largest score in log2 units less kPaUnder when m is set, moved only where a score passes
 // that by more than kPaLazy.  P = 2^(score - m) in f16 loses bits below 2^-14: set 7 under the maximum (P is then at
 // most 2^15) it loses none that weigh 2^-21 of the largest.  (bf16 has f32's exponents, and values near f32's end.)
@@ -42,7 +43,8 @@ struct PaSeq {
     int ntiles, nunits;
 };
 
-// of sequence s with rows [a, b)
+// of sequence s with rows [a, b), in tiles of TILE keys
+template <int TILE = kPaTile>
 DF_DEV PaSeq pa_seq(const PaArgs& A, int s, int a, int b, int mt) {
     PaSeq q;
     q.row0 = a;
@@ -51,7 +53,7 @@ DF_DEV PaSeq pa_seq(const PaArgs& A, int s, int a, int b, int mt) {
     q.p0 = max(len, -1) - q.rows;  // a length below 0 reads as -1: no position of any row is held
     q.hi = min(max(len, 0), A.R.cap);
     q.lo = A.window > 0 ? max(0, q.p0 - A.window + 1) : 0;
-    q.ntiles = max(1, (q.hi - q.lo + kPaTile - 1) / kPaTile);  // a sequence with rows but no keys: one tile of nothing
+    q.ntiles = max(1, (q.hi - q.lo + TILE - 1) / TILE);  // a sequence with rows but no keys: one tile of nothing
     q.nunits = (int)(((int64_t)q.rows * A.group + mt - 1) / mt) * A.C.kv_heads;
     return q;
 }
@@ -89,6 +91,7 @@ DF_DEV void rows_of_lane(const PagedRows& R, int s0, int from, int lane, int& a,
     }
 }
 // This CTA's share (warp-wide); `chunk`: the places of a share.
+template <int TILE = kPaTile>
 DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
     int64_t t64 = 0, v64 = 0;
     int w0 = 0, u0 = 0;
@@ -98,7 +101,7 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
         rows_of_lane(A.R, s0, from, lane, a, b);
         from = __shfl_sync(0xffffffffu, b, 31);
         if (s0 + lane >= A.R.n_seqs) continue;
-        const PaSeq q = pa_seq(A, s0 + lane, a, b, mt);
+        const PaSeq q = pa_seq<TILE>(A, s0 + lane, a, b, mt);
         const int64_t w = (int64_t)q.ntiles * q.nunits;
         if (s0 == 0) w0 = (int)w, u0 = q.nunits;
         t64 = min(t64 + w, (int64_t)1 << 40);
@@ -125,7 +128,7 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
         rows_of_lane(A.R, s0, from, lane, a, b);
         from = __shfl_sync(0xffffffffu, b, 31);
         if (s0 > 0) {
-            const PaSeq q = pa_seq(A, min(s0 + lane, A.R.n_seqs - 1), a, b, mt);
+            const PaSeq q = pa_seq<TILE>(A, min(s0 + lane, A.R.n_seqs - 1), a, b, mt);
             w = s0 + lane < A.R.n_seqs ? (q.ntiles + c.ov) * q.nunits : 0;
         }
         int in = w;
@@ -139,7 +142,7 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
             const int l = __ffs(hit) - 1;
             const int x = t - (run + __shfl_sync(0xffffffffu, in - w, l));
             c.s = s0 + l;
-            c.q = pa_seq(A, c.s, __shfl_sync(0xffffffffu, a, l), __shfl_sync(0xffffffffu, b, l), mt);
+            c.q = pa_seq<TILE>(A, c.s, __shfl_sync(0xffffffffu, a, l), __shfl_sync(0xffffffffu, b, l), mt);
             const int per = c.q.ntiles + c.ov;
             c.u = x / per;
             const int v = x - c.u * per;
@@ -154,6 +157,7 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
     }
     return c;
 }
+template <int TILE = kPaTile>
 DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c) {
     --c.left;
     if (++c.tile < c.q.ntiles) return;
@@ -171,7 +175,7 @@ DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c) {
             return;
         }
         const int a = c.q.row0 + c.q.rows;
-        c.q = pa_seq(A, c.s, a, rows_end(A.R, c.s, a), mt);
+        c.q = pa_seq<TILE>(A, c.s, a, rows_end(A.R, c.s, a), mt);
     } while (c.q.nunits == 0);
 }
 // The entry of a unit that begins in this CTA's share and has `rest` tiles after it.
@@ -191,6 +195,9 @@ DF_DEV void cp16(uint32_t dst, const void* src, uint32_t bytes) {
 }
 DF_DEV void cp4(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+DF_DEV void cp8(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 DF_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -269,14 +276,16 @@ DF_DEV void pa_mark_odd(unsigned char* row, int hd) {
 }
 
 // Whether the places of any line of such a call stay below 2^31.
-inline bool pa_line_fits(const PagedRows& R, int heads, int kv_heads) {
-    const double units = (double)R.n_rows * heads / 16 + (double)R.n_seqs * kv_heads;
-    return units * ((double)R.cap / kPaTile + 8) < 2147483648.0;
+inline bool pa_line_fits(const PagedRows& R, int heads, int kv_heads, int cache_dtype) {
+    const double units = (double)R.n_rows * heads / (cache_dtype == kE2M1 ? 8 : 16) + (double)R.n_seqs * kv_heads;
+    return units * ((double)R.cap / (cache_dtype == kE2M1 ? kP4Keys : kPaTile) + 8) < 2147483648.0;
 }
 // tiles' time that a unit's end and the next one's beginning take in the tcgen05 kernel (32 blocks over a
 // bf16 cache: 0 81.7 us, 2 73.3, 4 71.1)
 constexpr int kPtOver = 4;
 // The tcgen05 kernel (k_paged_attn_tc.cu): units of up to mt = 64 or 128 rows.
 int paged_attention_tc(const PaArgs& A, int cache_dtype, int hd, int mt, int num_sms, cudaStream_t st);
+// The warp-MMA kernel of the 4-bit cache (k_paged_attn4.cu): units of up to mt = 8 or 16 rows.
+int paged_attention4(const PaArgs& A, int hd, int mt, int num_sms, cudaStream_t st);
 
 }  // namespace dflash
