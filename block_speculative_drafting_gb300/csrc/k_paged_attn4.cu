@@ -52,6 +52,12 @@ DF_DEV uint32_t p4_transposed(uint32_t x) {  // an 8 x 8 matrix of 16-bit elemen
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+// a pair times the lower (upper) half of another
+DF_DEV uint32_t p4_times(uint32_t a, uint32_t s, bool upper) {
+    const __half2 x = *reinterpret_cast<const __half2*>(&a), y = *reinterpret_cast<const __half2*>(&s);
+    const __half2 z = __hmul2(x, upper ? __high2half2(y) : __low2half2(y));
+    return *reinterpret_cast<const uint32_t*>(&z);
+}
 template <int N>
 struct P4Words {
     uint32_t w[N];
@@ -141,32 +147,35 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
         if (put.left > 0) {
             const uint32_t st = base + stage_put * S::kStage;
             const bool held = page_held(ahead.id, A.C.n_pages);
-            const int64_t id = held ? ahead.id : 0, slot = held ? ahead.slot : 0;
-            const unsigned char* kp = A.C.k + id * A.C.ks[0] + slot * A.C.ks[1] + ahead.h * A.C.ks[2];
-            const unsigned char* vp = A.C.v + id * A.C.vs[0] + slot * A.C.vs[1] + ahead.h * A.C.vs[2];
-            const unsigned char* kb = A.C.kb + id * A.C.kbs[0] + slot * A.C.kbs[1] + ahead.h * A.C.kbs[2];
-            const unsigned char* vb = A.C.vb + id * A.C.vbs[0] + slot * A.C.vbs[1] + ahead.h * A.C.vbs[2];
+            // (strides of a 4-bit cache are below 2^31)
+            auto at = [&](unsigned char* p, const int64_t* strides) -> const unsigned char* {
+                const unsigned char* x = p + (int64_t)ahead.id * (int)strides[0] + (int64_t)ahead.slot * (int)strides[1] +
+                                         (int64_t)ahead.h * (int)strides[2];
+                return held ? x : A.q.p;  // (nothing is read)
+            };
+            const unsigned char *kp = at(A.C.k, A.C.ks), *vp = at(A.C.v, A.C.vs), *kb = at(A.C.kb, A.C.kbs), *vb = at(A.C.vb, A.C.vbs);
             const uint32_t bits = __ballot_sync(0xffffffffu, held);
             if (lane == 0) vbits[warp][stage_put] = bits;
             put_t += W;
-            settle();
+            if (put_t >= put_n) settle();
             if (put.left > 0) ahead = look();
             constexpr int RPI = 32 / CH;  // rows a copy instruction covers
+            const uint32_t to = st + p4_off<CH>(lane / CH, lane % CH);
+            const uint32_t mine = bits >> (lane / CH);
 #pragma unroll
             for (int i = 0; i < kP4Keys / RPI; ++i) {
-                const int r = i * RPI + lane / CH, c = lane % CH;
-                const uint64_t k = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(kp), r);
-                const uint64_t v = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(vp), r);
-                const uint32_t bytes = (bits >> r) & 1u ? 16 : 0;  // (else nothing is read)
-                cp16(st + p4_off<CH>(r, c), bytes ? reinterpret_cast<const unsigned char*>(k) + 16 * c : A.q.p, bytes);
-                cp16(st + S::kCodes + p4_off<CH>(r, c), bytes ? reinterpret_cast<const unsigned char*>(v) + 16 * c : A.q.p, bytes);
+                const uint64_t k = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(kp), i * RPI + lane / CH);
+                const uint64_t v = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(vp), i * RPI + lane / CH);
+                const uint32_t bytes = (mine >> (i * RPI) & 1u) << 4;
+                cp16(to + i * RPI * S::RB, reinterpret_cast<const unsigned char*>(k) + 16 * (lane % CH), bytes);
+                cp16(to + i * RPI * S::RB + S::kCodes, reinterpret_cast<const unsigned char*>(v) + 16 * (lane % CH), bytes);
             }
             if constexpr (SB == 8) {
-                cp8(st + 2 * S::kCodes + lane * SB, held ? kb : A.q.p, held ? 8 : 0);
-                cp8(st + 2 * S::kCodes + S::kScales + lane * SB, held ? vb : A.q.p, held ? 8 : 0);
+                cp8(st + 2 * S::kCodes + lane * SB, kb, held ? 8 : 0);
+                cp8(st + 2 * S::kCodes + S::kScales + lane * SB, vb, held ? 8 : 0);
             } else {
-                cp4(st + 2 * S::kCodes + lane * SB, held ? kb : A.q.p, held ? 4 : 0);
-                cp4(st + 2 * S::kCodes + S::kScales + lane * SB, held ? vb : A.q.p, held ? 4 : 0);
+                cp4(st + 2 * S::kCodes + lane * SB, kb, held ? 4 : 0);
+                cp4(st + 2 * S::kCodes + S::kScales + lane * SB, vb, held ? 4 : 0);
             }
             stage_put = stage_put + 1 == NST ? 0 : stage_put + 1;
         }
@@ -175,6 +184,8 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
 #pragma unroll
     for (int i = 0; i < NST - 1; ++i) copy();
 
+    // this lane's row and chunk of an ldmatrix of 16 rows by two chunks (the next two: 32 bytes on, as an exclusive or)
+    const uint32_t mat = p4_off<CH>(((lane >> 3) & 1) * 8 + (lane & 7), lane >> 4);
     int stage = 0, turn = 0;
     while (cur.left > 0) {
         // ------------------------------------------------------------ a unit
@@ -261,7 +272,6 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
             if (bits == 0) continue;
             // ---- scores: keys 16 k + gq (+ 8) of rows 2 tq, 2 tq + 1
             float sc[2][NT][4];
-            const int lrow = ((lane >> 3) & 1) * 8 + (lane & 7), lch = lane >> 4;  // the row and chunk of this lane's ldmatrix address
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -278,16 +288,14 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
 #pragma unroll
                 for (int j = 0; j < CH; j += 2) {
                     uint32_t r[4];
-                    p4_ldsm(r, sk + p4_off<CH>(16 * k + lrow, j + lch));
+                    p4_ldsm(r, (sk + 16 * k * S::RB + mat) ^ (16 * j));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         uint32_t a[4], b[4];
                         e2m1x8_f16x8(r[2 * i], a);
                         e2m1x8_f16x8(r[2 * i + 1], b);
-                        const uint32_t sa = __byte_perm(s[0][j >> 1], 0, i ? 0x3232 : 0x1010),
-                                       sb = __byte_perm(s[1][j >> 1], 0, i ? 0x3232 : 0x1010);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) a[e] = mul_f16x2(a[e], sa), b[e] = mul_f16x2(b[e], sb);
+                        for (int e = 0; e < 4; ++e) a[e] = p4_times(a[e], s[0][j >> 1], i), b[e] = p4_times(b[e], s[1][j >> 1], i);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             const uint4& q = qf[n][j + i];
@@ -435,7 +443,7 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
 #pragma unroll
                 for (int j = 0; j < CH; j += 2) {
                     uint32_t r[4];
-                    p4_ldsm_t(r, sv + p4_off<CH>(16 * k + lrow, j + lch));
+                    p4_ldsm_t(r, (sv + 16 * k * S::RB + mat) ^ (16 * j));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         uint32_t v[2][4];  // columns 0 .. 3 of keys 2 tq, 2 tq + 1 and of keys 8 on

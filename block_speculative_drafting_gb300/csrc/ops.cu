@@ -91,6 +91,8 @@ int check_cache(const dflash_paged_cache* c, PagedCache* out) {
             out->kbs[i] = c->k_block_strides[i];
             out->vbs[i] = c->v_block_strides[i];
             ok = ok && out->kbs[i] >= 0 && out->vbs[i] >= 0 && out->kbs[i] % row == 0 && out->vbs[i] % row == 0;
+            if (out->ks[i] > INT32_MAX || out->vs[i] > INT32_MAX || out->kbs[i] > INT32_MAX || out->vbs[i] > INT32_MAX)
+                return fail(DFLASH_EINVAL, "strides of an E2M1 cache must be below 2^31 bytes");
         }
         if (!ok)
             return fail(DFLASH_EINVAL, "block scales: base and strides must be multiples of %d bytes, strides not negative",

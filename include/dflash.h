@@ -525,8 +525,8 @@ DFLASH_API int dflash_attention_noalloc(dflash_model* model, dflash_seq* const* 
  * head h has the byte k_block + p * k_block_strides[0] + t *
  * k_block_strides[1] + h * k_block_strides[2] + d / 16, and an element is code
  * * block scale * head's scale.  Bases and strides of the block scales are
- * multiples of head_dim / 16 bytes, not negative.  (The fields from k_block on
- * are read with dtype E2M1 alone.)
+ * multiples of head_dim / 16 bytes, not negative; all strides are below 2^31.
+ * (The fields from k_block on are read with dtype E2M1 alone.)
  */
 typedef struct {
     void* k;
