@@ -52,32 +52,81 @@ struct Raw8 {
     }
 };
 
-// Eight values of a 4-bit cache's row, in units of the head's scale: with the eight of the neighbouring lane they are a
-// block of 16.  s = e4m3(min(max |x| / 6, 448)), codes e2m1(x / s) (nearest, ties to even, clamped to +-6; the
-// conversions and the division round as IEEE's do).  A NaN makes its block's scale NaN, and so all that the block stands for; a
-// block whose scale rounds to 0 is 0.  The even lane writes the scale.
-DF_DEV void store8_e2m1(unsigned char* p, unsigned char* block, const float (&x)[8], bool in, int c) {
-    float m = 0.f;
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        m = fmaxf(m, fabsf(x[i]));
-        nan |= x[i] != x[i];
-    }
-    if (nan) m = NAN;
-    const float o = __shfl_xor_sync(0xffffffffu, m, 1);
-    m = m != m || o != o ? NAN : fmaxf(m, o);
-    const float q = __fdiv_rn(m, 6.f);
-    const uint32_t s8 = m != m ? 0x7fu : __nv_cvt_float_to_fp8(fminf(q, 448.f), __NV_SATFINITE, __NV_E4M3);
-    const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s8, __NV_E4M3)));
-    float u[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = s > 0.f ? __fdiv_rn(x[i], s) : 0.f;
+// Two e2m1 codes a byte of eight values, the first in the lower bits: nearest, ties to even, clamped to +-6.
+DF_DEV uint32_t e2m1x8(const float (&u)[8]) {
     uint32_t w;
     asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
         " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
         : "=r"(w)
         : "f"(u[0]), "f"(u[1]), "f"(u[2]), "f"(u[3]), "f"(u[4]), "f"(u[5]), "f"(u[6]), "f"(u[7]));
+    return w;
+}
+DF_DEV float rcp_near(float d) {  // within 2^-22 of it
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d));
+    return y;
+}
+// x / d rounded as the division rounds it, y near 1 / d: with a quotient within a unit in the last place, q + y (x - q d)
+// rounds to the correct one (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990); the first such step brings x y within that unit.  For 2^-60 <= d <= 2^60 and |x| <= 2^60 (what underflows is far
+// below a block's smallest code).
+DF_DEV float quotient(float x, float d, float y) {
+    y = fmaf(fmaf(-d, y, 1.f), y, y);
+    float q = x * y;
+    q = fmaf(fmaf(-d, q, x), y, q);
+    return fmaf(fmaf(-d, q, x), y, q);
+}
+DF_DEV float max_nan(float a, float b) {  // NaN where one is
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+// The codes by the definition: t = x / scale and t / s, each rounded as the division rounds.
+__device__ __noinline__ uint32_t e2m1_defined(const float* x, float scale, float s) {
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = s > 0.f ? __fdiv_rn(__fdiv_rn(x[i], scale), s) : 0.f;
+    return e2m1x8(u);
+}
+// Eight values of a 4-bit cache's row; with the eight of the neighbouring lane they are a block of 16.  In units of the
+// head's scale, t = x / scale: s = e4m3(min(max |t| / 6, 448)) and codes e2m1(t / s), all rounded to nearest, ties to even.
+// A NaN makes its block's scale NaN, and so all that the block stands for; a block whose scale rounds to 0 is 0.  The
+// even lane writes the scale.  (All lanes take part.)
+//
+// The scale needs the quotient of the largest value alone (rounding keeps the order).  The codes come from one product with
+// the reciprocals of both scales, which is within 2^-21 of t / s, a little lower and a little higher: where the two agree
+// they are t / s's code; where some differ (one element of 10^5 lies that near to a border), the warp divides.  (8192 rows
+// of 8 + 8 heads: two divisions an element 30.7 us.)
+DF_DEV void store8_e2m1(unsigned char* p, unsigned char* block, const float (&x)[8], float scale, bool in, int c) {
+    float m = fabsf(x[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const bool plain = m <= 0x1p60f && scale >= 0x1p-60f && scale <= 0x1p60f;  // (false for NaN)
+    const float rs = rcp_near(scale);
+    float sixth = quotient(quotient(m, scale, rs), 6.f, 0x1.555556p-3f);
+    if (__any_sync(0xffffffffu, !plain)) sixth = __fdiv_rn(__fdiv_rn(m, scale), 6.f);
+    uint16_t s8;  // (clamped to 448; NaN stays)
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(sixth));
+    const float s = unpack2<false>(e4m3x2_f16x2(s8)).x;
+    const float ry = rcp_near(s), near = s > 0.f ? rs * ry : 0.f;
+    const float low = near * (1.f - 0x1p-20f), high = near * (1.f + 0x1p-20f);
+    float a[8], b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = x[i] * low, b[i] = x[i] * high;
+    uint32_t w = e2m1x8(a);
+    if (__any_sync(0xffffffffu, w != e2m1x8(b))) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = s > 0.f ? quotient(quotient(x[i], scale, rs), s, ry) : 0.f;
+        w = e2m1x8(a);
+    }
+    // (numbers near the ends of f32, where the products are not that near, and what is not a number)
+    if (__any_sync(0xffffffffu, !plain)) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = x[i];
+        w = e2m1_defined(v, scale, s);
+    }
     if (!in) return;
     *reinterpret_cast<uint32_t*>(p) = w;
     if ((c & 1) == 0) *block = (unsigned char)s8;
@@ -147,6 +196,10 @@ DF_DEV void head_loop(const HeadLoop& H, const float (&co)[8], const float (&si)
         for (int i = 0; i < AHEAD; ++i) {
             float x[8];
             next[i].values(x);
+            if (OUT == kE2M1 && h >= H.heads) {  // (nothing was loaded)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = 0.f;
+            }
             if (h + AHEAD * H.step < H.heads) next[i].load(from + AHEAD * H.from_step);
             if (H.gain != nullptr) {
                 float ss = 0.f;
@@ -179,15 +232,16 @@ DF_DEV void head_loop(const HeadLoop& H, const float (&co)[8], const float (&si)
                 }
             }
             if (OUT == kE2M1 || h < H.heads) {
-                if (H.scale != nullptr) {
-                    const float sc = H.scale[min(h, H.heads - 1)];
+                const float sc = H.scale != nullptr ? H.scale[min(h, H.heads - 1)] : 1.f;
+                if constexpr (OUT == kE2M1) {  // (all lanes: pairs of them share a block)
+                    store8_e2m1(to, block, x, sc, h < H.heads, threadIdx.x & (L - 1));
+                } else {
+                    if (H.scale != nullptr) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = __fdiv_rn(x[j], sc);
-                }
-                if constexpr (OUT == kE2M1)  // (all lanes: pairs of them share a block)
-                    store8_e2m1(to, block, x, h < H.heads, threadIdx.x & (L - 1));
-                else
+                        for (int j = 0; j < 8; ++j) x[j] = __fdiv_rn(x[j], sc);
+                    }
                     store8<OUT>(to, x);
+                }
             }
             h += H.step;
             if constexpr (OUT == kE2M1) block += H.block_step;
@@ -198,7 +252,7 @@ DF_DEV void head_loop(const HeadLoop& H, const float (&co)[8], const float (&si)
 }
 // IN: the type of q, k and v; QO, OUT: of the queries' destination and of the cache
 template <int HD, int IN, int QO, int OUT>
-__global__ void __launch_bounds__(kApWarps * 32, 4)
+__global__ void __launch_bounds__(kApWarps * 32, OUT == kE2M1 ? 3 : 4)
     paged_append_kernel(const __grid_constant__ PagedCache C, const __grid_constant__ PagedRows R,
                         const __grid_constant__ HeadRows k, const __grid_constant__ HeadRows v,
                         const __grid_constant__ HeadRows q, const __grid_constant__ HeadRows qo,
@@ -284,14 +338,14 @@ __global__ void __launch_bounds__(kApWarps * 32, 4)
 }
 
 // ---------------------------------------------------------------- rows read back
-// A cache's rows as values: 16 columns a lane and round (16 bytes of codes at most from an 8-bit cache, 8 from a 4-bit
-// one), warps over the call's rows as in the append.  Code times block scale is exact, the head's scale rounds in 32
-// bits, and the output's type once.  Positions that are not held read as zeros.
+// A cache's rows as values: eight columns a lane (so that a warp's stores are contiguous), warps over the call's rows as
+// in the append.  Code times block scale is exact, the head's scale rounds in 32 bits, and the output's type once.
+// Positions that are not held read as zeros.
 template <int HD, int CD, int OUT>
 __global__ void __launch_bounds__(kApWarps * 32)
     paged_read_kernel(const __grid_constant__ PagedCache C, const __grid_constant__ PagedRows R,
                       const __grid_constant__ HeadRows ko, const __grid_constant__ HeadRows vo, int warps_log2) {
-    constexpr int L = HD / 16;   // lanes of a head
+    constexpr int L = HD / 8;    // lanes of a head
     constexpr int HPW = 32 / L;  // heads a warp holds at once
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % L;
     const int64_t id = (int64_t)blockIdx.x * kApWarps + warp;
@@ -305,61 +359,57 @@ __global__ void __launch_bounds__(kApWarps * 32)
     const int64_t pos64 = (int64_t)R.kv_len[s] - (b - a) + (row - a);
     int slot = 0;
     const int64_t page = page_of(R, C.n_pages, s, (int)max(pos64, (int64_t)-1), slot);
-#pragma unroll 1
-    for (int side = 0; side < 2; ++side) {
-        const HeadRows& O = side == 0 ? ko : vo;
-        if (O.p == nullptr) continue;
-        const unsigned char* from = (side == 0 ? C.k : C.v) + max(page, (int64_t)0) * (side == 0 ? C.ks[0] : C.vs[0]) +
-                                    slot * (side == 0 ? C.ks[1] : C.vs[1]);
-        const int64_t hs = side == 0 ? C.ks[2] : C.vs[2];
-        const float* scale = side == 0 ? C.k_scale : C.v_scale;
-#pragma unroll 2
-        for (int h = share * HPW + lane / L; h < C.kv_heads; h += HPW << warps_log2) {
-            float x[2][8] = {};
-            if (page >= 0) {
-                const unsigned char* p = from + h * hs;
-                const float sc = scale != nullptr ? scale[h] : 1.f;
-                if constexpr (CD == kBF16 || CD == kF16) {
-                    Raw8<CD> r[2];
-                    r[0].load(p + 32 * c);
-                    r[1].load(p + 32 * c + 16);
-                    r[0].values(x[0]);
-                    r[1].values(x[1]);
-                } else {
-                    uint32_t y[8];
-                    float f = sc;
-                    if constexpr (CD == kE4M3) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(p + 16 * c);
-                        e4m3x4_f16x4(w.x, y[0], y[1]);
-                        e4m3x4_f16x4(w.y, y[2], y[3]);
-                        e4m3x4_f16x4(w.z, y[4], y[5]);
-                        e4m3x4_f16x4(w.w, y[6], y[7]);
-                    } else {
-                        const uint2 w = *reinterpret_cast<const uint2*>(p + 8 * c);
-                        const unsigned char* bl = side == 0 ? C.kb + page * C.kbs[0] + slot * C.kbs[1] + h * C.kbs[2]
-                                                            : C.vb + page * C.vbs[0] + slot * C.vbs[1] + h * C.vbs[2];
-                        const uint32_t s2 = __byte_perm(e4m3x2_f16x2(bl[c]), 0, 0x1010);
-                        uint32_t z[4];
-                        e2m1x8_f16x8(w.x, z);
+    const int64_t pg = max(page, (int64_t)0);
+    const unsigned char *k = C.k + pg * C.ks[0] + slot * C.ks[1], *v = C.v + pg * C.vs[0] + slot * C.vs[1];
+    const unsigned char *kb = C.kb + pg * C.kbs[0] + slot * C.kbs[1] + c / 2, *vb = C.vb + pg * C.vbs[0] + slot * C.vbs[1] + c / 2;
+    unsigned char *kt = ko.p + (int64_t)row * ko.rs + 8 * c * (OUT == kF32 ? 4 : 2), *vt = vo.p + (int64_t)row * vo.rs + 8 * c * (OUT == kF32 ? 4 : 2);
+    constexpr int E = CD == kE2M1 ? 4 : CD == kE4M3 ? 8 : 16;  // bytes of eight columns
+    struct Codes {
+        Raw8<CD == kF16 ? kF16 : kBF16> raw;
+        uint2 w;
+        uint32_t s;
+        float sc;
+    };
+    auto load = [&](const unsigned char* from, const unsigned char* blocks, const float* scale, int h) {
+        Codes x{};
+        if (page < 0) return x;
+        if constexpr (E == 16) x.raw.load(from + E * c);
+        if constexpr (E == 8) x.w = *reinterpret_cast<const uint2*>(from + E * c);
+        if constexpr (E == 4) x.w.x = *reinterpret_cast<const uint32_t*>(from + E * c), x.s = *blocks;
+        if constexpr (E < 16) x.sc = scale != nullptr ? scale[h] : 1.f;
+        return x;
+    };
+    auto store = [&](unsigned char* to, const Codes& x) {
+        float y[8];
+        if constexpr (E == 16) {
+            x.raw.values(y);
+        } else {
+            uint32_t z[4];
+            if constexpr (E == 8) {
+                e4m3x4_f16x4(x.w.x, z[0], z[1]);
+                e4m3x4_f16x4(x.w.y, z[2], z[3]);
+            } else {
+                e2m1x8_f16x8(x.w.x, z);
+                const uint32_t s2 = __byte_perm(e4m3x2_f16x2(x.s), 0, 0x1010);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) y[i] = mul_f16x2(z[i], s2);
-                        e2m1x8_f16x8(w.y, z);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) y[4 + i] = mul_f16x2(z[i], s2);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 v = unpack2<false>(y[i]);
-                        x[i >> 2][2 * (i & 3)] = v.x * f;
-                        x[i >> 2][2 * (i & 3) + 1] = v.y * f;
-                    }
-                }
+                for (int i = 0; i < 4; ++i) z[i] = mul_f16x2(z[i], s2);
             }
-            constexpr int E = OUT == kF32 ? 4 : 2;
-            unsigned char* to = O.p + (int64_t)row * O.rs + h * O.hs + 16 * c * E;
-            store8<OUT>(to, x[0]);
-            store8<OUT>(to + 8 * E, x[1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack2<false>(z[i]);
+                y[2 * i] = f.x * x.sc;
+                y[2 * i + 1] = f.y * x.sc;
+            }
         }
+        store8<OUT>(to, y);
+    };
+#pragma unroll 2
+    for (int h = share * HPW + lane / L; h < C.kv_heads; h += HPW << warps_log2) {
+        Codes x{}, y{};
+        if (ko.p != nullptr) x = load(k + h * C.ks[2], kb + h * C.kbs[2], C.k_scale, h);
+        if (vo.p != nullptr) y = load(v + h * C.vs[2], vb + h * C.vbs[2], C.v_scale, h);
+        if (ko.p != nullptr) store(kt + h * ko.hs, x);
+        if (vo.p != nullptr) store(vt + h * vo.hs, y);
     }
 }
 template <int HD, int CD>
@@ -386,6 +436,67 @@ int paged_read(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R,
                        vo, wl);
 }
 
+// Keys and values into a 4-bit cache as they come, no queries beside them: a warp a row and tensor (more where rows are
+// few), four rounds of heads on their way at once.  In registers enough for half as many warps the general kernel took
+// 25.5 us (8192 rows of 8 + 8 heads of 128), this one 17.9 us.
+template <int HD, int IN>
+__global__ void __launch_bounds__(kApWarps * 32, 4)
+    paged_append4_kernel(const __grid_constant__ PagedCache C, const __grid_constant__ PagedRows R,
+                         const __grid_constant__ HeadRows k, const __grid_constant__ HeadRows v, int warps_log2) {
+    constexpr int L = HD / 8, HPW = 32 / L, AHEAD = IN == kF32 ? 2 : 4, E = IN == kF32 ? 4 : 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % L;
+    const int64_t id = (int64_t)blockIdx.x * kApWarps + warp;
+    const int row = (int)(id >> (warps_log2 + 1)), side = (int)(id & 1), share = (int)(id >> 1) & ((1 << warps_log2) - 1);
+    pdl_wait();
+    pdl_trigger();
+    if (row >= R.n_rows) return;
+    const HeadRows& src = side == 0 ? k : v;
+    const int h0 = share * HPW + lane / L, step = HPW << warps_log2;
+    const unsigned char* from = src.p + (int64_t)row * src.rs + h0 * src.hs + 8 * c * E;
+    const int64_t from_step = step * src.hs;
+    Raw8<IN> raw[AHEAD];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (h + i * step < C.kv_heads) raw[i].load(from + i * from_step);
+    };
+    load(h0);
+    const int s = seq_of(R, row);
+    if (s < 0) return;
+    int a, b;
+    rows_of(R, s, a, b);
+    int slot = 0;
+    const int64_t page =
+        page_of(R, C.n_pages, s, (int)max((int64_t)R.kv_len[s] - (b - a) + (row - a), (int64_t)-1), slot);
+    if (page < 0) return;
+    const int64_t *st = side == 0 ? C.ks : C.vs, *bt = side == 0 ? C.kbs : C.vbs;
+    const float* scale = side == 0 ? C.k_scale : C.v_scale;
+    unsigned char* to = (side == 0 ? C.k : C.v) + page * st[0] + slot * st[1] + h0 * st[2] + 4 * c;
+    unsigned char* block = (side == 0 ? C.kb : C.vb) + page * bt[0] + slot * bt[1] + h0 * bt[2] + c / 2;
+#pragma unroll 1
+    for (int h = h0; h - lane / L < C.kv_heads; h += AHEAD * step) {
+        float sc[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) sc[i] = scale != nullptr ? scale[min(h + i * step, C.kv_heads - 1)] : 1.f;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const bool in = h + i * step < C.kv_heads;
+            if (h - lane / L + i * step >= C.kv_heads) break;  // (none of the warp's)
+            float x[8];
+            raw[i].values(x);
+            if (!in) {  // (nothing was loaded)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = 0.f;
+            }
+            store8_e2m1(to + i * step * st[2], block + i * step * bt[2], x, sc[i], in, c);
+        }
+        from += AHEAD * from_step;
+        load(h + AHEAD * step);
+        to += AHEAD * step * st[2];
+        block += AHEAD * step * bt[2];
+    }
+}
+
 template <int HD, int IN, int QO>
 static auto append_kernel(int out) {
     return out == kBF16  ? paged_append_kernel<HD, IN, QO, kBF16>
@@ -409,6 +520,18 @@ static auto append_kernel(int in, int qo, int out) {
 int paged_append(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& k, const HeadRows& v,
                  const HeadRows& q, const HeadRows& qo, const float* q_norm, const float* k_norm, float eps,
                  const Rotation& rot, const int32_t* evicted, int num_sms, cudaStream_t st) {
+    if (cache_dtype == kE2M1 && q.heads == 0 && k_norm == nullptr && rot.rotary == 0) {
+        auto kern = hd == 64 ? (k.dtype == kBF16  ? paged_append4_kernel<64, kBF16>
+                                : k.dtype == kF16 ? paged_append4_kernel<64, kF16>
+                                                  : paged_append4_kernel<64, kF32>)
+                             : (k.dtype == kBF16  ? paged_append4_kernel<128, kBF16>
+                                : k.dtype == kF16 ? paged_append4_kernel<128, kF16>
+                                                  : paged_append4_kernel<128, kF32>);
+        int wl = 0;
+        while (wl < 3 && ((int64_t)R.n_rows << (wl + 2)) <= (int64_t)num_sms * 20) ++wl;
+        const int64_t warps = (int64_t)R.n_rows << (wl + 1);
+        return (int)launch(kern, dim3((unsigned)((warps + kApWarps - 1) / kApWarps)), dim3(kApWarps * 32), 0, st, C, R, k, v, wl);
+    }
     const int qd = q.heads > 0 ? qo.dtype : k.dtype;
     auto kern = hd == 64 ? append_kernel<64>(k.dtype, qd, cache_dtype) : append_kernel<128>(k.dtype, qd, cache_dtype);
     // more warps a row while that leaves the SMs under a third of their warps (512 rows: one warp a row 12.7 us, four
