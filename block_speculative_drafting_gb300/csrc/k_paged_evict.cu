@@ -24,6 +24,8 @@ constexpr int kEvThreads = 1024, kEvWarps = kEvThreads / 32, kEvBins = 2048;
 // larger keys for larger weights; NaN counts as -inf, the zeros as one
 DF_DEV uint32_t ev_key(float w) { return float_order_key(w != w ? -INFINITY : w == 0.f ? 0.f : w); }
 
+constexpr int kEvRound = 4 * kEvThreads;  // tokens of a round: a warp 128 in a row, four a lane
+
 __global__ void __launch_bounds__(kEvThreads) paged_evict_select_kernel(const __grid_constant__ EvictArgs A) {
     __shared__ uint32_t hist[kEvBins];
     __shared__ uint32_t sums[kEvWarps];
@@ -84,19 +86,18 @@ __global__ void __launch_bounds__(kEvThreads) paged_evict_select_kernel(const __
         border = prefix;
         ties = need;
     }
-    // the slots that stay, in order: a warp 128 at a time, four ballots
+    // the slots that stay, in order
     uint32_t over = 0, at = 0;  // tokens before this round over the border (or kept in any case), and at it
     int buf = 0;
-    for (int base = 0; base < L; base += 4 * kEvThreads, buf ^= 1) {
+    auto round = [&](int base, const uint32_t (&key)[4]) {
         const int i0 = base + warp * 128 + lane;
         uint32_t go[4], ge[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int i = i0 + 32 * k;
             const bool mid = i >= lo && i < hi;
-            const uint32_t key = mid ? ev_key(w[i]) : 0u;
-            go[k] = __ballot_sync(0xffffffffu, i < L && (!mid || key > border));
-            ge[k] = __ballot_sync(0xffffffffu, mid && key == border && ties > 0);
+            go[k] = __ballot_sync(0xffffffffu, i < L && (!mid || key[k] > border));
+            ge[k] = __ballot_sync(0xffffffffu, mid && key[k] == border && ties > 0);
         }
         const uint32_t no = __popc(go[0]) + __popc(go[1]) + __popc(go[2]) + __popc(go[3]);
         const uint32_t ne = __popc(ge[0]) + __popc(ge[1]) + __popc(ge[2]) + __popc(ge[3]);
@@ -117,38 +118,58 @@ __global__ void __launch_bounds__(kEvThreads) paged_evict_select_kernel(const __
             o += __popc(go[k]);
             e += __popc(ge[k]);
         }
+        buf ^= 1;
+    };
+#pragma unroll 1
+    for (int base = 0; base < L; base += kEvRound) {
+        uint32_t key[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = base + warp * 128 + lane + 32 * k;
+            key[k] = i >= lo && i < hi ? ev_key(w[i]) : 0u;
+        }
+        round(base, key);
     }
 }
 
-constexpr int kMvThreads = 256, kMvRound = 4;  // vectors a thread and round
+constexpr int kMvRound = 4;  // vectors a thread and round
 
-// One head's kept rows of one tensor, `VR` vectors of type V a row from column `col` on: round by round.
-template <class V, int VR, class From, class To>
+// One head's kept rows of one tensor, `VR` vectors of type V a row from column `col` on: round by round, by T threads.
+template <class V, int VR, int T, class From, class To>
 DF_DEV void ev_move(const int32_t* kept, int count, From from, To to) {
-    constexpr int RR = kMvThreads * kMvRound / VR;  // rows of a round
+    constexpr int RR = T * kMvRound / VR;  // rows of a round
     const int t = threadIdx.x, c = t % VR;
     V x[2][kMvRound];
     bool on[2][kMvRound];
+    int src[kMvRound];  // the next round's slots, read a round ahead
+    auto slots = [&](int round) {
+#pragma unroll
+        for (int k = 0; k < kMvRound; ++k) {
+            const int i = round * RR + k * (T / VR) + t / VR;
+            src[k] = i < count ? kept[i] : -1;
+        }
+    };
     auto load = [&](int round, int b) {
 #pragma unroll
         for (int k = 0; k < kMvRound; ++k) {
-            const int i = round * RR + k * (kMvThreads / VR) + t / VR;
-            const int src = i < count ? kept[i] : -1;
-            const V* p = src > i ? from(src, c) : nullptr;
+            const int i = round * RR + k * (T / VR) + t / VR;
+            const V* p = src[k] > i ? from(src[k], c) : nullptr;
             on[b][k] = p != nullptr;
             if (p != nullptr) x[b][k] = *p;
         }
+        slots(round + 1);
     };
     auto store = [&](int round, int b) {
 #pragma unroll
         for (int k = 0; k < kMvRound; ++k) {
-            const int i = round * RR + k * (kMvThreads / VR) + t / VR;
+            const int i = round * RR + k * (T / VR) + t / VR;
             if (!on[b][k]) continue;
             V* p = to(i, c);
             if (p != nullptr) *p = x[b][k];
         }
     };
     const int rounds = (count + RR - 1) / RR;
+    slots(0);
     load(0, 0);
 #pragma unroll 1
     for (int r = 0; r < rounds; r += 2) {
@@ -161,9 +182,9 @@ DF_DEV void ev_move(const int32_t* kept, int count, From from, To to) {
     }
 }
 
-// RB: bytes of a row; SB: of a slice of it
-template <int RB, int SB>
-__global__ void __launch_bounds__(kMvThreads) paged_evict_move_kernel(const __grid_constant__ EvictArgs A, int block_bytes) {
+// RB: bytes of a row; SB: of a slice of it; T: threads
+template <int RB, int SB, int T>
+__global__ void __launch_bounds__(T) paged_evict_move_kernel(const __grid_constant__ EvictArgs A, int block_bytes) {
     constexpr int SL = RB / SB, JOBS = 2 * SL + 1;
     pdl_wait();
     pdl_trigger();
@@ -188,17 +209,28 @@ __global__ void __launch_bounds__(kMvThreads) paged_evict_move_kernel(const __gr
         const int64_t* st = job < SL ? A.C.ks : A.C.vs;
         const int64_t col = (int64_t)(job % SL) * SB;
         auto at = [&](int i, int c) { return reinterpret_cast<uint4*>(place(base, st, i, col + 16 * c)); };
-        ev_move<uint4, SB / 16>(kept, count, at, at);
+        ev_move<uint4, SB / 16, T>(kept, count, at, at);
         return;
     }
     const float* in = A.in.p + (int64_t)s * A.in.ss + (int64_t)h * A.in.hs;
     float* out = A.out.p + (int64_t)s * A.out.ss + (int64_t)h * A.out.hs;
     if (aside) {
-        for (int i = threadIdx.x; i < count; i += kMvThreads) out[i] = in[kept[i]];
+#pragma unroll 1
+        for (int i0 = threadIdx.x; i0 < count; i0 += 8 * T) {
+            int j[8];
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) j[k] = i0 + k * T < count ? kept[i0 + k * T] : 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = in[j[k]];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i0 + k * T < count) out[i0 + k * T] = x[k];
+        }
         if (len.x == len.y) return;
     } else {
         auto at = [&](int i, int) { return out + i; };
-        ev_move<float, 1>(kept, count, at, at);
+        ev_move<float, 1, T>(kept, count, at, at);
     }
     for (int side = 0; side < 2 && block_bytes > 0; ++side) {
         unsigned char* base = side == 0 ? A.C.kb : A.C.vb;
@@ -206,10 +238,10 @@ __global__ void __launch_bounds__(kMvThreads) paged_evict_move_kernel(const __gr
         __syncthreads();
         if (block_bytes == 8) {
             auto at = [&](int i, int) { return reinterpret_cast<uint2*>(place(base, st, i, 0)); };
-            ev_move<uint2, 1>(kept, count, at, at);
+            ev_move<uint2, 1, T>(kept, count, at, at);
         } else {
             auto at = [&](int i, int) { return reinterpret_cast<uint32_t*>(place(base, st, i, 0)); };
-            ev_move<uint32_t, 1>(kept, count, at, at);
+            ev_move<uint32_t, 1, T>(kept, count, at, at);
         }
     }
 }
@@ -219,11 +251,18 @@ int64_t paged_evict_workspace(int n_seqs, int kv_heads, int keep, bool own_kept)
     return lens + (own_kept ? (int64_t)n_seqs * kv_heads * keep * 4 : 0);
 }
 
-template <int RB, int SB>
-static int ev_launch(const EvictArgs& A, int block_bytes, cudaStream_t st) {
+// Few heads: each one's rows over as many CTAs as have a sector of 32 bytes each, of 1024 threads (eight heads of 32768
+// tokens, 256 bytes a row, cut to half: 175 us with slices of 64 bytes and 256 threads, 38 so); many: a CTA a tensor.
+template <int RB>
+static int ev_launch(const EvictArgs& A, int block_bytes, int num_sms, cudaStream_t st) {
     const int64_t units = (int64_t)A.R.n_seqs * A.C.kv_heads;
-    return (int)launch(paged_evict_move_kernel<RB, SB>, dim3((unsigned)(units * (2 * (RB / SB) + 1))), dim3(kMvThreads), 0,
-                       st, A, block_bytes);
+    if (units * 3 < num_sms) {
+        constexpr int T = 1024;
+        return (int)launch(paged_evict_move_kernel<RB, 32, T>, dim3((unsigned)(units * (2 * (RB / 32) + 1))), dim3(T), 0, st,
+                           A, block_bytes);
+    }
+    constexpr int T = 512;
+    return (int)launch(paged_evict_move_kernel<RB, RB, T>, dim3((unsigned)(units * 3)), dim3(T), 0, st, A, block_bytes);
 }
 
 int paged_evict(const EvictArgs& A, int cache_dtype, int hd, int num_sms, cudaStream_t st) {
@@ -232,11 +271,10 @@ int paged_evict(const EvictArgs& A, int cache_dtype, int hd, int num_sms, cudaSt
     if (e != 0) return e;
     const int rb = cache_dtype == kE2M1 ? hd / 2 : cache_dtype == kE4M3 ? hd : 2 * hd;
     const int bb = cache_dtype == kE2M1 ? hd / 16 : 0;
-    const bool few = units * 2 < 2 * num_sms;  // one head's rows over several CTAs
-    if (rb == 256) return few ? ev_launch<256, 64>(A, bb, st) : ev_launch<256, 256>(A, bb, st);
-    if (rb == 128) return few ? ev_launch<128, 32>(A, bb, st) : ev_launch<128, 128>(A, bb, st);
-    if (rb == 64) return few ? ev_launch<64, 32>(A, bb, st) : ev_launch<64, 64>(A, bb, st);
-    return ev_launch<32, 32>(A, bb, st);
+    return rb == 256   ? ev_launch<256>(A, bb, num_sms, st)
+           : rb == 128 ? ev_launch<128>(A, bb, num_sms, st)
+           : rb == 64  ? ev_launch<64>(A, bb, num_sms, st)
+                       : ev_launch<32>(A, bb, num_sms, st);
 }
 
 }  // namespace dflash
