@@ -25,7 +25,8 @@ BINDING = os.path.join(PKG, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX")
 BOUND_FOR = os.path.join(BUILD, "binding.txt")
 SOURCES = ["api.cu", "k_quant.cu", "k_gemm.cu", "k_layer.cu", "k_stream.cu", "k_tc.cu", "k_tc_pair.cu",
            "k_attn_tc.cu", "ops.cu", "k_paged_append.cu", "k_paged_attn.cu", "k_paged_attn_tc.cu", "k_paged_attn4.cu",
-           "k_paged_weights.cu", "k_paged_evict.cu", "k_verify.cu"]
+           "k_paged_weights.cu", "k_paged_weights_few.cu",
+           "k_paged_evict.cu", "k_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", os.path.join(ROOT, "include")]

@@ -252,7 +252,7 @@ int dflash_paged_key_weights(const dflash_paged_cache* cache, const dflash_paged
     if (window < 0 || window > 1 << 30) return fail(DFLASH_EINVAL, "window %d", window);
     if (!al4(lse) || (lse == nullptr && R.n_rows > 0)) return fail(DFLASH_EINVAL, "lse is NULL or not 4-byte aligned");
     TRY(check_weights(weights, "weights", R, &W));
-    if (!pa_line_fits(R, q->heads, cache->kv_heads, cache->dtype))
+    if (!pa_line_fits(R, q->heads, cache->kv_heads, DFLASH_E2M1))
         return fail(DFLASH_EINVAL, "%d sequences of %d positions: too many tiles of keys", R.n_seqs, R.cap);
     if (R.n_rows == 0) return DFLASH_OK;
     int n = 0;

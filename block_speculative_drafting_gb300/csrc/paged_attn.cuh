@@ -287,5 +287,8 @@ constexpr int kPtOver = 4;
 int paged_attention_tc(const PaArgs& A, int cache_dtype, int hd, int mt, int num_sms, cudaStream_t st);
 // The warp-MMA kernel of the 4-bit cache (k_paged_attn4.cu): units of up to mt = 8 or 16 rows.
 int paged_attention4(const PaArgs& A, int hd, int mt, int num_sms, cudaStream_t st);
+// The warp-MMA kernel of the key weights (k_paged_weights_few.cu).
+int paged_key_weights_few(const PaArgs& A, const KeyWeights& W, const float* lse, int cache_dtype, int hd, int num_sms,
+                          cudaStream_t st);
 
 }  // namespace dflash
