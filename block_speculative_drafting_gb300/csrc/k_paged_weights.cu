@@ -703,24 +703,27 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
                     if (ok && plain && (ctl.dead[qs][0] | ctl.dead[qs][1]) == 0) {
                         const uint64_t cs0 = pw_pair2(ctl.c[qs][0], ctl.c[qs][0]);
                         uint64_t part[2] = {0, 0};
-#pragma unroll 1
-                        for (int x = 0; x < kPwN; x += 64) {
-                            uint32_t v[64];
-                            pt_ld32(from + x, *reinterpret_cast<uint32_t(*)[32]>(v));
-                            pt_ld32(from + x + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+                        // 32 columns at a time, the next ones on their way meanwhile
+                        uint32_t v[2][32];
+                        pt_ld32(from, v[0]);
+#pragma unroll
+                        for (int x = 0; x < kPwN / 32; ++x) {
                             at_wait_ld();
-                            if (x + 64 == kPwN) {
+                            if (x + 1 < kPwN / 32) {
+                                pt_ld32(from + 32 * (x + 1), v[(x + 1) & 1]);
+                            } else {
                                 at_fence_before();
                                 __syncwarp();
                                 if (lane == 0) mbar_arrive(&ctl.d_empty[buf]);
                             }
+                            const uint32_t(&w)[32] = v[x & 1];
 #pragma unroll
-                            for (int y = 0; y < 64; y += 4) {
-                                const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(&ctl.nl[qs][x + y]);
+                            for (int y = 0; y < 32; y += 4) {
+                                const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(&ctl.nl[qs][32 * x + y]);
                                 ulonglong2 cs = make_ulonglong2(cs0, cs0);  // (16-bit queries: one scale)
-                                if constexpr (E8) cs = *reinterpret_cast<const ulonglong2*>(&ctl.c[qs][x + y]);
-                                pw_add2(part[0], pw_exp2(pw_fma2(pw_pair2(v[y], v[y + 1]), cs.x, nl.x)));
-                                pw_add2(part[1], pw_exp2(pw_fma2(pw_pair2(v[y + 2], v[y + 3]), cs.y, nl.y)));
+                                if constexpr (E8) cs = *reinterpret_cast<const ulonglong2*>(&ctl.c[qs][32 * x + y]);
+                                pw_add2(part[0], pw_exp2(pw_fma2(pw_pair2(w[y], w[y + 1]), cs.x, nl.x)));
+                                pw_add2(part[1], pw_exp2(pw_fma2(pw_pair2(w[y + 2], w[y + 3]), cs.y, nl.y)));
                             }
                         }
 #pragma unroll
