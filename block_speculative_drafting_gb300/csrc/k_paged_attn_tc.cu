@@ -106,14 +106,6 @@ DF_DEV uint32_t pt_ld1(uint32_t taddr) {
 DF_DEV void pt_st16(uint32_t taddr, const uint32_t (&w)[16]) {
     at_st16(taddr, *reinterpret_cast<const float(*)[16]>(w));
 }
-// at_mma_ts by the one lane with `on` (as pt_commit)
-DF_DEV void pt_mma(bool on, uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"((uint32_t)on)
-        : "memory");
-}
 // named barrier 1: the softmax threads
 DF_DEV void pt_soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kPtSoft) : "memory"); }
 DF_DEV bool pt_soft_or(bool v) {
@@ -387,7 +379,6 @@ __global__ void __launch_bounds__((PtShape<BF, CB, HD>::kThreads), 1)
         // three or four MMAs of the pipe, and one warp's waits left the pipe idle for 0.6 us a tile.
         // (whole-warp values, said so to the compiler: see pt_mma)
         auto whole_warp = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-        const bool on = lane == 0;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         constexpr uint32_t kType = PB ? (1u << 7) | (1u << 10) : 0u;  // A, B: bf16, or f16
         constexpr uint64_t kItemD = S::kItem >> 4;
@@ -410,15 +401,19 @@ __global__ void __launch_bounds__((PtShape<BF, CB, HD>::kThreads), 1)
                     fence_proxy_async_smem();
                     at_fence_after();
                     const uint64_t kd = dk0 + (uint64_t)slot * kItemD;
+                    if (pt_elect()) {
 #pragma unroll
-                    for (int j = 0; j < HD / 16; ++j)
-                        pt_mma(on, tm + S::kColS + (tg & 1) * 128, tm + (uint32_t)(S::kColQ + 8 * j),
-                               kd + (uint64_t)(((j >> 2) * (kPaTile * 128) + (j & 3) * 32) >> 4), idS, j > 0 ? 1u : 0u);
-                    pt_commit(on, &ctl.empty[0][slot]);
-                    pt_commit(on, &ctl.s_full[tg & 1]);
-                    if (on) mbar_arrive(&ctl.s_full[tg & 1]);
+                        for (int j = 0; j < HD / 16; ++j)
+                            at_mma_ts(tm + S::kColS + (tg & 1) * 128, tm + (uint32_t)(S::kColQ + 8 * j),
+                                      kd + (uint64_t)(((j >> 2) * (kPaTile * 128) + (j & 3) * 32) >> 4), idS, j > 0 ? 1u : 0u);
+                        at_commit(&ctl.empty[0][slot]);
+                        at_commit(&ctl.s_full[tg & 1]);
+                        mbar_arrive(&ctl.s_full[tg & 1]);
+                    }
+                    __syncwarp();
                 }
-                if (S::kQueryWarps > 0) pt_commit(on, &ctl.q_free);
+                if (S::kQueryWarps > 0 && pt_elect()) at_commit(&ctl.q_free);
+                __syncwarp();
             } else {
                 constexpr uint32_t idO = at_idesc(kPtM, HD, true) | kType;
                 const uint64_t dv0 = at_desc(smem_addr(ring) + S::kSlots * S::kItem, kPaTile * 128);
@@ -428,23 +423,27 @@ __global__ void __launch_bounds__((PtShape<BF, CB, HD>::kThreads), 1)
                     fence_proxy_async_smem();
                     at_fence_after();
                     const uint64_t vd = dv0 + (uint64_t)slot * kItemD;
+                    if (pt_elect()) {
 #pragma unroll
-                    for (int j = 0; j < kPaTile / 16; ++j) {
-                        // keys 16 j ..: eight columns of P, hi, and sixteen columns on its lo
-                        const uint32_t p = tm + (uint32_t)(S::kColS + (tg & 1) * 128 + 32 * (j >> 1) + 8 * (j & 1));
-                        const uint64_t v = vd + (uint64_t)((j * 2048) >> 4);
-                        pt_mma(on, tm + S::kColO, p, v, idO, 1u);
-                        if constexpr (S::kSplitP) pt_mma(on, tm + S::kColO, p + 16, v, idO, 1u);
+                        for (int j = 0; j < kPaTile / 16; ++j) {
+                            // keys 16 j ..: eight columns of P, hi, and sixteen columns on its lo
+                            const uint32_t p = tm + (uint32_t)(S::kColS + (tg & 1) * 128 + 32 * (j >> 1) + 8 * (j & 1));
+                            const uint64_t v = vd + (uint64_t)((j * 2048) >> 4);
+                            at_mma_ts(tm + S::kColO, p, v, idO, 1u);
+                            if constexpr (S::kSplitP) at_mma_ts(tm + S::kColO, p + 16, v, idO, 1u);
+                        }
+                        at_commit(&ctl.empty[1][slot]);
+                        at_commit(&ctl.o_done[tg & 1]);
                     }
-                    pt_commit(on, &ctl.empty[1][slot]);
-                    pt_commit(on, &ctl.o_done[tg & 1]);
+                    __syncwarp();
                 }
             }
             ++unit;
             pt_skip<MT>(A, c, tiles);
         }
         // every MMA issued has completed before the CTA moves on
-        pt_commit(on, &ctl.fin[warp - kPtQk]);
+        if (pt_elect()) at_commit(&ctl.fin[warp - kPtQk]);
+        __syncwarp();
         mbar_wait(&ctl.fin[warp - kPtQk], 0, kPtWait);
         __syncwarp();
     } else {

@@ -254,20 +254,13 @@ DF_DEV bool pw_wait(uint64_t* bar, int phase) {
     return __all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1)) || pw_wait_long(bar, phase & 1);
 }
 
-// kind::f16 products of two shared-memory operands, and of a tensor-memory operand with a shared-memory one; by one
-// lane that elect.sync chose: under that branch the compiler keeps the operands in uniform registers (an MMA of N 64
-// goes out every 32 clocks, its own time; predicated on a lane's number it took 59)
+// kind::f16 products of two shared-memory operands (by pt_elect's lane)
 DF_DEV void pw_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-DF_DEV bool pw_elect() {
-    uint32_t on;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(on));
-    return on != 0;
 }
 // pairs of f32 in one register pair
 DF_DEV uint64_t pw_pair2(uint32_t a, uint32_t b) {
@@ -579,7 +572,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
                 if (ok && i < nt) {
                     if (stays) {
                         ok = pw_wait(&ctl.stay[i], sn[i]++);
-                        if (pw_elect()) mbar_arrive(&ctl.k_empty[(kn + i) % S::kSlots]);
+                        if (pt_elect()) mbar_arrive(&ctl.k_empty[(kn + i) % S::kSlots]);
                     } else {
                         ok = pw_wait(&ctl.k_full[(kn + i) % S::kSlots], (kn + i) / S::kSlots);
                     }
@@ -601,7 +594,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
                         at_fence_after();
                         const uint32_t d = tm + (uint32_t)(S::kColS + buf * kPwN);
                         const uint64_t kd = dk0 + (uint64_t)(((kn + i) % S::kSlots) * (S::kItem >> 4));
-                        if (pw_elect()) {
+                        if (pt_elect()) {
                             if (stays) {
 #pragma unroll
                                 for (int j = 0; j < HD / 16; ++j)
@@ -619,9 +612,9 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
                         }
                         __syncwarp();
                     }
-                if ((qt < qe || !keeps) && pw_elect()) at_commit(&ctl.q_empty[qs]);
+                if ((qt < qe || !keeps) && pt_elect()) at_commit(&ctl.q_empty[qs]);
             }
-            if (!stays && pw_elect())
+            if (!stays && pt_elect())
                 for (int i = 0; i < nt; ++i) at_commit(&ctl.k_empty[(kn + i) % S::kSlots]);
             __syncwarp();
             kn += nt;
@@ -629,7 +622,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
             c = nx;
         }
         // every MMA issued has completed before the CTA moves on
-        if (pw_elect()) at_commit(&ctl.fin);
+        if (pt_elect()) at_commit(&ctl.fin);
         __syncwarp();
         mbar_wait(&ctl.fin, 0, kPwWait);
         __syncwarp();

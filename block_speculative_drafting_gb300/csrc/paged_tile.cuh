@@ -42,14 +42,13 @@ DF_DEV void tile_place(unsigned char* dst, int key, int ch, const uint4& x, uint
     }
 }
 
-// tcgen05 operations of the one lane with `on`, in code that the whole warp runs: the operands then stay in uniform
-// registers (issued under a divergent branch, each MMA took 60 ns to put together, twice its work)
-DF_DEV void pt_commit(bool on, uint64_t* bar) {
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar)),
-        "r"((uint32_t)on)
-        : "memory");
+// The lane that issues a warp's tcgen05 operations: under this branch the compiler keeps their operands in uniform
+// registers (an MMA of M 128 and N 64 then goes out every 32 clocks, its own time; predicated on a lane's number it took
+// 59, under a branch on it longer).  The same lane each time.
+DF_DEV bool pt_elect() {
+    uint32_t on;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(on));
+    return on != 0;
 }
 DF_DEV void pt_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
