@@ -322,8 +322,9 @@ __global__ void __launch_bounds__((PtShape<BF, CB, HD>::kThreads), 1)
             });
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
-            constexpr int CH = S::kRawCh, RPI = 32 / CH, LD = S::kRawLd;  // copies of a lane a half tile
-            const int ch = lane % CH;
+            using Lanes = TileLanes<CB, HD>;
+            constexpr int RPI = Lanes::RPI, LD = S::kRawLd;  // copies of a lane a half tile
+            const int ch = Lanes::place(lane), lane_row = Lanes::row(lane);
             const int self = threadIdx.x - kPtLoad * 32;
             unsigned char* raw = ring + 2 * S::kSlots * S::kItem + self * 16;
             unsigned char* raw_scale = ring + 2 * S::kSlots * S::kItem + S::kRawCodes + self * 4;
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__((PtShape<BF, CB, HD>::kThreads), 1)
                 unsigned char* dst = slots + slot * S::kItem;
 #pragma unroll
                 for (int i = 0; i < LD; ++i) {
-                    const int key = lw * S::KPW + ((half & 1) * LD + i) * RPI + lane / CH;
+                    const int key = lw * S::KPW + ((half & 1) * LD + i) * RPI + lane_row;
                     const uint4 x = *reinterpret_cast<const uint4*>(raw + ((half % S::kRaw) * LD + i) * kPlace);
                     uint32_t scales = 0;
                     if constexpr (CB == 4)
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__((PtShape<BF, CB, HD>::kThreads), 1)
                     const int half = 2 * n + hf;
 #pragma unroll
                     for (int i = 0; i < LD; ++i) {
-                        const int r = (hf * LD + i) * RPI + lane / CH;
+                        const int r = (hf * LD + i) * RPI + lane_row;
                         const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(rows), r);
                         const void* src = p ? reinterpret_cast<const unsigned char*>(p) + 16 * ch : A.q.p;  // (nothing is read)
                         cp16(smem_addr(raw) + ((half % S::kRaw) * LD + i) * kPlace, src, p ? 16 : 0);

@@ -395,8 +395,9 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
             });
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
-            constexpr int CH = S::kRawCh, RPI = 32 / CH, LD = S::kRawLd;  // copies of a lane a tile
-            const int ch = lane % CH, self = threadIdx.x - kPwKeys * 32;
+            using Lanes = TileLanes<CB, HD>;
+            constexpr int RPI = Lanes::RPI, LD = S::kRawLd;  // copies of a lane a tile
+            const int ch = Lanes::place(lane), lane_row = Lanes::row(lane), self = threadIdx.x - kPwKeys * 32;
             unsigned char *raw = rawring + self * 16, *raw_scale = rawring + S::kRawCodes + self * 4;
             constexpr int kPlace = S::kLoaders * 16;  // from one of a thread's places to the next
             auto write = [&](int tile) -> bool {
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
                 if (!wait_empty(tile)) return false;
 #pragma unroll
                 for (int i = 0; i < LD; ++i) {
-                    const int key = lw * S::KPW + i * RPI + lane / CH;
+                    const int key = lw * S::KPW + i * RPI + lane_row;
                     const uint4 x = *reinterpret_cast<const uint4*>(raw + ((tile % S::kRaw) * LD + i) * kPlace);
                     uint32_t scales = 0;
                     if constexpr (CB == 4)
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
             walk([&](const unsigned char* rows, const unsigned char* blocks) -> bool {
 #pragma unroll
                 for (int i = 0; i < LD; ++i) {
-                    const int r = i * RPI + lane / CH;
+                    const int r = i * RPI + lane_row;
                     const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(rows), r);
                     const void* src = p ? reinterpret_cast<const unsigned char*>(p) + 16 * ch : A.q.p;  // (nothing is read)
                     cp16(smem_addr(raw) + ((n % S::kRaw) * LD + i) * kPlace, src, p ? 16 : 0);

@@ -7,27 +7,34 @@
 
 namespace dflash {
 
+// The lanes of a warp over rows of CH places of 16 bytes: which row and place of an instruction's 32 / CH rows is a
+// lane's.  e2m1 codes, whose places become four chunks, have a row a lane first: lanes of a quarter warp then store one
+// chunk of eight rows, which are in different banks; e4m3 codes a place first, and the upper half's chunks in the other order.
+template <int CB, int HD>
+struct TileLanes {
+    static constexpr int CH = HD * CB / 128, RPI = 32 / CH;
+    static DF_DEV int row(int lane) { return CB == 4 ? lane % RPI : lane / CH; }
+    static DF_DEV int place(int lane) { return CB == 4 ? lane / RPI : lane % CH; }
+};
 // Sixteen bytes of codes (place `ch` of row `key`: 16 e4m3 or 32 e2m1 codes) as f16 (exact) in a tile at dst.  `scales`:
 // an e2m1 place's two block scales, e4m3 bytes (code times block scale is exact too: 2 bits times 4).
-// Places of a row's upper half write their chunks in another order: other banks.
 template <int CB, int HD>
 DF_DEV void tile_place(unsigned char* dst, int key, int ch, const uint4& x, uint32_t scales) {
     constexpr int CH = HD * CB / 128;  // places of a row
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    auto put = [&](int chunk, const uint4& v) {
-        *reinterpret_cast<uint4*>(dst + (chunk >> 3) * (kPaTile * 128) + at_swz(key, chunk & 7)) = v;
-    };
     if constexpr (CB == 4) {
         const uint32_t s2 = e4m3x2_f16x2(scales);
-        const int flip = ch >= CH / 2 ? 2 : 0;
+        // chunks 4 ch .. of the row: they differ in bits 4 and 5 of the swizzled place
+        const uint32_t at = smem_addr(dst) + (ch >> 1) * (kPaTile * 128) + at_swz(key, 4 * (ch & 1));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             // a word: eight columns of one block
-            const int up = j ^ flip;
-            const uint32_t word = flip ? w[j ^ 2] : w[j], s1 = __byte_perm(s2, 0, (up >> 1) ? 0x3232 : 0x1010);
+            const uint32_t s1 = __byte_perm(s2, 0, j >> 1 ? 0x3232 : 0x1010);
             uint32_t y[4];
-            e2m1x8_f16x8(word, y);
-            put(4 * ch + up, make_uint4(mul_f16x2(y[0], s1), mul_f16x2(y[1], s1), mul_f16x2(y[2], s1), mul_f16x2(y[3], s1)));
+            e2m1x8_f16x8(w[j], y);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at ^ (16 * j)), "r"(mul_f16x2(y[0], s1)), "r"(mul_f16x2(y[1], s1)),
+                         "r"(mul_f16x2(y[2], s1)), "r"(mul_f16x2(y[3], s1))
+                         : "memory");
         }
     } else {
         uint32_t y[8];
@@ -36,8 +43,9 @@ DF_DEV void tile_place(unsigned char* dst, int key, int ch, const uint4& x, uint
         const bool flip = ch >= CH / 2;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int up = flip ? 1 - j : j;
-            put(2 * ch + up, up ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]));
+            const int up = flip ? 1 - j : j, chunk = 2 * ch + up;
+            const uint4 v = up ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(dst + (chunk >> 3) * (kPaTile * 128) + at_swz(key, chunk & 7)) = v;
         }
     }
 }
