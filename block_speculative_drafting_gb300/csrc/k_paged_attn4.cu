@@ -100,7 +100,7 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
     constexpr int W = S::W, NST = S::NST, CH = S::CH, SB = S::SB, MT = 8 * NT, SW = SB / 4;
     extern __shared__ __align__(128) unsigned char sm[];
     __shared__ uint32_t vbits[W][NST];  // a stage's held keys
-    __shared__ float2 ml[2][W][MT];
+    __shared__ float2 ml[2][W][MT], sums[W][MT];  // the warps' references and sums at a unit's end, and those to one reference
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
     const uint32_t base = smem_addr(sm) + warp * NST * S::kStage;
     float* merge = reinterpret_cast<float*>(sm + (size_t)W * NST * S::kStage);
@@ -118,6 +118,22 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
         c.tile += n - 1;
         pa_next<kP4Keys>(A, MT, c);
     };
+
+    // Queries of row gq (and gq + 8), columns 32 j + 8 tq .., as they are: fetched before the first copies, and as the unit
+    // before ends.
+    uint4 qf[NT][CH];
+    auto fetch = [&](const PaCur& c) {
+        const int h = c.u % A.C.kv_heads, rt = c.u / A.C.kv_heads;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int mm = rt * MT + gq + 8 * n, r = mm / A.group, hq = h * A.group + mm - r * A.group;
+            const unsigned char* p = A.q.p + (int64_t)(c.q.row0 + r) * A.q.rs + (int64_t)hq * A.q.hs + 16 * tq;
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+                qf[n][j] = mm < c.q.rows * A.group ? *reinterpret_cast<const uint4*>(p + 64 * j) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    fetch(cur);
 
     // ---------------------------------------------------------------- copies
     // Lane l holds the place of a stage's key l; `ahead` belongs to the stage to copy next.
@@ -194,47 +210,32 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
         const int tiles = tiles_of(unit);
         const int h = unit.u % A.C.kv_heads, rt = unit.u / A.C.kv_heads;
         const int mvalid = min(MT, sq.rows * A.group - rt * MT);
-        // queries: of row gq (and gq + 8) columns 32 c + 8 tq .., in f16, by a power of two where they are bf16
-        uint4 qf[NT][CH];
+        // the queries in f16, by a power of two where they are bf16
         float c[NT][2];  // scores of rows 2 tq, 2 tq + 1 in log2 units: S c; never 0, so that -inf stays -inf
         const float ks = A.scale_log2 * (A.C.k_scale != nullptr ? A.C.k_scale[h] : 1.f);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int m = gq + 8 * n, mm = rt * MT + m, r = mm / A.group, hq = h * A.group + mm % A.group;
-            const bool in = m < mvalid;
-            const unsigned char* p = A.q.p + (int64_t)(sq.row0 + r) * A.q.rs + (int64_t)hq * A.q.hs;
-            const bool qb = A.q.dtype == kBF16;
-            float mx = 0.f;
+            float rf = 1.f;
+            if (A.q.dtype == kBF16) {
+                // a row times 2^-x, its largest element in [1, 2): what f16 cannot hold of it then is under 2^-25 of that
+                uint32_t(&w)[4 * CH] = *reinterpret_cast<uint32_t(*)[4 * CH]>(qf[n]);
+                float mx = 0.f, down = 1.f;
 #pragma unroll
-            for (int j = 0; j < CH; ++j) {
-                qf[n][j] = in ? *reinterpret_cast<const uint4*>(p + 64 * j + 16 * tq) : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t w[4] = {qf[n][j].x, qf[n][j].y, qf[n][j].z, qf[n][j].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4 * CH; ++i) {
                     const float2 f = unpack2<true>(w[i]);
                     mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
                 }
-            }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            float rf = 1.f;
-            if (qb) {
-                // a row times 2^-x, its largest element in [1, 2): what f16 cannot hold of it then is under 2^-25 of that
-                float down = 1.f;
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 if (mx > 0.f && mx < INFINITY) {
                     const int x = min(max(ilogbf(mx), -120), 120);
                     down = ldexpf(1.f, -x);
                     rf = ldexpf(1.f, x);
                 }
 #pragma unroll
-                for (int j = 0; j < CH; ++j) {
-                    uint32_t w[4] = {qf[n][j].x, qf[n][j].y, qf[n][j].z, qf[n][j].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = unpack2<true>(w[i]);
-                        w[i] = pack2<false>(f.x * down, f.y * down);
-                    }
-                    qf[n][j] = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int i = 0; i < 4 * CH; ++i) {
+                    const float2 f = unpack2<true>(w[i]);
+                    w[i] = pack2<false>(f.x * down, f.y * down);
                 }
             }
 #pragma unroll
@@ -488,40 +489,44 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    // to the largest reference of the warps
                     const int row = 8 * n + 2 * tq + e;
                     float big = -INFINITY;
-#pragma unroll 4
-                    for (int w = 0; w < active; ++w) big = fmaxf(big, part[w][row].x);
-                    const float f = m[n][e] == -INFINITY ? 1.f : pa_exp2(m[n][e] - big);
+#pragma unroll
+                    for (int w = 0; w < W; ++w) big = w < active ? fmaxf(big, part[w][row].x) : big;
+                    const float f = m[n][e] == -INFINITY ? 1.f : pa_exp2(m[n][e] - big);  // (a NaN sum without a maximum stays)
                     float* to = merge + (size_t)(warp * MT + row) * S::kRow + 4 * gq;
 #pragma unroll
                     for (int j = 0; j < CH; ++j)
                         *reinterpret_cast<float4*>(to + 32 * j) = make_float4(o[n][j][0][e] * f, o[n][j][0][2 + e] * f,
                                                                               o[n][j][1][e] * f, o[n][j][1][2 + e] * f);
+                    if (gq == 0) sums[warp][row] = make_float2(big, l[n][e] * f);
                 }
         }
-        __syncthreads();
         const bool whole = unit.tile == 0 && tiles == sq.ntiles;
-        if (!whole && unit.tile == 0 && threadIdx.x == 0)
-            A.ws_join[blockIdx.x] = pa_join_entry(unit, rt, MT, mvalid, h, sq.ntiles - tiles, chunk);
         // a part of a shared unit: its start goes to the CTA's second slot, any other part to the first
         const int slot = blockIdx.x * 2 + (unit.tile == 0 ? 1 : 0);
+        const int row0 = sq.row0;
+        if (!whole && unit.tile == 0 && threadIdx.x == 0)
+            A.ws_join[blockIdx.x] = pa_join_entry(unit, rt, MT, mvalid, h, sq.ntiles - tiles, chunk);
+        skip(cur, tiles);
+        if (cur.left > 0) fetch(cur);
+        __syncthreads();
 #pragma unroll 1
         for (int i = threadIdx.x; i < mvalid * (HD / 4); i += S::kThreads) {
             const int row = i / (HD / 4), col = 4 * (i % (HD / 4));
-            float big = -INFINITY, sum = 0.f;
+            const float big = sums[0][row].x;
+            float sum = 0.f;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int w = 0; w < active; ++w) big = fmaxf(big, part[w][row].x);
-#pragma unroll 4
-            for (int w = 0; w < active; ++w) {
-                const float2 x = part[w][row];
-                sum += x.x == -INFINITY ? x.y : x.y * pa_exp2(x.x - big);  // (a NaN sum without a maximum stays)
-                const float4 z = *reinterpret_cast<const float4*>(merge + (size_t)(w * MT + row) * S::kRow + col);
-                y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
-            }
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                if (w < active) {
+                    const float4 z = *reinterpret_cast<const float4*>(merge + (size_t)(w * MT + row) * S::kRow + col);
+                    y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+                    sum += sums[w][row].y;
+                }
             if (whole) {
-                const int mm = rt * MT + row, r = sq.row0 + mm / A.group, hq = h * A.group + mm % A.group;
+                const int mm = rt * MT + row, r = row0 + mm / A.group, hq = h * A.group + mm % A.group;
                 const float inv = sum == 0.f ? 0.f : (A.C.v_scale != nullptr ? A.C.v_scale[h] : 1.f) / sum;
                 uint2 w;
                 if (A.out.dtype == kBF16)
@@ -537,7 +542,6 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
                 if (col == 0) A.ws_ml[(int64_t)slot * MT + row] = make_float2(big, sum);
             }
         }
-        skip(cur, tiles);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }

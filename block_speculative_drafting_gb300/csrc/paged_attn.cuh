@@ -94,17 +94,19 @@ DF_DEV void rows_of_lane(const PagedRows& R, int s0, int from, int lane, int& a,
 template <int TILE = kPaTile>
 DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
     int64_t t64 = 0, v64 = 0;
-    int w0 = 0, u0 = 0;
+    // (the first 32 sequences are looked at once)
+    PaSeq q0{};
+    int a0 = 0, b0 = 0;
     const int first = A.R.row_start == nullptr ? 0 : row_start_at(A.R, 0);
     for (int s0 = 0, from = first; s0 < A.R.n_seqs; s0 += 32) {
         int a, b;
         rows_of_lane(A.R, s0, from, lane, a, b);
         from = __shfl_sync(0xffffffffu, b, 31);
+        if (s0 == 0) a0 = a, b0 = b;
         if (s0 + lane >= A.R.n_seqs) continue;
         const PaSeq q = pa_seq<TILE>(A, s0 + lane, a, b, mt);
-        const int64_t w = (int64_t)q.ntiles * q.nunits;
-        if (s0 == 0) w0 = (int)w, u0 = q.nunits;
-        t64 = min(t64 + w, (int64_t)1 << 40);
+        if (s0 == 0) q0 = q;
+        t64 = min(t64 + (int64_t)q.ntiles * q.nunits, (int64_t)1 << 40);
         v64 = min(v64 + q.nunits, (int64_t)1 << 40);
     }
     PaCur c{};
@@ -124,13 +126,14 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
     const int t = (int)blockIdx.x * chunk;
     int run = 0;
     for (int s0 = 0, from = first; s0 < A.R.n_seqs; s0 += 32) {
-        int w = w0 + c.ov * u0, a, b;
-        rows_of_lane(A.R, s0, from, lane, a, b);
-        from = __shfl_sync(0xffffffffu, b, 31);
+        PaSeq q = q0;
+        int a = a0, b = b0;
         if (s0 > 0) {
-            const PaSeq q = pa_seq<TILE>(A, min(s0 + lane, A.R.n_seqs - 1), a, b, mt);
-            w = s0 + lane < A.R.n_seqs ? (q.ntiles + c.ov) * q.nunits : 0;
+            rows_of_lane(A.R, s0, from, lane, a, b);
+            q = pa_seq<TILE>(A, min(s0 + lane, A.R.n_seqs - 1), a, b, mt);
         }
+        from = __shfl_sync(0xffffffffu, b, 31);
+        const int w = s0 + lane < A.R.n_seqs ? (q.ntiles + c.ov) * q.nunits : 0;
         int in = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -142,7 +145,13 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
             const int l = __ffs(hit) - 1;
             const int x = t - (run + __shfl_sync(0xffffffffu, in - w, l));
             c.s = s0 + l;
-            c.q = pa_seq<TILE>(A, c.s, __shfl_sync(0xffffffffu, a, l), __shfl_sync(0xffffffffu, b, l), mt);
+            c.q.row0 = __shfl_sync(0xffffffffu, q.row0, l);
+            c.q.rows = __shfl_sync(0xffffffffu, q.rows, l);
+            c.q.p0 = __shfl_sync(0xffffffffu, q.p0, l);
+            c.q.lo = __shfl_sync(0xffffffffu, q.lo, l);
+            c.q.hi = __shfl_sync(0xffffffffu, q.hi, l);
+            c.q.ntiles = __shfl_sync(0xffffffffu, q.ntiles, l);
+            c.q.nunits = __shfl_sync(0xffffffffu, q.nunits, l);
             const int per = c.q.ntiles + c.ov;
             c.u = x / per;
             const int v = x - c.u * per;
