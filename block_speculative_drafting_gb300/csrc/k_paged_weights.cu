@@ -40,7 +40,14 @@ namespace dflash {
 constexpr int kPwSum = 8, kPwMma = 8, kPwQueries = 9, kPwKeys = 12, kPwWarps = 16;  // warps
 constexpr int kPwThreads = kPwWarps * 32, kPwQThreads = (kPwKeys - kPwQueries) * 32;
 constexpr int kPwN = 128, kPwQSlots = 3, kPwScores = 3;  // rows of a query tile, tiles in their ring, score buffers
-constexpr int kPwStay = 3;  // steps from which on a pair of keys goes to tensor memory
+// Barriers on which a half waits for its score buffers, in its own order, and for the end of a pair without a tile for it
+// (else it could run so far ahead that a barrier's last phase but one would look like the one it waits for): more than can be
+// open at once, three buffers and as many pairs' ends as there are query tiles in the ring.
+constexpr int kPwFull = 8;
+// Query tiles from which on a pair of keys goes to tensor memory.  bf16 queries over codes need no conversion then, so for
+// them two (64 rows of four query heads over 32768 e2m1 keys 66 -> 43 us); else three (over bf16 keys
+// 33.9 us from three on, 35.1 from two).
+constexpr int kPwStay = 3, kPwStayMixed = 2;
 constexpr int kPwBits = 32;  // tiles whose key masks are kept: more than the loaders can be ahead of the sums
 constexpr uint64_t kPwWait = 1000000000ull;
 
@@ -51,7 +58,7 @@ struct PwArgs {
     KeyWeights W;
     const float* lse;
     float scale_log2;
-    int window, group;
+    int window, group, stay;
     FastDiv by_group;
 };
 
@@ -76,7 +83,7 @@ struct PwShape {
 };
 
 struct PwCtl {
-    uint64_t k_full[8], k_empty[8], q_full[kPwQSlots], q_empty[kPwQSlots], d_full[kPwScores], d_empty[kPwScores], stay[2], fin;
+    uint64_t k_full[8], k_empty[8], q_full[kPwQSlots], q_empty[kPwQSlots], d_full[2][kPwFull], d_empty[kPwScores], stay[2], fin;
     uint32_t tmem;
     int seq, head, tile, left, row0, rows;  // where this CTA's share begins
     uint32_t bits[kPwBits][4];              // a tile's held keys
@@ -140,10 +147,10 @@ DF_DEV void pw_next(const PwArgs& A, PwCur& c) {
     }
     pw_pair(A, c);
 }
-DF_DEV bool pw_stays(const PwCur& c) { return c.qe - c.qt + 1 >= kPwStay; }
+DF_DEV bool pw_stays(const PwArgs& A, const PwCur& c) { return c.qe - c.qt + 1 >= A.stay; }
 // whether b, the pair after a, begins with the query tile that a ends with (in the form that it has there)
-DF_DEV bool pw_keeps(const PwCur& a, const PwCur& b) {
-    return b.left > 0 && a.s == b.s && a.h == b.h && a.qe == b.qt && pw_stays(a) == pw_stays(b);
+DF_DEV bool pw_keeps(const PwArgs& A, const PwCur& a, const PwCur& b) {
+    return b.left > 0 && a.s == b.s && a.h == b.h && a.qe == b.qt && pw_stays(A, a) == pw_stays(A, b);
 }
 
 // Cost of a head's first k tiles: the query tiles that see each (but for the rounding; with a window all of them, which
@@ -305,10 +312,11 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
             mbar_init(&ctl.q_full[i], 2 * kPwQThreads);  // (the copies, and their threads beside them)
             mbar_init(&ctl.q_empty[i], 1 + kPwSum);
         }
-        for (int i = 0; i < kPwScores; ++i) {
-            // (the commit, and an arrival of the MMA thread's own that orders the key masks)
-            mbar_init(&ctl.d_full[i], 2);
-            mbar_init(&ctl.d_empty[i], 4);
+        for (int i = 0; i < kPwScores; ++i) mbar_init(&ctl.d_empty[i], 4);
+        // (the commit, and an arrival of the MMA thread's own that orders the key masks)
+        for (int i = 0; i < kPwFull; ++i) {
+            mbar_init(&ctl.d_full[0][i], 2);
+            mbar_init(&ctl.d_full[1][i], 2);
         }
         mbar_init(&ctl.stay[0], 4);
         mbar_init(&ctl.stay[1], 4);
@@ -465,10 +473,10 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
         for (PwCur c = cur; ok && c.left > 0;) {
             PwCur nx = c;
             pw_next(A, nx);
-            const bool keeps = pw_keeps(c, nx);
+            const bool keeps = pw_keeps(A, c, nx);
             const float cs = A.scale_log2 * (E8 && A.C.k_scale != nullptr ? A.C.k_scale[c.h] : 1.f);
             const int all = c.q.rows * A.group;
-            const bool qcopy = !mixed || pw_stays(c);
+            const bool qcopy = !mixed || pw_stays(A, c);
             const unsigned char* base = A.q.p + (int64_t)c.q.row0 * A.q.rs + (int64_t)(c.h * A.group) * A.q.hs;
 #pragma unroll 1
             for (int qt = c.qt + (kept ? 1 : 0); qt <= c.qe; ++qt) {
@@ -555,15 +563,15 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t dk0 = at_desc(smem_addr(ring), 16), dq0 = at_desc(smem_addr(qring), 16);
         int kn = 0, qn = 0;       // key tiles before this pair, query tiles so far
-        int dn = 0, sn[2] = {};   // score buffers filled, pairs that stayed of each half
+        int dn = 0, hn[2] = {}, sn[2] = {};  // score buffers filled; of each half what it waits for, and pairs that stayed
         bool ok = true, kept = false;
         PwCur c = cur;
         while (ok && whole_warp((int)(c.left > 0)) != 0) {
             const int nt = whole_warp(c.nt), q0 = whole_warp(c.qt), qe = whole_warp(c.qe);
-            const bool stays = whole_warp((int)pw_stays(c)) != 0;
+            const bool stays = whole_warp((int)pw_stays(A, c)) != 0;
             PwCur nx = c;
             pw_next(A, nx);
-            const bool keeps = whole_warp((int)pw_keeps(c, nx)) != 0;
+            const bool keeps = whole_warp((int)pw_keeps(A, c, nx)) != 0;
             // few columns where the query tile has few rows
             const uint32_t idesc = (whole_warp((int)(c.q.rows * A.group <= 16)) ? at_idesc(128, 16, false)
                                                                                : at_idesc(128, kPwN, false)) |
@@ -607,12 +615,22 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
                                     pw_mma(d, kd + (uint64_t)(((j >> 2) * (kPaTile * 128) + (j & 3) * 32) >> 4),
                                            qd + (uint64_t)(((j >> 2) * (kPwN * 128) + (j & 3) * 32) >> 4), idesc, j > 0 ? 1u : 0u);
                             }
-                            at_commit(&ctl.d_full[buf]);
-                            // (an arrival of this thread's own, which orders the key masks)
-                            mbar_arrive(&ctl.d_full[buf]);
+                            uint64_t* full = &ctl.d_full[i][hn[i] % kPwFull];
+                            at_commit(full);
+                            mbar_arrive(full);  // (an arrival of this thread's own, which orders the key masks)
                         }
+                        ++hn[i];
                         __syncwarp();
                     }
+                if (ok && nt == 1 && qt == qe) {
+                    if (pt_elect()) {
+                        uint64_t* full = &ctl.d_full[1][hn[1] % kPwFull];
+                        at_commit(full);
+                        mbar_arrive(full);
+                    }
+                    ++hn[1];
+                    __syncwarp();
+                }
                 if ((qt < qe || !keeps) && pt_elect()) at_commit(&ctl.q_empty[qs]);
             }
             if (!stays && pt_elect())
@@ -632,21 +650,22 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
         const int half = warp >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         bool ok = true, kept = false;
-        int kn = 0, qn = 0, dn = 0;  // key tiles before this pair, query tiles and score buffers so far
+        int kn = 0, qn = 0;          // key tiles before this pair, query tiles so far
+        int buf0 = 0, hn = 0;        // the next score buffer, this half's waits so far
         PwCur c = cur;
         while (c.left > 0) {
             bool keeps;
             {
                 PwCur nx = c;
                 pw_next(A, nx);
-                keeps = pw_keeps(c, nx);
+                keeps = pw_keeps(A, c, nx);
             }
             const bool mine = half < c.nt;
             const PaSeq& sq = c.q;
             const int kfirst = sq.lo + (c.kt + half) * kPaTile, r = (warp & 3) * 32 + lane, j = kfirst + r;
             float* w = A.W.p + (int64_t)c.s * A.W.ss + (int64_t)c.h * A.W.hs + j;
             const float old = mine && j < sq.hi && j < sq.p0 ? *w : 0.f;  // (a position that the call brings starts at 0)
-            if (mine && pw_stays(c)) {
+            if (mine && pw_stays(A, c)) {
                 // this lane's key to tensor memory (the products that read the one before are done: their sums were taken)
                 const int slot = (kn + half) % S::kSlots;
                 ok = ok && pw_wait(&ctl.k_full[slot], (kn + half) / S::kSlots);
@@ -688,8 +707,9 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
                 // (tiles of the other half too, one by one: a warp that ran ahead would release a tile twice)
                 ok = ok && pw_wait(&ctl.q_full[qs], (qn - 1) / kPwQSlots);
                 if (mine) {
-                    const int buf = (dn + half) % kPwScores;
-                    ok = ok && pw_wait(&ctl.d_full[buf], (dn + half) / kPwScores);
+                    const int buf = buf0 + half < kPwScores ? buf0 + half : buf0 + half - kPwScores;
+                    ok = ok && pw_wait(&ctl.d_full[half][hn % kPwFull], hn / kPwFull);
+                    ++hn;
                     const uint32_t from = lane_addr + S::kColS + buf * kPwN;
                     bool plain = qt >= clear && qt < full;
                     if (A.window > 0) plain = plain && kfirst > sq.p0 + div_by(A.by_group, qt * kPwN + kPwN - 1) - A.window;
@@ -751,7 +771,11 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_weights_kernel(const __gr
                         if (lane == 0) mbar_arrive(&ctl.d_empty[buf]);
                     }
                 }
-                dn += c.nt;
+                if (!mine && qt == c.qe) {
+                    ok = ok && pw_wait(&ctl.d_full[half][hn % kPwFull], hn / kPwFull);
+                    ++hn;
+                }
+                buf0 = buf0 + c.nt < kPwScores ? buf0 + c.nt : buf0 + c.nt - kPwScores;
                 if ((qt < c.qe || !keeps) && lane == 0) mbar_arrive(&ctl.q_empty[qs]);
             }
             const uint32_t held = ctl.bits[(kn + half) % kPwBits][warp & 3];
@@ -792,9 +816,11 @@ int paged_key_weights(const PagedCache& C, int cache_dtype, int hd, const PagedR
     A.C = C, A.R = R, A.q = q, A.W = W, A.lse = lse, A.window = window;
     A.scale_log2 = scale * 1.4426950408889634f;
     A.group = q.heads / C.kv_heads;
+    A.stay = (cache_dtype == kE4M3 || cache_dtype == kE2M1) && q.dtype == kBF16 ? kPwStayMixed : kPwStay;
     A.by_group = fast_div(A.group);
     if (R.cap == 0) return 0;
-    // few rows a sequence's head, on average: the warp MMAs (@FEW@)
+    // few rows a sequence's head, on average: the warp MMAs (over 32768 e2m1 keys of 8 heads, four query heads each:
+    // 16 rows 22 us and 28 below, 20 rows 34 and 30; 32 sequences of 2048 bf16 keys: one row 28 and 39, 16 rows 45 and 42)
     const int64_t per = ((int64_t)R.n_rows + R.n_seqs - 1) / R.n_seqs * A.group;
     if (per <= 64) {
         PaArgs F{};

@@ -115,20 +115,17 @@ def paged_key_weights(weights, q, lse, k_cache, table, kv_len, row_start=None, s
             at = slot_of(table[s], page_size, n_pages, j)
             if at is None:
                 continue
+            first = max(0, j - (L - n))  # the rows that see j
+            past = min(n, j + window - (L - n)) if window else n
             for h in range(kvh):
-                tot = 0.0
-                for i in range(n):
-                    p = L - n + i
-                    if j > p or (window and j <= p - window):
-                        continue
-                    for e in range(h * g, (h + 1) * g):
-                        if lse[a + i, e] == -np.inf:
-                            continue
-                        with np.errstate(all="ignore"):
-                            w = np.exp(scale * (q[a + i, e] @ k_cache[at[0], at[1], h]) - lse[a + i, e])
-                        tot += w
-                        amp[s, h, j] += w * scale * (np.abs(q[a + i, e]) @ np.abs(k_cache[at[0], at[1], h]))
-                out[s, h, j] = tot + (out[s, h, j] if j < L - n else 0.0)
+                rows = q[a + first:a + max(first, past), h * g:(h + 1) * g].reshape(-1, hd)
+                ls = np.asarray(lse, np.float64)[a + first:a + max(first, past), h * g:(h + 1) * g].reshape(-1)
+                rows, ls = rows[ls != -np.inf], ls[ls != -np.inf]
+                key = k_cache[at[0], at[1], h]
+                with np.errstate(all="ignore"):
+                    w = np.exp(scale * (rows @ key) - ls)
+                    amp[s, h, j] += (w * scale * (np.abs(rows) @ np.abs(key))).sum()
+                out[s, h, j] = w.sum() + (out[s, h, j] if j < L - n else 0.0)
     return out, amp
 
 

@@ -646,6 +646,18 @@ def test_weights_lengths(length):
 
 
 @gpu
+@pytest.mark.parametrize("kind,hd", [("bf16", 128), ("e4m3", 64), ("e2m1", 128)])
+@pytest.mark.parametrize("rows", [9, 18, 34])
+def test_weights_many_short_sequences(kind, hd, rows):
+    """Shares of many heads, some of one tile of keys: the warps with a pair's second tile then skip it, and must not
+    take what they wait for next for done."""
+    rng = np.random.default_rng(rows)
+    r = rng.integers(rows - 1, rows + 1, 50)
+    lens = [int(a + rng.integers(0, 60) if rng.random() < 0.4 else a + rng.integers(0, 330)) for a in r]
+    _check_weights(kind, hd=hd, heads=64, kvh=8, rows=tuple(int(x) for x in r), lens=tuple(lens), page=64, seed=rows)
+
+
+@gpu
 @pytest.mark.parametrize("window", [1, 7, 16, 100, 5000])
 @pytest.mark.parametrize("rows", [1, 6, 33])
 def test_weights_windows(window, rows):
