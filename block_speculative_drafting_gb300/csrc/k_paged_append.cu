@@ -16,6 +16,10 @@
 // of 128, bf16, half of each rotated: 39.7 us, 5.1 TB/s (75 % of a copy).  512
 // rows with head norms into an e4m3 cache: 9.0 us, the chain of a row's norms
 // and rotations; one row: 4.5 us, launch and lookups.
+//
+// Into a 4-bit cache, where two elements are a byte, a lane holds sixteen columns of keys or values alone
+// (paged_append4_kernel), one block with its scale: 8192 rows of 8 heads 18 us, a third of them the
+// conversions' and scales' chain; the read of them as bf16 another 9.  32 blocks of 16 rows: 6.7 us together.
 #include "kernels.cuh"
 #include "paged_attn.cuh"
 

@@ -23,6 +23,12 @@
 // P is one f16 for bf16 outputs, off by 2^-11 of each key's part at most, an
 // eighth of the output's own 2^-8, and a hi + lo pair for f16 outputs.
 //
+// 16 sequences of 32768 keys, 8 heads of 128: 223 us, 2.7 TB/s (40 % of a copy); 32 of
+// 1024 to 4096 keys, four query heads each: 45 us.  Issue bound: some 880
+// instructions a tile of 32 keys, 0.53 a clock and SM quarter, and a unit's ends
+// (about 4 us, two or three a CTA with the shorter ones).  One sequence of 2048 keys: 9.2 us,
+// launch, share, first tiles and join one after the other.
+//
 // Masking: as in k_paged_attn.cu.  Codes are finite, so a value that is not can
 // only be a block scale of NaN: where rows see different keys, such tiles add P V key by
 // key with the hidden ones left out.

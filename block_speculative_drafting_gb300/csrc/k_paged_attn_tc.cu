@@ -40,9 +40,11 @@
 // finite (0 times an infinity would not be 0), those elements are taken out of
 // the tile and added to the rows that see them.
 //
-// Per tile 1.37 us with a bf16 cache, the memory's rate (19 blocks over 16384 keys x
-// 8 heads: 187 us, 6.8 TB/s), 1.27 us with an e4m3 one (178 us), 0.35 of it the codes'
-// way through shared memory.  A unit's end and the next one's beginning take about
+// Per tile 1.36 us with a bf16 cache, the memory's rate (19 blocks over 16384 keys x
+// 8 heads: 186 us, 6.8 TB/s), 1.26 us with an e4m3 one (173 us) and 1.25 with 4 bits (171 us), the
+// softmax and the codes' way into the slots (an e2m1 lane's 16 bytes are 32 elements of a row and
+// two block scales: paged_tile.cuh).  32 blocks over 1024 to 4096 keys: 65, 64 and 65 us; f16
+// queries over e4m3 67.  A unit's end and the next one's beginning take about
 // 4 us, of which a tile that some rows see in part 2 and the outputs 2; start,
 // epilogue and join of a call 13.
 //

@@ -14,6 +14,11 @@
 // are other CTAs' and need not wait), in rounds of some thousand vectors, each read whole
 // before it is written; the next round's reads are on their way meanwhile, whose
 // slots lie past everything this round writes.
+//
+// One sequence of 32768 tokens, 8 heads of 128 in bf16, cut to 16384: 65 us, 25 of them the choice
+// (eight CTAs, four times over their weights: latency) and 38 the move (3.5 TB/s: its threads find the
+// place of every 16 bytes, some 130 instructions a warp's).  32 sequences of 1024 to 4096 tokens in e4m3
+// cut to 2048: 52 us, 11 and 41.
 #include "kernels.cuh"
 #include "paged.cuh"
 

@@ -9,8 +9,10 @@
 // are k_paged_attn.cu's, a unit being a (sequence, key/value head) with all its
 // rows; each warp has its own ring of stages, filled by asynchronous copies.
 //
-// With one token a sequence the keys' bytes bound it, with a block the
-// exponentials and conversions.  Rows beyond 64 go by in sets of 64, the CTA's
+// With one token a sequence the keys' bytes bound it (32 sequences of 1024 to 4096
+// bf16 keys, 8 heads of 128: 33 us, 4.9 TB/s, where k_paged_weights.cu takes 40), with a
+// block the MMAs and, over 4 bits, the conversions (16 rows of four query heads over
+// 32768 keys: 22 us and 28; the MMAs alone, one of 16 x 8 x 16 every two clocks and SM, 7).  Rows beyond 64 go by in sets of 64, the CTA's
 // warps in step (a sequence that has many more rows than the call's average).
 //
 // Keys that only some rows see, rows of lse -inf and columns without a row are

@@ -229,6 +229,8 @@ int dflash_paged_read(const dflash_paged_cache* cache, const dflash_paged_rows* 
     if (v_out != nullptr) TRY(check_heads(v_out, "v_out", cache->kv_heads, 1, R.n_rows, &V));
     if (k_out != nullptr && v_out != nullptr && k_out->dtype != v_out->dtype)
         return fail(DFLASH_EINVAL, "k_out and v_out need one type");
+    if (k_out != nullptr && v_out != nullptr && R.n_rows > 0 && k_out->data == v_out->data)
+        return fail(DFLASH_EINVAL, "k_out and v_out are one memory");
     if (R.n_rows == 0) return DFLASH_OK;
     int n = 0;
     TRY(sms(&n));

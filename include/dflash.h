@@ -630,8 +630,9 @@ DFLASH_API int dflash_paged_append_at(const dflash_paged_cache* cache, const dfl
 /*
  * The keys and values that the cache holds for the call's rows, as values:
  * code * block scale * head's scale (or the element itself), rounded to the
- * output's type once.  k_out, v_out: kv_heads heads, one type; either may be
- * NULL.  A row whose position is not held reads as zeros.
+ * output's type once.  k_out, v_out: kv_heads heads, one type, apart from each
+ * other and from the cache; either may be NULL.  A row whose position is not
+ * held reads as zeros.
  * Errors: EINVAL, EGEOM, ECUDA.
  */
 DFLASH_API int dflash_paged_read(const dflash_paged_cache* cache, const dflash_paged_rows* rows,
@@ -652,8 +653,8 @@ DFLASH_API int dflash_paged_read(const dflash_paged_cache* cache, const dflash_p
  * memory, 16-byte aligned, needing no initial contents; calls that may
  * overlap need one each.
  * Errors: EINVAL (also where sequences x heads x positions of the table come
- * to more than 2^31 tiles of 128 keys), EGEOM, ECAPACITY (workspace too small),
- * ECUDA.
+ * to more than 2^31 tiles of 128 keys, or of 32 keys of an E2M1 cache), EGEOM,
+ * ECAPACITY (workspace too small), ECUDA.
  */
 DFLASH_API int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_rows* rows,
                                       const dflash_head_rows* q, const dflash_head_rows* out, float* lse, float scale,
@@ -688,7 +689,7 @@ typedef struct {
  * 32 bits and in one order: equal calls give equal bits.  Only the cache's keys
  * are read (v may be k).  weights of different sequences and heads are apart.
  * Errors: EINVAL (also where sequences x heads x positions of the table come to
- * more than 2^31 tiles of 128 keys), EGEOM, ECUDA.
+ * more than 2^31 tiles of 32 keys), EGEOM, ECUDA.
  */
 DFLASH_API int dflash_paged_key_weights(const dflash_paged_cache* cache, const dflash_paged_rows* rows,
                                         const dflash_head_rows* q, const float* lse, float scale, int32_t window,

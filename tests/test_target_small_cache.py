@@ -59,7 +59,8 @@ def _weights_struct(**kw):
 
 
 BAD_BLOCKS = [dict(k_block=None), dict(v_block=None), dict(k_block=4098), dict(k_strides=(1024, 72, 32)),
-              dict(v_block_strides=(128, 8, 6)), dict(k_block_strides=(-128, 8, 4)), dict(k_scale=4096)]
+              dict(v_block_strides=(128, 8, 6)), dict(k_block_strides=(-128, 8, 4)), dict(k_scale=4096),
+              dict(v_strides=(1 << 31, 64, 32)), dict(k_block_strides=(1 << 31, 8, 4))]
 
 
 @pytest.mark.parametrize("bad", BAD_BLOCKS, ids=lambda b: next(iter(b)))
@@ -83,11 +84,11 @@ def test_paged_calls_refuse_bad_block_scales(lib, bad):
 def test_paged_read_refuses_bad_arguments(lib):
     from block_speculative_drafting_gb300 import _abi
 
-    def call(c=_cache4(), r=_rows_struct(), k=_head_struct(2), v=_head_struct(2)):
+    def call(c=_cache4(), r=_rows_struct(), k=_head_struct(2), v=_head_struct(2, data=8192)):
         ref = lambda x: None if x is None else C.byref(x)  # noqa: E731
         return lib.dflash_paged_read(ref(c), ref(r), ref(k), ref(v), None)
 
-    for bad in (dict(c=None), dict(r=None), dict(k=None, v=None), dict(k=_head_struct(3)), dict(v=_head_struct(2, dtype=0)),
+    for bad in (dict(c=None), dict(r=None), dict(k=None, v=None), dict(v=_head_struct(2)), dict(k=_head_struct(3)), dict(v=_head_struct(2, dtype=0)),
                 dict(v=_head_struct(2, dtype=3), k=None), dict(k=_head_struct(2, data=4104)),
                 dict(k=_head_struct(2, row_stride=130)), dict(r=_rows_struct(n_rows=5)), dict(r=_rows_struct(table=None))):
         assert call(**bad) == _abi.DFLASH_EINVAL, bad
