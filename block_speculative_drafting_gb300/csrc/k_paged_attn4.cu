@@ -12,22 +12,19 @@
 // where a unit has up to 8 rows (two such halves where it has up to 16).  Codes come by
 // ldmatrix, four bytes a lane: of a key row those are eight columns, two MMAs'
 // operands in any order that the queries follow; of values, transposed in
-// two-byte units, four columns of two keys each.  A byte is converted by the
-// hardware (two e2m1 codes -> a pair of f16) and multiplied by its block's scale in
-// f16, exactly.  A pair of value columns is not an MMA's pair of keys; rather than
-// take the pairs apart (two byte permutations a byte, in the pipe that the
-// conversions need) both columns go through as if they were two keys, once with
-// weights (p, 0) and once with (0, p): the tensor pipe has the time (16 x 32768
-// keys: 228 -> 223 us).  The weights go from rows of S^T to columns of P^T by movmatrix.
+// two-byte units, four columns of two keys each.  A code is converted by the
+// hardware (e2m1 pairs -> f16 pairs) and multiplied by its block's scale in
+// f16, exactly.  The weights go from rows of S^T to columns of P^T by movmatrix.
 //
 // P is one f16 for bf16 outputs, off by 2^-11 of each key's part at most, an
 // eighth of the output's own 2^-8, and a hi + lo pair for f16 outputs.
 //
-// 16 sequences of 32768 keys, 8 heads of 128: 223 us, 2.7 TB/s (40 % of a copy); 32 of
-// 1024 to 4096 keys, four query heads each: 45 us.  Issue bound: some 880
-// instructions a tile of 32 keys, 0.53 a clock and SM quarter, and a unit's ends
-// (about 4 us, two or three a CTA with the shorter ones).  One sequence of 2048 keys: 9.2 us,
-// launch, share, first tiles and join one after the other.
+// 16 sequences of 32768 keys, 8 heads of 128: 228 us, 2.65 TB/s (39 % of a copy); 32 of
+// 1024 to 4096 keys, four query heads each: 45 us.  Bound by a tile's chain of some 900
+// instructions in the four warps of an SM quarter, 0.53 of them a clock (ALU pipe 46 %;
+// fewer of its instructions for twice the value MMAs took the same time), and by a unit's
+// ends (about 4 us, two or three a CTA with the shorter ones).  One sequence of 2048
+// keys: 9.2 us, launch, share, first tiles and join one after the other.
 //
 // Masking: as in k_paged_attn.cu.  Codes are finite, so a value that is not can
 // only be a block scale of NaN: where rows see different keys, such tiles add P V key by
@@ -257,7 +254,7 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
         const int pmax = sq.p0 + (rt * MT + mvalid - 1) / A.group;
         const int wtop = A.window > 0 ? pmax - A.window + 1 : 0;
 
-        float o[NT][CH][2][4];  // columns 32 j + 4 gq + t (and 2 on) of rows 8 n + 2 tq + {0, 1}
+        float o[NT][CH][2][4];  // columns 32 c + 4 gq + 2 t + {0, 1} of rows 8 n + 2 tq + {0, 1}
         float m[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -417,8 +414,8 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
 #pragma unroll
                                     for (int e = 0; e < 2; ++e)
                                         if (!((hb >> e) & 1u)) {
-                                            o[n][j][0][2 * t2 + e] = fmaf(p[e], f.x * s, o[n][j][0][2 * t2 + e]);
-                                            o[n][j][1][2 * t2 + e] = fmaf(p[e], f.y * s, o[n][j][1][2 * t2 + e]);
+                                            o[n][j][t2][e] = fmaf(p[e], f.x * s, o[n][j][t2][e]);
+                                            o[n][j][t2][2 + e] = fmaf(p[e], f.y * s, o[n][j][t2][2 + e]);
                                         }
                                 }
                             }
@@ -427,55 +424,55 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
                     continue;
                 }
             }
-            // ---- values: O^T += V^T P^T, eight keys at a time
-            [[maybe_unused]] uint32_t two[4];  // (heads of 64: sixteen keys' codes at once)
+            // ---- values: O^T += V^T P^T
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                // weights of keys 2 tq, 2 tq + 1 of row gq, each with a 0 beside it: for even columns, and for odd ones
-                uint32_t pe[NT][2], po[NT][2], le[NT][2], lo[NT][2];
+            for (int k = 0; k < 2; ++k) {
+                uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float x = sc[k >> 1][n][2 * (k & 1)], y = sc[k >> 1][n][2 * (k & 1) + 1];
-                    const uint32_t hi = pack2<false>(x, y);
-                    const uint32_t p = p4_transposed(hi);
-                    pe[n][0] = p & 0xffffu, pe[n][1] = p >> 16;
-                    po[n][0] = p << 16, po[n][1] = p & 0xffff0000u;
-                    if constexpr (PAIR) {
-                        const float2 f = unpack2<false>(hi);
-                        const uint32_t q = p4_transposed(pack2<false>(x - f.x, y - f.y));
-                        le[n][0] = q & 0xffffu, le[n][1] = q >> 16;
-                        lo[n][0] = q << 16, lo[n][1] = q & 0xffff0000u;
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t hi = pack2<false>(sc[k][n][2 * y], sc[k][n][2 * y + 1]);
+                        ph[n][y] = p4_transposed(hi);
+                        if constexpr (PAIR) {
+                            const float2 f = unpack2<false>(hi);
+                            pl[n][y] = p4_transposed(pack2<false>(sc[k][n][2 * y] - f.x, sc[k][n][2 * y + 1] - f.y));
+                        }
                     }
-                }
-                uint32_t s[4];  // scales of keys 2 tq and 2 tq + 1, of this lane's block of each chunk
-                {
-                    const auto x = p4_scales<2 * SW>(bv + (8 * k + 2 * tq) * SB);
+                uint32_t s[2][4];  // scales of keys 2 tq, 2 tq + 1 (and 8 on), of this lane's block of each chunk
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const auto x = p4_scales<2 * SW>(bv + (16 * k + 8 * y + 2 * tq) * SB);
                     const uint32_t pick = gq & 4 ? (SW == 2 ? 0x7531 : 0x3131) : (SW == 2 ? 0x6420 : 0x2020);
                     const uint32_t k0 = __byte_perm(x.w[0], x.w[SW - 1], pick), k1 = __byte_perm(x.w[SW], x.w[2 * SW - 1], pick);
-                    e4m3x4_f16x4(__byte_perm(k0, k1, 0x5140), s[0], s[1]);
-                    if constexpr (CH == 4) e4m3x4_f16x4(__byte_perm(k0, k1, 0x7362), s[2], s[3]);
-                }
-                // codes: of chunk j two column pairs of key 2 tq, then of key 2 tq + 1, four bytes that are four operands
-                uint32_t r[4];
-                if constexpr (CH == 4) {
-                    p4_ldsm_t(r, sv + p4_off<CH>(8 * k + (lane & 7), lane >> 3));
-                } else if ((k & 1) == 0) {
-                    p4_ldsm_t(two, sv + p4_off<CH>(8 * k + 8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1));
+                    e4m3x4_f16x4(__byte_perm(k0, k1, 0x5140), s[y][0], s[y][1]);
+                    if constexpr (CH == 4) e4m3x4_f16x4(__byte_perm(k0, k1, 0x7362), s[y][2], s[y][3]);
                 }
 #pragma unroll
-                for (int j = 0; j < CH; ++j) {
-                    uint32_t v[4];
-                    e2m1x8_f16x8(CH == 4 ? r[j] : two[2 * (k & 1) + j], v);
-                    v[0] = p4_times(v[0], s[j], false), v[1] = p4_times(v[1], s[j], false);
-                    v[2] = p4_times(v[2], s[j], true), v[3] = p4_times(v[3], s[j], true);
+                for (int j = 0; j < CH; j += 2) {
+                    uint32_t r[4];
+                    p4_ldsm_t(r, (sv + 16 * k * S::RB + mat) ^ (16 * j));
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        p4_mma(o[n][j][0], v[0], v[1], v[2], v[3], pe[n][0], pe[n][1]);
-                        p4_mma(o[n][j][1], v[0], v[1], v[2], v[3], po[n][0], po[n][1]);
-                        if constexpr (PAIR) {
-                            p4_mma(o[n][j][0], v[0], v[1], v[2], v[3], le[n][0], le[n][1]);
-                            p4_mma(o[n][j][1], v[0], v[1], v[2], v[3], lo[n][0], lo[n][1]);
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t v[2][4];  // columns 0 .. 3 of keys 2 tq, 2 tq + 1 and of keys 8 on
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            uint32_t x[4];
+                            e2m1x8_f16x8(r[2 * i + y], x);
+                            const uint32_t sy = s[y][j + i];
+                            v[y][0] = mul_f16x2(__byte_perm(x[0], x[2], 0x5410), sy);
+                            v[y][1] = mul_f16x2(__byte_perm(x[0], x[2], 0x7632), sy);
+                            v[y][2] = mul_f16x2(__byte_perm(x[1], x[3], 0x5410), sy);
+                            v[y][3] = mul_f16x2(__byte_perm(x[1], x[3], 0x7632), sy);
                         }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int t2 = 0; t2 < 2; ++t2) {
+                                p4_mma(o[n][j + i][t2], v[0][2 * t2], v[0][2 * t2 + 1], v[1][2 * t2], v[1][2 * t2 + 1], ph[n][0], ph[n][1]);
+                                if constexpr (PAIR)
+                                    p4_mma(o[n][j + i][t2], v[0][2 * t2], v[0][2 * t2 + 1], v[1][2 * t2], v[1][2 * t2 + 1], pl[n][0], pl[n][1]);
+                            }
                     }
                 }
             }
@@ -508,8 +505,8 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
                     float* to = merge + (size_t)(warp * MT + row) * S::kRow + 4 * gq;
 #pragma unroll
                     for (int j = 0; j < CH; ++j)
-                        *reinterpret_cast<float4*>(to + 32 * j) = make_float4(o[n][j][0][e] * f, o[n][j][1][e] * f,
-                                                                              o[n][j][0][2 + e] * f, o[n][j][1][2 + e] * f);
+                        *reinterpret_cast<float4*>(to + 32 * j) = make_float4(o[n][j][0][e] * f, o[n][j][0][2 + e] * f,
+                                                                              o[n][j][1][e] * f, o[n][j][1][2 + e] * f);
                     if (gq == 0) sums[warp][row] = make_float2(big, l[n][e] * f);
                 }
         }
