@@ -621,18 +621,26 @@ DF_DEV void pa_odd_row(const PaArgs& A, int r, int hq, bool mine) {
 }
 // The shared units' parts joined: CTA (c, y) takes rows 16 y .. of the unit that
 // starts in share c and ends in another, a warp a row.
-template <int HD>
+template <int HD, bool TOGETHER>
 __global__ void __launch_bounds__(kPaThreads) paged_join_kernel(const __grid_constant__ PaArgs A, int mt, int e8) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     const int odd = A.ws_odd[blockIdx.x];
     bool any = false;
     const PaJoin e = A.ws_join[blockIdx.x];
-    const int c0 = blockIdx.x, c1 = e.last, h = e.head;
+    const int c0 = blockIdx.x, c1 = e.last;
+    int h = e.head;
     if (c1 > c0) {
+    const int rows = TOGETHER && e.together > 1 ? e.together * e.mt : e.rows;
 #pragma unroll 1
-    for (int mrow = 16 * blockIdx.y + warp; mrow < min(e.rows, 16 * (int)blockIdx.y + 16); mrow += kPaWarps) {
-    const int mm = e.m0 + mrow, row = e.row0 + mm / A.group, hq = h * A.group + mm % A.group;
+    for (int mrow = 16 * blockIdx.y + warp; mrow < min(rows, 16 * (int)blockIdx.y + 16); mrow += kPaWarps) {
+    int of = mrow;  // of its head
+    if (TOGETHER && e.together > 1) {
+        h = e.head + mrow / e.mt;
+        of = mrow % e.mt;
+        if (of >= e.rows) continue;
+    }
+    const int mm = e.m0 + of, row = e.row0 + mm / A.group, hq = h * A.group + mm % A.group;
     constexpr int V = HD / 32;  // columns a lane
     float m = -INFINITY, l = 0.f, o[V] = {};
     // parts in order, 32 references and sums at a time, 8 outputs in flight (16 are more code: 40.3 -> 42.6 us, one block
@@ -740,9 +748,14 @@ static int pa_tile_rows(int cache_dtype, int n_seqs, int64_t n_rows, int group) 
     return cache_dtype == kE2M1 && m <= 8 ? 8 : m <= kPaM ? kPaM : m <= 64 ? 64 : 128;
 }
 
+// Rows of a part of a unit in the workspace.
+static int pa_part_rows(int cache_dtype, int mt, int kv_heads) {
+    return cache_dtype == kE2M1 && mt <= kPaM ? mt * pa_together(mt, kv_heads) : mt;
+}
+
 int64_t paged_attention_workspace(int cache_dtype, int hd, int n_seqs, int64_t n_rows, int heads, int kv_heads,
                                   int num_sms) {
-    const int64_t mt = pa_tile_rows(cache_dtype, n_seqs, n_rows, heads / kv_heads);
+    const int64_t mt = pa_part_rows(cache_dtype, pa_tile_rows(cache_dtype, n_seqs, n_rows, heads / kv_heads), kv_heads);
     return num_sms * (2 * mt * (hd * 4 + 8) + (int64_t)sizeof(PaJoin) + (int64_t)sizeof(int32_t));
 }
 
@@ -772,18 +785,22 @@ int paged_attention(const PagedCache& C, int cache_dtype, int hd, const PagedRow
     A.group = q.heads / C.kv_heads;
     const int mt = pa_tile_rows(cache_dtype, R.n_seqs, R.n_rows, A.group);
     A.ws_o = static_cast<float*>(ws);
-    A.ws_ml = reinterpret_cast<float2*>(A.ws_o + 2 * (int64_t)num_sms * mt * hd);
-    A.ws_join = reinterpret_cast<PaJoin*>(A.ws_ml + 2 * (int64_t)num_sms * mt);
+    // (a table whose line cannot be long enough: head by head)
+    const int part = cache_dtype == kE2M1 && mt <= kPaM && p4_many(A, mt, num_sms) ? pa_part_rows(cache_dtype, mt, C.kv_heads) : mt;
+    A.together = part / mt;
+    A.ws_ml = reinterpret_cast<float2*>(A.ws_o + 2 * (int64_t)num_sms * part * hd);
+    A.ws_join = reinterpret_cast<PaJoin*>(A.ws_ml + 2 * (int64_t)num_sms * part);
     A.ws_odd = reinterpret_cast<int32_t*>(A.ws_join + num_sms);
     const int e = mt > kPaM                ? paged_attention_tc(A, cache_dtype, hd, mt, num_sms, st)
                   : cache_dtype == kE2M1 ? paged_attention4(A, hd, mt, num_sms, st)
                   : hd == 64 ? pa_type<64>(A, cache_dtype, num_sms, st)
                              : pa_type<128>(A, cache_dtype, num_sms, st);
     if (e != 0) return e;
-    const dim3 grid(num_sms, (mt + 15) / 16);
+    const dim3 grid(num_sms, (part + 15) / 16);
     const int e8 = cache_dtype == kE4M3 || cache_dtype == kE2M1;
-    return hd == 64 ? (int)launch(paged_join_kernel<64>, grid, dim3(kPaThreads), 0, st, A, mt, e8)
-                    : (int)launch(paged_join_kernel<128>, grid, dim3(kPaThreads), 0, st, A, mt, e8);
+    auto join = part > mt ? (hd == 64 ? paged_join_kernel<64, true> : paged_join_kernel<128, true>)
+                          : (hd == 64 ? paged_join_kernel<64, false> : paged_join_kernel<128, false>);
+    return (int)launch(join, grid, dim3(kPaThreads), 0, st, A, part, e8);
 }
 
 }  // namespace dflash

@@ -36,6 +36,8 @@ namespace dflash {
 
 // tiles' time that a unit's end and the next one's beginning take
 constexpr int kP4Over = 8;
+// rounds of a CTA's warps from which on a unit is the heads of a key together
+constexpr int kP4Many = 2;
 
 DF_DEV void p4_ldsm(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -100,7 +102,8 @@ DF_DEV uint32_t p4_off(int r, int c) {
     return (uint32_t)(r * CH * 16 + ((CH == 4 ? c ^ ((r >> 1) & 3) : c ^ ((r >> 2) & 1)) << 4));
 }
 
-template <bool PAIR, int HD, int NT>
+// TOGETHER: a unit may be several heads
+template <bool PAIR, int HD, int NT, bool TOGETHER>
 __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
     paged_attn4_kernel(const __grid_constant__ PaArgs A) {
     using S = P4Shape<PAIR, HD, NT>;
@@ -114,8 +117,11 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
     pdl_wait();
     pdl_trigger();
 
-    int chunk;
-    PaCur cur = pa_share<kP4Keys>(A, MT, kP4Over, lane, chunk);
+    int chunk, heads = 1;
+    PaCur cur = pa_share<kP4Keys, TOGETHER>(A, MT, kP4Over, lane, chunk, kP4Many * W * (int)gridDim.x, &heads);
+    const int G = TOGETHER ? heads : 1;
+    // heads hg G .. of a unit u = (row tile, hg): this warp's among them, and its turn among the P warps of that head
+    const int groups = A.C.kv_heads / G, P = W / G, wg = warp % G, wk = warp / G;
     if (threadIdx.x == 0) A.ws_join[blockIdx.x].last = -1, A.ws_odd[blockIdx.x] = 0;
     if (cur.left <= 0) return;
     // the part of a unit that the share holds, and the unit after it
@@ -123,14 +129,14 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
     auto skip = [&](PaCur& c, int n) {
         c.left -= n - 1;
         c.tile += n - 1;
-        pa_next<kP4Keys>(A, MT, c);
+        pa_next<kP4Keys, TOGETHER>(A, MT, c, G);
     };
 
     // Queries of row gq (and gq + 8), columns 32 j + 8 tq .., as they are: fetched before the first copies, and as the unit
     // before ends.
     uint4 qf[NT][CH];
     auto fetch = [&](const PaCur& c) {
-        const int h = c.u % A.C.kv_heads, rt = c.u / A.C.kv_heads;
+        const int h = c.u % groups * G + wg, rt = c.u / groups;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int mm = rt * MT + gq + 8 * n, r = mm / A.group, hq = h * A.group + mm - r * A.group;
@@ -148,16 +154,16 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
         int id, slot, h;
     };
     PaCur put = cur;
-    int put_n = tiles_of(put), put_t = warp;  // this warp's tile among the unit's
+    int put_n = tiles_of(put), put_t = wk;  // this warp's tile among the unit's
     auto settle = [&]() {  // to the next unit with a tile for this warp
         while (put.left > 0 && put_t >= put_n) {
             skip(put, put_n);
             put_n = tiles_of(put);
-            put_t = warp;
+            put_t = wk;
         }
     };
     auto look = [&]() -> Look {
-        Look k{-1, 0, put.u % A.C.kv_heads};
+        Look k{-1, 0, put.u % groups * G + wg};
         const int key = put.q.lo + (put.tile + put_t) * kP4Keys + lane;
         if (key < put.q.hi) k.id = page_entry(A.R, put.s, key, k.slot);
         return k;
@@ -179,7 +185,7 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
             const unsigned char *kp = at(A.C.k, A.C.ks), *vp = at(A.C.v, A.C.vs), *kb = at(A.C.kb, A.C.kbs), *vb = at(A.C.vb, A.C.vbs);
             const uint32_t bits = __ballot_sync(0xffffffffu, held);
             if (lane == 0) vbits[warp][stage_put] = bits;
-            put_t += W;
+            put_t += P;
             if (put_t >= put_n) settle();
             if (put.left > 0) ahead = look();
             constexpr int RPI = 32 / CH;  // rows a copy instruction covers
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
         const PaCur unit = cur;
         const PaSeq& sq = unit.q;
         const int tiles = tiles_of(unit);
-        const int h = unit.u % A.C.kv_heads, rt = unit.u / A.C.kv_heads;
+        const int h0 = unit.u % groups * G, h = h0 + wg, rt = unit.u / groups;
         const int mvalid = min(MT, sq.rows * A.group - rt * MT);
         // the queries in f16, by a power of two where they are bf16
         float c[NT][2];  // scores of rows 2 tq, 2 tq + 1 in log2 units: S c; never 0, so that -inf stays -inf
@@ -269,7 +275,7 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
         }
 
 #pragma unroll 1
-        for (int t = warp; t < tiles; t += W) {
+        for (int t = wk; t < tiles; t += P) {
             cp_wait<NST - 2>();
             __syncwarp();
             copy();
@@ -478,8 +484,8 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
             }
         }
 
-        // ------------------------------------------------------------ the unit's end: the warps that had tiles join
-        const int active = min(W, tiles);
+        // ------------------------------------------------------------ the unit's end: the warps of a head that had tiles join
+        const int active = min(P, tiles);
         float2(&part)[W][MT] = ml[turn & 1];
         ++turn;
 #pragma unroll
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
                 if (gq == 0) part[warp][8 * n + 2 * tq + e] = make_float2(m[n][e], l[n][e]);
             }
         __syncthreads();
-        if (warp < active) {
+        if (wk < active) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -500,7 +506,7 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
                     const int row = 8 * n + 2 * tq + e;
                     float big = -INFINITY;
 #pragma unroll
-                    for (int w = 0; w < W; ++w) big = w < active ? fmaxf(big, part[w][row].x) : big;
+                    for (int w = 0; w < W; ++w) big = w < active ? fmaxf(big, part[wg + w * G][row].x) : big;
                     const float f = m[n][e] == -INFINITY ? 1.f : pa_exp2(m[n][e] - big);  // (a NaN sum without a maximum stays)
                     float* to = merge + (size_t)(warp * MT + row) * S::kRow + 4 * gq;
 #pragma unroll
@@ -514,27 +520,30 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
         // a part of a shared unit: its start goes to the CTA's second slot, any other part to the first
         const int slot = blockIdx.x * 2 + (unit.tile == 0 ? 1 : 0);
         const int row0 = sq.row0;
-        if (!whole && unit.tile == 0 && threadIdx.x == 0)
-            A.ws_join[blockIdx.x] = pa_join_entry(unit, rt, MT, mvalid, h, sq.ntiles - tiles, chunk);
+        if (!whole && unit.tile == 0 && threadIdx.x == 0) {
+            PaJoin e = pa_join_entry(unit, rt, MT, mvalid, h0, sq.ntiles - tiles, chunk);
+            e.together = G, e.mt = MT;
+            A.ws_join[blockIdx.x] = e;
+        }
         skip(cur, tiles);
         if (cur.left > 0) fetch(cur);
         __syncthreads();
 #pragma unroll 1
-        for (int i = threadIdx.x; i < mvalid * (HD / 4); i += S::kThreads) {
-            const int row = i / (HD / 4), col = 4 * (i % (HD / 4));
-            const float big = sums[0][row].x;
+        for (int i = threadIdx.x; i < G * mvalid * (HD / 4); i += S::kThreads) {
+            const int at = i / (HD / 4), col = 4 * (i % (HD / 4)), g = G > 1 ? at / mvalid : 0, row = at - g * mvalid;
+            const float big = sums[g][row].x;
             float sum = 0.f;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < W; ++w)
                 if (w < active) {
-                    const float4 z = *reinterpret_cast<const float4*>(merge + (size_t)(w * MT + row) * S::kRow + col);
+                    const float4 z = *reinterpret_cast<const float4*>(merge + (size_t)((g + w * G) * MT + row) * S::kRow + col);
                     y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
-                    sum += sums[w][row].y;
+                    sum += sums[g + w * G][row].y;
                 }
             if (whole) {
-                const int mm = rt * MT + row, r = row0 + mm / A.group, hq = h * A.group + mm % A.group;
-                const float inv = sum == 0.f ? 0.f : (A.C.v_scale != nullptr ? A.C.v_scale[h] : 1.f) / sum;
+                const int mm = rt * MT + row, r = row0 + mm / A.group, hq = (h0 + g) * A.group + mm % A.group;
+                const float inv = sum == 0.f ? 0.f : (A.C.v_scale != nullptr ? A.C.v_scale[h0 + g] : 1.f) / sum;
                 uint2 w;
                 if (A.out.dtype == kBF16)
                     w = make_uint2(pack2<true>(y.x * inv, y.y * inv), pack2<true>(y.z * inv, y.w * inv));
@@ -545,28 +554,38 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
                     A.lse[(int64_t)r * A.q.heads + hq] =
                         sum == 0.f ? -INFINITY : (big == -INFINITY ? sum : (big + log2f(sum)) * 0.69314718056f);
             } else {
-                *reinterpret_cast<float4*>(A.ws_o + ((int64_t)slot * MT + row) * HD + col) = y;
-                if (col == 0) A.ws_ml[(int64_t)slot * MT + row] = make_float2(big, sum);
+                const int64_t place = (int64_t)slot * MT * A.together + g * MT + row;
+                *reinterpret_cast<float4*>(A.ws_o + place * HD + col) = y;
+                if (col == 0) A.ws_ml[place] = make_float2(big, sum);
             }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <bool PAIR, int HD, int NT>
+template <bool PAIR, int HD, int NT, bool TOGETHER>
 static int p4_launch(const PaArgs& A, int num_sms, cudaStream_t st) {
     using S = P4Shape<PAIR, HD, NT>;
     static size_t limit[kMaxDevices] = {};
-    auto kern = paged_attn4_kernel<PAIR, HD, NT>;
+    auto kern = paged_attn4_kernel<PAIR, HD, NT, TOGETHER>;
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return (int)e;
     if (cudaError_t e = raise_smem_limit(kern, S::kSmem, &limit[dev])) return (int)e;
     return (int)launch(kern, dim3(num_sms), dim3(S::kThreads), S::kSmem, st, A);
 }
+template <bool PAIR, int HD, int NT>
+static int p4_launch(const PaArgs& A, int num_sms, cudaStream_t st) {
+    return A.together > 1 ? p4_launch<PAIR, HD, NT, true>(A, num_sms, st) : p4_launch<PAIR, HD, NT, false>(A, num_sms, st);
+}
 template <bool PAIR>
 static int p4_shape(const PaArgs& A, int hd, int mt, int num_sms, cudaStream_t st) {
     if (mt == 8) return hd == 64 ? p4_launch<PAIR, 64, 1>(A, num_sms, st) : p4_launch<PAIR, 128, 1>(A, num_sms, st);
     return hd == 64 ? p4_launch<PAIR, 64, 2>(A, num_sms, st) : p4_launch<PAIR, 128, 2>(A, num_sms, st);
+}
+bool p4_many(const PaArgs& A, int mt, int num_sms) {
+    const double units = (double)A.R.n_rows * A.group / mt + A.R.n_seqs;
+    const int warps = mt == 8 ? P4Shape<false, 64, 1>::W : P4Shape<false, 64, 2>::W;
+    return units * A.C.kv_heads * (A.R.cap / kP4Keys + 1) >= (double)kP4Many * warps * num_sms;
 }
 int paged_attention4(const PaArgs& A, int hd, int mt, int num_sms, cudaStream_t st) {
     return A.out.dtype == kF16 ? p4_shape<true>(A, hd, mt, num_sms, st) : p4_shape<false>(A, hd, mt, num_sms, st);

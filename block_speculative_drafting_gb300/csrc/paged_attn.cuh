@@ -21,19 +21,21 @@ struct PaArgs {
     PagedRows R;
     HeadRows q, out;
     float* lse;
-    float* ws_o;     // [2 CTAs][MT][HD]
-    float2* ws_ml;   // [2 CTAs][MT]
+    float* ws_o;     // [2 CTAs][rows of a part][HD]
+    float2* ws_ml;   // [2 CTAs][rows of a part]
     struct PaJoin* ws_join;  // [CTAs]
     int32_t* ws_odd;         // [CTAs]: outputs of the CTA's whole units wait for pa_odd_row
     float scale_log2;
     int window, group;
+    int together;  // key/value heads that may be one unit's (pa_share)
 };
 
 // A unit that starts in a CTA's share and ends in another's, for the join:
 // its parts are this CTA's second slot and the first slots of the CTAs up to
 // `last` (below 0: this CTA starts no such unit).
 struct __align__(16) PaJoin {
-    int32_t last, row0, m0, rows, head, seq, pad[2];  // rows from m0 on of sequence seq, whose rows start at row0; kv head
+    int32_t last, row0, m0, rows, head, seq;  // rows from m0 on of sequence seq, whose rows start at row0; kv head
+    int32_t together, mt;  // above 1: as many heads from `head` on, each with mt rows of the part
 };
 
 // What the walk needs of one sequence.
@@ -90,9 +92,10 @@ DF_DEV void rows_of_lane(const PagedRows& R, int s0, int from, int lane, int& a,
         if (lane == 0) a = from;
     }
 }
-// This CTA's share (warp-wide); `chunk`: the places of a share.
-template <int TILE = kPaTile>
-DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
+// This CTA's share (warp-wide); `chunk`: the places of a share.  TOGETHER: in a line of at least `many` tiles a unit is
+// A.together heads (of one row tile), a tile the keys of all of them; `heads`: as many as a unit has.
+template <int TILE = kPaTile, bool TOGETHER = false>
+DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk, int many = 0, int* heads = nullptr) {
     int64_t t64 = 0, v64 = 0;
     // (the first 32 sequences are looked at once)
     PaSeq q0{};
@@ -117,7 +120,14 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
     };
     t64 = sum(t64);
     v64 = sum(v64);
+    if constexpr (TOGETHER) *heads = 1;
     if (t64 + ovh * v64 >= 1ll << 31) return c;  // (never: pa_line_fits)
+    if constexpr (TOGETHER)
+        if (t64 >= many) {
+            *heads = A.together;
+            t64 /= A.together, v64 /= A.together;
+            ovh = max(1, ovh / A.together);
+        }
     const int tiles = (int)t64, units = (int)v64;
     c.ov = tiles > 2 * (int)gridDim.x ? ovh : 0;
     const int total = tiles + c.ov * units, grid = (int)gridDim.x;
@@ -132,6 +142,7 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
             rows_of_lane(A.R, s0, from, lane, a, b);
             q = pa_seq<TILE>(A, min(s0 + lane, A.R.n_seqs - 1), a, b, mt);
         }
+        if constexpr (TOGETHER) q.nunits /= *heads;
         from = __shfl_sync(0xffffffffu, b, 31);
         const int w = s0 + lane < A.R.n_seqs ? (q.ntiles + c.ov) * q.nunits : 0;
         int in = w;
@@ -166,8 +177,8 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk) {
     }
     return c;
 }
-template <int TILE = kPaTile>
-DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c) {
+template <int TILE = kPaTile, bool TOGETHER = false>
+DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c, int heads = 1) {
     --c.left;
     if (++c.tile < c.q.ntiles) return;
     c.tile = 0;
@@ -185,6 +196,7 @@ DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c) {
         }
         const int a = c.q.row0 + c.q.rows;
         c.q = pa_seq<TILE>(A, c.s, a, rows_end(A.R, c.s, a), mt);
+        if constexpr (TOGETHER) c.q.nunits /= heads;
     } while (c.q.nunits == 0);
 }
 // The entry of a unit that begins in this CTA's share and has `rest` tiles after it.
@@ -296,6 +308,14 @@ constexpr int kPtOver = 4;
 int paged_attention_tc(const PaArgs& A, int cache_dtype, int hd, int mt, int num_sms, cudaStream_t st);
 // The warp-MMA kernel of the 4-bit cache (k_paged_attn4.cu): units of up to mt = 8 or 16 rows.
 int paged_attention4(const PaArgs& A, int hd, int mt, int num_sms, cudaStream_t st);
+// Whether its line may be long enough for units of several heads.
+bool p4_many(const PaArgs& A, int mt, int num_sms);
+// Key/value heads that may be one of its units: a divisor of the warps that a unit has.
+inline int pa_together(int mt, int kv_heads) {
+    int g = mt == 8 ? 8 : 4;
+    while (kv_heads % g) g >>= 1;
+    return g;
+}
 // The warp-MMA kernel of the key weights (k_paged_weights_few.cu).
 int paged_key_weights_few(const PaArgs& A, const KeyWeights& W, const float* lse, int cache_dtype, int hd, int num_sms,
                           cudaStream_t st);
