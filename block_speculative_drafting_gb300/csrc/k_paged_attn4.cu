@@ -19,11 +19,14 @@
 // P is one f16 for bf16 outputs, off by 2^-11 of each key's part at most, an
 // eighth of the output's own 2^-8, and a hi + lo pair for f16 outputs.
 //
-// 16 sequences of 32768 keys, 8 heads of 128: 228 us, 2.65 TB/s (39 % of a copy); 32 of
-// 1024 to 4096 keys, four query heads each: 45 us.  Bound by a tile's chain of some 900
-// instructions in the four warps of an SM quarter, 0.53 of them a clock (ALU pipe 46 %;
-// fewer of its instructions for twice the value MMAs took the same time), and by a unit's
-// ends (about 4 us, two or three a CTA with the shorter ones).  One sequence of 2048
+// With enough units, or keys beyond what L2 holds, a unit is all (up to eight) heads
+// of a key, each with its own warps: the heads' bytes share their lines (kP4Far).
+//
+// 16 sequences of 32768 keys, 8 heads of 128: 146 us, 4.15 TB/s (61 % of a copy); 32 of
+// 1024 to 4096 keys, four query heads each: 41 us.  Bound by issue: a tile's chain of some
+// 900 instructions in the four warps of an SM quarter, 0.67 of them a clock (half of them the
+// ALU pipe's; twice the value MMAs for fewer of those took 148 us), and by a unit's
+// ends (about 4 us, one or two a CTA with the shorter ones).  One sequence of 2048
 // keys: 9.2 us, launch, share, first tiles and join one after the other.
 //
 // Masking: as in k_paged_attn.cu.  Codes are finite, so a value that is not can
@@ -36,8 +39,13 @@ namespace dflash {
 
 // tiles' time that a unit's end and the next one's beginning take
 constexpr int kP4Over = 8;
-// rounds of a CTA's warps from which on a unit is the heads of a key together
-constexpr int kP4Many = 2;
+// Bytes of keys and values from which on a unit is the heads of a key together, about twice what L2 holds: a head's 64
+// bytes of a key and 8 of its scales share their lines with the other heads', and heads that go by at their own times
+// fetch those again (16 sequences of 32768 keys read 1530 MB for 605: 228 -> 146 us; of 8192 keys, which L2 holds: 53 and 54).
+// It is so, too, where each CTA would begin a unit of its own and end others (32 sequences of 4096 keys 60 -> 53 us, 128 of
+// 512 52 -> 41); with few units all CTAs have parts of every head, and the join takes longer (one sequence of 131072 keys
+// 46 us head by head, 71 together).
+constexpr double kP4Far = 256e6;
 
 DF_DEV void p4_ldsm(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -118,7 +126,7 @@ __global__ void __launch_bounds__((P4Shape<PAIR, HD, NT>::kThreads), 1)
     pdl_trigger();
 
     int chunk, heads = 1;
-    PaCur cur = pa_share<kP4Keys, TOGETHER>(A, MT, kP4Over, lane, chunk, kP4Many * W * (int)gridDim.x, &heads);
+    PaCur cur = pa_share<kP4Keys, TOGETHER>(A, MT, kP4Over, lane, chunk, (int)(kP4Far / S::kStage), &heads);
     const int G = TOGETHER ? heads : 1;
     // heads hg G .. of a unit u = (row tile, hg): this warp's among them, and its turn among the P warps of that head
     const int groups = A.C.kv_heads / G, P = W / G, wg = warp % G, wk = warp / G;
@@ -583,9 +591,8 @@ static int p4_shape(const PaArgs& A, int hd, int mt, int num_sms, cudaStream_t s
     return hd == 64 ? p4_launch<PAIR, 64, 2>(A, num_sms, st) : p4_launch<PAIR, 128, 2>(A, num_sms, st);
 }
 bool p4_many(const PaArgs& A, int mt, int num_sms) {
-    const double units = (double)A.R.n_rows * A.group / mt + A.R.n_seqs;
-    const int warps = mt == 8 ? P4Shape<false, 64, 1>::W : P4Shape<false, 64, 2>::W;
-    return units * A.C.kv_heads * (A.R.cap / kP4Keys + 1) >= (double)kP4Many * warps * num_sms;
+    const double units = ((double)A.R.n_rows * A.group / mt + A.R.n_seqs) * A.C.kv_heads;
+    return units >= num_sms || units * (A.R.cap / kP4Keys + 1) >= kP4Far / P4Shape<false, 128, 1>::kStage;
 }
 int paged_attention4(const PaArgs& A, int hd, int mt, int num_sms, cudaStream_t st) {
     return A.out.dtype == kF16 ? p4_shape<true>(A, hd, mt, num_sms, st) : p4_shape<false>(A, hd, mt, num_sms, st);

@@ -92,8 +92,8 @@ DF_DEV void rows_of_lane(const PagedRows& R, int s0, int from, int lane, int& a,
         if (lane == 0) a = from;
     }
 }
-// This CTA's share (warp-wide); `chunk`: the places of a share.  TOGETHER: in a line of at least `many` tiles a unit is
-// A.together heads (of one row tile), a tile the keys of all of them; `heads`: as many as a unit has.
+// This CTA's share (warp-wide); `chunk`: the places of a share.  TOGETHER: in a line of at least `many` tiles, or with a unit
+// for each CTA, a unit is A.together heads (of one row tile), a tile the keys of all of them; `heads`: as many as a unit has.
 template <int TILE = kPaTile, bool TOGETHER = false>
 DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk, int many = 0, int* heads = nullptr) {
     int64_t t64 = 0, v64 = 0;
@@ -123,7 +123,7 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk, in
     if constexpr (TOGETHER) *heads = 1;
     if (t64 + ovh * v64 >= 1ll << 31) return c;  // (never: pa_line_fits)
     if constexpr (TOGETHER)
-        if (t64 >= many) {
+        if (t64 >= many || v64 >= gridDim.x) {
             *heads = A.together;
             t64 /= A.together, v64 /= A.together;
             ovh = max(1, ovh / A.together);

@@ -505,13 +505,13 @@ def test_attention4_ragged_padded_and_bad_pages():
 @pytest.mark.parametrize("src,hd,heads,kvh,rows,window", [("bf16", 128, 32, 8, 1, 0), ("f16", 64, 16, 8, 1, 0),
                                                           ("bf16", 128, 12, 12, 2, 0), ("bf16", 64, 12, 6, 4, 0),
                                                           ("bf16", 128, 32, 8, 3, 0), ("f16", 128, 12, 4, 5, 0),
-                                                          ("bf16", 128, 16, 8, 2, 900)])
+                                                          ("bf16", 128, 16, 8, 2, 90)])
 def test_attention4_heads_together(src, hd, heads, kvh, rows, window):
-    """Lines long enough for the heads of a key to go together, over more sequences than a warp looks at in one go."""
+    """Units enough for the heads of a key to go together, over more sequences than a warp looks at in one go."""
     rng = np.random.default_rng(heads + rows)
-    n = 70 if kvh >= 8 else 140
+    n = 45 if kvh >= 6 else 60
     r = tuple(int(x) for x in rng.integers(0, rows + 1, n - 3)) + (rows,) * 3
-    lens = tuple(int(x) for x in rng.integers(1, 1100, n - 3)) + (0, 2900, 33)
+    lens = tuple(int(x) for x in rng.integers(1, 700, n - 3)) + (0, 2900, 33)
     _check_attention4(src, hd=hd, heads=heads, kvh=kvh, rows=r, lens=lens, window=window, page=48, bad=((1, 0), (4, 1)),
                       seed=rows)
 
