@@ -620,7 +620,8 @@ DF_DEV void pa_odd_row(const PaArgs& A, int r, int hq, bool mine) {
             out[i] = (uint16_t)(sum[i] == 0.f || sum[i] != sum[i] ? 0x7fffu : (top & 0xffffu) | (sum[i] < 0.f ? 0x8000u : 0u));
 }
 // The shared units' parts joined: CTA (c, y) takes rows 16 y .. of the unit that
-// starts in share c and ends in another, a warp a row.
+// starts in share c and ends in another, a warp a row (TOGETHER: a unit may be
+// several heads, whose rows follow one another).
 template <int HD, bool TOGETHER>
 __global__ void __launch_bounds__(kPaThreads) paged_join_kernel(const __grid_constant__ PaArgs A, int mt, int e8) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
