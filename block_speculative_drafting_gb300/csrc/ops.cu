@@ -286,6 +286,9 @@ int dflash_paged_evict(const dflash_paged_cache* cache, const dflash_paged_rows*
     if (A.R.n_seqs == 0) return DFLASH_OK;
     if (A.R.kv_len == nullptr || (A.R.max_pages > 0 && A.R.table == nullptr))
         return fail(DFLASH_EINVAL, "kv_len or table is NULL");
+    // (rows of both would be moved at once)
+    if (A.C.n_pages > 0 && (A.C.k == A.C.v || (cache->dtype == DFLASH_E2M1 && A.C.kb == A.C.vb)))
+        return fail(DFLASH_EINVAL, "k and v of the cache are one memory");
     TRY(check_weights(weights, "weights", A.R, &A.in));
     TRY(check_weights(out, "out", A.R, &A.out));
     if (A.in.p == A.out.p && (A.in.ss != A.out.ss || A.in.hs != A.out.hs))

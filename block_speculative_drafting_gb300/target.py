@@ -205,8 +205,8 @@ def paged_evict(k_cache, v_cache, weights, table, kv_len, keep: int, *, first: i
     kept         int32 [sequences][kv_heads][keep] to fill with the position that each token had (-1: no token)
     evicted      int32 [sequences] that grows by the number of tokens taken out, for `paged_append`
     workspace    uint8 tensor of `paged_evict_workspace` bytes (calls that may overlap need one each); None: allocated
-    No page may hold tokens of two sequences, and k_cache and v_cache are apart.  Cached keys keep their rotation, so a window over an evicted cache counts
-    the tokens that are left.
+    No page may hold tokens of two sequences, and k_cache and v_cache, as k_block and v_block, are apart.  Cached keys
+    keep their rotation, so a window over an evicted cache counts the tokens that are left.
     """
     if torch is None:
         _init()

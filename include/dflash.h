@@ -705,7 +705,7 @@ DFLASH_API int dflash_paged_key_weights(const dflash_paged_cache* cache, const d
  * them stays where it was.  Shorter sequences stay as they are.
  *   seqs       n_seqs, max_pages, kv_len and table (n_rows 0, row_start NULL);
  *              no two entries of the table that hold tokens name one page,
- *              and k and v are apart
+ *              and k and v, as their block scales, are apart
  *   out        where the weights go: weights itself, or memory apart from it
  *   new_len    int32 [n_seqs]: min(L, keep); may be kv_len itself
  *   kept       int32 [n_seqs][kv_heads][keep] or NULL: the position that each

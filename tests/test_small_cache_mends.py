@@ -1,0 +1,46 @@
+"""Calls around a target's small cache that once answered wrongly or were never made by a test."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from oracle import target as O
+from test_target_ops import _cache_struct, _dfl, _rows_struct, _torch
+from test_target_small_cache import _cache4, _good, _weights_struct
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from block_speculative_drafting_gb300.csrc.build import build
+    build()
+    return _dfl().lib()
+
+
+# --------------------------------------------------------------------------- evict: keys and values are apart
+@pytest.mark.parametrize("cache,bad", [(_cache_struct, dict(v=4096)), (_cache4, dict(v=4096)), (_cache4, dict(v_block=4096)),
+                                       (_cache4, dict(v=4096, v_block=4096))], ids=["bf16", "codes", "blocks", "both"])
+def test_evict_refuses_keys_and_values_in_one_memory(lib, cache, bad):
+    """Rows of both would move at once, over one another."""
+    from block_speculative_drafting_gb300 import _abi
+    w, r = _weights_struct(), _rows_struct(n_rows=0)
+    call = lambda c, r=r: lib.dflash_paged_evict(C.byref(c), C.byref(r), 8, 2, 3, C.byref(w), C.byref(w), 4096, None,  # noqa: E731
+                                                 None, 4096, 16, None)
+    assert call(cache(**bad)) == _abi.DFLASH_EINVAL and b"one memory" in lib.dflash_last_error(None)
+    assert call(cache()) == _abi.DFLASH_ECAPACITY  # apart: the next check is the workspace's
+    assert call(cache(k=None, v=None, k_block=None, v_block=None, n_pages=0)) == _abi.DFLASH_ECAPACITY
+    assert call(cache(**bad), _rows_struct(n_rows=0, n_seqs=0)) == 0
+
+
+@gpu
+def test_evict_refuses_one_tensor_as_keys_and_values():
+    torch, dfl = _torch(), _dfl()
+    args = _good(torch)["paged_evict"]
+    for bad in (dict(v_cache=args["k_cache"]), dict(v_block=args["k_block"])):
+        with pytest.raises(dfl.DFlashError, match="one memory"):
+            dfl.paged_evict(**{**args, **bad})
+    # pages that hold both, one behind the other, are apart
+    both = torch.zeros(6, 2, 16, 2, 32, dtype=torch.uint8, device="cuda")
+    dfl.paged_evict(**{**args, "k_cache": both[:, 0], "v_cache": both[:, 1]})
+    torch.cuda.synchronize()
