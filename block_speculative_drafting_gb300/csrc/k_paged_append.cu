@@ -524,7 +524,9 @@ static auto append_kernel(int in, int qo, int out) {
 int paged_append(const PagedCache& C, int cache_dtype, int hd, const PagedRows& R, const HeadRows& k, const HeadRows& v,
                  const HeadRows& q, const HeadRows& qo, const float* q_norm, const float* k_norm, float eps,
                  const Rotation& rot, const int32_t* evicted, int num_sms, cudaStream_t st) {
-    if (cache_dtype == kE2M1 && q.heads == 0 && k_norm == nullptr && rot.rotary == 0) {
+    // (keys and values into one memory are the general kernel's: its lanes write values after keys, here warps do both at once)
+    const bool apart = C.k != C.v && C.kb != C.vb;
+    if (cache_dtype == kE2M1 && q.heads == 0 && k_norm == nullptr && rot.rotary == 0 && apart) {
         auto kern = hd == 64 ? (k.dtype == kBF16  ? paged_append4_kernel<64, kBF16>
                                 : k.dtype == kF16 ? paged_append4_kernel<64, kF16>
                                                   : paged_append4_kernel<64, kF32>)

@@ -608,7 +608,8 @@ typedef struct {
  * rotation.  q NULL: keys and values alone.  q, k and v have one type; q_out
  * may be q itself, or apart from it and of another type.  A row whose position is not held is
  * not written to the cache (its q' is written).  A table that maps two of the
- * call's rows to one slot leaves either row's elements there.
+ * call's rows to one slot leaves either row's elements there.  Where k and v of
+ * the cache are one memory, it holds v.
  * Errors: EINVAL, EGEOM, ECUDA.
  */
 DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_rows* rows,

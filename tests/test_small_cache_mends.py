@@ -1,10 +1,8 @@
 """Calls around a target's small cache that once answered wrongly or were never made by a test."""
 import ctypes as C
 
-import numpy as np
 import pytest
 
-from oracle import target as O
 from test_target_ops import _cache_struct, _dfl, _rows_struct, _torch
 from test_target_small_cache import _cache4, _good, _weights_struct
 
@@ -44,3 +42,30 @@ def test_evict_refuses_one_tensor_as_keys_and_values():
     both = torch.zeros(6, 2, 16, 2, 32, dtype=torch.uint8, device="cuda")
     dfl.paged_evict(**{**args, "k_cache": both[:, 0], "v_cache": both[:, 1]})
     torch.cuda.synchronize()
+
+
+# --------------------------------------------------------------------------- append: one memory holds the values
+@gpu
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e2m1"])
+@pytest.mark.parametrize("rows", [1, 900])
+def test_append_into_one_memory_leaves_the_values_there(kind, rows):
+    torch, dfl = _torch(), _dfl()
+    gen = torch.Generator("cuda").manual_seed(rows)
+    k, v = torch.randn(2, rows, 3, 128, device="cuda", generator=gen).to(torch.bfloat16)
+    pages = -(-rows // 16)
+    table, lens = torch.arange(pages, dtype=torch.int32, device="cuda")[None], torch.tensor([rows], dtype=torch.int32).cuda()
+    scale = torch.full((3,), 0.25, device="cuda") if kind != "bf16" else None
+    type_ = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "e2m1": torch.uint8}[kind]
+
+    def cache():
+        c = torch.zeros(pages, 16, 3, 64 if kind == "e2m1" else 128, device="cuda").to(type_)
+        return c, torch.zeros(pages, 16, 3, 8, device="cuda").to(torch.float8_e4m3fn) if kind == "e2m1" else None
+
+    (one, blocks), (a, a_blocks), (b, b_blocks) = cache(), cache(), cache()
+    kw = dict(k_scale=scale, v_scale=scale)
+    for _ in range(5):
+        dfl.paged_append(one, one, k, v, table, lens, k_block=blocks, v_block=blocks, **kw)
+        dfl.paged_append(a, b, k, v, table, lens, k_block=a_blocks, v_block=b_blocks, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(one.view(torch.uint8), b.view(torch.uint8)) and not torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert blocks is None or torch.equal(blocks.view(torch.uint8), b_blocks.view(torch.uint8))
