@@ -124,15 +124,16 @@ def paged_append(k_cache, v_cache, k, v, table, kv_len, *, row_start=None, q=Non
 def paged_read(k_cache, v_cache, table, kv_len, rows: int, *, row_start=None, k_scale=None, v_scale=None, k_block=None,
                v_block=None, dtype=None, k_out=None, v_out=None, stream=None):
     """The keys and values that a paged cache holds for `rows` rows in all, as values: returns (k, v)
-    [rows][kv_heads][head_dim] of `dtype` (float32, bfloat16 or float16; None: float16 from a float16 cache, else
-    bfloat16).  Rows are `paged_append`'s: the last ones of each sequence (all of them with row_start = the running sum
+    [rows][kv_heads][head_dim] of `dtype` (float32, bfloat16 or float16; None: that of k_out or v_out, without them float16
+    from a float16 cache, else bfloat16).  Rows are `paged_append`'s: the last ones of each sequence (all of them with row_start = the running sum
     of kv_len).  Positions that are not held read as zeros.  k_out, v_out: where they go, of any row and head strides.
     The other arguments are `paged_append`'s.
     """
     if torch is None:
         _init()
-    if dtype is None and k_out is not None:
-        dtype = k_out.dtype
+    given = k_out if k_out is not None else v_out
+    if dtype is None and given is not None:
+        dtype = given.dtype
     return _binding.paged_read(k_cache, v_cache, table, kv_len, rows, row_start, k_scale, v_scale, k_block, v_block, dtype,
                                k_out, v_out, stream)
 

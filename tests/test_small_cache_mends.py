@@ -69,3 +69,17 @@ def test_append_into_one_memory_leaves_the_values_there(kind, rows):
         torch.cuda.synchronize()
         assert torch.equal(one.view(torch.uint8), b.view(torch.uint8)) and not torch.equal(a.view(torch.uint8), b.view(torch.uint8))
         assert blocks is None or torch.equal(blocks.view(torch.uint8), b_blocks.view(torch.uint8))
+
+
+# --------------------------------------------------------------------------- read: either output alone names the type
+@gpu
+@pytest.mark.parametrize("given", ["k_out", "v_out"])
+def test_read_takes_its_type_from_either_output(given):
+    torch, dfl = _torch(), _dfl()
+    args = {k: v for k, v in _good(torch)["paged_read"].items() if k not in ("k_out", "v_out", "dtype")}
+    to = torch.full((4, 2, 64), 7.0, device="cuda")
+    got = dfl.paged_read(**args, **{given: to})
+    want = dfl.paged_read(**args, dtype=torch.float32)
+    assert got["kv".index(given[0])] is to
+    assert all(x.dtype == torch.float32 and torch.equal(x, y) for x, y in zip(got, want))
+    assert dfl.paged_read(**args)[0].dtype == torch.bfloat16
