@@ -1,12 +1,25 @@
 """Calls around a target's small cache that once answered wrongly or were never made by a test."""
 import ctypes as C
+import os
+import re
 
+import numpy as np
 import pytest
 
-from test_target_ops import _cache_struct, _dfl, _rows_struct, _torch
-from test_target_small_cache import _cache4, _good, _weights_struct
+from oracle import target as O
+from test_target_ops import _cache_struct, _dfl, _i32, _layout, _rows_struct, _starts, _torch, _types, f64
+from test_target_small_cache import _any_cache, _cache4, _good, _weights_struct
 
 gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from block_speculative_drafting_gb300.csrc.build import build
+    build()
+    return _dfl().lib()
+
+
 
 
 @pytest.fixture(scope="module")
@@ -83,3 +96,167 @@ def test_read_takes_its_type_from_either_output(given):
     assert got["kv".index(given[0])] is to
     assert all(x.dtype == torch.float32 and torch.equal(x, y) for x, y in zip(got, want))
     assert dfl.paged_read(**args)[0].dtype == torch.bfloat16
+
+# --------------------------------------------------------------------------- key weights of many rows
+def _few_rows():
+    """Rows times group a sequence, on average, up to which the warp-MMA kernel serves a call."""
+    src = os.path.join(os.path.dirname(_dfl().__file__), "csrc", "k_paged_weights.cu")
+    with open(src) as f:
+        (most,) = re.findall(r"if \(per <= (\d+)\)", f.read())
+    return int(most)
+
+
+def _check_many(kind, src, group, rows, lens, kvh=1, hd=128, page=16, window=0, uniform=False, bad=(), order="slot", extra=0,
+                scale=None, seed=0, spread=1.0, poison=None, nothing=()):
+    """A call that the tcgen05 kernel serves, against the formula in 64 bits.  Tolerances as in test_target_small_cache.py."""
+    torch, dfl = _torch(), _dfl()
+    rng = np.random.default_rng(seed)
+    table, n_pages = _layout(torch, rng, [max(l, 0) for l in lens], rows, page, bad=bad)
+    R, heads, cap, starts = sum(rows) + extra, group * kvh, table.shape[1] * page, None if uniform else _starts(rows)
+    assert -(-R // len(lens)) * group > _few_rows()
+    q = torch.from_numpy(spread * rng.standard_normal((R, heads, hd)).astype(np.float32)).cuda().to(_types()[src])
+    kc, kb, ks, k64 = _any_cache(torch, rng, (n_pages, page, kvh, hd), kind, order)
+    if poison is not None:
+        k64 = poison(torch, kc, kb, table, k64.copy())
+    factor, q64 = hd ** -0.5 if scale is None else scale, f64(q)
+    lse, seen = np.full((R, heads), -np.inf, np.float32), {}
+    for s, a, n in O.rows_of(len(lens), R, starts):
+        L = min(max(lens[s], 0), cap) if n else 0
+        j = np.arange(L)
+        ids = table[s][j // page] if L else np.zeros(0, int)
+        held = (ids >= 0) & (ids < n_pages)
+        keys = k64[np.where(held, ids, 0), j % page]
+        p = lens[s] - n + np.arange(n)[:, None]
+        see = (j <= p) & held & ((j > p - window) if window else True)
+        for h in range(kvh):
+            x = q64[a:a + n, h * group:(h + 1) * group].reshape(n * group, hd)
+            with np.errstate(all="ignore"):
+                sc = np.where(np.repeat(see, group, 0), factor * (x @ keys[:, h].T), -np.inf)
+                size = factor * (np.abs(x) @ np.abs(keys[:, h]).T)
+                real = np.where(np.isnan(sc), -np.inf, sc)  # (the lse is an argument: it need not be NaN)
+                m = real.max(1, initial=-1e300, keepdims=True)
+                ls = (m + np.log(np.exp(real - m).sum(1, keepdims=True)))[:, 0]
+            lse[a:a + n, h * group:(h + 1) * group] = ls.reshape(n, group)
+            seen[s, h] = a, n, L, held, sc, size
+    for r, h in nothing:
+        lse[r, h] = -np.inf
+    w0 = rng.random((len(lens), kvh, cap + 5)).astype(np.float32)
+    want, amp = w0.astype(np.float64), np.zeros(w0.shape)
+    for (s, h), (a, n, L, held, sc, size) in seen.items():
+        ls = lse[a:a + n, h * group:(h + 1) * group].reshape(-1, 1).astype(np.float64)
+        with np.errstate(all="ignore"):
+            w = np.where(ls == -np.inf, 0.0, np.exp(sc - ls))
+            size = np.where(w == 0, 0.0, w * size)
+        old = np.where(np.arange(L) < lens[s] - n, want[s, h, :L], 0.0)
+        want[s, h, :L] = np.where(held, old + w.sum(0), want[s, h, :L])
+        amp[s, h, :L] = size.sum(0)
+    W = torch.from_numpy(w0).cuda()
+    got = dfl.paged_key_weights(W, q, kc, _i32(torch, table), _i32(torch, lens), torch.from_numpy(lse).cuda(),
+                                row_start=None if uniform else _i32(torch, starts), scale=scale, window=window, k_scale=ks,
+                                k_block=kb)
+    torch.cuda.synchronize()
+    assert got is W
+    g, terms = f64(W), max(rows) * group
+    with np.errstate(all="ignore"):
+        tol = hd * 2.0 ** -23 * amp + (2.0 ** -19 + terms * 2.0 ** -24) * np.abs(want) + 1e-37
+        assert np.array_equal(np.isnan(want), np.isnan(g))
+        off = np.where(np.isnan(want), 0.0, np.abs(g - want) / tol)
+    assert off.max() <= 1, (off.max(), np.argwhere(off > 1)[:4])
+    still = want == w0  # what the call does not reach stays
+    assert np.array_equal(g[still], want[still])
+
+
+KINDS = [("bf16", "bf16"), ("f16", "f16"), ("e4m3", "bf16"), ("e4m3", "f16"), ("e2m1", "bf16"), ("e2m1", "f16")]
+# a sequence's rows under a group of 8: one tile of 128 queries, three, six (the keys stay from two or three on)
+MANY = [9, 38, 88]
+
+
+@gpu
+@pytest.mark.parametrize("kind,src", KINDS)
+@pytest.mark.parametrize("rows", MANY)
+def test_weights_of_many_rows_windows(kind, src, rows):
+    """Windows shorter than a tile of keys, of some tiles, and longer than the sequence."""
+    for window, hd in ((5, 128), (140, 64), (333, 128), (5000, 64)):
+        _check_many(kind, src, 8, (rows, rows + 1), (rows + 420, rows + 90), hd=hd, window=window, page=48, seed=window)
+
+
+@gpu
+@pytest.mark.parametrize("kind,src", KINDS)
+@pytest.mark.parametrize("rows", MANY)
+def test_weights_of_many_rows_holes(kind, src, rows):
+    """Pages that are not held, rows of no sequence, a sequence without rows, rows before position 0, rows of lse -inf,
+    uniform rows (row_start None), both orders of slots and heads."""
+    nothing = [(r, h) for r in range(0, 3 * rows, 5) for h in (0, 3)] + [(rows // 2, h) for h in range(8)]
+    _check_many(kind, src, 8, (rows, 0, 3 * rows, 3), (rows + 300, 9, 3 * rows - rows // 2, 150), extra=4, nothing=nothing,
+                bad=((0, 1), (0, 2), (2, 0), (3, 1)), page=64, order="head", seed=rows)
+    _check_many(kind, src, 8, (rows,) * 3, (rows + 200, rows // 2, rows + 129), uniform=True, hd=64, nothing=nothing, kvh=2,
+                page=33, seed=rows + 1)
+
+
+@gpu
+@pytest.mark.parametrize("kind,src", KINDS)
+@pytest.mark.parametrize("rows", MANY)
+def test_weights_of_many_rows_values(kind, src, rows):
+    """Keys of NaN that all rows, some rows and one row see, and behind the last token; large scores; large queries."""
+    lens, page = (rows + 200, rows + 131), 16
+
+    def nan(kc, kb, at):
+        if kb is None:
+            kc[at][0, 7] = float("nan")
+        else:
+            kb.view(_torch().uint8)[at][0, 2] = 0x7f
+
+    def poison(torch, kc, kb, table, k64):
+        for s, p in ((0, 150), (0, lens[0] - 1 - rows // 2), (1, lens[1] - 1), (1, 3)):
+            at = int(table[s][p // page]), p % page
+            nan(kc, kb, at)
+            k64[at][0, 7] = np.nan
+        for s, l in enumerate(lens):
+            for slot in range(l % page, page if l % page else 0):
+                nan(kc, kb, (int(table[s][l // page]), slot))
+        return k64
+
+    _check_many(kind, src, 8, (rows, rows), lens, poison=poison, seed=rows, page=page)
+    _check_many(kind, src, 8, (rows, rows), lens, spread=20.0, scale=0.5, seed=rows)
+    wide = 1e3 if src == "f16" else 1e6
+    _check_many(kind, src, 8, (rows, rows), lens, spread=wide, scale=1 / wide, hd=64, seed=rows + 1)
+
+
+@gpu
+@pytest.mark.parametrize("kind,src", KINDS)
+def test_weights_of_many_rows_one_long_among_short(kind, src):
+    """One sequence's rows alone put the average over the rule; the others have one or none; heads of several groups."""
+    _check_many(kind, src, 3, (1, 1, 0, 200, 1, 1, 1, 1), (700, 40, 30, 700, 1, 129, 128, 257), kvh=3, page=7, hd=64)
+    _check_many(kind, src, 1, (300, 2), (300, 2), kvh=2, page=16)
+
+
+@gpu
+@pytest.mark.parametrize("kind,src", KINDS)
+@pytest.mark.parametrize("rows", [9, 88])
+def test_weights_of_many_rows_repeat_bit_for_bit(kind, src, rows):
+    torch, dfl = _torch(), _dfl()
+    rng = np.random.default_rng(rows)
+    lens = (1500 + rows, rows, 300 + rows)
+    table, n_pages = _layout(torch, rng, lens, (rows,) * 3, 16)
+    kc, kb, ks, k64 = _any_cache(torch, rng, (n_pages, 16, 2, 128), kind)
+    q = torch.from_numpy(rng.standard_normal((3 * rows, 16, 128)).astype(np.float32)).cuda().to(_types()[src])
+    table, lens = _i32(torch, table), _i32(torch, lens)
+    lse = torch.empty(3 * rows, 16, device="cuda")
+    same = dict(k_scale=ks, k_block=kb)
+    dfl.paged_attention(q, kc, kc, table, lens, v_block=kb, v_scale=ks, lse=lse, **same)
+    assert rows * 8 > _few_rows()
+    make = lambda: torch.zeros(3, 2, table.shape[1] * 16, device="cuda")  # noqa: E731
+    call = lambda w, **kw: dfl.paged_key_weights(w, q, kc, table, lens, lse, **same, **kw)  # noqa: E731
+    want = call(make())
+    # each row and query head hands out a weight of 1 in all, but for the scores' rounding (a sum of 128 products kept to 24
+    # bits each), the lse's too, and the exponential's
+    norm = lambda x: np.linalg.norm(x, axis=-1).max()  # noqa: E731
+    off = 2 * 128 * 2.0 ** -24 * 128 ** -0.5 * norm(f64(q)) * norm(k64) + 2.0 ** -19
+    assert (want.double().sum(-1) - 8 * rows).abs().max() <= 8 * rows * off
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    bufs = [make() for _ in range(9)]
+    torch.cuda.synchronize()
+    for i, w in enumerate(bufs):
+        call(w, stream=streams[i % 3].cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(w, want) for w in bufs)
