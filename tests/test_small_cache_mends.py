@@ -8,7 +8,7 @@ import pytest
 
 from oracle import target as O
 from test_target_ops import _cache_struct, _dfl, _i32, _layout, _rows_struct, _starts, _torch, _types, f64
-from test_target_small_cache import _any_cache, _cache4, _good, _weights_struct
+from test_target_small_cache import _any_cache, _cache4, _cached4, _good, _raw, _values4, _weights_struct
 
 gpu = pytest.mark.gpu
 
@@ -260,3 +260,88 @@ def test_weights_of_many_rows_repeat_bit_for_bit(kind, src, rows):
         call(w, stream=streams[i % 3].cuda_stream)
     torch.cuda.synchronize()
     assert all(torch.equal(w, want) for w in bufs)
+
+
+# --------------------------------------------------------------------------- 4-bit append of keys and values as they come
+def _check_bare(src="bf16", hd=128, kvh=2, page=16, rows=(1, 3), lens=(5, 40), bad=(), order="slot", extra=0, uniform=False,
+                powers=False, scaled=True, put=None, seed=0):
+    """Without queries, norms and a rotation: the kernel that is written for such calls."""
+    torch, dfl = _torch(), _dfl()
+    rng = np.random.default_rng(seed)
+    table, n_pages = _layout(torch, rng, lens, rows, page, bad=bad)
+    R = sum(rows) + extra
+    kv = torch.from_numpy(rng.standard_normal((R, 2 * kvh + 1, hd)).astype(np.float32)).cuda().to(_types()[src])
+    k, v = kv[:, :kvh], kv[:, kvh + 1:]  # slices of a wider projection
+    if put is not None:
+        put(k, v)
+    caches = [_cached4(torch, rng, (n_pages, page, kvh, hd), order)[:2] for _ in range(2)]
+    old = [[_raw(x) for x in c] for c in caches]
+    make = lambda: torch.from_numpy((np.exp2(-rng.integers(3, 7, kvh)) if powers else (0.5 + rng.random(kvh)) / 64)  # noqa: E731
+                                    .astype(np.float32)).cuda()
+    sc = [make(), make()] if scaled else [None, None]
+    starts = None if uniform else _starts(rows)
+    got = dfl.paged_append(caches[0][0], caches[1][0], k, v, _i32(torch, table), _i32(torch, lens),
+                           row_start=None if uniform else _i32(torch, starts), k_scale=sc[0], v_scale=sc[1],
+                           k_block=caches[0][1], v_block=caches[1][1])
+    torch.cuda.synchronize()
+    assert got is None
+    slots = O.paged_append(f64(k), f64(v), None, table, lens, page, n_pages, starts)[0]
+    at = tuple(np.array(x, dtype=int) for x in zip(*slots)) if slots else (np.zeros(0, int),) * 2
+    for side, (codes, blocks) in enumerate(caches):
+        # every other slot as it was
+        for x, was in zip((codes, blocks), old[side]):
+            now, before = (y.reshape(n_pages, page, kvh, -1).copy() for y in (_raw(x), was))
+            now[at] = before[at] = 0
+            assert np.array_equal(now, before)
+        if not slots:
+            continue
+        t = np.stack([kv_[side] for kv_ in slots.values()])
+        t = t / (f64(sc[side])[:, None] if scaled else 1.0)
+        g = t.reshape(*t.shape[:-1], -1, 16)
+        s, y = f64(blocks)[at], _values4(codes, blocks)[at].reshape(g.shape)
+        # x / scale and t / s (or max|t| / 6) round in 32 bits, half a step each; x / a power of two is exact
+        e = (2 if scaled and not powers else 1) * 2.0 ** -24
+        with np.errstate(all="ignore"):
+            top = np.abs(g).max(-1) / 6
+            lo, hi = O.round_e4m3(top * (1 - e)), O.round_e4m3(top * (1 + e))
+            assert np.array_equal(np.isnan(s), np.isnan(top)) and (np.isnan(s) | ((s >= lo) & (s <= hi))).all()
+            u = np.where(s[..., None] > 0, g / s[..., None], 0.0).clip(-64, 64)
+            a, b = O.round_e2m1(u * (1 - e)), O.round_e2m1(u * (1 + e))
+            y = np.where(s[..., None] > 0, y / s[..., None], 0.0)
+            ok = np.isnan(s)[..., None] | ((y >= np.minimum(a, b)) & (y <= np.maximum(a, b)))
+        assert ok.all(), (side, np.argwhere(~ok)[:4])
+
+
+def _odd_values(k, v):
+    """Blocks of zeros, of values under the smallest scale, with NaN and infinities, ties, and far beyond the largest scale."""
+    torch = _torch()
+    k[0, 0, :16] = 0.0
+    k[0, 0, 16:32] = 1e-6
+    k[0, 0, 32] = float("nan")
+    k[0, -1, 3] = float("inf")
+    k[0, -1, 20] = -float("inf")
+    v[-1, 0, 5] = 6e4
+    v[-1, 0, 6] = -6e4
+    v[-1, -1, :16] = torch.arange(16, device="cuda") / 4
+    v[-1, -1, 16:32] = -torch.arange(16, device="cuda") / 128
+    v[-1, -1, 63] = float("nan")
+
+
+@gpu
+@pytest.mark.parametrize("src", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_bare_append4(src, hd):
+    _check_bare(src, hd, powers=True, put=_odd_values, seed=hd)
+    _check_bare(src, hd, kvh=3, rows=(2, 0, 5), lens=(2, 9, 130), put=_odd_values, seed=1)
+    _check_bare(src, hd, kvh=9, scaled=False, rows=(4, 3), lens=(2, 41), extra=3, page=7, order="head", seed=2)
+    _check_bare(src, hd, kvh=1, rows=(4,) * 3, lens=(9, 4, 64), uniform=True, page=1, seed=3)
+    _check_bare(src, hd, kvh=40, rows=(4, 3, 40), lens=(2, 40, 41), bad=((1, 2), (2, 0), (2, 1), (2, 2)), page=16, extra=2, seed=5)
+
+
+@gpu
+@pytest.mark.parametrize("src", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("hd,kvh", [(64, 40), (128, 19)])
+def test_bare_append4_rounds_of_heads(src, hd, kvh):
+    """Rows enough for a warp each, with more heads than it has on their way at once."""
+    _check_bare(src, hd, kvh=kvh, rows=(900, 1), lens=(1000, 2000), page=64, powers=True, put=_odd_values, seed=6)
+    _check_bare(src, hd, kvh=kvh, rows=(300, 700), lens=(300, 700), page=48, order="head", seed=7)
