@@ -8,7 +8,7 @@ import pytest
 
 from oracle import target as O
 from test_target_ops import _cache_struct, _dfl, _i32, _layout, _rows_struct, _starts, _torch, _types, f64
-from test_target_small_cache import _any_cache, _cache4, _cached4, _good, _raw, _values4, _weights_struct
+from test_target_small_cache import (_any_cache, _cache4, _cached4, _check_evict, _good, _raw, _values4, _weights_struct)
 
 gpu = pytest.mark.gpu
 
@@ -345,3 +345,23 @@ def test_bare_append4_rounds_of_heads(src, hd, kvh):
     """Rows enough for a warp each, with more heads than it has on their way at once."""
     _check_bare(src, hd, kvh=kvh, rows=(900, 1), lens=(1000, 2000), page=64, powers=True, put=_odd_values, seed=6)
     _check_bare(src, hd, kvh=kvh, rows=(300, 700), lens=(300, 700), page=48, order="head", seed=7)
+
+
+# --------------------------------------------------------------------------- eviction from many heads
+# (type, head_dim): rows that a CTA moves at a time where a (sequence, head)'s keys are one CTA's
+ROUND = {("bf16", 128): 128, ("f16", 64): 256, ("e4m3", 128): 256, ("e2m1", 128): 512, ("e4m3", 64): 512, ("e2m1", 64): 1024}
+
+
+@gpu
+@pytest.mark.parametrize("kind,hd", ROUND)
+@pytest.mark.parametrize("rounds,aside", [(2, False), (3, True), (5, False)])
+def test_evict_many_heads_in_rounds(kind, hd, rounds, aside):
+    """Heads enough for the whole-row form, an even and odd number of rounds, the last one whole or not; weights and
+    block scales, whose rounds are 2048 tokens, take several too with the longest."""
+    keep = rounds * ROUND[kind, hd] - (0 if rounds == 2 else 5)
+    n, kvh = (8, 8) if keep < 3000 else (13, 4)
+    assert 3 * n * kvh >= _torch().cuda.get_device_properties(0).multi_processor_count
+    rng = np.random.default_rng(keep)
+    lens = [keep, keep + 1, keep - 1, 2 * keep + 7] + [int(keep + rng.integers(2, keep)) for _ in range(n - 4)]
+    _check_evict(kind, hd, kvh=kvh, page=48, lens=lens, keep=keep, first=3, recent=keep // 4, aside=aside, order="head" if aside else "slot",
+                 given=not aside, bad=((3, 1),), seed=rounds)
