@@ -20,15 +20,6 @@ def lib():
     return _dfl().lib()
 
 
-
-
-@pytest.fixture(scope="module")
-def lib():
-    from block_speculative_drafting_gb300.csrc.build import build
-    build()
-    return _dfl().lib()
-
-
 # --------------------------------------------------------------------------- evict: keys and values are apart
 @pytest.mark.parametrize("cache,bad", [(_cache_struct, dict(v=4096)), (_cache4, dict(v=4096)), (_cache4, dict(v_block=4096)),
                                        (_cache4, dict(v=4096, v_block=4096))], ids=["bf16", "codes", "blocks", "both"])
