@@ -632,79 +632,79 @@ __global__ void __launch_bounds__(kPaThreads) paged_join_kernel(const __grid_con
     const int c0 = blockIdx.x, c1 = e.last;
     int h = e.head;
     if (c1 > c0) {
-    const int rows = TOGETHER && e.together > 1 ? e.together * e.mt : e.rows;
+        const int rows = TOGETHER && e.together > 1 ? e.together * e.mt : e.rows;
 #pragma unroll 1
-    for (int mrow = 16 * blockIdx.y + warp; mrow < min(rows, 16 * (int)blockIdx.y + 16); mrow += kPaWarps) {
-    int of = mrow;  // of its head
-    if (TOGETHER && e.together > 1) {
-        h = e.head + mrow / e.mt;
-        of = mrow % e.mt;
-        if (of >= e.rows) continue;
-    }
-    const int mm = e.m0 + of, row = e.row0 + mm / A.group, hq = h * A.group + mm % A.group;
-    constexpr int V = HD / 32;  // columns a lane
-    float m = -INFINITY, l = 0.f, o[V] = {};
-    // parts in order, 32 references and sums at a time, 8 outputs in flight (16 are more code: 40.3 -> 42.6 us, one block
-    // over 32768 keys)
-    for (int b = c0; b <= c1; b += 32) {
-        const int n = min(32, c1 - b + 1);
-        float2 x = make_float2(-INFINITY, 0.f);
-        auto slot = [&](int c) { return (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * mt + mrow; };
-        if (lane < n) x = A.ws_ml[slot(b + lane)];
-        constexpr int U = 8;
-        float y[U][V];
-        auto load = [&](int k0) {
+        for (int mrow = 16 * blockIdx.y + warp; mrow < min(rows, 16 * (int)blockIdx.y + 16); mrow += kPaWarps) {
+            int of = mrow;  // of its head
+            if (TOGETHER && e.together > 1) {
+                h = e.head + mrow / e.mt;
+                of = mrow % e.mt;
+                if (of >= e.rows) continue;
+            }
+            const int mm = e.m0 + of, row = e.row0 + mm / A.group, hq = h * A.group + mm % A.group;
+            constexpr int V = HD / 32;  // columns a lane
+            float m = -INFINITY, l = 0.f, o[V] = {};
+            // parts in order, 32 references and sums at a time, 8 outputs in flight (16 are more code: 40.3 -> 42.6 us, one
+            // block over 32768 keys)
+            for (int b = c0; b <= c1; b += 32) {
+                const int n = min(32, c1 - b + 1);
+                float2 x = make_float2(-INFINITY, 0.f);
+                auto slot = [&](int c) { return (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * mt + mrow; };
+                if (lane < n) x = A.ws_ml[slot(b + lane)];
+                constexpr int U = 8;
+                float y[U][V];
+                auto load = [&](int k0) {
 #pragma unroll
-            for (int k = 0; k < U; ++k)
-                if (k0 + k < n) {
-                    const float* p = A.ws_o + slot(b + k0 + k) * HD + V * lane;
-                    if constexpr (V == 4) {
-                        const float4 q = *reinterpret_cast<const float4*>(p);
-                        y[k][0] = q.x, y[k][1] = q.y, y[k][2] = q.z, y[k][3] = q.w;
-                    } else {
-                        const float2 q = *reinterpret_cast<const float2*>(p);
-                        y[k][0] = q.x, y[k][1] = q.y;
+                    for (int k = 0; k < U; ++k)
+                        if (k0 + k < n) {
+                            const float* p = A.ws_o + slot(b + k0 + k) * HD + V * lane;
+                            if constexpr (V == 4) {
+                                const float4 q = *reinterpret_cast<const float4*>(p);
+                                y[k][0] = q.x, y[k][1] = q.y, y[k][2] = q.z, y[k][3] = q.w;
+                            } else {
+                                const float2 q = *reinterpret_cast<const float2*>(p);
+                                y[k][0] = q.x, y[k][1] = q.y;
+                            }
+                        }
+                };
+                load(0);
+                const float to = fmaxf(m, warp_max(x.x));
+                const float fm = m == to ? 1.f : pa_exp2(m - to);
+                const float f = x.x == -INFINITY ? 1.f : pa_exp2(x.x - to);  // (without a maximum the sums are 0 or NaN)
+                m = to;
+                l = l * fm + warp_sum(x.y * f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[i] *= fm;
+                for (int k0 = 0; k0 < n; k0 += U) {
+                    if (k0 > 0) load(k0);
+#pragma unroll
+                    for (int k = 0; k < U; ++k) {
+                        const float w = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+                        if (k0 + k < n) {
+#pragma unroll
+                            for (int i = 0; i < V; ++i) o[i] = fmaf(w, y[k][i], o[i]);
+                        }
                     }
                 }
-        };
-        load(0);
-        const float to = fmaxf(m, warp_max(x.x));
-        const float fm = m == to ? 1.f : pa_exp2(m - to);
-        const float f = x.x == -INFINITY ? 1.f : pa_exp2(x.x - to);  // (without a maximum the sums are 0 or NaN)
-        m = to;
-        l = l * fm + warp_sum(x.y * f);
+            }
+            const float inv = l == 0.f ? 0.f : (e8 && A.C.v_scale != nullptr ? A.C.v_scale[h] : 1.f) / l;
+            unsigned char* p = A.out.p + (int64_t)row * A.out.rs + (int64_t)hq * A.out.hs + V * lane * 2;
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] *= fm;
-        for (int k0 = 0; k0 < n; k0 += U) {
-            if (k0 > 0) load(k0);
+            for (int i = 0; i < V; i += 2)
+                *reinterpret_cast<uint32_t*>(p + 2 * i) = A.out.dtype == kBF16 ? pack2<true>(o[i] * inv, o[i + 1] * inv)
+                                                                               : pack2<false>(o[i] * inv, o[i + 1] * inv);
+            if (A.lse != nullptr && lane == 0)
+                A.lse[(int64_t)row * A.q.heads + hq] =
+                    l == 0.f ? -INFINITY : (m == -INFINITY ? l : (m + log2f(l)) * 0.69314718056f);
+            if (!e8 && pa_weighs(l)) {
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const float w = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
-                if (k0 + k < n) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) o[i] = fmaf(w, y[k][i], o[i]);
-                }
+                for (int i = 0; i < V; ++i)
+                    if (o[i] != o[i]) {
+                        reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(A.out.dtype == kBF16 ? kPaOdd<true> : kPaOdd<false>);
+                        any = true;
+                    }
             }
         }
-    }
-    const float inv = l == 0.f ? 0.f : (e8 && A.C.v_scale != nullptr ? A.C.v_scale[h] : 1.f) / l;
-    unsigned char* p = A.out.p + (int64_t)row * A.out.rs + (int64_t)hq * A.out.hs + V * lane * 2;
-#pragma unroll
-    for (int i = 0; i < V; i += 2)
-        *reinterpret_cast<uint32_t*>(p + 2 * i) = A.out.dtype == kBF16 ? pack2<true>(o[i] * inv, o[i + 1] * inv)
-                                                                       : pack2<false>(o[i] * inv, o[i + 1] * inv);
-    if (A.lse != nullptr && lane == 0)
-        A.lse[(int64_t)row * A.q.heads + hq] =
-            l == 0.f ? -INFINITY : (m == -INFINITY ? l : (m + log2f(l)) * 0.69314718056f);
-    if (!e8 && pa_weighs(l)) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (o[i] != o[i]) {
-                reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(A.out.dtype == kBF16 ? kPaOdd<true> : kPaOdd<false>);
-                any = true;
-            }
-    }
-    }
     }
     // this warp's joined rows with NaN that is kept apart; then, where the share's whole units have some, all of the call's
     // rows, dealt out over the warps of all such shares
