@@ -13,7 +13,8 @@
 // bf16 keys, 8 heads of 128: 33 us, 4.9 TB/s, where k_paged_weights.cu takes 40), with a
 // block the MMAs and, over 4 bits, the conversions (16 rows of four query heads over
 // 32768 keys: 22 us and 28; the MMAs alone, one of 16 x 8 x 16 every two clocks and SM, 7).  Rows beyond 64 go by in sets of 64, the CTA's
-// warps in step (a sequence that has many more rows than the call's average).
+// warps in step (a sequence that has many more rows than the call's average); its tiles count once for each set in the
+// line (400 rows and 31 single ones over 4096 keys each: 200 us; with tiles alike, a few CTAs had all of those rows' work, 1956).
 //
 // Keys that only some rows see, rows of lse -inf and columns without a row are
 // left out of a tile's sums one by one.
@@ -88,13 +89,13 @@ __global__ void __launch_bounds__((PfShape<CB, HD>::kThreads), 1) paged_weights_
     pdl_trigger();
 
     int chunk;
-    PaCur cur = pa_share<kPfKeys>(A, kAll, kPfOver, lane, chunk);
+    PaCur cur = pa_share<kPfKeys, false, kPfRows>(A, kAll, kPfOver, lane, chunk);
     if (cur.left <= 0) return;
-    auto tiles_of = [](const PaCur& c) { return min(c.q.ntiles - c.tile, c.left); };
+    auto tiles_of = [&](const PaCur& c) { return pa_tiles<kPfRows>(A, c); };
     auto skip = [&](PaCur& c, int n) {
-        c.left -= n - 1;
+        c.left -= (n - 1) * pa_places<kPfRows>(A, c.q);
         c.tile += n - 1;
-        pa_next<kPfKeys>(A, kAll, c);
+        pa_next<kPfKeys, false, kPfRows>(A, kAll, c);
     };
 
     // Rows 64 x .. of a unit to shared memory, in the MMAs' order: a warp takes eight rows, lane (gq, tq) of row gq the columns

@@ -1,4 +1,4 @@
-// What the two kernels of the attention over a paged cache share: the line of
+// What the kernels of the attention over a paged cache and of its keys' weights share: the line of
 // work that the CTAs cut into equal parts and the walk along it, asynchronous
 // copies, and conversions of 16-bit and 8-bit floats.
 #pragma once
@@ -65,12 +65,25 @@ DF_DEV PaSeq pa_seq(const PaArgs& A, int s, int a, int b, int mt) {
 // CTA to end one unit and begin another, so that shares of equal length take
 // equal time.  ov is 0 where most CTAs hold a tile or two: there a place
 // without a tile would be an idle CTA.  (The line is shorter than 2^31: pa_line_fits.)
+// SET > 0: a unit is all rows of a sequence's head, SET of them at a time, and a tile takes as many places as there are
+// such sets; it is in the share that holds its first one.
 struct PaCur {
     PaSeq q;
     int s, u, tile;  // tile `tile` of unit `u` of sequence `s`
     int ov;
-    int left;  // places of the CTA's share from here on (0: none)
+    int left;  // places of the CTA's share from here on (0 or below: none)
 };
+template <int SET>
+DF_DEV int pa_places(const PaArgs& A, const PaSeq& q) {
+    return SET > 0 ? max(1, (q.rows * A.group + SET - 1) / max(SET, 1)) : 1;
+}
+// Tiles of the unit at c that are the share's.
+static __device__ __noinline__ int pa_ceil_div(int a, int b) { return (a + b - 1) / b; }
+template <int SET>
+DF_DEV int pa_tiles(const PaArgs& A, const PaCur& c) {
+    const int n = pa_places<SET>(A, c.q);
+    return min(c.q.ntiles - c.tile, n == 1 ? c.left : pa_ceil_div(c.left, n));
+}
 // The end of sequence s's rows, which start at a.
 DF_DEV int rows_end(const PagedRows& R, int s, int a) {
     return R.row_start == nullptr ? a + R.per : max(row_start_at(R, s + 1), a);
@@ -92,9 +105,45 @@ DF_DEV void rows_of_lane(const PagedRows& R, int s0, int from, int lane, int& a,
         if (lane == 0) a = from;
     }
 }
+// One tile on.
+template <int TILE = kPaTile, bool TOGETHER = false, int SET = 0>
+DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c, int heads = 1) {
+    c.left -= pa_places<SET>(A, c.q);
+    if (++c.tile < c.q.ntiles) return;
+    c.tile = 0;
+    c.left -= c.ov;
+    if (c.left <= 0) {
+        c.left = 0;
+        return;
+    }
+    if (++c.u < c.q.nunits) return;
+    c.u = 0;
+    do {
+        if (++c.s >= A.R.n_seqs) {  // (never, while the lengths stay as they were counted)
+            c.left = 0;
+            return;
+        }
+        const int a = c.q.row0 + c.q.rows;
+        c.q = pa_seq<TILE>(A, c.s, a, rows_end(A.R, c.s, a), mt);
+        if constexpr (TOGETHER) c.q.nunits /= heads;
+    } while (c.q.nunits == 0);
+}
+// From c.tile places into a unit to the first tile that begins there or later (out of line, as is the division: few calls
+// have such units, and their code is fetched once a call).
+template <int TILE, int SET>
+__device__ __noinline__ void pa_begin(const PaArgs& A, int mt, PaCur& c) {
+    const int places = pa_places<SET>(A, c.q), at = c.tile;
+    c.tile = (at + places - 1) / places;
+    c.left = max(c.left - (c.tile * places - at), 0);
+    if (c.left > 0 && c.tile == c.q.ntiles) {  // (another unit's)
+        --c.tile;
+        c.left += places;
+        pa_next<TILE, false, SET>(A, mt, c);
+    }
+}
 // This CTA's share (warp-wide); `chunk`: the places of a share.  TOGETHER: in a line of at least `many` tiles, or with a unit
 // for each CTA, a unit is A.together heads (of one row tile), a tile the keys of all of them; `heads`: as many as a unit has.
-template <int TILE = kPaTile, bool TOGETHER = false>
+template <int TILE = kPaTile, bool TOGETHER = false, int SET = 0>
 DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk, int many = 0, int* heads = nullptr) {
     int64_t t64 = 0, v64 = 0;
     // (the first 32 sequences are looked at once)
@@ -109,7 +158,7 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk, in
         if (s0 + lane >= A.R.n_seqs) continue;
         const PaSeq q = pa_seq<TILE>(A, s0 + lane, a, b, mt);
         if (s0 == 0) q0 = q;
-        t64 = min(t64 + (int64_t)q.ntiles * q.nunits, (int64_t)1 << 40);
+        t64 = min(t64 + (int64_t)q.ntiles * q.nunits * pa_places<SET>(A, q), (int64_t)1 << 40);
         v64 = min(v64 + q.nunits, (int64_t)1 << 40);
     }
     PaCur c{};
@@ -144,7 +193,7 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk, in
         }
         if constexpr (TOGETHER) q.nunits /= *heads;
         from = __shfl_sync(0xffffffffu, b, 31);
-        const int w = s0 + lane < A.R.n_seqs ? (q.ntiles + c.ov) * q.nunits : 0;
+        const int w = s0 + lane < A.R.n_seqs ? (q.ntiles * pa_places<SET>(A, q) + c.ov) * q.nunits : 0;
         int in = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -163,41 +212,25 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk, in
             c.q.hi = __shfl_sync(0xffffffffu, q.hi, l);
             c.q.ntiles = __shfl_sync(0xffffffffu, q.ntiles, l);
             c.q.nunits = __shfl_sync(0xffffffffu, q.nunits, l);
-            const int per = c.q.ntiles + c.ov;
+            const int places = pa_places<SET>(A, c.q), per = c.q.ntiles * places + c.ov;
             c.u = x / per;
             const int v = x - c.u * per;
             c.left = min(chunk, total - t);
-            if (v < c.ov)
+            if (v < c.ov) {
                 c.left = max(c.left - (c.ov - v), 0);
-            else
+            } else {
                 c.tile = v - c.ov;
+                if (SET > 0 && places > 1) {
+                    PaCur x = c;  // (the copy alone is in memory)
+                    pa_begin<TILE, SET>(A, mt, x);
+                    c = x;
+                }
+            }
             return c;
         }
         run += __shfl_sync(0xffffffffu, in, 31);
     }
     return c;
-}
-template <int TILE = kPaTile, bool TOGETHER = false>
-DF_DEV void pa_next(const PaArgs& A, int mt, PaCur& c, int heads = 1) {
-    --c.left;
-    if (++c.tile < c.q.ntiles) return;
-    c.tile = 0;
-    c.left -= c.ov;
-    if (c.left <= 0) {
-        c.left = 0;
-        return;
-    }
-    if (++c.u < c.q.nunits) return;
-    c.u = 0;
-    do {
-        if (++c.s >= A.R.n_seqs) {  // (never, while the lengths stay as they were counted)
-            c.left = 0;
-            return;
-        }
-        const int a = c.q.row0 + c.q.rows;
-        c.q = pa_seq<TILE>(A, c.s, a, rows_end(A.R, c.s, a), mt);
-        if constexpr (TOGETHER) c.q.nunits /= heads;
-    } while (c.q.nunits == 0);
 }
 // The entry of a unit that begins in this CTA's share and has `rest` tiles after it.
 DF_DEV PaJoin pa_join_entry(const PaCur& c, int rt, int mt, int rows, int head, int rest, int chunk) {

@@ -98,13 +98,13 @@ def _few_rows():
 
 
 def _check_many(kind, src, group, rows, lens, kvh=1, hd=128, page=16, window=0, uniform=False, bad=(), order="slot", extra=0,
-                scale=None, seed=0, spread=1.0, poison=None, nothing=()):
-    """A call that the tcgen05 kernel serves, against the formula in 64 bits.  Tolerances as in test_target_small_cache.py."""
+                scale=None, seed=0, spread=1.0, poison=None, nothing=(), few=False):
+    """A call that the tcgen05 kernel serves (or with `few` the warp-MMA one), against the formula in 64 bits.  Tolerances as in test_target_small_cache.py."""
     torch, dfl = _torch(), _dfl()
     rng = np.random.default_rng(seed)
     table, n_pages = _layout(torch, rng, [max(l, 0) for l in lens], rows, page, bad=bad)
     R, heads, cap, starts = sum(rows) + extra, group * kvh, table.shape[1] * page, None if uniform else _starts(rows)
-    assert -(-R // len(lens)) * group > _few_rows()
+    assert (-(-R // len(lens)) * group > _few_rows()) != few
     q = torch.from_numpy(spread * rng.standard_normal((R, heads, hd)).astype(np.float32)).cuda().to(_types()[src])
     kc, kb, ks, k64 = _any_cache(torch, rng, (n_pages, page, kvh, hd), kind, order)
     if poison is not None:
@@ -251,6 +251,48 @@ def test_weights_of_many_rows_repeat_bit_for_bit(kind, src, rows):
         call(w, stream=streams[i % 3].cuda_stream)
     torch.cuda.synchronize()
     assert all(torch.equal(w, want) for w in bufs)
+
+
+# --------------------------------------------------------------------------- key weights, many rows of one sequence among few
+@gpu
+@pytest.mark.parametrize("kind,src", KINDS)
+@pytest.mark.parametrize("hd", [64, 128])
+def test_weights_of_one_long_sequence_among_short_ones(kind, src, hd):
+    """Sequences of several sets of 64 rows in a call that the warp-MMA kernel serves: shares of the line end in their tiles."""
+    rng = np.random.default_rng(hd)
+    for at, long, group, kvh, window, n in ((0, 75, 8, 2, 0, 20), (30, 150, 4, 1, 0, 31), (7, 260, 3, 2, 200, 40), (35, 40, 5, 3, 0, 36)):
+        rows = [int(x) for x in rng.integers(0, 2, n)]
+        lens = [int(x) for x in rng.integers(1, 200, n)]
+        rows[at], lens[at] = long, long + int(rng.integers(300, 700))
+        rows[n // 2], lens[n // 2] = long // 2, long // 3  # (rows before position 0, and few keys)
+        _check_many(kind, src, group, tuple(rows), tuple(lens), kvh=kvh, hd=hd, window=window, page=48, few=True, seed=at)
+
+
+@gpu
+def test_weights_of_one_long_sequence_among_short_ones_cost_what_both_do():
+    """31 sequences of one row and one of 400: once 26 times the two calls on their own (a few CTAs had all of its rows).  The
+    bound is 5 times: fixed times, and a kernel for few rows."""
+    torch, dfl = _torch(), _dfl()
+    L, page = 4096, 64
+    kc = torch.randn(32 * L // page, page, 8, 128, device="cuda").to(torch.bfloat16)
+    table = torch.arange(32 * L // page, dtype=torch.int32, device="cuda").view(32, -1)
+
+    def time(rows):
+        n, R = len(rows), sum(rows)
+        q, lse = torch.randn(R, 32, 128, device="cuda").to(torch.bfloat16), torch.full((R, 32), 9.0, device="cuda")
+        w, start, lens = torch.zeros(n, 8, L, device="cuda"), _i32(torch, _starts(rows)), _i32(torch, (L,) * n)
+        t = []
+        for _ in range(7):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(4):
+                dfl.paged_key_weights(w, q, kc, table[:n], lens, lse, row_start=start)
+            b.record()
+            torch.cuda.synchronize()
+            t.append(a.elapsed_time(b))
+        return sorted(t)[3]
+
+    assert time((1,) * 31 + (400,)) < 5 * (time((1,) * 32) + time((400,)))
 
 
 # --------------------------------------------------------------------------- 4-bit append of keys and values as they come
