@@ -295,6 +295,7 @@ int dflash_paged_evict(const dflash_paged_cache* cache, const dflash_paged_rows*
         return fail(DFLASH_EINVAL, "out in weights' place needs its strides");
     if (new_len == nullptr || !al4(new_len) || !al4(kept) || !al4(evicted))
         return fail(DFLASH_EINVAL, "new_len is NULL, or new_len, kept or evicted not 4-byte aligned");
+    if (new_len == evicted) return fail(DFLASH_EINVAL, "new_len and evicted are one memory");
     if (workspace == nullptr || !al16(workspace))
         return fail(DFLASH_EINVAL, "workspace is NULL or not 16-byte aligned");
     if (workspace_bytes < need)

@@ -712,7 +712,7 @@ DFLASH_API int dflash_paged_key_weights(const dflash_paged_cache* cache, const d
  *   kept       int32 [n_seqs][kv_heads][keep] or NULL: the position that each
  *              token of the new cache had (-1 from the new length on)
  *   evicted    int32 [n_seqs] or NULL: grows by L - new_len, as
- *              dflash_paged_append_at takes it
+ *              dflash_paged_append_at takes it; apart from new_len
  * A token moves from or to a position that is not held: its keys and values are
  * not written.  keep >= 1, first and recent >= 0, first + recent <= keep.
  * workspace: at least dflash_paged_evict_workspace bytes (own_kept: 1 where

@@ -35,6 +35,16 @@ def test_evict_refuses_keys_and_values_in_one_memory(lib, cache, bad):
     assert call(cache(**bad), _rows_struct(n_rows=0, n_seqs=0)) == 0
 
 
+def test_evict_refuses_lengths_and_counts_in_one_memory(lib):
+    """The counts grow by what is taken out, the lengths are set: of one memory they were the sum of both."""
+    from block_speculative_drafting_gb300 import _abi
+    w, r, c = _weights_struct(), _rows_struct(n_rows=0), _cache4()
+    call = lambda new, evicted: lib.dflash_paged_evict(C.byref(c), C.byref(r), 8, 2, 3, C.byref(w), C.byref(w), new, None,  # noqa: E731
+                                                       evicted, 4096, 16, None)
+    assert call(8192, 8192) == _abi.DFLASH_EINVAL and b"one memory" in lib.dflash_last_error(None)
+    assert call(8192, 12288) == call(4096, 8192) == _abi.DFLASH_ECAPACITY  # (4096 is kv_len: new_len may be)
+
+
 @gpu
 def test_evict_refuses_one_tensor_as_keys_and_values():
     torch, dfl = _torch(), _dfl()
