@@ -12,9 +12,11 @@
 // is then rescaled in place.  P is a hi + lo pair (the products then add no
 // rounding of their own to the output's; with a 16-bit cache the tensor pipe has the
 // time: a tile's MMAs take 0.8 us, its 64 KB 1.4 us of this SM's share of the
-// memory).  Only bf16 outputs over an e4m3 cache take P as one f16: off by 2^-11 of
-// each key's part at most, an eighth of the output's own 2^-8, where the pair costs
-// 17 % (32 blocks 65.5 -> 76.5 us: the softmax's registers and conversions).
+// memory).  Only bf16 outputs over 8 or 4 bits take P as one f16: off by 2^-11 of
+// each key's part at most, an eighth of the output's own 2^-8 (32 blocks over 4 bits are
+// 1.671e-3 of their norm from 64 bits, 1.659e-3 with the pair), where the pair costs
+// 7 to 8 % (32 blocks over e4m3 64.2 -> 68.8 us, over 4 bits 65.0 -> 70.3: the softmax's
+// registers and conversions).
 //
 // An MMA of M 128 costs what it costs with fewer rows, so a unit of up to 64
 // rows holds every query twice: lanes r and r + 64 take the lower and the upper
@@ -44,7 +46,7 @@
 // 8 heads: 186 us, 6.8 TB/s), 1.26 us with an e4m3 one (173 us) and 1.25 with 4 bits (171 us), the
 // softmax and the codes' way into the slots (an e2m1 lane's 16 bytes are 32 elements of a row and
 // two block scales: paged_tile.cuh).  32 blocks over 1024 to 4096 keys: 65, 64 and 65 us; f16
-// queries over e4m3 67.  A unit's end and the next one's beginning take about
+// queries over e4m3 67, over 4 bits 69.  A unit's end and the next one's beginning take about
 // 4 us, of which a tile that some rows see in part 2 and the outputs 2; start,
 // epilogue and join of a call 13.
 //
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__((PtShape<BF, CB, HD>::kThreads), 1)
         // ------------------------------------------------------------ MMAs
         // Two warps, so that the waits of one fall into the other's MMAs: an issuing thread is held up to within
         // three or four MMAs of the pipe, and one warp's waits left the pipe idle for 0.6 us a tile.
-        // (whole-warp values, said so to the compiler: see pt_mma)
+        // (whole-warp values, said so to the compiler: see pt_elect in paged_tile.cuh)
         auto whole_warp = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         constexpr uint32_t kType = PB ? (1u << 7) | (1u << 10) : 0u;  // A, B: bf16, or f16

@@ -24,9 +24,9 @@
 // score buffers of 128 columns go round: the next products run while the last ones'
 // exponentials do.  Codes and bf16 queries meet in f16 where the keys go by (a
 // query row is brought into it by a power of two), and in bf16 where they stay (codes
-// times block scales, of 6 bits at most, are exact in either).  (Fewer than 64 rows a head, on average, are k_paged_weights_few.cu's.)
+// times block scales, of 6 bits at most, are exact in either).  (Up to 64 rows a head, on average, are k_paged_weights_few.cu's.)
 //
-// 2048 rows of four query heads over 16384 bf16 keys x 8 heads: 289 us, 0.9 PFLOP/s, 49 % of
+// 2048 rows of four query heads over 16384 bf16 keys x 8 heads: 289 us, 0.89 PFLOP/s, 47 % of
 // a large product's rate.  The sums bound it: two warps a quarter of an SM take some 2000 clocks for
 // a step's 256 x 128 scores, whose exponentials alone are 1024; the CTAs' shares end 15 % apart.
 //
@@ -824,7 +824,8 @@ int paged_key_weights(const PagedCache& C, int cache_dtype, int hd, const PagedR
     A.by_group = fast_div(A.group);
     if (R.cap == 0) return 0;
     // few rows a sequence's head, on average: the warp MMAs (over 32768 e2m1 keys of 8 heads, four query heads each:
-    // 16 rows 22 us and 28 below, 20 rows 34 and 30; 32 sequences of 2048 bf16 keys: one row 28 and 39, 16 rows 45 and 42)
+    // 16 rows 22 us and 28 below, 20 rows 34 and 30; 32 sequences of 2048 bf16 keys: one row 28 and 39, 16 rows 45 and 42;
+    // rows unlike each other: 31 single ones over 4096 keys and one sequence of 400 200 us there, of 600 103 here)
     const int64_t per = ((int64_t)R.n_rows + R.n_seqs - 1) / R.n_seqs * A.group;
     if (per <= 64) {
         PaArgs F{};

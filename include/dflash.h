@@ -630,8 +630,8 @@ DFLASH_API int dflash_paged_append_at(const dflash_paged_cache* cache, const dfl
 
 /*
  * The keys and values that the cache holds for the call's rows, as values:
- * code * block scale * head's scale (or the element itself), rounded to the
- * output's type once.  k_out, v_out: kv_heads heads, one type, apart from each
+ * code * block scale (exact) times the head's scale, rounded to 32 bits and then
+ * to the output's type (or the element itself, rounded to the output's type).  k_out, v_out: kv_heads heads, one type, apart from each
  * other and from the cache; either may be NULL.  A row whose position is not
  * held reads as zeros.
  * Errors: EINVAL, EGEOM, ECUDA.
