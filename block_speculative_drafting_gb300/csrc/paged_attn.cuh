@@ -221,9 +221,9 @@ DF_DEV PaCur pa_share(const PaArgs& A, int mt, int ovh, int lane, int& chunk, in
             } else {
                 c.tile = v - c.ov;
                 if (SET > 0 && places > 1) {
-                    PaCur x = c;  // (the copy alone is in memory)
-                    pa_begin<TILE, SET>(A, mt, x);
-                    c = x;
+                    PaCur y = c;  // (the copy alone is in memory)
+                    pa_begin<TILE, SET>(A, mt, y);
+                    c = y;
                 }
             }
             return c;
